@@ -622,6 +622,148 @@ int qmm_decode_attention(const void *q, const void *K, const void *V, const int 
                          int B, int Hq, int Hkv, int Lmax, int D, float scale, int splits_req,
                          void *workspace, size_t ws_bytes, void *stream, int *splits_used);
 
+/* ---- paged KV cache: append with rotation, tree attention, accepted path ---
+ *
+ * Speculative decoding around the matmuls above ("Optimize Prefill vs Decode
+ * Kernels": decode runs few query tokens against a long history): a draft
+ * model proposes a tree of tokens, one pass of the target model verifies all
+ * of them, and the accepted path stays in the cache.  With one token per
+ * sequence the same calls are plain decode, with a chain they append and
+ * verify in order.  One step of one layer:
+ *   qmm_kv_append       rotate q and k, write k and v behind the history
+ *   qmm_tree_attention  every drafted token attends to the history, its
+ *                       ancestors and itself
+ * and, once per step for all layers,
+ *   qmm_tree_accept     follow the target's choices down the tree and move the
+ *                       accepted rows to the front of the drafted ones.
+ *
+ * The cache of one layer.  K and V are pools of pages of page_size slots,
+ *   K, V   [num_pages, Hkv, page_size, D], dtype elements, the D values of a
+ *          row contiguous; the other strides are the caller's (page_stride,
+ *          head_stride, slot_stride, in elements, the same for K and V), so
+ *          pages of [page_size, Hkv, D] fit as well.  16-byte aligned, each
+ *          stride a multiple of 16 bytes and at least D where its extent is
+ *          over 1.
+ *   table  device int32 [B, max_pages]: slot s of sequence b is row
+ *          s % page_size of page table[b, s / page_size].  An entry outside
+ *          [0, num_pages) is no page: nothing is written there and attention
+ *          leaves its positions out.  No page may hold slots of two
+ *          sequences that a call writes.
+ *   lens   device int32 [B]: the tokens already in the cache (values outside
+ *          [0, max_pages * page_size] are clamped).  The calls' new tokens
+ *          take slots lens[b], lens[b] + 1, ...; slots past the table's end
+ *          do not exist.
+ *   dtype  QMM_CACHE_BF16, or QMM_CACHE_E4M3: a stored value stands for
+ *          k_scale (v_scale) times its E4M3 number.  k_scale and v_scale are
+ *          positive and finite; 1 for BF16.
+ * D is 64 or 128; page_size a power of two from 8 to 65536. */
+enum { QMM_CACHE_BF16 = 0, QMM_CACHE_E4M3 = 1 };
+typedef struct {
+    void *K, *V;       /* device */
+    const int *table;  /* device */
+    const int *lens;   /* device */
+    int64_t page_stride, head_stride, slot_stride;
+    int B, num_pages, page_size, max_pages, Hkv, D, dtype;
+    float k_scale, v_scale;
+} qmm_kv_cache;
+
+/* The rotation of q and k, and the per-head norm before it.
+ *   cos_sin      device FP32 [rows, dim]: row p holds cos(p w_j) for
+ *                j = 0 .. dim/2-1, then sin(p w_j)
+ *   dim          rotated leading values of each head: a multiple of 16, at
+ *                most D; 0 rotates nothing (cos_sin may be NULL)
+ *   interleaved  0: pair j is (j, j + dim/2); 1: (2j, 2j + 1)
+ *   q_norm, k_norm  device BF16 [D], nullable: x * w / sqrt(mean(x^2) + eps)
+ *                per head, before the rotation */
+typedef struct {
+    const float *cos_sin;
+    const void *q_norm, *k_norm;
+    int rows, dim, interleaved;
+    float eps;
+} qmm_rope;
+
+/* Rotate and append N new tokens, those of a sequence side by side.
+ *   cu   device int32 [B + 1], nullable: tokens cu[b] .. cu[b+1]-1 are
+ *        sequence b's (ascending, cu[B] <= N; tokens outside every range are
+ *        left alone).  NULL: N / B tokens each (N a multiple of B).
+ *   Token i of sequence b, with q, k, v rows of Hq, Hkv, Hkv heads of D BF16
+ *   values (the heads contiguous, token strides q_stride, k_stride, v_stride
+ *   and q_out_stride in elements, multiples of 8):
+ *     K[slot lens[b] + i] = rotated k, V[same slot] = v, q_out = rotated q,
+ *   in FP32 with one rounding: to BF16, or for an E4M3 cache of x / scale to
+ *   the nearest E4M3 number, at most +-448.
+ *   positions  device int32 [N], nullable: the rows of cos_sin; NULL:
+ *        lens[b] + i.  A token whose position is outside [0, rows) is left
+ *        alone when there is a rotation: no q_out row, nothing stored.
+ *   q and q_out may be NULL with Hq = 0 (only append); q_out may be q itself
+ *   (same stride), and overlaps no other input.  rope may be NULL.
+ * A sequence's new slots may not repeat another's pages.  lens is not
+ * changed.  One launch.  Returns QMM_OK, QMM_EINVAL, QMM_ESHAPE, QMM_EALIGN,
+ * QMM_ENODEV or QMM_ECUDA. */
+int qmm_kv_append(const qmm_kv_cache *cache, const void *q, const void *k, const void *v,
+                  void *q_out, int N, int Hq, int64_t q_stride, int64_t k_stride,
+                  int64_t v_stride, int64_t q_out_stride, const int *cu, const int *positions,
+                  const qmm_rope *rope, void *stream);
+
+/* Attention of up to T drafted tokens per sequence over the cache, which
+ * already holds their keys and values at slots lens[b] + i (qmm_kv_append).
+ *   q     BF16 [N, Hq, D], token stride q_stride (elements, a multiple of 8),
+ *         heads contiguous; Hq a multiple of Hkv, at most 64 query heads per
+ *         KV head
+ *   O     BF16 [N, Hq, D], contiguous; rows of no sequence are left alone
+ *   cu    as in qmm_kv_append; NULL: T tokens each and N = B * T.  A range of
+ *         more than T tokens counts as its first T.
+ *   parents  device int32 [N], nullable: the parent of token i within its
+ *         sequence, 0 <= parent < i; any other value makes it a root.  NULL: a
+ *         chain (parent i - 1).
+ * Token i attends to slots 0 .. lens[b]-1 and lens[b] + j for j = i and every
+ * ancestor j of i:  O = sum_l softmax_l(scale * q . K_l) V_l, scores, softmax
+ * and sums in FP32, the weights rounded once for the product with V.  scale <= 0
+ * means 1/sqrt(D).  A token that sees no position (none of its pages exists)
+ * gets zeros.  Positions out of sight do not enter the sums, whatever their
+ * slots hold, except that a drafted token's V row must be finite where some
+ * other token of its sequence does not see it.
+ *   T     1 .. 256
+ *   workspace  device, 16-byte aligned, ws_bytes at least
+ *         qmm_tree_attention_workspace_bytes: partial states of the work
+ *         split over the history.  Calls that may overlap on the GPU need
+ *         workspaces of their own.  Nothing is kept in it between calls.
+ * The result does not depend on timing: the same call gives the same bits.
+ * Returns QMM_OK, QMM_EINVAL, QMM_ESHAPE, QMM_EALIGN, QMM_ENODEV,
+ * QMM_EWORKSPACE or QMM_ECUDA. */
+int qmm_tree_attention(const qmm_kv_cache *cache, const void *q, int64_t q_stride, void *O, int N,
+                       int T, int Hq, const int *cu, const int *parents, float scale,
+                       void *workspace, size_t ws_bytes, void *stream);
+
+/* Workspace bytes of qmm_tree_attention for this cache (its shapes and dtype),
+ * whatever the lengths.  num_sms <= 0 queries the device.  0 for invalid
+ * arguments.  Host only. */
+size_t qmm_tree_attention_workspace_bytes(const qmm_kv_cache *cache, int Hq, int T, int num_sms);
+
+/* Greedy verification of a drafted tree.  Token 0 of a sequence is its last
+ * sampled token and always stays; from token i the walk goes on to the first
+ * child c (parents[c] == i, lowest c) with tokens[c] == targets[i], the
+ * target model's choice after token i, and ends where there is none.
+ *   tokens, targets, parents, cu, N, T   as in qmm_tree_attention (device
+ *                int32 [N])
+ *   path         device int32 [B, T]: the tokens kept, -1 behind the last
+ *   count        device int32 [B]: their number (0 for a sequence without
+ *                tokens)
+ *   next         device int32 [B], nullable: targets of the last one kept, the
+ *                next step's token 0; -1 for a sequence without tokens
+ *   new_lens     device int32 [B], nullable: lens[b] + count[b]; not lens
+ *                itself
+ *   caches       host, n of them (one per layer), all with the same table,
+ *                lens, sizes, strides and dtype: slot lens[b] + j takes the K
+ *                and V rows of slot lens[b] + path[j], j < count[b], in every
+ *                one.  n may be 1 .. 1024; QMM_EINVAL if they differ.
+ * A row whose page is missing on either side is not moved.  One launch per 64
+ * caches.  Returns QMM_OK, QMM_EINVAL, QMM_ESHAPE, QMM_EALIGN, QMM_ENODEV or
+ * QMM_ECUDA. */
+int qmm_tree_accept(const qmm_kv_cache *caches, int n, const int *tokens, const int *targets,
+                    const int *parents, const int *cu, int N, int T, int *path, int *count,
+                    int *next, int *new_lens, void *stream);
+
 /* ---- streaming host activations through the matmul ----------------------
  *
  * gpu-kernels-explained, "Split-K, streams and overlap" (first Concept

@@ -1111,6 +1111,145 @@ int qmm_decode_attention(const void* q, const void* K, const void* V, const int*
     return rc;
 }
 
+// ---- paged KV cache ----
+
+// A stride of a dimension of `extent` rows, in elements of e bytes: rows do
+// not overlap, start on 16 bytes, and stay within a tensor map's range.
+static bool stride_ok(int64_t stride, int extent, int D, int e) {
+    if (extent == 1) return true;
+    return stride >= D && (stride * e) % 16 == 0 && stride < (int64_t{1} << 40) / e;
+}
+
+static int check_cache(const qmm_kv_cache* c) {
+    if (!c || !c->K || !c->V || !c->table || !c->lens || c->B < 1 || c->num_pages < 1 ||
+        c->page_size < 1 || c->max_pages < 1 || c->Hkv < 1 ||
+        (c->dtype != QMM_CACHE_BF16 && c->dtype != QMM_CACHE_E4M3) || !(c->k_scale > 0.f) ||
+        !(c->v_scale > 0.f) || !std::isfinite(c->k_scale) || !std::isfinite(c->v_scale))
+        return QMM_EINVAL;
+    const int e = c->dtype == QMM_CACHE_E4M3 ? 1 : 2;
+    if ((c->D != 64 && c->D != 128) || c->page_size < 8 || c->page_size > 65536 ||
+        (c->page_size & (c->page_size - 1)) || c->B > 65535 || c->Hkv > 65535 ||
+        static_cast<int64_t>(c->max_pages) * c->page_size > 0x7fff0000LL ||
+        !stride_ok(c->page_stride, c->num_pages, c->D, e) ||
+        !stride_ok(c->head_stride, c->Hkv, c->D, e) ||
+        !stride_ok(c->slot_stride, c->page_size, c->D, e))
+        return QMM_ESHAPE;
+    if (!aligned(c->K, 16) || !aligned(c->V, 16) || !aligned(c->table, 4) || !aligned(c->lens, 4))
+        return QMM_EALIGN;
+    return QMM_OK;
+}
+
+// Token ranges: cu's, or N / B tokens each (T each where T > 0).
+static bool ranges_ok(const int* cu, int N, int B, int T) {
+    if (N < 1) return false;
+    if (cu) return true;
+    return T > 0 ? static_cast<int64_t>(B) * T == N : N % B == 0;
+}
+
+int qmm_kv_append(const qmm_kv_cache* cache, const void* q, const void* k, const void* v,
+                  void* q_out, int N, int Hq, int64_t q_stride, int64_t k_stride,
+                  int64_t v_stride, int64_t q_out_stride, const int* cu, const int* positions,
+                  const qmm_rope* rope, void* stream) {
+    int rc = check_cache(cache);
+    if (rc == QMM_EINVAL) return rc;
+    if (!k || !v || Hq < 0 || (Hq > 0) != (q != nullptr) || (Hq > 0) != (q_out != nullptr) ||
+        !ranges_ok(cu, N, cache->B, 0))
+        return QMM_EINVAL;
+    if (rope && (rope->dim < 0 || (rope->dim > 0 && (!rope->cos_sin || rope->rows < 1)) ||
+                 (rope->interleaved != 0 && rope->interleaved != 1) ||
+                 ((rope->q_norm || rope->k_norm) && !(rope->eps >= 0.f && std::isfinite(rope->eps)))))
+        return QMM_EINVAL;
+    if (rc != QMM_OK) return rc;
+    const int D = cache->D;
+    const int64_t kw = static_cast<int64_t>(cache->Hkv) * D, qw = static_cast<int64_t>(Hq) * D;
+    if ((rope && (rope->dim % 16 || rope->dim > D)) || Hq > 65535 || k_stride % 8 || v_stride % 8 ||
+        k_stride < kw || v_stride < kw ||
+        (Hq > 0 && (q_stride % 8 || q_out_stride % 8 || q_stride < qw || q_out_stride < qw)) ||
+        (q_out && q_out == q && q_out_stride != q_stride))
+        return QMM_ESHAPE;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) ||
+        !aligned(cu, 4) || !aligned(positions, 4) ||
+        (rope && (!aligned(rope->cos_sin, 16) || !aligned(rope->q_norm, 16) ||
+                  !aligned(rope->k_norm, 16))))
+        return QMM_EALIGN;
+    rc = check_device();
+    if (rc != QMM_OK) return rc;
+    return launched(qmm::launch_kv_append(*cache, q, k, v, q_out, N, Hq, q_stride, k_stride,
+                                          v_stride, q_out_stride, cu, positions, rope, stream));
+}
+
+// Sizes of a tree attention call; QMM_OK, QMM_EINVAL or QMM_ESHAPE.
+static int check_tree(const qmm_kv_cache* c, int Hq, int T) {
+    if (Hq < 1 || T < 1 || Hq % c->Hkv) return QMM_EINVAL;
+    return T > qmm::kMaxTree || Hq / c->Hkv > 64 ? QMM_ESHAPE : QMM_OK;
+}
+
+size_t qmm_tree_attention_workspace_bytes(const qmm_kv_cache* cache, int Hq, int T, int num_sms) {
+    if (check_cache(cache) != QMM_OK || check_tree(cache, Hq, T) != QMM_OK) return 0;
+    if (num_sms <= 0 && device_sms(&num_sms) != QMM_OK) return 0;
+    return qmm::tree_attention_workspace(cache->D, T * (Hq / cache->Hkv), num_sms);
+}
+
+int qmm_tree_attention(const qmm_kv_cache* cache, const void* q, int64_t q_stride, void* O, int N,
+                       int T, int Hq, const int* cu, const int* parents, float scale,
+                       void* workspace, size_t ws_bytes, void* stream) {
+    int rc = check_cache(cache);
+    if (rc == QMM_EINVAL) return rc;
+    if (!q || !O || T < 1 || Hq < 1 || Hq % cache->Hkv || !std::isfinite(scale) ||
+        !ranges_ok(cu, N, cache->B, T))
+        return QMM_EINVAL;
+    if (rc == QMM_OK) rc = check_tree(cache, Hq, T);
+    if (rc != QMM_OK) return rc;
+    if (q_stride % 8 || q_stride < static_cast<int64_t>(Hq) * cache->D) return QMM_ESHAPE;
+    if (!aligned(q, 16) || !aligned(O, 16) || !aligned(cu, 4) || !aligned(parents, 4))
+        return QMM_EALIGN;
+    rc = check_device();
+    if (rc != QMM_OK) return rc;
+    int sms = 0;
+    rc = device_sms(&sms);
+    if (rc != QMM_OK) return rc;
+    if (!workspace ||
+        ws_bytes < qmm::tree_attention_workspace(cache->D, T * (Hq / cache->Hkv), sms))
+        return QMM_EWORKSPACE;
+    if (!aligned(workspace, 16)) return QMM_EALIGN;
+    const float sc = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(cache->D));
+    return launched(qmm::launch_tree_attention(*cache, q, q_stride, O, N, T, Hq, cu, parents, sc,
+                                               static_cast<float*>(workspace), sms, stream));
+}
+
+int qmm_tree_accept(const qmm_kv_cache* caches, int n, const int* tokens, const int* targets,
+                    const int* parents, const int* cu, int N, int T, int* path, int* count,
+                    int* next, int* new_lens, void* stream) {
+    if (!caches || n < 1 || n > 1024) return QMM_EINVAL;
+    int rc = QMM_OK;
+    for (int i = 0; i < n; ++i) {
+        const int r = check_cache(&caches[i]);
+        if (r == QMM_EINVAL) return r;
+        if (rc == QMM_OK) rc = r;
+        const qmm_kv_cache &a = caches[0], &b = caches[i];
+        if (a.table != b.table || a.lens != b.lens || a.page_stride != b.page_stride ||
+            a.head_stride != b.head_stride || a.slot_stride != b.slot_stride || a.B != b.B ||
+            a.num_pages != b.num_pages || a.page_size != b.page_size ||
+            a.max_pages != b.max_pages || a.Hkv != b.Hkv || a.D != b.D || a.dtype != b.dtype)
+            return QMM_EINVAL;
+    }
+    if (!tokens || !targets || !path || !count || T < 1 || new_lens == caches[0].lens ||
+        !ranges_ok(cu, N, caches[0].B, T))
+        return QMM_EINVAL;
+    if (rc != QMM_OK) return rc;
+    if (T > qmm::kMaxTree) return QMM_ESHAPE;
+    if (!aligned(tokens, 4) || !aligned(targets, 4) || !aligned(parents, 4) || !aligned(cu, 4) ||
+        !aligned(path, 4) || !aligned(count, 4) || !aligned(next, 4) || !aligned(new_lens, 4))
+        return QMM_EALIGN;
+    rc = check_device();
+    if (rc != QMM_OK) return rc;
+    for (int i = 0; i < n && rc == QMM_OK; i += qmm::kMaxAcceptCaches)
+        rc = launched(qmm::launch_tree_accept(caches + i, std::min(n - i, qmm::kMaxAcceptCaches),
+                                              tokens, targets, parents, cu, N, T, path, count, next,
+                                              new_lens, i == 0, stream));
+    return rc;
+}
+
 static int pipeline_config(int bm, int gpp, int smem_limit, int* out, bool persistent) {
     if (!out || gpp < 1 || smem_limit < 1) return QMM_EINVAL;
     qmm::TcPipeline pl;

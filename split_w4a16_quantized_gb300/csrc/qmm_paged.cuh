@@ -1,0 +1,69 @@
+// The paged KV cache on the device: token ranges of a batch and addresses of
+// slots, shared by the append, tree attention and accept kernels.
+#pragma once
+
+#include <cstdint>
+
+#include "qmm.h"
+
+namespace qmm {
+
+struct PagedDims {
+    const int* table;
+    const int* lens;
+    int64_t page_stride, head_stride, slot_stride;  // elements
+    int B, num_pages, max_pages, page_shift, Hkv;
+    int cap;  // slots of a sequence's table
+};
+
+inline PagedDims paged_dims(const qmm_kv_cache& c) {
+    PagedDims d;
+    d.table = c.table;
+    d.lens = c.lens;
+    // a dimension of one row has no stride: whatever the caller holds there
+    // (views of one head or one page) must not reach an address or a map
+    d.page_stride = c.num_pages > 1 ? c.page_stride : c.D;
+    d.head_stride = c.Hkv > 1 ? c.head_stride : c.D;
+    d.slot_stride = c.page_size > 1 ? c.slot_stride : c.D;
+    d.B = c.B;
+    d.num_pages = c.num_pages;
+    d.max_pages = c.max_pages;
+    d.page_shift = 0;
+    while ((1 << d.page_shift) < c.page_size) ++d.page_shift;
+    d.Hkv = c.Hkv;
+    d.cap = c.max_pages * c.page_size;
+    return d;
+}
+
+// Tokens in the cache of sequence b before the call.
+__device__ __forceinline__ int cached_tokens(const PagedDims& d, int b) {
+    const int len = d.lens[b];
+    return len < 0 ? 0 : (len > d.cap ? d.cap : len);
+}
+
+// New tokens of sequence b: rows [first, first + n).  cu's values are the
+// caller's device data, so they are clamped to the N rows there are.
+__device__ __forceinline__ void token_range(const int* cu, int N, int T, int b, int* first,
+                                            int* n) {
+    if (!cu) {
+        *first = b * T;
+        *n = T;
+        return;
+    }
+    int a = cu[b], e = cu[b + 1];
+    a = a < 0 ? 0 : (a > N ? N : a);
+    e = e < a ? a : (e > N ? N : e);
+    *first = a;
+    *n = e - a < T ? e - a : T;
+}
+
+// Element offset of slot s of sequence b for head 0, or -1 where it has no page.
+__device__ __forceinline__ int64_t slot_offset(const PagedDims& d, int b, int s) {
+    const int pi = s >> d.page_shift;
+    if (s < 0 || pi >= d.max_pages) return -1;
+    const int page = d.table[static_cast<int64_t>(b) * d.max_pages + pi];
+    if (page < 0 || page >= d.num_pages) return -1;
+    return page * d.page_stride + (s & ((1 << d.page_shift) - 1)) * d.slot_stride;
+}
+
+}  // namespace qmm

@@ -81,10 +81,28 @@ class qmm_group_call(ctypes.Structure):
                 ("Kred", ctypes.c_int), ("Nout", ctypes.c_int)]
 
 
+class qmm_kv_cache(ctypes.Structure):
+    """The paged KV cache of one layer (see qmm.h); kv_cache() builds it."""
+    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64),
+                ("B", ctypes.c_int), ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("max_pages", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+class qmm_rope(ctypes.Structure):
+    """Rotation and per-head norm of qmm_kv_append (see qmm.h); rope() builds it."""
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("q_norm", ctypes.c_void_p),
+                ("k_norm", ctypes.c_void_p), ("rows", ctypes.c_int), ("dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("eps", ctypes.c_float)]
+
+
 _lock = threading.Lock()
 _lib = None
 
 _P, _I, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_L = ctypes.c_int64
 _SIGS = {
     "qmm_policy_preset": (_I, [_I, _I, _I, ctypes.POINTER(qmm_policy)]),
     "qmm_kernel_tile": (_I, [_I, ctypes.POINTER(_I), ctypes.POINTER(_I)]),
@@ -139,6 +157,10 @@ _SIGS = {
     "qmm_stream_arena_bytes": (_SZ, [ctypes.POINTER(qmm_stream_call), _I, _I]),
     "qmm_w4a16_g128_stream": (_I, [ctypes.POINTER(qmm_stream_call), _I, _I, _P, _SZ, _P, _P, _P,
                                    ctypes.POINTER(_I)]),
+    "qmm_kv_append": (_I, [_P, _P, _P, _P, _P, _I, _I, _L, _L, _L, _L, _P, _P, _P, _P]),
+    "qmm_tree_attention": (_I, [_P, _P, _L, _P, _I, _I, _I, _P, _P, ctypes.c_float, _P, _SZ, _P]),
+    "qmm_tree_attention_workspace_bytes": (_SZ, [_P, _I, _I, _I]),
+    "qmm_tree_accept": (_I, [_P, _I, _P, _P, _P, _P, _I, _I, _P, _P, _P, _P, _P]),
     "qmm_overlap_schedule": (_I, [_I, _I, ctypes.POINTER(ctypes.c_double),
                                   ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_double),
                                   _I, ctypes.POINTER(ctypes.c_double),
@@ -658,6 +680,182 @@ def qmm_w4a16_g128_grouped(calls, workspace: torch.Tensor | None = None,
     else:
         _check(lib().qmm_w4a16_g128_grouped(*args), "qmm_w4a16_g128_grouped")
     return list(used)
+
+
+# ---- paged KV cache: append, tree attention, accepted path ----------------------
+
+QMM_CACHE_BF16, QMM_CACHE_E4M3 = 0, 1
+_CACHE_DTYPES = {torch.bfloat16: QMM_CACHE_BF16, torch.float8_e4m3fn: QMM_CACHE_E4M3}
+_INT32 = (torch.int32,)
+
+
+def kv_cache(K: torch.Tensor, V: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+             k_scale: float = 1.0, v_scale: float = 1.0) -> qmm_kv_cache:
+    """The cache of one layer: K, V [num_pages, Hkv, page_size, D] (bf16 or
+    float8_e4m3fn, any strides that keep a row's D values together, both the
+    same: pages of [page_size, Hkv, D] come as K.transpose(1, 2)), table int32
+    [B, max_pages], lens int32 [B].  Checked once here; the tensors are kept
+    alive by the result, whose pointers stay theirs."""
+    if not (isinstance(K, torch.Tensor) and isinstance(V, torch.Tensor) and K.is_cuda and V.is_cuda):
+        raise TypeError("K and V must be CUDA tensors")
+    if K.dtype not in _CACHE_DTYPES or V.dtype != K.dtype:
+        raise TypeError("K and V must both be bfloat16 or float8_e4m3fn")
+    if K.dim() != 4 or V.shape != K.shape or V.stride() != K.stride():
+        raise ValueError("K and V must be [num_pages, Hkv, page_size, D] with equal strides")
+    if K.stride(3) != 1:
+        raise ValueError("a cache row's values must be contiguous")
+    _dev(table, _INT32, "table")
+    _dev(lens, _INT32, "lens")
+    if table.dim() != 2 or tuple(lens.shape) != (table.shape[0],):
+        raise ValueError("table must be [B, max_pages] and lens [B]")
+    if len({t.get_device() for t in (K, V, table, lens)}) != 1:
+        raise ValueError("the cache's tensors are on different devices")
+    pages, Hkv, page, D = K.shape
+    c = qmm_kv_cache(K.data_ptr(), V.data_ptr(), table.data_ptr(), lens.data_ptr(), K.stride(0),
+                     K.stride(1), K.stride(2), table.shape[0], pages, page, table.shape[1], Hkv, D,
+                     _CACHE_DTYPES[K.dtype], float(k_scale), float(v_scale))
+    c.tensors = (K, V, table, lens)
+    c.device = K.get_device()
+    c.ref = ctypes.addressof(c)
+    return c
+
+
+def kv_caches(caches) -> "ctypes.Array":
+    """The layers' caches as the array qmm_tree_accept takes."""
+    arr = (qmm_kv_cache * len(caches))(*caches)
+    arr.tensors = [c.tensors for c in caches]
+    arr.device = caches[0].device
+    if any(c.device != arr.device for c in caches):
+        raise ValueError("the caches are on different devices")
+    return arr
+
+
+def rope(cos_sin: torch.Tensor | None = None, interleaved: bool = False,
+         q_norm: torch.Tensor | None = None, k_norm: torch.Tensor | None = None,
+         eps: float = 1e-6) -> qmm_rope:
+    """Rotation by cos_sin (float32 [rows, dim], cosines then sines) and the
+    optional per-head norm weights q_norm, k_norm (bf16 [D]) of qmm_kv_append."""
+    rows, dim = (0, 0) if cos_sin is None else cos_sin.shape
+    p = [None if t is None else _dev(t, d, n).value for t, d, n in
+         ((cos_sin, (torch.float32,), "cos_sin"), (q_norm, _BF16, "q_norm"),
+          (k_norm, _BF16, "k_norm"))]
+    r = qmm_rope(p[0], p[1], p[2], rows, dim, int(bool(interleaved)), float(eps))
+    r.tensors = (cos_sin, q_norm, k_norm)
+    r.head_dims = {t.numel() for t in (q_norm, k_norm) if t is not None}
+    r.devices = {t.get_device() for t in r.tensors if t is not None}
+    r.ref = ctypes.addressof(r)
+    return r
+
+
+def _on(device: int, *tensors):
+    """Every tensor on `device`, and `device` the current one: the kernels run
+    there."""
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError("a tensor is not on the cache's device")
+    if _cur_device is not None and torch.cuda.is_initialized() and _cur_device() != device:
+        raise ValueError("the cache's device is not the current one")
+
+
+def _heads(t: torch.Tensor, D: int, name: str) -> int:
+    """The token stride of [N, H, D] bf16 rows whose heads are contiguous."""
+    if t.dtype != torch.bfloat16 or not t.is_cuda:
+        raise TypeError("%s must be a bfloat16 CUDA tensor" % name)
+    s0, s1, s2 = t.stride()
+    H = t.shape[1]
+    if s2 != 1 or (s1 != D and H > 1):
+        raise ValueError("%s: the heads of a token must be contiguous" % name)
+    return s0 if t.shape[0] > 1 else H * D
+
+
+def _tokens(t, N: int, name: str):
+    """Pointer of an optional int32 vector of N elements."""
+    if t is None:
+        return None
+    if t.numel() != N:
+        raise ValueError("%s must have %d elements" % (name, N))
+    return _ptr(t, _INT32, name)
+
+
+def qmm_kv_append(cache: qmm_kv_cache, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
+                  q_out: torch.Tensor | None = None, rope: qmm_rope | None = None,
+                  positions: torch.Tensor | None = None, cu: torch.Tensor | None = None,
+                  stream=None) -> None:
+    """Rotate q [N, Hq, D] into q_out and append k, v [N, Hkv, D] (bf16; token
+    strides free, so views of one fused projection do) behind the cached
+    tokens.  q may be None (only append); q_out may be q.  positions int32 [N]
+    and cu int32 [B + 1]: see qmm.h."""
+    N, Hkv, D = k.shape
+    if Hkv != cache.Hkv or D != cache.D or v.shape != k.shape:
+        raise ValueError("qmm_kv_append: inconsistent shapes")
+    Hq, qs, qos, qp, qop = 0, 0, 0, None, None
+    if q is not None:
+        Hq = q.shape[1]
+        if q_out is None or tuple(q.shape) != (N, Hq, D) or q_out.shape != q.shape:
+            raise ValueError("qmm_kv_append: inconsistent shapes")
+        qs, qos = _heads(q, D, "q"), _heads(q_out, D, "q_out")
+        qp, qop = q.data_ptr(), q_out.data_ptr()
+    r = None
+    if rope is not None:
+        if any(d != D for d in rope.head_dims):
+            raise ValueError("qmm_kv_append: norm weights must have D elements")
+        if any(d != cache.device for d in rope.devices):
+            raise ValueError("a tensor is not on the cache's device")
+        r = rope.ref
+    _on(cache.device, q, k, v, q_out, positions, cu)
+    rc = (_lib or lib()).qmm_kv_append(
+        cache.ref, qp, k.data_ptr(), v.data_ptr(), qop, N, Hq, qs, _heads(k, D, "k"),
+        _heads(v, D, "v"), qos, _tokens(cu, cache.B + 1, "cu"), _tokens(positions, N, "positions"),
+        r, _stream(stream))
+    if rc != QMM_OK:
+        raise QmmError(rc, "qmm_kv_append")
+
+
+def qmm_tree_attention_workspace_bytes(cache: qmm_kv_cache, Hq: int, T: int,
+                                       num_sms: int = 0) -> int:
+    return int(lib().qmm_tree_attention_workspace_bytes(ctypes.byref(cache), Hq, T, num_sms))
+
+
+def qmm_tree_attention(cache: qmm_kv_cache, q: torch.Tensor, O: torch.Tensor, T: int,
+                       parents: torch.Tensor | None = None, cu: torch.Tensor | None = None,
+                       scale: float = 0.0, workspace: torch.Tensor | None = None,
+                       stream=None) -> None:
+    """O [N, Hq, D] = attention of the drafted tokens q [N, Hq, D] (at most T a
+    sequence, their keys already appended) over the cache; parents int32 [N]
+    gives the trees, None a chain (see qmm.h)."""
+    N, Hq, D = q.shape
+    if D != cache.D or O.shape != q.shape:
+        raise ValueError("qmm_tree_attention: inconsistent shapes")
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        ws, ws_bytes = _ptr(workspace, (workspace.dtype,), "workspace"), workspace.nbytes
+    _on(cache.device, q, O, parents, cu, workspace)
+    rc = (_lib or lib()).qmm_tree_attention(
+        cache.ref, q.data_ptr(), _heads(q, D, "q"), _ptr(O, _BF16, "O"), N, T, Hq,
+        _tokens(cu, cache.B + 1, "cu"), _tokens(parents, N, "parents"), scale, ws, ws_bytes,
+        _stream(stream))
+    if rc != QMM_OK:
+        raise QmmError(rc, "qmm_tree_attention")
+
+
+def qmm_tree_accept(caches, tokens: torch.Tensor, targets: torch.Tensor, T: int,
+                    path: torch.Tensor, count: torch.Tensor, next: torch.Tensor | None = None,
+                    new_lens: torch.Tensor | None = None, parents: torch.Tensor | None = None,
+                    cu: torch.Tensor | None = None, stream=None) -> None:
+    """Follow targets down the drafted trees (tokens, parents int32 [N]) and
+    move the accepted rows in every cache of `caches` (kv_caches()).  path
+    int32 [B, T], count, next and new_lens int32 [B] (see qmm.h)."""
+    N, B = tokens.numel(), caches[0].B
+    _on(caches.device, tokens, targets, path, count, next, new_lens, parents, cu)
+    if path.numel() != B * T:
+        raise ValueError("qmm_tree_accept: path must be [B, T]")
+    rc = (_lib or lib()).qmm_tree_accept(
+        caches, len(caches), _ptr(tokens, _INT32, "tokens"), _tokens(targets, N, "targets"),
+        _tokens(parents, N, "parents"), _tokens(cu, B + 1, "cu"), N, T, _ptr(path, _INT32, "path"),
+        _tokens(count, B, "count"), _tokens(next, B, "next"), _tokens(new_lens, B, "new_lens"),
+        _stream(stream))
+    if rc != QMM_OK:
+        raise QmmError(rc, "qmm_tree_accept")
 
 
 # ---- split-KV decode attention ---------------------------------------------
