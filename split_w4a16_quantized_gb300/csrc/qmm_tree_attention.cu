@@ -21,21 +21,10 @@
 // a CTA, and the merge kernel adds them in run order: the bits do not depend
 // on timing.  Equal runs keep every SM busy to the end whatever the lengths,
 // and the workspace is two states per CTA whatever the batch.
-#include <cuda.h>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
-#include <cuda_runtime.h>
-
-#include <cmath>
-#include <cstdint>
 #include <mutex>
 
 #include "qmm.h"
-#include "qmm_device.cuh"
-#include "qmm_internal.h"
-#include "qmm_paged.cuh"
-#include "qmm_sm100.cuh"
+#include "qmm_tree.cuh"
 
 namespace qmm {
 
@@ -46,148 +35,12 @@ bool encode_tiled(CUtensorMap* map, CUtensorMapDataType type, int rank, const vo
 
 namespace {
 
-constexpr int kTile = 64;      // positions per tile
 constexpr int kRows = 16;      // query rows per work item
 constexpr int kWarps = 4;      // compute warps
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kKeys = kTile / kWarps;   // positions per compute warp
 constexpr int kStages = 3;
 constexpr int kCtasPerSm = 2;
-constexpr int kMinRun = 2;     // tiles of the shortest run
-constexpr int kWords = kMaxTree / 32;
-
-struct TreeParams {
-    PagedDims d;
-    const __nv_bfloat16* q;
-    __nv_bfloat16* O;
-    const int *cu, *parents;
-    float* ws;    // partial states: m [2 ctas][kRows], l the same, o [2 ctas][kRows][D]
-    int* status;
-    int64_t q_stride;
-    int N, T, Hq, QG, ctas;
-    int box_shift;   // log2 of the positions of one copy: min(page, tile)
-    float qscale;    // scale * log2(e) * k_scale
-    float vscale;
-};
-
-// ---- work split ----------------------------------------------------------------
-
-struct Seq {
-    int first, n;      // its rows of q
-    int len, total;    // cached tokens; with the new ones
-    int tiles;         // of 64 positions
-    int row_tiles;
-};
-
-__device__ __forceinline__ Seq sequence(const TreeParams& p, int b) {
-    Seq s;
-    token_range(p.cu, p.N, p.T, b, &s.first, &s.n);
-    s.len = cached_tokens(p.d, b);
-    s.total = s.len + s.n < p.d.cap ? s.len + s.n : p.d.cap;
-    s.tiles = (s.total + kTile - 1) / kTile;
-    s.row_tiles = (s.n * p.QG + kRows - 1) / kRows;
-    return s;
-}
-__device__ __forceinline__ long long tiles_of(const TreeParams& p, const Seq& s) {
-    return static_cast<long long>(s.tiles) * s.row_tiles * p.d.Hkv;
-}
-
-// Sum of v over the block and over the threads before this one.  Every thread
-// of the block calls it; red is kThreads / 32 values of shared memory.
-template <int kN>
-__device__ __forceinline__ long long block_scan(long long v, long long* red, long long* total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    if (lane == 31) red[warp] = x;
-    __syncthreads();
-    long long before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < kN / 32; ++w) {
-        if (w < warp) before += red[w];
-        all += red[w];
-    }
-    *total = all;
-    return before + x - v;
-}
-
-__device__ __forceinline__ long long run_length(const TreeParams& p, long long all) {
-    const long long r = (all + p.ctas - 1) / p.ctas;
-    return r < kMinRun ? kMinRun : r;
-}
-
-// A CTA's place in the list of tiles.
-struct Run {
-    int b;            // sequence
-    long long at;     // tile within the sequence's list
-    long long left;   // tiles of the run still to do
-};
-
-// The CTA's run: whole block; sh: shared scratch.
-struct RunShared {
-    long long red[kThreads / 32];
-    long long at;
-    int b;
-};
-__device__ __forceinline__ Run find_run(const TreeParams& p, RunShared& sh) {
-    const int per = (p.d.B + kThreads - 1) / kThreads;
-    const int b0 = min(p.d.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.d.B, b0 + per);
-    long long mine = 0, all;
-    for (int b = b0; b < b1; ++b) mine += tiles_of(p, sequence(p, b));
-    if (threadIdx.x == 0) sh.b = -1;
-    const long long before = block_scan<kThreads>(mine, sh.red, &all);
-    const long long len = run_length(p, all);
-    const long long start = len * blockIdx.x;
-    if (start >= before && start < before + mine) {
-        // this thread's sequences hold the start
-        long long at = start - before;
-        for (int b = b0; b < b1; ++b) {
-            const long long t = tiles_of(p, sequence(p, b));
-            if (at < t) {
-                sh.b = b;
-                sh.at = at;
-                break;
-            }
-            at -= t;
-        }
-    }
-    __syncthreads();
-    Run r;
-    r.b = sh.b;
-    r.at = sh.at;
-    r.left = r.b < 0 ? 0 : (all - start < len ? all - start : len);
-    return r;
-}
-
-// The next stretch of one work item in the run.
-struct Stretch {
-    Seq s;
-    int b, g, row0;    // sequence, KV head, first row
-    int t0, t1;        // tiles
-};
-__device__ __forceinline__ bool next_stretch(const TreeParams& p, Run& r, Stretch* x) {
-    if (r.left <= 0) return false;
-    x->s = sequence(p, r.b);
-    while (r.at >= tiles_of(p, x->s)) {
-        r.at -= tiles_of(p, x->s);
-        if (++r.b >= p.d.B) return false;   // (not reached: the run ends with the list)
-        x->s = sequence(p, r.b);
-    }
-    const int item = static_cast<int>(r.at / x->s.tiles);
-    x->b = r.b;
-    x->g = item / x->s.row_tiles;
-    x->row0 = (item % x->s.row_tiles) * kRows;
-    x->t0 = static_cast<int>(r.at % x->s.tiles);
-    const long long end = x->t0 + r.left;
-    x->t1 = end < x->s.tiles ? static_cast<int>(end) : x->s.tiles;
-    r.at += x->t1 - x->t0;
-    r.left -= x->t1 - x->t0;
-    return true;
-}
 
 // ---- shared memory tiles ----------------------------------------------------
 
@@ -224,17 +77,6 @@ struct Smem {
     alignas(16) float ex[kWarps][kRows][D / kWarps];   // outputs on their way to another warp
 };
 
-// 4-D tile load (c0 innermost), completion counted on `bar` in bytes.
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint64_t* bar,
-                                            int c0, int c1, int c2, int c3) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6];\n" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
-        "r"(smem_addr(bar))
-        : "memory");
-}
-
 __device__ __forceinline__ void ldmatrix_x4_t(uint32_t r[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -253,19 +95,6 @@ __device__ __forceinline__ void mma16816(float d[4], const uint32_t a[4], uint32
     else
         mma_bf16_16816(d, a, b0, b1);
 }
-
-// Two E4M3 numbers (the low 16 bits) as an F16 pair; every E4M3 number is an F16.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v), __NV_E4M3);
-    return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    const __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-// Maximum that every later exp2 can subtract: 0 while nothing is visible.
-__device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0.f : m; }
 
 // ---- the kernel -------------------------------------------------------------
 //
@@ -315,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
     pdl_wait();
     __syncthreads();
-    Run run = find_run(p, sm.run);
+    Run run = find_run<kThreads>(p, sm.run);
     const int box = 1 << p.box_shift;            // positions of one copy
     const int pieces = kTile >> p.box_shift;     // copies of a tile, per column block and pool
     Stretch x;
@@ -549,12 +378,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                         const float mn = fmaxf(m_run[h], mx);
                         const float mf = finite_max(mn);
-                        corr[h] = exp2f(m_run[h] - mf);
+                        corr[h] = fast_exp2(m_run[h] - mf);
                         m_run[h] = mn;
                         float rs = 0.f;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            pw[h][e] = exp2f(v[e] - mf);
+                            pw[h][e] = fast_exp2(v[e] - mf);
                             rs += pw[h][e];
                         }
                         l_run[h] = l_run[h] * corr[h] + rs;
@@ -649,8 +478,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 const float mf = finite_max(M[h]);
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w)
-                    den[h] = fmaf(exp2f(sm.wm[w][gr + 8 * h] - mf), sm.wl[w][gr + 8 * h], den[h]);
-                fac[h] = exp2f(m_run[h] - mf);
+                    den[h] = fmaf(fast_exp2(sm.wm[w][gr + 8 * h] - mf), sm.wl[w][gr + 8 * h], den[h]);
+                fac[h] = fast_exp2(m_run[h] - mf);
             }
             float acc[NQ][2 * H];
 #pragma unroll
@@ -693,10 +522,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             // ---- O, or the partial state ----
             const bool whole = x.t0 == 0 && x.t1 == x.s.tiles;
             const int slot = 2 * blockIdx.x + (x.t0 == 0 ? 1 : 0);
-            float* pm = p.ws + static_cast<size_t>(slot) * kRows;
-            float* pl = pm + static_cast<size_t>(2) * p.ctas * kRows;
-            float* po = p.ws + static_cast<size_t>(4) * p.ctas * kRows +
-                        static_cast<size_t>(slot) * kRows * D;
+            const PartialAt part = partial_at<D>(p, slot);
 #pragma unroll
             for (int h = 0; h < H; ++h) {
                 const int r = gr + 8 * h;
@@ -705,8 +531,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                                                         : (den[h] == 0.f ? 0.f : den[h]))
                                         : 1.f;
                 if (!whole && warp == 0 && tq == 0) {
-                    pm[r] = M[h];
-                    pl[r] = den[h];
+                    part.m[r] = M[h];
+                    part.l[r] = den[h];
                 }
                 const int rr = x.row0 + r;
                 __nv_bfloat16* out = p.O + (static_cast<int64_t>(x.s.first + rr / p.QG) * p.Hq +
@@ -724,13 +550,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                             *reinterpret_cast<uint2*>(out + c) =
                                 make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
                         else
-                            *reinterpret_cast<float4*>(po + r * D + c) = v;
+                            *reinterpret_cast<float4*>(part.o + r * D + c) = v;
                     } else {
                         const float2 v = make_float2(acc[n][2 * h] * inv, acc[n][2 * h + 1] * inv);
                         if (whole)
                             *reinterpret_cast<uint32_t*>(out + c) = pack_bf16x2(v.x, v.y);
                         else
-                            *reinterpret_cast<float2*>(po + r * D + c) = v;
+                            *reinterpret_cast<float2*>(part.o + r * D + c) = v;
                     }
                 }
             }
@@ -741,17 +567,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
 // The items that a run border cuts: O = sum_c 2^(m_c - M) o_c / sum_c
 // 2^(m_c - M) l_c over the runs c that hold a stretch, in ascending c.  One
-// block per item; a block whose item lies in one run leaves at once.
+// block per item and 16 of its rows; a block whose item lies in one run leaves
+// at once.
 constexpr int kMergeThreads = 128;
+constexpr int kMergeRows = 16;
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TreeParams p,
-                                                                   int max_row_tiles) {
+                                                                   int max_row_tiles, int chunks) {
     __shared__ long long red[kMergeThreads / 32];
     pdl_trigger();
     pdl_wait();
-    const int rt = blockIdx.x % max_row_tiles, g = blockIdx.x / max_row_tiles, b = blockIdx.y;
+    const int chunk = blockIdx.x % chunks, item = blockIdx.x / chunks;
+    const int rt = item % max_row_tiles, g = item / max_row_tiles, b = blockIdx.y;
     const Seq s = sequence(p, b);
-    if (rt >= s.row_tiles) return;
+    const int row0 = rt << p.row_shift;
+    const int rows = min(1 << p.row_shift, s.n * p.QG - row0);
+    if (rt >= s.row_tiles || chunk * kMergeRows >= rows) return;
     long long mine = 0, upto = 0, all, total;
     for (int i = threadIdx.x; i < p.d.B; i += kMergeThreads) {
         const long long t = tiles_of(p, sequence(p, i));
@@ -765,19 +596,13 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
     const long long start = total + (static_cast<long long>(g) * s.row_tiles + rt) * s.tiles;
     const int c0 = static_cast<int>(start / len), c1 = static_cast<int>((start + s.tiles - 1) / len);
     if (c0 == c1) return;
-    const int rows = min(kRows, s.n * p.QG - rt * kRows);
-    const float* pm = p.ws;
-    const float* pl = pm + static_cast<size_t>(2) * p.ctas * kRows;
-    const float* po = pl + static_cast<size_t>(2) * p.ctas * kRows;
     constexpr int V = D / 32;   // values per lane
     const int lane = threadIdx.x & 31;
-    for (int r = threadIdx.x >> 5; r < rows; r += kMergeThreads / 32) {
-        // run c's slot: its last stretch (1) where the item starts in it, else its first
-        auto slot = [&](int c) {
-            return static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)) * kRows + r;
-        };
+    const int end = min(rows, (chunk + 1) * kMergeRows);
+    for (int r = chunk * kMergeRows + (threadIdx.x >> 5); r < end; r += kMergeThreads / 32) {
+        auto part = [&](int c) { return partial_at<D>(p, 2 * c + (c == c0 ? 1 : 0)); };
         float M = -INFINITY;
-        for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, pm[slot(c)]);
+        for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, part(c).m[r]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         M = finite_max(M);
@@ -785,14 +610,15 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
 #pragma unroll
         for (int j = 0; j < V; ++j) num[j] = 0.f;
         for (int c = c0; c <= c1; ++c) {
-            const float f = exp2f(pm[slot(c)] - M);
-            den = fmaf(f, pl[slot(c)], den);
-            const float* o = po + slot(c) * D + lane * V;
+            const PartialAt x = part(c);
+            const float f = fast_exp2(x.m[r] - M);
+            den = fmaf(f, x.l[r], den);
+            const float* o = x.o + static_cast<size_t>(r) * D + lane * V;
 #pragma unroll
             for (int j = 0; j < V; ++j) num[j] = fmaf(f, o[j], num[j]);
         }
         const float inv = den > 0.f ? p.vscale / den : (den == 0.f ? 0.f : den);
-        const int rr = rt * kRows + r;
+        const int rr = row0 + r;
         __nv_bfloat16* out = p.O + (static_cast<int64_t>(s.first + rr / p.QG) * p.Hq + g * p.QG +
                                     rr % p.QG) * D + lane * V;
 #pragma unroll
@@ -820,16 +646,21 @@ int launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    const int rc = cudaLaunchKernelEx(&cfg, kern, kmap, vmap, p);
-    if (rc != cudaSuccess) return rc;
-    const int row_tiles = (p.T * p.QG + kRows - 1) / kRows;
-    cudaLaunchConfig_t mc = {};
-    LaunchAttrs mla;
-    apply_pdl(mc, mla);
-    mc.gridDim = dim3(static_cast<unsigned>(row_tiles) * p.d.Hkv, p.d.B, 1);
-    mc.blockDim = dim3(kMergeThreads, 1, 1);
-    mc.stream = st;
-    return cudaLaunchKernelEx(&mc, tree_merge_kernel<D>, p, row_tiles);
+    return cudaLaunchKernelEx(&cfg, kern, kmap, vmap, p);
+}
+
+int launch_merge(const TreeParams& p, int D, cudaStream_t st) {
+    const int rows = p.T * p.QG, item_rows = 1 << p.row_shift;
+    const int row_tiles = (rows + item_rows - 1) >> p.row_shift;
+    const int chunks = ((rows < item_rows ? rows : item_rows) + kMergeRows - 1) / kMergeRows;
+    cudaLaunchConfig_t cfg = {};
+    LaunchAttrs la;
+    apply_pdl(cfg, la);
+    cfg.gridDim = dim3(static_cast<unsigned>(row_tiles) * chunks * p.d.Hkv, p.d.B, 1);
+    cfg.blockDim = dim3(kMergeThreads, 1, 1);
+    cfg.stream = st;
+    return D == 128 ? cudaLaunchKernelEx(&cfg, tree_merge_kernel<128>, p, row_tiles, chunks)
+                    : cudaLaunchKernelEx(&cfg, tree_merge_kernel<64>, p, row_tiles, chunks);
 }
 
 template <int D, bool kFp8>
@@ -839,11 +670,23 @@ int launch_rows(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreePara
                            : launch<D, kFp8, false>(kmap, vmap, p, st);
 }
 
+// The kernel for `rows` query rows per KV head, its rows per work item, CTAs
+// per SM and shortest run.
+struct Variant {
+    bool tc;
+    int row_shift, ctas_per_sm, min_run;
+};
+Variant variant(int rows) {
+    if (rows <= kRows) return {false, 4, kCtasPerSm, 2};
+    return {true, rows <= 128 ? 7 : 8, 1, 4};
+}
+
 }  // namespace
 
 size_t tree_attention_workspace(int D, int rows, int num_sms) {
-    (void)rows;
-    return static_cast<size_t>(2) * kCtasPerSm * num_sms * kRows * (D + 2) * sizeof(float);
+    const Variant v = variant(rows);
+    return (static_cast<size_t>(2 * v.ctas_per_sm * num_sms) << v.row_shift) * (D + 2) *
+           sizeof(float);
 }
 
 int launch_tree_attention(const qmm_kv_cache& c, const void* q, int64_t q_stride, void* O, int N,
@@ -863,7 +706,10 @@ int launch_tree_attention(const qmm_kv_cache& c, const void* q, int64_t q_stride
     p.T = T;
     p.Hq = Hq;
     p.QG = Hq / c.Hkv;
-    p.ctas = kCtasPerSm * num_sms;
+    const Variant var = variant(T * p.QG);
+    p.ctas = var.ctas_per_sm * num_sms;
+    p.row_shift = var.row_shift;
+    p.min_run = var.min_run;
     p.box_shift = p.d.page_shift < 6 ? p.d.page_shift : 6;
     p.qscale = scale * 1.4426950408889634f * c.k_scale;  // log2(e): exp2 of the scaled score
     p.vscale = c.v_scale;
@@ -886,10 +732,16 @@ int launch_tree_attention(const qmm_kv_cache& c, const void* q, int64_t q_stride
         !encode_tiled(&vmap, type, 4, c.V, dims, strides, box, sw))
         return cudaErrorInvalidValue;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (c.D == 128)
-        return fp8 ? launch_rows<128, true>(kmap, vmap, p, st)
-                   : launch_rows<128, false>(kmap, vmap, p, st);
-    return fp8 ? launch_rows<64, true>(kmap, vmap, p, st) : launch_rows<64, false>(kmap, vmap, p, st);
+    int rc;
+    if (var.tc)
+        rc = launch_tree_tc(kmap, vmap, p, c.D, fp8, st);
+    else if (c.D == 128)
+        rc = fp8 ? launch_rows<128, true>(kmap, vmap, p, st)
+                 : launch_rows<128, false>(kmap, vmap, p, st);
+    else
+        rc = fp8 ? launch_rows<64, true>(kmap, vmap, p, st)
+                 : launch_rows<64, false>(kmap, vmap, p, st);
+    return rc == cudaSuccess ? launch_merge(p, c.D, st) : rc;
 }
 
 }  // namespace qmm
