@@ -1181,7 +1181,12 @@ int qmm_kv_append(const qmm_kv_cache* cache, const void* q, const void* k, const
 // Sizes of a tree attention call; QMM_OK, QMM_EINVAL or QMM_ESHAPE.
 static int check_tree(const qmm_kv_cache* c, int Hq, int T) {
     if (Hq < 1 || T < 1 || Hq % c->Hkv) return QMM_EINVAL;
-    return T > qmm::kMaxTree || Hq / c->Hkv > 64 ? QMM_ESHAPE : QMM_OK;
+    if (T > qmm::kMaxTree || Hq / c->Hkv > 64) return QMM_ESHAPE;
+    // the kernels count a sequence's units of work in 32 bits; at most this many
+    // (tiles of 64 positions and a few more, row tiles of 16, heads)
+    const int64_t cap = static_cast<int64_t>(c->max_pages) * c->page_size;
+    const int64_t rows = ceil_div(static_cast<int64_t>(T) * (Hq / c->Hkv), 16);
+    return (cap / 64 + 16) * rows * c->Hkv > INT_MAX ? QMM_ESHAPE : QMM_OK;
 }
 
 size_t qmm_tree_attention_workspace_bytes(const qmm_kv_cache* cache, int Hq, int T, int num_sms) {

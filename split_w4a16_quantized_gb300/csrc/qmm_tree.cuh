@@ -19,7 +19,6 @@
 
 namespace qmm {
 
-constexpr int kTile = 64;              // positions per tile
 constexpr int kWords = kMaxTree / 32;  // ancestor bits of a token
 
 struct TreeParams {
@@ -32,7 +31,9 @@ struct TreeParams {
     int64_t q_stride;
     int N, T, Hq, QG, ctas;
     int row_shift;   // log2 of the query rows of a work item
-    int min_run;     // tiles of the shortest run
+    int tile_shift;  // log2 of the positions of a tile
+    int min_run;     // units of the shortest run
+    int setup;       // units an item counts for beside its tiles
     int box_shift;   // log2 of the positions of one copy: min(page, tile)
     float qscale;    // scale * log2(e) * k_scale
     float vscale;
@@ -43,7 +44,7 @@ struct TreeParams {
 struct Seq {
     int first, n;      // its rows of q
     int len, total;    // cached tokens; with the new ones
-    int tiles;         // of 64 positions
+    int tiles;
     int row_tiles;
 };
 
@@ -52,12 +53,17 @@ __device__ __forceinline__ Seq sequence(const TreeParams& p, int b) {
     token_range(p.cu, p.N, p.T, b, &s.first, &s.n);
     s.len = cached_tokens(p.d, b);
     s.total = s.len + s.n < p.d.cap ? s.len + s.n : p.d.cap;
-    s.tiles = (s.total + kTile - 1) / kTile;
+    s.tiles = (s.total + (1 << p.tile_shift) - 1) >> p.tile_shift;
     s.row_tiles = (s.n * p.QG + (1 << p.row_shift) - 1) >> p.row_shift;
     return s;
 }
-__device__ __forceinline__ long long tiles_of(const TreeParams& p, const Seq& s) {
-    return static_cast<long long>(s.tiles) * s.row_tiles * p.d.Hkv;
+// Units of work of one item, and of all the sequence's items (the host keeps a
+// sequence's below 2^31).
+__device__ __forceinline__ int item_units(const TreeParams& p, const Seq& s) {
+    return s.tiles + p.setup;
+}
+__device__ __forceinline__ int units_of(const TreeParams& p, const Seq& s) {
+    return s.row_tiles * p.d.Hkv * item_units(p, s);
 }
 
 // Sum of v over the block and over the threads before this one.  Every thread
@@ -88,25 +94,24 @@ __device__ __forceinline__ long long run_length(const TreeParams& p, long long a
     return r < p.min_run ? p.min_run : r;
 }
 
-// A CTA's place in the list of tiles.
+// A CTA's place in the list of units.
 struct Run {
     int b;            // sequence
-    long long at;     // tile within the sequence's list
-    long long left;   // tiles of the run still to do
+    int at;           // unit within the sequence's list
+    long long left;   // units of the run still to do
 };
 
 // The CTA's run: whole block of kN threads; sh: shared scratch.
 struct RunShared {
     long long red[32];
-    long long at;
-    int b;
+    int at, b;
 };
 template <int kN>
 __device__ __forceinline__ Run find_run(const TreeParams& p, RunShared& sh) {
     const int per = (p.d.B + kN - 1) / kN;
     const int b0 = min(p.d.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.d.B, b0 + per);
     long long mine = 0, all;
-    for (int b = b0; b < b1; ++b) mine += tiles_of(p, sequence(p, b));
+    for (int b = b0; b < b1; ++b) mine += units_of(p, sequence(p, b));
     if (threadIdx.x == 0) sh.b = -1;
     const long long before = block_scan<kN>(mine, sh.red, &all);
     const long long len = run_length(p, all);
@@ -115,13 +120,13 @@ __device__ __forceinline__ Run find_run(const TreeParams& p, RunShared& sh) {
         // this thread's sequences hold the start
         long long at = start - before;
         for (int b = b0; b < b1; ++b) {
-            const long long t = tiles_of(p, sequence(p, b));
-            if (at < t) {
+            const int u = units_of(p, sequence(p, b));
+            if (at < u) {
                 sh.b = b;
-                sh.at = at;
+                sh.at = static_cast<int>(at);
                 break;
             }
-            at -= t;
+            at -= u;
         }
     }
     __syncthreads();
@@ -139,23 +144,28 @@ struct Stretch {
     int t0, t1;        // tiles
 };
 __device__ __forceinline__ bool next_stretch(const TreeParams& p, Run& r, Stretch* x) {
-    if (r.left <= 0) return false;
-    x->s = sequence(p, r.b);
-    while (r.at >= tiles_of(p, x->s)) {
-        r.at -= tiles_of(p, x->s);
-        if (++r.b >= p.d.B) return false;   // (not reached: the run ends with the list)
+    while (r.left > 0) {
         x->s = sequence(p, r.b);
+        while (r.at >= units_of(p, x->s)) {
+            r.at -= units_of(p, x->s);
+            if (++r.b >= p.d.B) return false;   // (not reached: the run ends with the list)
+            x->s = sequence(p, r.b);
+        }
+        const int units = item_units(p, x->s);
+        const int item = r.at / units, u0 = r.at - item * units;
+        x->b = r.b;
+        x->g = item / x->s.row_tiles;
+        x->row0 = (item - x->g * x->s.row_tiles) << p.row_shift;
+        const int u1 = r.left < units - u0 ? u0 + static_cast<int>(r.left) : units;
+        r.at += u1 - u0;
+        r.left -= u1 - u0;
+        // the first `setup` units stand for the item's fixed cost: a run that
+        // ends among them leaves the whole item to the next
+        x->t0 = u0 > p.setup ? u0 - p.setup : 0;
+        x->t1 = u1 - p.setup;
+        if (x->t1 > x->t0) return true;
     }
-    const int item = static_cast<int>(r.at / x->s.tiles);
-    x->b = r.b;
-    x->g = item / x->s.row_tiles;
-    x->row0 = (item % x->s.row_tiles) << p.row_shift;
-    x->t0 = static_cast<int>(r.at % x->s.tiles);
-    const long long end = x->t0 + r.left;
-    x->t1 = end < x->s.tiles ? static_cast<int>(end) : x->s.tiles;
-    r.at += x->t1 - x->t0;
-    r.left -= x->t1 - x->t0;
-    return true;
+    return false;
 }
 
 // Where partial state `slot` lies: run c's last stretch, when the item starts
@@ -185,6 +195,84 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+// One lane of a converged warp, the same one every time.  The compiler knows
+// that a block under it has a single active thread, and feeds the copies' and
+// MMAs' uniform operands straight from registers; under `lane == 0` it goes
+// through the active lanes in a loop, which measured 160 clocks per MMA and 400
+// per copy.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}\n"
+                 : "=r"(one));
+    return one != 0;
+}
+
+// Page numbers of the copies of one tile, for the thread that issues them; a
+// missing page (or a piece past the last position) is num_pages: outside the
+// map, where a copy fills zeros.
+template <int kTile>
+struct TilePages {
+    static constexpr int kMax = kTile / 8;   // pieces of the smallest pages
+    int page[kMax];
+    int have;   // one bit per piece that exists
+};
+
+// The table entries of a stretch, looked up by a warp 32 pieces at a time and
+// one batch ahead.
+template <int kTile>
+struct PageWalk {
+    const int* row;
+    int c_end, c0, cur, nxt;
+    __device__ __forceinline__ int entry(const TreeParams& p, int c) const {
+        return c < c_end ? row[(c << p.box_shift) >> p.d.page_shift] : -1;
+    }
+    __device__ __forceinline__ void start(const TreeParams& p, const Stretch& x, int lane) {
+        c_end = (x.s.total + (1 << p.box_shift) - 1) >> p.box_shift;   // pieces that hold positions
+        row = p.d.table + static_cast<int64_t>(x.b) * p.d.max_pages;
+        c0 = x.t0 * (kTile >> p.box_shift);
+        cur = entry(p, c0 + lane);
+        nxt = entry(p, c0 + 32 + lane);
+    }
+    // whole warp
+    __device__ __forceinline__ TilePages<kTile> tile(const TreeParams& p, int t, int lane) {
+        const int pieces = kTile >> p.box_shift;
+        if (t * pieces >= c0 + 32) {
+            c0 += 32;
+            cur = nxt;
+            nxt = entry(p, c0 + 32 + lane);
+        }
+        const int at = t * pieces - c0;
+        const bool real = cur >= 0 && cur < p.d.num_pages;
+        const uint32_t ok = __ballot_sync(0xffffffffu, real);
+        const int pg = real ? cur : p.d.num_pages;
+        TilePages<kTile> r;
+        r.have = static_cast<int>((ok >> at) & ((1u << pieces) - 1u));
+#pragma unroll
+        for (int k = 0; k < TilePages<kTile>::kMax; ++k)
+            r.page[k] = __shfl_sync(0xffffffffu, pg, (at + k) & 31);
+        return r;
+    }
+};
+
+// The copies of one K or V tile, issued by one thread: page pieces by
+// column blocks of `kBox` bytes (kElems values), kTile rows of a block together.
+template <int kTile, int kBoxes, int kBox, int kElems>
+__device__ __forceinline__ void copy_tile(const TreeParams& p, const CUtensorMap* map, uint64_t* bar,
+                                          uint32_t dst, const TilePages<kTile>& pg, int t,
+                                          int g) {
+    const int pieces = kTile >> p.box_shift;
+    const int slot_mask = (1 << p.d.page_shift) - 1;
+#pragma unroll
+    for (int k = 0; k < TilePages<kTile>::kMax; ++k) {
+        if (k >= pieces) break;
+        const int row = k << p.box_shift;
+#pragma unroll
+        for (int x = 0; x < kBoxes; ++x)
+            tma_load_4d(dst + x * (kTile * kBox) + row * kBox, map, bar, x * kElems,
+                        (t * kTile + row) & slot_mask, g, pg.page[k]);
+    }
+}
+
 // Two E4M3 numbers (the low 16 bits) as an F16 pair; every E4M3 number is an F16.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v), __NV_E4M3);
@@ -205,8 +293,9 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return y;
 }
 
-// One launch of the tcgen05 kernel (qmm_tree_attention_tc.cu); the merge
-// kernel is the caller's.
+// One launch of the tcgen05 kernel (qmm_tree_attention_tc.cu: tiles of 128
+// positions); the merge kernel is the caller's.
+constexpr int kTcTileShift = 7;
 int launch_tree_tc(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int D,
                    bool fp8, cudaStream_t st);
 

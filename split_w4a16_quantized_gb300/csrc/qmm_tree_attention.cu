@@ -10,12 +10,13 @@
 // K and V row is read once for all of them: R flop per byte of a BF16 cache,
 // HBM-bound up to a few hundred rows.
 //
-// Work split.  A work item is (sequence b, KV head g, tile of kRows rows), of
-// ceil(L_b / 64) tiles of 64 positions, L_b = lens[b] + n_b.  Lengths live on
-// the device and differ widely in a batch, so the grid does not know them: it
-// is a fixed number of CTAs, and the tiles of all items, laid end to end, are
-// cut into that many equal runs.  Each CTA sums the batch's tile counts, finds
-// its run and walks it; the copies run ahead across item borders.  An item
+// Work split.  A work item is (sequence b, KV head g, tile of query rows), of
+// ceil(L_b / tile) tiles of positions, L_b = lens[b] + n_b, and counts for its
+// tiles and a few more units of work (its q, its output).  Lengths live on the
+// device and differ widely in a batch, so the grid does not know them: it is a
+// fixed number of CTAs, and the units of all items, laid end to end, are cut
+// into that many equal runs.  Each CTA sums the batch's units, finds its run
+// and walks it; the copies run ahead across item borders.  An item
 // inside one run is written to O.  An item that a border cuts leaves a partial
 // softmax state (maximum, sum, unnormalized output, FP32) per run, at most two
 // a CTA, and the merge kernel adds them in run order: the bits do not depend
@@ -35,6 +36,7 @@ bool encode_tiled(CUtensorMap* map, CUtensorMapDataType type, int rank, const vo
 
 namespace {
 
+constexpr int kTile = 64;      // positions per tile
 constexpr int kRows = 16;      // query rows per work item
 constexpr int kWarps = 4;      // compute warps
 constexpr int kThreads = 32 * (kWarps + 1);
@@ -131,7 +133,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     volatile int* abort = &abort_flag;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    pdl_trigger();
     if (tid == 0) {
         abort_flag = 0;
         for (int i = 0; i < kStages; ++i) {
@@ -143,63 +144,41 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         tma_prefetch_map(&vmap);
     }
     pdl_wait();
+    // (after the wait: the merge kernel plans with lens and cu before its own)
+    pdl_trigger();
     __syncthreads();
     Run run = find_run<kThreads>(p, sm.run);
-    const int box = 1 << p.box_shift;            // positions of one copy
     const int pieces = kTile >> p.box_shift;     // copies of a tile, per column block and pool
     Stretch x;
 
     if (warp == kWarps) {
         // ---- copy warp ----
         const uint32_t ring_a = smem_addr(ring);
-        // this lane's copy of a tile: piece, K or V, column block
-        const int my_piece = lane / (2 * C::BOXES), my_rest = lane % (2 * C::BOXES);
-        const int my_pool = my_rest / C::BOXES, my_box = my_rest % C::BOXES;
-        // (8 pieces x 4 copies fill the 32 lanes exactly)
-        const bool copies = my_piece < pieces;
-        const uint32_t my_off = my_pool * C::TILE + my_box * (kTile * C::BOX) +
-                                (my_piece << p.box_shift) * C::BOX;
         int it = 0;   // tiles copied so far
-        while (next_stretch(p, run, &x)) {
-            // table entries of 32 pieces, and of the 32 after them
-            const int c_end = (x.s.total + box - 1) >> p.box_shift;   // pieces that hold positions
-            const int* row = p.d.table + static_cast<int64_t>(x.b) * p.d.max_pages;
-            auto entry = [&](int c) {
-                return c < c_end ? row[(c << p.box_shift) >> p.d.page_shift] : -1;
-            };
-            int c0 = x.t0 * pieces;
-            int cur = entry(c0 + lane), nxt = entry(c0 + 32 + lane);
+        bool ok = true;
+        while (ok && next_stretch(p, run, &x)) {
+            PageWalk<kTile> walk;
+            walk.start(p, x, lane);
             for (int t = x.t0; t < x.t1; ++t, ++it) {
-                if (t * pieces >= c0 + 32) {
-                    c0 += 32;
-                    cur = nxt;
-                    nxt = entry(c0 + 32 + lane);
-                }
+                const TilePages<kTile> pg = walk.tile(p, t, lane);
                 const int st = it % kStages;
-                if (it >= kStages &&
-                    !mbar_wait_warp(&sm.empty[st], ((it / kStages) & 1) ^ 1, abort, p.status))
-                    break;
-                const int at = t * pieces - c0;
-                const uint32_t ok = __ballot_sync(0xffffffffu, cur >= 0 && cur < p.d.num_pages);
-                const int page = __shfl_sync(0xffffffffu, cur, (at + my_piece) & 31);
-                if (lane == 0) {
-                    sm.have[st] = static_cast<int>((ok >> at) & ((1u << pieces) - 1u));
+                ok = it < kStages ||
+                     mbar_wait_warp(&sm.empty[st], ((it / kStages) & 1) ^ 1, abort, p.status);
+                if (!ok) break;
+                if (elect_one()) {
+                    sm.have[st] = pg.have;
+                    // the compute warps read (and may have zeroed) the stage with
+                    // ordinary accesses
+                    fence_proxy_async_smem();
                     mbar_arrive_expect_tx(&sm.full[st], C::STAGE);
+                    constexpr int E = C::BOX / (kFp8 ? 1 : 2);
+                    copy_tile<kTile, C::BOXES, C::BOX, E>(p, &kmap, &sm.full[st], ring_a + st * C::STAGE,
+                                                   pg, t, x.g);
+                    copy_tile<kTile, C::BOXES, C::BOX, E>(p, &vmap, &sm.full[st],
+                                                   ring_a + st * C::STAGE + C::TILE, pg, t, x.g);
                 }
                 __syncwarp();
-                if (copies) {
-                    // the compute warps read (and may have zeroed) the stage
-                    // with ordinary accesses
-                    fence_proxy_async_smem();
-                    const int pos = (t * kTile) + (my_piece << p.box_shift);
-                    const bool real = (ok >> (at + my_piece)) & 1u;
-                    tma_load_4d(ring_a + st * C::STAGE + my_off, my_pool ? &vmap : &kmap,
-                                &sm.full[st], my_box * (C::BOX / (kFp8 ? 1 : 2)),
-                                pos & ((1 << p.d.page_shift) - 1), x.g,
-                                real ? page : p.d.num_pages);
-                }
             }
-            if (*abort) break;
         }
         if (*abort && lane == 0) {  // let the copies in flight land before the CTA exits
             for (int j = it > kStages ? it - kStages : 0; j < it; ++j)
@@ -567,64 +546,78 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
 // The items that a run border cuts: O = sum_c 2^(m_c - M) o_c / sum_c
 // 2^(m_c - M) l_c over the runs c that hold a stretch, in ascending c.  One
-// block per item and 16 of its rows; a block whose item lies in one run leaves
-// at once.
-constexpr int kMergeThreads = 128;
-constexpr int kMergeRows = 16;
+// block per item and 8 of its rows, a warp a row.  The plan is worked out while
+// the attention kernel still runs: that kernel lets this one start only after
+// everything before it has ended, so lens and cu are final.
+constexpr int kMergeThreads = 256;
+constexpr int kMergeRows = kMergeThreads / 32;
+constexpr int kMergeAhead = 4;   // states whose loads a lane has in flight
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TreeParams p,
-                                                                   int max_row_tiles, int chunks) {
-    __shared__ long long red[kMergeThreads / 32];
-    pdl_trigger();
-    pdl_wait();
+__global__ void __launch_bounds__(kMergeThreads)
+    tree_merge_kernel(const __grid_constant__ TreeParams p, int max_row_tiles, int chunks) {
+    __shared__ long long red[2][kMergeThreads / 32];
     const int chunk = blockIdx.x % chunks, item = blockIdx.x / chunks;
     const int rt = item % max_row_tiles, g = item / max_row_tiles, b = blockIdx.y;
     const Seq s = sequence(p, b);
     const int row0 = rt << p.row_shift;
     const int rows = min(1 << p.row_shift, s.n * p.QG - row0);
-    if (rt >= s.row_tiles || chunk * kMergeRows >= rows) return;
-    long long mine = 0, upto = 0, all, total;
-    for (int i = threadIdx.x; i < p.d.B; i += kMergeThreads) {
-        const long long t = tiles_of(p, sequence(p, i));
-        mine += t;
-        if (i < b) upto += t;
-    }
-    block_scan<kMergeThreads>(mine, red, &all);
-    __syncthreads();
-    block_scan<kMergeThreads>(upto, red, &total);
-    const long long len = run_length(p, all);
-    const long long start = total + (static_cast<long long>(g) * s.row_tiles + rt) * s.tiles;
-    const int c0 = static_cast<int>(start / len), c1 = static_cast<int>((start + s.tiles - 1) / len);
-    if (c0 == c1) return;
-    constexpr int V = D / 32;   // values per lane
-    const int lane = threadIdx.x & 31;
-    const int end = min(rows, (chunk + 1) * kMergeRows);
-    for (int r = chunk * kMergeRows + (threadIdx.x >> 5); r < end; r += kMergeThreads / 32) {
-        auto part = [&](int c) { return partial_at<D>(p, 2 * c + (c == c0 ? 1 : 0)); };
-        float M = -INFINITY;
-        for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, part(c).m[r]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        M = finite_max(M);
-        float num[V], den = 0.f;
-#pragma unroll
-        for (int j = 0; j < V; ++j) num[j] = 0.f;
-        for (int c = c0; c <= c1; ++c) {
-            const PartialAt x = part(c);
-            const float f = fast_exp2(x.m[r] - M);
-            den = fmaf(f, x.l[r], den);
-            const float* o = x.o + static_cast<size_t>(r) * D + lane * V;
-#pragma unroll
-            for (int j = 0; j < V; ++j) num[j] = fmaf(f, o[j], num[j]);
+    const int r = chunk * kMergeRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    int c0 = 0, c1 = 0;
+    if (rt < s.row_tiles && chunk * kMergeRows < rows) {
+        long long mine = 0, upto = 0, all, before;
+        for (int i = threadIdx.x; i < p.d.B; i += kMergeThreads) {
+            const int u = units_of(p, sequence(p, i));
+            mine += u;
+            if (i < b) upto += u;
         }
-        const float inv = den > 0.f ? p.vscale / den : (den == 0.f ? 0.f : den);
-        const int rr = row0 + r;
-        __nv_bfloat16* out = p.O + (static_cast<int64_t>(s.first + rr / p.QG) * p.Hq + g * p.QG +
-                                    rr % p.QG) * D + lane * V;
-#pragma unroll
-        for (int j = 0; j < V; j += 2)
-            *reinterpret_cast<uint32_t*>(out + j) = pack_bf16x2(num[j] * inv, num[j + 1] * inv);
+        block_scan<kMergeThreads>(mine, red[0], &all);
+        block_scan<kMergeThreads>(upto, red[1], &before);
+        const long long len = run_length(p, all);
+        const int units = item_units(p, s);
+        const long long start = before + static_cast<long long>(g * s.row_tiles + rt) * units;
+        c0 = static_cast<int>((start + p.setup) / len);
+        c1 = static_cast<int>((start + units - 1) / len);
     }
+    pdl_trigger();
+    pdl_wait();
+    if (c0 == c1 || r >= rows) return;
+    constexpr int V = D / 32;   // values per lane
+    auto part = [&](int c) { return partial_at<D>(p, 2 * c + (c == c0 ? 1 : 0)); };
+    float M = -INFINITY;
+    for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, part(c).m[r]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    M = finite_max(M);
+    float num[V], den = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) num[j] = 0.f;
+    for (int c = c0; c <= c1; c += kMergeAhead) {
+        float m[kMergeAhead], l[kMergeAhead], o[kMergeAhead][V];
+#pragma unroll
+        for (int k = 0; k < kMergeAhead; ++k) {
+            if (c + k > c1) break;
+            const PartialAt x = part(c + k);
+            m[k] = x.m[r];
+            l[k] = x.l[r];
+#pragma unroll
+            for (int j = 0; j < V; ++j) o[k][j] = x.o[static_cast<size_t>(r) * D + lane * V + j];
+        }
+#pragma unroll
+        for (int k = 0; k < kMergeAhead; ++k) {
+            if (c + k > c1) break;
+            const float f = fast_exp2(m[k] - M);
+            den = fmaf(f, l[k], den);
+#pragma unroll
+            for (int j = 0; j < V; ++j) num[j] = fmaf(f, o[k][j], num[j]);
+        }
+    }
+    const float inv = den > 0.f ? p.vscale / den : (den == 0.f ? 0.f : den);
+    const int rr = row0 + r;
+    __nv_bfloat16* out = p.O + (static_cast<int64_t>(s.first + rr / p.QG) * p.Hq + g * p.QG +
+                                rr % p.QG) * D + lane * V;
+#pragma unroll
+    for (int j = 0; j < V; j += 2)
+        *reinterpret_cast<uint32_t*>(out + j) = pack_bf16x2(num[j] * inv, num[j + 1] * inv);
 }
 
 template <int D, bool kFp8, bool kHalf>
@@ -674,11 +667,11 @@ int launch_rows(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreePara
 // per SM and shortest run.
 struct Variant {
     bool tc;
-    int row_shift, ctas_per_sm, min_run;
+    int row_shift, tile_shift, ctas_per_sm, min_run, setup;
 };
 Variant variant(int rows) {
-    if (rows <= kRows) return {false, 4, kCtasPerSm, 2};
-    return {true, rows <= 128 ? 7 : 8, 1, 4};
+    if (rows <= kRows) return {false, 4, 6, kCtasPerSm, 2, 1};
+    return {true, rows <= 128 ? 7 : 8, kTcTileShift, 1, 4, 2};
 }
 
 }  // namespace
@@ -709,8 +702,10 @@ int launch_tree_attention(const qmm_kv_cache& c, const void* q, int64_t q_stride
     const Variant var = variant(T * p.QG);
     p.ctas = var.ctas_per_sm * num_sms;
     p.row_shift = var.row_shift;
+    p.tile_shift = var.tile_shift;
     p.min_run = var.min_run;
-    p.box_shift = p.d.page_shift < 6 ? p.d.page_shift : 6;
+    p.setup = var.setup;
+    p.box_shift = p.d.page_shift < p.tile_shift ? p.d.page_shift : p.tile_shift;
     p.qscale = scale * 1.4426950408889634f * c.k_scale;  // log2(e): exp2 of the scaled score
     p.vscale = c.v_scale;
     // K and V as [pages, heads, slots, D], copied a page piece and 128 bytes of

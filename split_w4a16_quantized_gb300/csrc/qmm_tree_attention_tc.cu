@@ -2,20 +2,21 @@
 // the products on the 5th-generation tensor cores.
 //
 // The formulas and the work split are those of qmm_tree_attention.cu.  Here a
-// work item is up to 128 or 256 rows, the MMA's M, and a tile is two MMAs with
-// the accumulators in tensor memory:
-//   S [128 x 64]  = Q [128 x D] K^T    A = Q in tensor memory, B = the K tile
-//   O [128 x D]  += P [128 x 64] V     A = P in tensor memory, B = the V tile
-// Rows past the item's are computed and dropped: at 128 rows a tile's products
-// take about a fifth of the time its 32 KB of K and V take from HBM, so the
-// padding is free where there are few rows, and full tiles are what it is for.
+// work item is up to 128 or 256 rows, the MMA's M, and a tile is 128 positions:
+//   S [128 x 128] = Q [128 x D] K^T    Q and the K tile in shared memory
+//   O [128 x D]  += P [128 x 128] V    P in tensor memory, V in shared memory
+// with S and O accumulated in tensor memory.  Rows past the item's are computed
+// and dropped: at 128 rows a tile's products take less than half the time its
+// K and V take from HBM, so padding costs nothing where there are few rows, and
+// full tiles are what the layout is for.
 //
-// One CTA per SM, 12 warps:
-//   warp 0     copies: K and V tiles, each to its own slot of a ring
+// One CTA per SM:
+//   warp 0     copies: K and V tiles into a ring each
 //   warp 1     issues the MMAs and owns the tensor memory
-//   warps 2-3  E4M3 cache: convert the copied tiles to F16 in a second ring
+//   warps 2-3  bring the next item's q
 //   warps 4-7, 8-11  two softmax groups of 128 threads, one thread a row
-// Two streams of (Q, S/P, O) keep the tensor cores and the exponentials busy at
+//   warps 12-15  E4M3 cache: V tiles to F16
+// Two streams of (S/P, O) keep the tensor cores and the exponentials busy at
 // the same time: while a group turns its S into P, the other stream's products
 // run.  An item of more than 128 rows gives each stream half of the rows and
 // the same tiles; an item of at most 128 gives both streams all rows and every
@@ -25,6 +26,20 @@
 // issue order, so a group that sees S of its next tile also knows that its last
 // P V is done, and may rescale O.
 //
+// Few rows.  An item of at most 64 (32) rows is put into the 128 twice (four
+// times).  The MMA computes all copies' scores anyway; copy c of a row takes
+// columns [c w, (c + 1) w) of the tile, w = 128 / copies, and zeros elsewhere
+// in P, so a row's exponentials are spread over that many warps, which would
+// idle otherwise.  The copies' states are added at the end.
+//
+// An item's first scores need only its q and K: they are issued right behind
+// the last products of the item before, while the groups still write that
+// item's output.
+//
+// Why 128 positions: an MMA takes about 68 clocks for any N up to 128 (measured:
+// with 64 positions a tile the same products took 1.5 times as long), and the
+// hand-overs between the roles cost the same per tile whatever its size.
+//
 // A row's maximum is followed lazily: P = 2^(s - ref) with a reference that is
 // raised only when a score passes it by more than 8, so P stays below 2^8 and O
 // is rescaled a few times per item instead of every tile.  The result is the
@@ -33,8 +48,18 @@
 // keeps two: the second would double the P V products, and its error is that of
 // rounding the output.
 //
-// Tensor memory (512 columns): Q 2 x 64, S/P 2 x 64, O 2 x 128 for D = 128.
+// E4M3 cache.  Q K^T runs on the 8-bit keys as they are: a BF16 number has 8
+// significant bits, so a row of q, scaled by a power of two to a maximum in
+// [128, 256), is the sum of two E4M3 numbers, exactly for what lies within 2^-9
+// of the row's maximum and to 2^-17 of that maximum below.  P V needs more bits
+// of P than two E4M3 terms give far below the maximum (a long flat tail under
+// one large weight would vanish), so V is converted to F16, exactly, and P is
+// F16.
+//
+// Tensor memory (512 columns): S/P 2 x 128, O 2 x 128.
+#include <cstddef>
 #include <mutex>
+#include <type_traits>
 
 #include "qmm.h"
 #include "qmm_tree.cuh"
@@ -42,56 +67,82 @@
 namespace qmm {
 namespace {
 
-constexpr int kTcThreads = 384;
-constexpr int kConvWarps = 2;       // warps 2 and 3
-constexpr int kSoftmaxWarp0 = 4;
+constexpr int kTile = 1 << kTcTileShift;
+constexpr int kSoftmaxWarp0 = 4, kConvWarp0 = 12;
+constexpr int kConvWarps = 4;
+constexpr int kMaxSlots = 8;        // of one ring
+constexpr int kConvSlots = 2;
 constexpr int kHave = 16;           // tiles whose page bits are kept
 constexpr float kLazy = 8.f;        // log2 units a score may pass the reference by
-
-constexpr uint32_t kColQ = 0, kColS = 128, kColO = 256;   // stream s: + 64 s, + 64 s, + 128 s
+constexpr uint32_t kColS = 0, kColO = 256;   // stream s: + 128 s
 
 template <int D, bool kFp8>
 struct Tc {
-    static constexpr int ROW = D * (kFp8 ? 1 : 2);
-    static constexpr int BOX = ROW < 128 ? ROW : 128;
+    // registers: the launch gives every thread the same share; the softmax groups
+    // hold a row of S (128 values) and take over what the others do not need
+    static constexpr int THREADS = kFp8 ? 512 : 384;
+    static constexpr int REGS_CTL = kFp8 ? 56 : 88;
+    static constexpr int REGS_SOFTMAX = kFp8 ? 200 : 208;
+    static constexpr int REGS_CONV = 56;
+    static_assert(kFp8 ? 128 * (REGS_CTL + 2 * REGS_SOFTMAX + REGS_CONV) <= THREADS * 128
+                       : 128 * (REGS_CTL + 2 * REGS_SOFTMAX) <= THREADS * 168, "registers");
+    static constexpr int ROW = D * (kFp8 ? 1 : 2);           // bytes of a cache row
+    static constexpr int BOX = ROW < 128 ? ROW : 128;        // row bytes of one copy
     static constexpr int BOXES = ROW / BOX;
-    static constexpr int COPY = kTile * ROW;                 // bytes of a copied tile
-    static constexpr int MMA = kTile * D * 2;                // of an MMA operand tile
-    static constexpr int SLOTS = kFp8 ? 8 : (D == 128 ? 12 : 16);   // copy ring
-    static constexpr int CONV = kFp8 ? 8 : 0;                // converted ring
-    static constexpr int RING = SLOTS * COPY + CONV * MMA;
-    static constexpr int KS = D / 16;
-    static constexpr int COLS_Q = D / 2;                     // tensor memory columns of Q
+    static constexpr int SLOT = kTile * ROW;                 // a copied tile
+    static constexpr int Q = 128 * D * 2;                    // a stream's Q: BF16, or two E4M3 terms
+    static constexpr int CONV = kTile * D * 2;               // a converted V tile
 };
 
-template <int D, bool kFp8>
 struct TcSmem {
-    uint64_t full[Tc<D, kFp8>::SLOTS], empty[Tc<D, kFp8>::SLOTS];
-    uint64_t cfull[8], cempty[8];       // converted ring
+    uint64_t kfull[kMaxSlots], kempty[kMaxSlots], vfull[kMaxSlots], vempty[kMaxSlots];
+    uint64_t cfull[kConvSlots], cempty[kConvSlots];
     uint64_t sfull[2];                  // S of a stream's next tile is there
     uint64_t pready[2];                 // P is, and O may take its product
     uint64_t ofull[2];                  // O is complete
-    uint64_t qready;
+    uint64_t qready, qfree;             // an item's q is there; its products have read it
+    uint64_t odone;                     // O, m and l of an item are read by all
     uint64_t drained;                   // abort: every MMA issued has ended
     uint32_t tmem;
     int have[kHave];                    // pages of a tile that exist, one bit a copy
     float m[2][128], l[2][128];
+    float qs[2][256];                   // E4M3: the rows' scales, by stretch parity
     int16_t par[kMaxTree];
-    uint32_t anc[256][kWords + 1];      // a thread's own row: ancestors and itself
+    union alignas(16) {
+        uint32_t anc[128][kWords + 1];  // a thread's own row: ancestors and itself
+        float x[96][16];                // columns of O from other copies of the rows
+    } u[2];                             // of each group
     RunShared run;
 };
+static_assert(offsetof(TcSmem, u) % 16 == 0 && sizeof(TcSmem::u) % 32 == 0, "16-byte accesses");
+constexpr int kSmemHead = (sizeof(TcSmem) + 1023) / 1024 * 1024;
 
-// Instruction descriptor: kind::f16, FP32 accumulate, K-major A in tensor
-// memory, B K-major or (transposed) N-major.
-__host__ __device__ constexpr uint32_t idesc(int N, bool f16, bool b_n_major) {
-    return (1u << 4) | ((f16 ? 0u : 1u) << 7) | ((f16 ? 0u : 1u) << 10) |
-           ((b_n_major ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
+// A ring position.
+struct Cursor {
+    int slot = 0, phase = 0;
+    __device__ __forceinline__ void next(int slots) {
+        if (++slot == slots) slot = 0, phase ^= 1;
+    }
+};
+
+// Instruction descriptor, FP32 accumulate, M = 128, K-major A, B K-major or
+// N-major; format 0: F16 (kind::f16) or E4M3 (kind::f8f6f4), 1: BF16.
+__host__ __device__ constexpr uint32_t idesc(int N, uint32_t format, bool b_n_major) {
+    return (1u << 4) | (format << 7) | (format << 10) | ((b_n_major ? 1u : 0u) << 16) |
+           (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
 }
 
-// Shared-memory descriptor of a V tile as B, N-major with the 128-byte
-// swizzle: rows are positions (the MMA's K), 64 values of the head wide; the
-// next 64 values are kTile rows on (leading offset), the next 8 positions 1024
-// bytes (stride offset).
+// Shared-memory descriptor, K-major rows of kRow (128 or 64) bytes with the
+// swizzle of that width; 8 rows apart: 8 kRow bytes.
+template <int kRow>
+__device__ __forceinline__ uint64_t sdesc_k_major(uint32_t saddr) {
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1) << 16) |
+           (static_cast<uint64_t>((8 * kRow) >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+           (static_cast<uint64_t>(kRow == 128 ? 2 : 4) << 61);
+}
+// A V tile as B, N-major with the 128-byte swizzle: rows are positions (the
+// MMA's K), 64 values of the head wide; the next 64 values are kTile rows on
+// (leading offset), the next 8 positions 1024 bytes (stride offset).
 __device__ __forceinline__ uint64_t sdesc_n_major(uint32_t saddr) {
     return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) |
            (static_cast<uint64_t>((kTile * 128) >> 4) << 16) |
@@ -99,44 +150,109 @@ __device__ __forceinline__ uint64_t sdesc_n_major(uint32_t saddr) {
            (static_cast<uint64_t>(2) << 61);
 }
 
-// Offset of 16-byte chunk c of row r: copied tile (boxes of 64 rows), and
-// operand tile (64 values, 128 bytes a row).
-template <int BOX>
-__device__ __forceinline__ uint32_t copy_off(int r, int c) {
-    if (BOX == 128)
-        return static_cast<uint32_t>((c >> 3) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+// D[tmem] (+)= A[smem] B[smem].
+template <bool kF8>
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t accumulate) {
+    if (kF8)
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+            " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+            " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+
+// 32 lanes x 32 columns.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+          "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]),
+          "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]),
+          "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr)
+        : "memory");
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegs));
+}
+
+// Offset of 16-byte chunk c of row r in a tile of 128 rows: boxes of kBox bytes
+// a row, the chunk permuted by the swizzle of that width.
+template <int kBox>
+__device__ __forceinline__ uint32_t tile_off(int r, int c) {
+    if (kBox == 128)
+        return static_cast<uint32_t>((c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
     return static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
-// Positions of a tile (64 bits, from its first) that a row sees.
 __device__ __forceinline__ uint64_t low_bits(int n) {
     return n <= 0 ? 0ull : (n >= 64 ? ~0ull : (1ull << n) - 1ull);
 }
 
+// 64 of a row's bits, from bit `from` on (negative: zeros first).
+__device__ __forceinline__ uint64_t bits_from(const uint32_t* anc, int from) {
+    const int lead = from < 0 ? -from : 0;
+    if (lead >= 64) return 0;
+    if (from < 0) from = 0;
+    uint64_t bits = 0;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        const int w = (from >> 5) + k;
+        const uint64_t b = w < kWords ? anc[w] : 0u;
+        const int sh = 32 * k - (from & 31);
+        bits |= sh >= 0 ? (sh < 64 ? b << sh : 0ull) : b >> -sh;
+    }
+    return bits << lead;
+}
+
+struct Layout {
+    int k_slots, v_slots;
+};
+
+// How often an item's rows stand in the 128 of a product.
+__device__ __forceinline__ int copies_of(int rows) { return rows <= 32 ? 4 : (rows <= 64 ? 2 : 1); }
+
 template <int D, bool kFp8>
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap kmap,
-                   const __grid_constant__ CUtensorMap vmap, const __grid_constant__ TreeParams p) {
+                   const __grid_constant__ CUtensorMap vmap, const __grid_constant__ TreeParams p,
+                   const Layout lay) {
     using C = Tc<D, kFp8>;
-    using Sm = TcSmem<D, kFp8>;
-    constexpr int SLOTS = C::SLOTS, KS = C::KS;
     extern __shared__ uint8_t tree_tc_smem_raw[];
-    uint8_t* ring = reinterpret_cast<uint8_t*>(
+    uint8_t* base_s = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(tree_tc_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    Sm& sm = *reinterpret_cast<Sm*>(ring + C::RING);
+    TcSmem& sm = *reinterpret_cast<TcSmem*>(base_s);
+    uint8_t* q_s = base_s + kSmemHead;
+    uint8_t* conv_s = q_s + (C::Q << (p.row_shift - 7));
+    uint8_t* k_s = conv_s + (kFp8 ? kConvSlots * C::CONV : 0);
+    uint8_t* v_s = k_s + lay.k_slots * C::SLOT;
     __shared__ int abort_flag;
     volatile int* abort = &abort_flag;
-    const uint32_t ring_a = smem_addr(ring);
-    const uint32_t conv_a = ring_a + SLOTS * C::COPY;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         abort_flag = 0;
-        for (int i = 0; i < SLOTS; ++i) {
-            mbar_init(&sm.full[i], 1);
-            mbar_init(&sm.empty[i], kFp8 ? kConvWarps : 1);
+        for (int i = 0; i < kMaxSlots; ++i) {
+            mbar_init(&sm.kfull[i], 1);
+            mbar_init(&sm.kempty[i], 1);
+            mbar_init(&sm.vfull[i], 1);
+            mbar_init(&sm.vempty[i], kFp8 ? kConvWarps : 1);
         }
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < kConvSlots; ++i) {
             mbar_init(&sm.cfull[i], kConvWarps);
             mbar_init(&sm.cempty[i], 1);
         }
@@ -145,7 +261,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(&sm.pready[s], 4);
             mbar_init(&sm.ofull[s], 1);
         }
-        mbar_init(&sm.qready, 8);
+        mbar_init(&sm.qready, 2);
+        mbar_init(&sm.qfree, 1);
+        mbar_init(&sm.odone, 8);
         mbar_init(&sm.drained, 1);
         mbar_fence_init();
         tma_prefetch_map(&kmap);
@@ -164,233 +282,308 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_after();
     pdl_trigger();
     const uint32_t tmem = sm.tmem;
-    Run run = find_run<kTcThreads>(p, sm.run);
-    const int box = 1 << p.box_shift;
+    Run run = find_run<C::THREADS>(p, sm.run);
     const int pieces = kTile >> p.box_shift;
     Stretch x;
+    auto waits = [&](uint64_t* bar, int phase) {
+        return mbar_wait_warp(bar, phase, abort, p.status);
+    };
 
-    if (warp == 0) {
-        // ---- copies ----
-        const int my_piece = lane / C::BOXES, my_box = lane % C::BOXES;
-        const bool copies = my_piece < pieces;
-        const uint32_t my_off = my_box * (kTile * C::BOX) + (my_piece << p.box_shift) * C::BOX;
-        int it = 0, ks = 0;    // tiles; tiles whose K and V both went out
-        int slot = 0, round = 0;
-        bool ok_run = true;
-        while (ok_run && next_stretch(p, run, &x)) {
-            const int c_end = (x.s.total + box - 1) >> p.box_shift;
-            const int* row = p.d.table + static_cast<int64_t>(x.b) * p.d.max_pages;
-            auto entry = [&](int c) {
-                return c < c_end ? row[(c << p.box_shift) >> p.d.page_shift] : -1;
-            };
-            int c0 = x.t0 * pieces;
-            int cur = entry(c0 + lane), nxt = entry(c0 + 32 + lane);
-            for (int t = x.t0; ok_run && t < x.t1; ++t, ++it) {
-                if (t * pieces >= c0 + 32) {
-                    c0 += 32;
-                    cur = nxt;
-                    nxt = entry(c0 + 32 + lane);
-                }
-                const int at = t * pieces - c0;
-                const uint32_t ok = __ballot_sync(0xffffffffu, cur >= 0 && cur < p.d.num_pages);
-                const int page = __shfl_sync(0xffffffffu, cur, (at + my_piece) & 31);
-                const int pos = (t * kTile + (my_piece << p.box_shift)) &
-                                ((1 << p.d.page_shift) - 1);
-                const bool real = (ok >> ((at + my_piece) & 31)) & 1u;
-#pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    if (round > 0 && !mbar_wait_warp(&sm.empty[slot], (round - 1) & 1, abort, p.status)) {
-                        ok_run = false;
-                        break;
-                    }
-                    if (lane == 0) {
-                        if (v == 0)
-                            sm.have[it % kHave] = static_cast<int>((ok >> at) & ((1u << pieces) - 1u));
-                        mbar_arrive_expect_tx(&sm.full[slot], C::COPY);
+    if (warp < kSoftmaxWarp0) {
+        regs_dec<C::REGS_CTL>();
+        if (warp == 0) {
+            // ---- copies ----
+            constexpr int E = C::BOX / (kFp8 ? 1 : 2);
+            Cursor kc, vc;
+            int it = 0, nv = 0;   // tiles of K and of V issued
+            bool ok = true;
+            while (ok && next_stretch(p, run, &x)) {
+                PageWalk<kTile> walk;
+                walk.start(p, x, lane);
+                for (int t = x.t0; t < x.t1; ++t) {
+                    const TilePages<kTile> pg = walk.tile(p, t, lane);
+                    if (!(ok = waits(&sm.kempty[kc.slot], kc.phase ^ 1))) break;
+                    if (elect_one()) {
+                        sm.have[it % kHave] = pg.have;
+                        mbar_arrive_expect_tx(&sm.kfull[kc.slot], C::SLOT);
+                        copy_tile<kTile, C::BOXES, C::BOX, E>(p, &kmap, &sm.kfull[kc.slot],
+                                                              smem_addr(k_s) + kc.slot * C::SLOT,
+                                                              pg, t, x.g);
                     }
                     __syncwarp();
-                    if (copies) {
-                        // the slot may have been read or zeroed with ordinary accesses
+                    ++it;
+                    kc.next(lay.k_slots);
+                    if (!(ok = waits(&sm.vempty[vc.slot], vc.phase ^ 1))) break;
+                    if (elect_one()) {
+                        // the slot was converted from with ordinary loads, or perhaps
+                        // zeroed in part with ordinary stores
                         fence_proxy_async_smem();
-                        tma_load_4d(ring_a + slot * C::COPY + my_off, v ? &vmap : &kmap,
-                                    &sm.full[slot], my_box * (C::BOX / (kFp8 ? 1 : 2)), pos, x.g,
-                                    real ? page : p.d.num_pages);
+                        mbar_arrive_expect_tx(&sm.vfull[vc.slot], C::SLOT);
+                        copy_tile<kTile, C::BOXES, C::BOX, E>(p, &vmap, &sm.vfull[vc.slot],
+                                                              smem_addr(v_s) + vc.slot * C::SLOT,
+                                                              pg, t, x.g);
                     }
-                    ++ks;
-                    if (++slot == SLOTS) slot = 0, ++round;
+                    __syncwarp();
+                    ++nv;
+                    vc.next(lay.v_slots);
                 }
             }
-        }
-        if (*abort && lane == 0) {  // let the copies in flight land before the CTA exits
-            for (int j = ks > SLOTS ? ks - SLOTS : 0; j < ks; ++j)
-                mbar_wait(&sm.full[j % SLOTS], (j / SLOTS) & 1, nullptr, p.status);
-        }
-    } else if (warp == 1) {
-        // ---- MMAs ----
-        // operand tiles in the order K(0), V(0), K(1), V(1), ... of the run
-        constexpr int OPS = kFp8 ? C::CONV : SLOTS;
-        uint64_t* full = kFp8 ? sm.cfull : sm.full;
-        uint64_t* empty = kFp8 ? sm.cempty : sm.empty;
-        const uint32_t op_a = kFp8 ? conv_a : ring_a;
-        constexpr uint32_t iqk = idesc(kTile, kFp8, false);
-        constexpr uint32_t ipv = idesc(D, kFp8, true);
-        int base = 0;                   // tiles of the run before this stretch
-        int np[2] = {0, 0}, nq = 0;     // P's and Q's taken
-        bool go = true;
-        auto wait_op = [&](int j) {
-            return mbar_wait_warp(&full[j % OPS], (j / OPS) & 1, abort, p.status);
-        };
-        auto qk = [&](int s, int j) {   // S of stream s from operand tile j
-            if (lane == 0) {
-                const uint32_t b = op_a + (j % OPS) * C::MMA;
-#pragma unroll
-                for (int k = 0; k < KS; ++k)
-                    umma_bf16_tmem_a(tmem + kColS + 64 * s, tmem + kColQ + 64 * s + 8 * k,
-                                     sdesc_kmajor_sw128(b + (k >> 2) * (kTile * 128) + (k & 3) * 32),
-                                     iqk, k > 0);
+            if (!ok) {  // let the copies in flight land before the CTA exits
+                for (int j = max(0, it - lay.k_slots); j < it; ++j)
+                    mbar_wait(&sm.kfull[j % lay.k_slots], (j / lay.k_slots) & 1, nullptr, p.status);
+                for (int j = max(0, nv - lay.v_slots); j < nv; ++j)
+                    mbar_wait(&sm.vfull[j % lay.v_slots], (j / lay.v_slots) & 1, nullptr, p.status);
             }
-        };
-        auto pv = [&](int s, int j, bool first) {
-            if (lane == 0) {
-                const uint32_t b = op_a + (j % OPS) * C::MMA;
+        } else if (warp == 1) {
+            // ---- MMAs ----
+            constexpr uint32_t iqk = idesc(kTile, kFp8 ? 0u : 1u, false);
+            constexpr uint32_t ipv = idesc(D, kFp8 ? 0u : 1u, true);
+            const uint64_t q_desc = sdesc_k_major<C::BOX>(smem_addr(q_s));
+            const uint64_t k_desc = sdesc_k_major<C::BOX>(smem_addr(k_s));
+            const uint64_t v_desc = sdesc_n_major(smem_addr(kFp8 ? conv_s : v_s));
+            uint64_t* vfull = kFp8 ? sm.cfull : sm.vfull;
+            uint64_t* vempty = kFp8 ? sm.cempty : sm.vempty;
+            constexpr int VSLOT = kFp8 ? C::CONV : C::SLOT;
+            const int v_slots = kFp8 ? kConvSlots : lay.v_slots;
+            Cursor kc, vc;
+            int np[2] = {0, 0}, nq = 0;     // P's and Q's taken
+            int todo = 0;                   // products with this stretch's Q to come
+            bool go = true;
+            auto qk = [&](int s, bool own_q) {   // S of stream s from the K tile at kc
+                const uint64_t a = q_desc + (own_q ? (C::Q >> 4) * s : 0);
+                const uint64_t b = k_desc + static_cast<uint32_t>(kc.slot * C::SLOT >> 4);
+                if (kFp8) {
+                    // 32 values a step; q's two terms
 #pragma unroll
-                for (int k = 0; k < kTile / 16; ++k)
-                    umma_bf16_tmem_a(tmem + kColO + 128 * s, tmem + kColS + 64 * s + 8 * k,
-                                     sdesc_n_major(b + k * 2048), ipv, !first || k > 0);
-            }
-        };
-        auto release = [&](int j) {
-            if (lane == 0) umma_commit(&empty[j % OPS]);
-        };
-        auto s_done = [&](int s) {
-            if (lane == 0) {
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k)
+                            umma_ss<true>(tmem + kColS + 128 * s, a + ((h * 128 * D + k * 32) >> 4),
+                                          b + ((k * 32) >> 4), iqk, h > 0 || k > 0);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t off = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
+                        umma_ss<false>(tmem + kColS + 128 * s, a + off, b + off, iqk, k > 0);
+                    }
+                }
                 umma_commit(&sm.sfull[s]);
                 // this thread has seen the tile's copy complete, and with it the
                 // copy warp's page bits: hand that on
                 mbar_arrive(&sm.sfull[s]);
-            }
-        };
-        while (go && next_stretch(p, run, &x)) {
-            const int nt = x.t1 - x.t0;
-            const bool both = x.s.n * p.QG - x.row0 > 128;   // two halves of the rows
-            if (!mbar_wait_warp(&sm.qready, nq & 1, abort, p.status)) break;
-            ++nq;
-            tc_fence_after();
-            // first S of each stream
-            for (int i = 0; go && i < (both ? 1 : min(nt, 2)); ++i) {
-                const int j = 2 * (base + i);
-                if (!(go = wait_op(j))) break;
-                qk(both ? 0 : i, j);
-                s_done(both ? 0 : i);
-                if (both) {
-                    qk(1, j);
-                    s_done(1);
-                }
-                release(j);
-            }
-            for (int i = 0; go && i < nt; ++i) {
-                for (int u = 0; go && u < (both ? 2 : 1); ++u) {
-                    const int s = both ? u : i & 1;
-                    const int next = i + (both ? 1 : 2);     // the stream's next tile
-                    const bool last = both ? u == 1 : true;  // last reader of the tile
-                    if (!(go = mbar_wait_warp(&sm.pready[s], np[s] & 1, abort, p.status))) break;
-                    ++np[s];
-                    if (!(go = wait_op(2 * (base + i) + 1))) break;
+                if (todo == 1) umma_commit(&sm.qfree);
+            };
+            auto pv = [&](int s, bool first) {
+                const uint64_t b = v_desc + static_cast<uint32_t>(vc.slot * VSLOT >> 4);
+#pragma unroll
+                for (int k = 0; k < kTile / 16; ++k)
+                    umma_bf16_tmem_a(tmem + kColO + 128 * s, tmem + kColS + 128 * s + 8 * k,
+                                     b + ((k * 2048) >> 4), ipv, !first || k > 0);
+            };
+            while (go && next_stretch(p, run, &x)) {
+                const int nt = x.t1 - x.t0;
+                const bool both = x.s.n * p.QG - x.row0 > 128;   // two halves of the rows
+                const int step = both ? 1 : 2;
+                if (!(go = waits(&sm.qready, nq & 1))) break;
+                todo = both ? 2 * nt : nt;
+                // first S of each stream
+                for (int i = 0; i < (both ? 1 : min(nt, 2)); ++i) {
+                    if (!(go = waits(&sm.kfull[kc.slot], kc.phase))) break;
                     tc_fence_after();
-                    pv(s, 2 * (base + i) + 1, i < (both ? 1 : 2));
-                    if (last) release(2 * (base + i) + 1);
-                    if (next < nt) {
-                        if (!(go = wait_op(2 * (base + next)))) break;
-                        qk(s, 2 * (base + next));
-                        s_done(s);
-                        if (last) release(2 * (base + next));
-                    } else if (lane == 0) {
-                        umma_commit(&sm.ofull[s]);
+                    for (int u = 0; u < (both ? 2 : 1); ++u, --todo) {
+                        if (elect_one()) {
+                            qk(both ? u : i, both);
+                            if (!both || u == 1) umma_commit(&sm.kempty[kc.slot]);
+                        }
+                        __syncwarp();
+                    }
+                    kc.next(lay.k_slots);
+                }
+                // O is free once the last stretch's has been read
+                if (go && nq > 0) go = waits(&sm.odone, (nq - 1) & 1);
+                ++nq;
+                for (int i = 0; go && i < nt; ++i) {
+                    const bool more = i + step < nt;
+                    for (int u = 0; u < (both ? 2 : 1); ++u) {
+                        const int s = both ? u : i & 1;
+                        const bool last = !both || u == 1;   // last reader of the tiles
+                        if (!(go = waits(&sm.pready[s], np[s] & 1))) break;
+                        ++np[s];
+                        if (u == 0 && !(go = waits(&vfull[vc.slot], vc.phase))) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            pv(s, i < step);
+                            if (last) umma_commit(&vempty[vc.slot]);
+                            if (!more) umma_commit(&sm.ofull[s]);
+                        }
+                        __syncwarp();
+                        if (last) vc.next(v_slots);
+                        if (!more) continue;
+                        if (u == 0 && !(go = waits(&sm.kfull[kc.slot], kc.phase))) break;
+                        if (elect_one()) {
+                            qk(s, both);
+                            if (last) umma_commit(&sm.kempty[kc.slot]);
+                        }
+                        __syncwarp();
+                        --todo;
+                        if (last) kc.next(lay.k_slots);
                     }
                 }
             }
-            base += nt;
-        }
-        if (*abort) {  // MMAs in flight end before the tensor memory goes back
-            if (lane == 0) {
-                umma_commit(&sm.drained);
-                mbar_wait(&sm.drained, 0, nullptr, p.status);
+            if (!go) {  // MMAs in flight end before the tensor memory goes back
+                if (elect_one()) umma_commit(&sm.drained);
+                __syncwarp();
+                mbar_wait_warp(&sm.drained, 0, nullptr, p.status);
             }
-            __syncwarp();
-        }
-    } else if (warp < kSoftmaxWarp0) {
-        // ---- E4M3 -> F16 ----
-        if (kFp8) {
+        } else {
+            // ---- q of each item to shared memory, all its copies ----
             const int t64 = tid - 64;
-            int j = 0;
-            bool go = true;
-            while (go && next_stretch(p, run, &x)) {
-                for (int t = x.t0; go && t < x.t1; ++t) {
-                    const int valid = x.s.total - t * kTile;
-                    for (int v = 0; v < 2; ++v, ++j) {
-                        if (!(go = mbar_wait_warp(&sm.full[j % SLOTS], (j / SLOTS) & 1, abort,
-                                                  p.status)))
-                            break;
-                        const int cs = j % 8;
-                        if (j >= 8 && !(go = mbar_wait_warp(&sm.cempty[cs], ((j / 8) & 1) ^ 1, abort,
-                                                            p.status)))
-                            break;
-                        const uint8_t* src = ring + (j % SLOTS) * C::COPY;
-                        uint8_t* dst = ring + SLOTS * C::COPY + cs * C::MMA;
-                        // thread: row t64, every 16-value chunk
-                        uint4 in[D / 16];
+            for (int k = 0; next_stretch(p, run, &x); ++k) {
+                const int rows = min(1 << p.row_shift, x.s.n * p.QG - x.row0);
+                const int copies = copies_of(rows);
+                if (k > 0 && !waits(&sm.qfree, (k - 1) & 1)) break;
+                if (k > 0) fence_proxy_async_smem();
+                const __nv_bfloat16* q0 = p.q + x.s.first * p.q_stride + x.g * p.QG * D;
+                auto row_of = [&](int r) {
+                    const int rr = x.row0 + r;
+                    return q0 + (rr / p.QG) * p.q_stride + (rr % p.QG) * D;
+                };
+                if (kFp8) {
+                    for (int r = t64; r < rows; r += 64) {
+                        const __nv_bfloat16* qv = row_of(r);
+                        uint32_t big = 0;   // largest magnitude, as bits: NaN above all
+#pragma unroll 8
+                        for (int c = 0; c < D / 8; ++c) {
+                            const uint4 v = *reinterpret_cast<const uint4*>(qv + 8 * c);
+                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                        for (int c = 0; c < D / 16; ++c)
-                            in[c] = *reinterpret_cast<const uint4*>(src + copy_off<C::BOX>(t64, c));
-                        if (t64 >= valid) {
-                            // slots past the last position may hold anything, and
-                            // 0 * NaN is not 0
-#pragma unroll
-                            for (int c = 0; c < D / 16; ++c) in[c] = make_uint4(0, 0, 0, 0);
+                            for (int i = 0; i < 4; ++i)
+                                big = max(big, max((w[i] & 0x7fffu) << 16, w[i] & 0x7fff0000u));
                         }
-#pragma unroll
+                        // 2^e <= big < 2^(e+1); a row that holds infinities or NaN
+                        // becomes NaN (what its softmax would be)
+                        int e = static_cast<int>(big >> 23) - 127;
+                        const bool bad = e >= 128;
+                        e = big > 0 && !bad ? max(-110, min(126, e)) : 0;
+                        const float up = bad ? __int_as_float(0x7fffffff)
+                                             : __uint_as_float(static_cast<uint32_t>(134 - e) << 23);
+                        sm.qs[k & 1][r] = __uint_as_float(static_cast<uint32_t>(120 + e) << 23);
+#pragma unroll 2
                         for (int c = 0; c < D / 16; ++c) {
-                            const uint32_t w[4] = {in[c].x, in[c].y, in[c].z, in[c].w};
-                            uint32_t f[8];
+                            uint32_t hi[4], lo[4];
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                f[2 * i] = e4m3x2_to_f16x2(w[i] & 0xffffu);
-                                f[2 * i + 1] = e4m3x2_to_f16x2(w[i] >> 16);
+                                const uint2 w = *reinterpret_cast<const uint2*>(qv + 16 * c + 4 * i);
+                                const float f[4] = {__uint_as_float(w.x << 16) * up,
+                                                    __uint_as_float(w.x & 0xffff0000u) * up,
+                                                    __uint_as_float(w.y << 16) * up,
+                                                    __uint_as_float(w.y & 0xffff0000u) * up};
+                                uint32_t h2[2], l2[2];
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    h2[j] = __nv_cvt_float2_to_fp8x2(
+                                        make_float2(f[2 * j], f[2 * j + 1]), __NV_SATFINITE, __NV_E4M3);
+                                    const uint32_t b = e4m3x2_to_f16x2(h2[j]);
+                                    const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&b));
+                                    l2[j] = __nv_cvt_float2_to_fp8x2(
+                                        make_float2(f[2 * j] - g.x, f[2 * j + 1] - g.y), __NV_SATFINITE,
+                                        __NV_E4M3);
+                                }
+                                hi[i] = h2[0] | (h2[1] << 16);
+                                lo[i] = l2[0] | (l2[1] << 16);
                             }
-                            *reinterpret_cast<uint4*>(dst + copy_off<128>(t64, 2 * c)) =
-                                make_uint4(f[0], f[1], f[2], f[3]);
-                            *reinterpret_cast<uint4*>(dst + copy_off<128>(t64, 2 * c + 1)) =
-                                make_uint4(f[4], f[5], f[6], f[7]);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(&sm.empty[j % SLOTS]);
-                            mbar_arrive(&sm.cfull[cs]);
+                            uint8_t* dst = q_s + (r >> 7) * C::Q;
+                            for (int y = 0; y < copies; ++y) {
+                                const uint32_t o = tile_off<C::BOX>((r & 127) + y * (128 / copies), c);
+                                *reinterpret_cast<uint4*>(dst + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                                *reinterpret_cast<uint4*>(dst + 128 * D + o) =
+                                    make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                            }
                         }
                     }
+                } else {
+                    constexpr int CH = D / 8;   // 16-byte chunks of a row
+                    const uint32_t dst = smem_addr(q_s);
+                    for (int i = t64; i < rows * CH; i += 64) {
+                        const int r = i / CH, c = i % CH;
+                        const __nv_bfloat16* src = row_of(r) + 8 * c;
+                        for (int y = 0; y < copies; ++y)
+                            cp_async16(dst + (r >> 7) * C::Q +
+                                           tile_off<128>((r & 127) + y * (128 / copies), c),
+                                       src, true);
+                    }
+                    cp_async_commit();
+                    cp_async_wait<0>();
                 }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.qready);
+            }
+        }
+    } else if (kFp8 && warp >= kConvWarp0) {
+        // ---- V to F16: thread = position ----
+        regs_dec<C::REGS_CONV>();
+        const int r = tid - 32 * kConvWarp0;
+        Cursor vc, cc;
+        bool go = true;
+        while (go && next_stretch(p, run, &x)) {
+            for (int t = x.t0; t < x.t1; ++t) {
+                const int valid = x.s.total - t * kTile;
+                if (!(go = waits(&sm.vfull[vc.slot], vc.phase))) break;
+                if (!(go = waits(&sm.cempty[cc.slot], cc.phase ^ 1))) break;
+                const uint8_t* src = v_s + vc.slot * C::SLOT;
+                uint8_t* dst = conv_s + cc.slot * C::CONV;
+                uint4 in[D / 16];
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c)
+                    in[c] = *reinterpret_cast<const uint4*>(src + tile_off<C::BOX>(r, c));
+                if (r >= valid) {
+                    // slots past the last position may hold anything, and 0 * NaN
+                    // is not 0
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c) in[c] = make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) {
+                    const uint32_t w[4] = {in[c].x, in[c].y, in[c].z, in[c].w};
+                    uint32_t f[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        f[2 * i] = e4m3x2_to_f16x2(w[i] & 0xffffu);
+                        f[2 * i + 1] = e4m3x2_to_f16x2(w[i] >> 16);
+                    }
+                    *reinterpret_cast<uint4*>(dst + tile_off<128>(r, 2 * c)) =
+                        make_uint4(f[0], f[1], f[2], f[3]);
+                    *reinterpret_cast<uint4*>(dst + tile_off<128>(r, 2 * c + 1)) =
+                        make_uint4(f[4], f[5], f[6], f[7]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sm.vempty[vc.slot]);
+                    mbar_arrive(&sm.cfull[cc.slot]);
+                }
+                vc.next(lay.v_slots);
+                cc.next(kConvSlots);
             }
         }
     } else {
         // ---- softmax groups ----
+        regs_inc<C::REGS_SOFTMAX>();
         const int s = (warp - kSoftmaxWarp0) >> 2;
-        const int gt = tid - 32 * kSoftmaxWarp0;          // 0 .. 255
-        const int r128 = (warp & 3) * 32 + lane;          // row of the stream = tensor memory lane
+        const int gt = (warp & 3) * 32 + lane;            // thread of the group = tensor memory lane
         const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t tS = tmem + quarter + kColS + 64 * s;
-        const uint32_t tQ = tmem + quarter + kColQ + 64 * s;
+        const uint32_t tS = tmem + quarter + kColS + 128 * s;
         const uint32_t tO = tmem + quarter + kColO;       // stream 0's; stream 1's + 128
         int base = 0;             // tiles of the run before this stretch
         int ns = 0, no = 0;       // S's and O's taken
-        auto waits = [&](uint64_t* bar, int phase) {
-            return !__any_sync(0xffffffffu, *abort) && mbar_wait_warp(bar, phase, abort, p.status);
-        };
-        while (next_stretch(p, run, &x)) {
+        for (int k = 0; next_stretch(p, run, &x); ++k) {
             const int nt = x.t1 - x.t0;
             const int rows = min(1 << p.row_shift, x.s.n * p.QG - x.row0);
-            const bool both = x.s.n * p.QG - x.row0 > 128;
-            const int r = both ? r128 + 128 * s : r128;              // row of the item
+            const bool both = rows > 128;
+            const int copies = copies_of(rows), span = 128 / copies;   // lanes, and columns, of a copy
+            const int copy = gt / span;
+            const int r = both ? gt + 128 * s : gt - copy * span;    // row of the item
             const bool on = r < rows;
             const bool warp_on = __any_sync(0xffffffffu, on);
             const int node = (x.row0 + (on ? r : 0)) / p.QG;
@@ -399,7 +592,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (x.t1 * kTile > x.s.len) {
                 if (p.parents) {
                     named_bar_sync(1, 256);   // the last stretch's walks are done
-                    for (int i = gt; i < x.s.n; i += 256) {
+                    for (int i = tid - 32 * kSoftmaxWarp0; i < x.s.n; i += 256) {
                         const int v = p.parents[x.s.first + i];
                         sm.par[i] = static_cast<int16_t>(v >= 0 && v < i ? v : -1);
                     }
@@ -416,145 +609,118 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             if (j == i >> 5) w[j] |= 1u << (i & 31);
                     }
 #pragma unroll
-                for (int j = 0; j < kWords; ++j) sm.anc[gt][j] = w[j];
+                for (int j = 0; j < kWords; ++j) sm.u[s].anc[gt][j] = w[j];
             }
-            // ---- Q to tensor memory ----
-            float qs = p.qscale;
-            if (warp_on) {
-                const __nv_bfloat16* qv = p.q + (x.s.first + node) * p.q_stride + head * D;
-                float down = 1.f;
-                if (kFp8) {
-                    // F16 keeps 11 bits between 2^-14 and 2^16: with the row's
-                    // maximum brought to [1, 2), rounding to it is 2^-25 at most
-                    float big = 0.f;
-#pragma unroll 4
-                    for (int c = 0; c < D / 8; ++c) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(qv + 8 * c);
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+
+            float qs = p.qscale, ref = -INFINITY, sum = 0.f;
+            int mine = 0;   // tiles of this stream
+
+            // One tile: NC columns from the copy's first on.
+            auto tile = [&](auto nc, int t, int at) {
+                constexpr int NC = decltype(nc)::value;
+                const int col0 = copy * NC;
+                uint32_t v[NC];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            big = fmaxf(big, fmaxf(__uint_as_float((w[i] & 0x7fffu) << 16),
-                                                   __uint_as_float(w[i] & 0x7fff0000u)));
+                for (int c = 0; c < NC; c += 32) tmem_ld32(tS + col0 + c, v + c);
+                // what the row sees of the tile
+                const uint32_t have = static_cast<uint32_t>(sm.have[at % kHave]);
+                const int j0 = t * kTile + col0 - x.s.len;   // drafted token of the first position
+                const int valid = x.s.total - t * kTile - col0;
+                const bool cut = j0 + NC > 0 || have != (1u << pieces) - 1u;
+                tmem_ld_wait();
+                if (cut) {
+#pragma unroll
+                    for (int h = 0; h < NC; h += 64) {
+                        // history, then the ancestors
+                        uint64_t see = ~0ull;
+                        const int j = j0 + h;
+                        if (j + 64 > 0)
+                            see = (low_bits(-j) | bits_from(sm.u[s].anc[gt], j)) & low_bits(valid - h);
+                        for (int q = 0; q < pieces; ++q)
+                            if (!((have >> q) & 1u)) {
+                                const int lo = (q << p.box_shift) - col0 - h;
+                                see &= ~(low_bits(lo + (1 << p.box_shift)) & ~low_bits(lo));
+                            }
+#pragma unroll
+                        for (int c = 0; c < (NC < 64 ? NC : 64); ++c)
+                            if (!((see >> c) & 1ull)) v[h + c] = 0xff800000u;   // -inf
                     }
-                    int e = static_cast<int>(__float_as_uint(big) >> 23) - 127;
-                    e = big > 0.f && e < 128 ? max(-126, min(126, e)) : 0;
-                    down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                    qs *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
                 }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < C::COLS_Q; c += 16) {
-                    uint32_t w[16];
+                for (int c = 0; c < NC; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(v[c]));
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * qs;
+                // raise the reference
+                const bool raise = top > ref + kLazy;
+                if (__any_sync(0xffffffffu, raise)) {
+                    const float now = fmaxf(ref, top);
+                    const float f = now == -INFINITY ? 1.f : fast_exp2(ref - now);
+                    sum *= f;
+                    ref = now;
+                    if (mine > 0) {
+                        const uint32_t o = tO + 128 * s;
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t w[16];
+                            tmem_ld16(o + c, w);
+                            tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(qv + 2 * (c + i));
-                        w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+                            for (int q = 0; q < 16; ++q)
+                                w[q] = __float_as_uint(__uint_as_float(w[q]) * f);
+                            tmem_st16(o + c, w);
+                        }
+                        tmem_st_wait();
                     }
-                    if (kFp8)
+                }
+                const float sub = finite_max(ref);
+                float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            w[i] = pack_f16x2(__uint_as_float(w[i] << 16) * down,
-                                              __uint_as_float(w[i] & 0xffff0000u) * down);
-                    tmem_st16(tQ + c, w);
+                for (int h = 0; h < NC; h += 32) {
+                    uint32_t pw[16];
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2) {
+                        const float a = fast_exp2(fmaf(__uint_as_float(v[h + c]), qs, -sub));
+                        const float b = fast_exp2(fmaf(__uint_as_float(v[h + c + 1]), qs, -sub));
+                        part[c / 2 & 3] += a + b;
+                        pw[c / 2] = kFp8 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
+                    }
+                    tmem_st16(tS + (col0 + h) / 2, pw);
+                }
+                sum += (part[0] + part[1]) + (part[2] + part[3]);
+                if (NC < kTile) {   // the other copies' columns
+                    uint32_t z[16];
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) z[q] = 0;
+#pragma unroll
+                    for (int c = 0; c < kTile; c += 32)
+                        if (c < col0 || c >= col0 + NC) tmem_st16(tS + c / 2, z);
                 }
                 tmem_st_wait();
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.qready);
+            };
 
-            float ref = -INFINITY, sum = 0.f;
-            int mine = 0;   // tiles of this stream
             for (int i = both ? 0 : s; i < nt; i += both ? 1 : 2, ++mine) {
                 if (!waits(&sm.sfull[s], ns & 1)) break;
                 ++ns;
                 tc_fence_after();
+                if (kFp8 && mine == 0) qs = p.qscale * sm.qs[k & 1][on ? r : 0];
                 const int t = x.t0 + i;
                 const int valid = x.s.total - t * kTile;
                 if (!kFp8 && valid < kTile) {
                     // slots past the last position may hold anything, and 0 * NaN
                     // is not 0: their V rows become zeros before P V reads them
-                    const int j = 2 * (base + i) + 1;
-                    if (!waits(&sm.full[j % SLOTS], (j / SLOTS) & 1)) break;
-                    uint8_t* v = ring + (j % SLOTS) * C::COPY;
-                    for (int c = gt & 127; c < (kTile - valid) * (C::ROW / 16); c += 128)
-                        *reinterpret_cast<uint4*>(v + copy_off<C::BOX>(valid + c / (C::ROW / 16),
+                    const int j = base + i;
+                    if (!waits(&sm.vfull[j % lay.v_slots], (j / lay.v_slots) & 1)) break;
+                    uint8_t* v = v_s + (j % lay.v_slots) * C::SLOT;
+                    for (int c = gt; c < (kTile - valid) * (C::ROW / 16); c += 128)
+                        *reinterpret_cast<uint4*>(v + tile_off<C::BOX>(valid + c / (C::ROW / 16),
                                                                        c % (C::ROW / 16))) =
                             make_uint4(0, 0, 0, 0);
                     fence_proxy_async_smem();
                 }
                 if (warp_on) {
-                    uint32_t v[64];
-#pragma unroll
-                    for (int c = 0; c < 64; c += 16) tmem_ld16(tS + c, v + c);
-                    // what the row sees of the tile
-                    const uint32_t have = static_cast<uint32_t>(sm.have[(base + i) % kHave]);
-                    const int past = t * kTile + kTile - x.s.len;   // drafted positions and beyond
-                    uint64_t see = ~0ull;
-                    if (past > 0) {
-                        // history, then the ancestors' bits from token j0 on
-                        const int j0 = t * kTile - x.s.len;
-                        const int hist = j0 < 0 ? -j0 : 0;
-                        const int from = j0 > 0 ? j0 : 0;
-                        uint64_t bits = 0;
-#pragma unroll
-                        for (int k = 0; k < 3; ++k) {
-                            const int w = (from >> 5) + k;
-                            const uint64_t b = w < kWords ? sm.anc[gt][w] : 0u;
-                            const int sh = 32 * k - (from & 31);
-                            bits |= sh >= 0 ? (sh < 64 ? b << sh : 0ull) : b >> -sh;
-                        }
-                        see = (hist < 64 ? bits << hist : 0ull) | low_bits(hist);
-                        see &= low_bits(valid);
-                    }
-                    if (have != (1u << pieces) - 1u)
-                        for (int k = 0; k < pieces; ++k)
-                            if (!((have >> k) & 1u)) see &= ~(low_bits(box) << (k << p.box_shift));
-                    tmem_ld_wait();
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    if (__any_sync(0xffffffffu, see != ~0ull)) {
-#pragma unroll
-                        for (int c = 0; c < 64; ++c)
-                            if (!((see >> c) & 1ull)) v[c] = 0xff800000u;   // -inf
-                    }
-#pragma unroll
-                    for (int c = 0; c < 64; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(v[c]));
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * qs;
-                    // raise the reference
-                    const bool raise = top > ref + kLazy || (ref == -INFINITY && top != -INFINITY);
-                    if (__any_sync(0xffffffffu, raise)) {
-                        const float now = fmaxf(ref, top);
-                        const float f = now == -INFINITY ? 1.f : fast_exp2(ref - now);
-                        sum *= f;
-                        ref = now;
-                        if (mine > 0) {
-                            const uint32_t o = tO + 128 * s;
-#pragma unroll 1
-                            for (int c = 0; c < D; c += 16) {
-                                uint32_t w[16];
-                                tmem_ld16(o + c, w);
-                                tmem_ld_wait();
-#pragma unroll
-                                for (int k = 0; k < 16; ++k)
-                                    w[k] = __float_as_uint(__uint_as_float(w[k]) * f);
-                                tmem_st16(o + c, w);
-                            }
-                            tmem_st_wait();
-                        }
-                    }
-                    const float sub = finite_max(ref);
-                    float part[4] = {0.f, 0.f, 0.f, 0.f};
-                    uint32_t pw[32];
-#pragma unroll
-                    for (int c = 0; c < 64; c += 2) {
-                        const float a = fast_exp2(fmaf(__uint_as_float(v[c]), qs, -sub));
-                        const float b = fast_exp2(fmaf(__uint_as_float(v[c + 1]), qs, -sub));
-                        part[c / 2 & 3] += a + b;
-                        pw[c / 2] = kFp8 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
-                    }
-                    sum += (part[0] + part[1]) + (part[2] + part[3]);
-                    tmem_st16(tS, pw);
-                    tmem_st16(tS + 16, pw + 16);
-                    tmem_st_wait();
+                    if (copies == 4) tile(std::integral_constant<int, 32>(), t, base + i);
+                    else if (copies == 2) tile(std::integral_constant<int, 64>(), t, base + i);
+                    else tile(std::integral_constant<int, 128>(), t, base + i);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -567,7 +733,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 tc_fence_after();
             }
             // ---- O, or the partial state.  With tiles shared out, both groups
-            // exchange their statistics and each adds half of the columns ----
+            // exchange their statistics and each adds half of the columns, over
+            // the two streams and then over the copies of a row ----
             float f0 = 1.f, f1 = 0.f, M = ref, den = sum;
             int c_lo = 0, c_hi = D;
             bool two = false;
@@ -575,64 +742,103 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 // (a group without tiles leaves its place alone: the other one may
                 // still be reading it for the stretch before)
                 if (mine > 0) {
-                    sm.m[s][r128] = ref;
-                    sm.l[s][r128] = sum;
+                    sm.m[s][gt] = ref;
+                    sm.l[s][gt] = sum;
                 }
                 tc_fence_before();
                 named_bar_sync(1, 256);
                 tc_fence_after();
                 two = nt > 1;
-                const float m0 = sm.m[0][r128], m1 = two ? sm.m[1][r128] : -INFINITY;
-                M = fmaxf(m0, m1);
+                M = -INFINITY;
+                for (int y = 0; y < copies; ++y) {
+                    M = fmaxf(M, sm.m[0][(gt & (span - 1)) + y * span]);
+                    if (two) M = fmaxf(M, sm.m[1][(gt & (span - 1)) + y * span]);
+                }
                 const float mf = finite_max(M);
-                f0 = fast_exp2(m0 - mf);
-                f1 = fast_exp2(m1 - mf);
-                den = f0 * sm.l[0][r128] + (two ? f1 * sm.l[1][r128] : 0.f);
+                den = 0.f;
+                for (int y = 0; y < copies; ++y) {
+                    const int l = (gt & (span - 1)) + y * span;
+                    const float a = fast_exp2(sm.m[0][l] - mf);
+                    den = fmaf(a, sm.l[0][l], den);
+                    if (y == copy) f0 = a;
+                    if (two) {
+                        const float c = fast_exp2(sm.m[1][l] - mf);
+                        den = fmaf(c, sm.l[1][l], den);
+                        if (y == copy) f1 = c;
+                    }
+                }
                 c_lo = s * (D / 2);
                 c_hi = c_lo + D / 2;
             }
-            if (warp_on && !__any_sync(0xffffffffu, *abort)) {
-                const bool whole = x.t0 == 0 && x.t1 == x.s.tiles;
-                const PartialAt part = partial_at<D>(p, 2 * blockIdx.x + (x.t0 == 0 ? 1 : 0));
-                const float inv =
-                    whole ? (den > 0.f ? p.vscale / den : (den == 0.f ? 0.f : den)) : 1.f;
-                if (on && !whole && c_lo == 0) {
-                    part.m[r] = M;
-                    part.l[r] = den;
-                }
-                __nv_bfloat16* out = p.O + (static_cast<int64_t>(x.s.first + node) * p.Hq + head) * D;
-                float* po = part.o + static_cast<size_t>(r) * D;
-                const uint32_t o0 = both ? tO + 128 * s : tO;
+            const bool whole = x.t0 == 0 && x.t1 == x.s.tiles;
+            const PartialAt part = partial_at<D>(p, 2 * blockIdx.x + (x.t0 == 0 ? 1 : 0));
+            const float inv = whole ? (den > 0.f ? p.vscale / den : (den == 0.f ? 0.f : den)) : 1.f;
+            const bool writes = on && copy == 0 && !*abort;
+            if (writes && !whole && c_lo == 0) {
+                part.m[r] = M;
+                part.l[r] = den;
+            }
+            __nv_bfloat16* out = p.O + (static_cast<int64_t>(x.s.first + node) * p.Hq + head) * D;
+            float* po = part.o + static_cast<size_t>(r) * D;
+            const uint32_t o0 = both ? tO + 128 * s : tO;
 #pragma unroll 1
-                for (int c = c_lo; c < c_hi; c += 16) {
+            for (int c = c_lo; c < c_hi; c += 16) {
+                float y[16];
+                if (warp_on) {
                     uint32_t a[16], b[16];
                     tmem_ld16(o0 + c, a);
                     if (two) tmem_ld16(tO + 128 + c, b);
                     tmem_ld_wait();
-                    float y[16];
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        y[k] = __uint_as_float(a[k]) * f0;
-                        if (two) y[k] = fmaf(__uint_as_float(b[k]), f1, y[k]);
-                        y[k] *= inv;
+                    for (int q = 0; q < 16; ++q) {
+                        y[q] = __uint_as_float(a[q]) * f0;
+                        if (two) y[q] = fmaf(__uint_as_float(b[q]), f1, y[q]);
                     }
-                    if (on && whole) {
+                }
+                if (copies > 1) {   // (uniform in the group; the other copies hand over)
+                    float4* mine_x = reinterpret_cast<float4*>(sm.u[s].x[copy > 0 ? gt - span : 0]);
+                    if (on && copy > 0)
 #pragma unroll
-                        for (int k = 0; k < 16; k += 8)
-                            *reinterpret_cast<uint4*>(out + c + k) = make_uint4(
-                                pack_bf16x2(y[k], y[k + 1]), pack_bf16x2(y[k + 2], y[k + 3]),
-                                pack_bf16x2(y[k + 4], y[k + 5]), pack_bf16x2(y[k + 6], y[k + 7]));
-                    } else if (on) {
+                        for (int q = 0; q < 4; ++q)
+                            mine_x[(q + gt) & 3] = make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2],
+                                                               y[4 * q + 3]);
+                    named_bar_sync(2 + s, 128);
+                    if (on && copy == 0)
+                        for (int z = 1; z < copies; ++z) {
+                            const int l = gt + z * span;
+                            const float4* in = reinterpret_cast<const float4*>(sm.u[s].x[l - span]);
 #pragma unroll
-                        for (int k = 0; k < 16; k += 4)
-                            *reinterpret_cast<float4*>(po + c + k) =
-                                make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
+                            for (int q = 0; q < 4; ++q) {
+                                const float4 v = in[(q + l) & 3];
+                                y[4 * q] += v.x;
+                                y[4 * q + 1] += v.y;
+                                y[4 * q + 2] += v.z;
+                                y[4 * q + 3] += v.w;
+                            }
+                        }
+                    named_bar_sync(2 + s, 128);
+                }
+                if (writes) {
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) y[q] *= inv;
+                    if (whole) {
+#pragma unroll
+                        for (int q = 0; q < 16; q += 8)
+                            *reinterpret_cast<uint4*>(out + c + q) = make_uint4(
+                                pack_bf16x2(y[q], y[q + 1]), pack_bf16x2(y[q + 2], y[q + 3]),
+                                pack_bf16x2(y[q + 4], y[q + 5]), pack_bf16x2(y[q + 6], y[q + 7]));
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 16; q += 4)
+                            *reinterpret_cast<float4*>(po + c + q) =
+                                make_float4(y[q], y[q + 1], y[q + 2], y[q + 3]);
                     }
                 }
             }
-            // The next stretch's products start when every warp of both groups has
-            // brought its Q: until then O, m and l stay as they are.
+            // the next stretch's P V waits for all eight warps
             tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.odone);
         }
     }
     tc_fence_before();
@@ -645,29 +851,33 @@ template <int D, bool kFp8>
 int launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, cudaStream_t st) {
     using C = Tc<D, kFp8>;
     auto kern = tree_tc_kernel<D, kFp8>;
-    const size_t smem = 1024 + static_cast<size_t>(C::RING) + sizeof(TcSmem<D, kFp8>);
-    static int ok = -1;
+    static int limit = -1;
     static std::once_flag once;
-    std::call_once(once, [&] {
-        ok = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  static_cast<int>(smem)) == cudaSuccess;
-    });
-    if (ok != 1) return cudaErrorInvalidValue;
+    std::call_once(once, [&] { limit = set_max_dynamic_smem(reinterpret_cast<const void*>(kern)); });
+    // the rings share what Q and the converted tiles leave
+    const int fixed = 1024 + kSmemHead + (C::Q << (p.row_shift - 7)) +
+                      (kFp8 ? kConvSlots * C::CONV : 0);
+    const int slots = (limit - fixed) / C::SLOT;
+    if (limit < 0 || slots < 4) return cudaErrorInvalidValue;
+    Layout lay;
+    lay.v_slots = slots / 2 < kMaxSlots ? slots / 2 : kMaxSlots;
+    lay.k_slots = slots - lay.v_slots < kMaxSlots ? slots - lay.v_slots : kMaxSlots;
     cudaLaunchConfig_t cfg = {};
     LaunchAttrs la;
     apply_pdl(cfg, la);
     cfg.gridDim = dim3(p.ctas, 1, 1);
-    cfg.blockDim = dim3(kTcThreads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
+    cfg.blockDim = dim3(C::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = fixed + static_cast<size_t>(lay.k_slots + lay.v_slots) * C::SLOT;
     cfg.stream = st;
-    return cudaLaunchKernelEx(&cfg, kern, kmap, vmap, p);
+    return cudaLaunchKernelEx(&cfg, kern, kmap, vmap, p, lay);
 }
 
 }  // namespace
 
 int launch_tree_tc(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int D,
                    bool fp8, cudaStream_t st) {
-    if (D == 128) return fp8 ? launch<128, true>(kmap, vmap, p, st) : launch<128, false>(kmap, vmap, p, st);
+    if (D == 128)
+        return fp8 ? launch<128, true>(kmap, vmap, p, st) : launch<128, false>(kmap, vmap, p, st);
     return fp8 ? launch<64, true>(kmap, vmap, p, st) : launch<64, false>(kmap, vmap, p, st);
 }
 
