@@ -96,7 +96,8 @@ __device__ __forceinline__ long long run_length(const TreeParams& p, long long a
 
 // A CTA's place in the list of units.
 struct Run {
-    int b;            // sequence
+    Seq s;            // sequence b
+    int b;
     int at;           // unit within the sequence's list
     long long left;   // units of the run still to do
 };
@@ -133,6 +134,7 @@ __device__ __forceinline__ Run find_run(const TreeParams& p, RunShared& sh) {
     Run r;
     r.b = sh.b;
     r.at = sh.at;
+    r.s = sequence(p, r.b < 0 ? 0 : r.b);
     r.left = r.b < 0 ? 0 : (all - start < len ? all - start : len);
     return r;
 }
@@ -145,12 +147,12 @@ struct Stretch {
 };
 __device__ __forceinline__ bool next_stretch(const TreeParams& p, Run& r, Stretch* x) {
     while (r.left > 0) {
-        x->s = sequence(p, r.b);
-        while (r.at >= units_of(p, x->s)) {
-            r.at -= units_of(p, x->s);
+        while (r.at >= units_of(p, r.s)) {
+            r.at -= units_of(p, r.s);
             if (++r.b >= p.d.B) return false;   // (not reached: the run ends with the list)
-            x->s = sequence(p, r.b);
+            r.s = sequence(p, r.b);
         }
+        x->s = r.s;
         const int units = item_units(p, x->s);
         const int item = r.at / units, u0 = r.at - item * units;
         x->b = r.b;
@@ -170,8 +172,15 @@ __device__ __forceinline__ bool next_stretch(const TreeParams& p, Run& r, Stretc
 
 // Where partial state `slot` lies: run c's last stretch, when the item starts
 // in it, is slot 2c + 1, its first slot 2c.
+// o is [D / 4][rows][4]: the tcgen05 kernel's threads hold a row each, so
+// neighbouring lanes store neighbouring 16 bytes (row after row, 512 bytes
+// apart, its stores took 32 passes through the load/store unit each).
 struct PartialAt {
-    float *m, *l, *o;   // of the item's row 0; o rows are D values
+    float *m, *l, *o;
+    int row_shift;
+    __device__ __forceinline__ float* at(int r, int c) const {
+        return o + ((static_cast<size_t>(c >> 2) << row_shift) + r) * 4 + (c & 3);
+    }
 };
 template <int D>
 __device__ __forceinline__ PartialAt partial_at(const TreeParams& p, int slot) {
@@ -181,6 +190,7 @@ __device__ __forceinline__ PartialAt partial_at(const TreeParams& p, int slot) {
     a.m = p.ws + r;
     a.l = p.ws + all + r;
     a.o = p.ws + 2 * all + r * D;
+    a.row_shift = p.row_shift;
     return a;
 }
 

@@ -529,13 +529,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                             *reinterpret_cast<uint2*>(out + c) =
                                 make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
                         else
-                            *reinterpret_cast<float4*>(part.o + r * D + c) = v;
+                            *reinterpret_cast<float4*>(part.at(r, c)) = v;
                     } else {
                         const float2 v = make_float2(acc[n][2 * h] * inv, acc[n][2 * h + 1] * inv);
                         if (whole)
                             *reinterpret_cast<uint32_t*>(out + c) = pack_bf16x2(v.x, v.y);
                         else
-                            *reinterpret_cast<float2*>(part.o + r * D + c) = v;
+                            *reinterpret_cast<float2*>(part.at(r, c)) = v;
                     }
                 }
             }
@@ -546,22 +546,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
 // The items that a run border cuts: O = sum_c 2^(m_c - M) o_c / sum_c
 // 2^(m_c - M) l_c over the runs c that hold a stretch, in ascending c.  One
-// block per item and 8 of its rows, a warp a row.  The plan is worked out while
-// the attention kernel still runs: that kernel lets this one start only after
-// everything before it has ended, so lens and cu are final.
+// block per item and 16 of its rows: a thread takes a row and every 16th (D =
+// 128; 64: 8th) group of 4 columns.  The plan is worked out while the attention
+// kernel still runs: that kernel lets this one start only after everything
+// before it has ended, so lens and cu are final.
 constexpr int kMergeThreads = 256;
-constexpr int kMergeRows = kMergeThreads / 32;
-constexpr int kMergeAhead = 4;   // states whose loads a lane has in flight
+constexpr int kMergeRows = 16;
+constexpr int kMergeAhead = 4;   // states whose loads a thread has in flight
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads)
     tree_merge_kernel(const __grid_constant__ TreeParams p, int max_row_tiles, int chunks) {
     __shared__ long long red[2][kMergeThreads / 32];
+    __shared__ __align__(16) uint2 stage[kMergeRows][D / 4 + 2];   // BF16 rows, padded by 16 bytes
     const int chunk = blockIdx.x % chunks, item = blockIdx.x / chunks;
     const int rt = item % max_row_tiles, g = item / max_row_tiles, b = blockIdx.y;
     const Seq s = sequence(p, b);
     const int row0 = rt << p.row_shift;
     const int rows = min(1 << p.row_shift, s.n * p.QG - row0);
-    const int r = chunk * kMergeRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     int c0 = 0, c1 = 0;
     if (rt < s.row_tiles && chunk * kMergeRows < rows) {
         long long mine = 0, upto = 0, all, before;
@@ -580,44 +581,65 @@ __global__ void __launch_bounds__(kMergeThreads)
     }
     pdl_trigger();
     pdl_wait();
-    if (c0 == c1 || r >= rows) return;
-    constexpr int V = D / 32;   // values per lane
-    auto part = [&](int c) { return partial_at<D>(p, 2 * c + (c == c0 ? 1 : 0)); };
-    float M = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, part(c).m[r]);
+    if (c0 == c1) return;
+    constexpr int GROUPS = D / 4;
+    constexpr int TURNS = GROUPS / (kMergeThreads / kMergeRows);   // column groups of a thread
+    const int i = threadIdx.x % kMergeRows, r = chunk * kMergeRows + i;
+    const int j0 = threadIdx.x / kMergeRows;
+    if (r < rows) {
+        auto part = [&](int c) { return partial_at<D>(p, 2 * c + (c == c0 ? 1 : 0)); };
+        float M = -INFINITY;
+#pragma unroll 4
+        for (int c = c0; c <= c1; ++c) M = fmaxf(M, part(c).m[r]);
+        M = finite_max(M);
+        float4 num[TURNS];
+        float den = 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    M = finite_max(M);
-    float num[V], den = 0.f;
+        for (int u = 0; u < TURNS; ++u) num[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = c0; c <= c1; c += kMergeAhead) {
+            float m[kMergeAhead], l[kMergeAhead];
+            float4 o[kMergeAhead][TURNS];
 #pragma unroll
-    for (int j = 0; j < V; ++j) num[j] = 0.f;
-    for (int c = c0; c <= c1; c += kMergeAhead) {
-        float m[kMergeAhead], l[kMergeAhead], o[kMergeAhead][V];
+            for (int k = 0; k < kMergeAhead; ++k) {
+                if (c + k > c1) break;
+                const PartialAt x = part(c + k);
+                m[k] = x.m[r];
+                l[k] = x.l[r];
 #pragma unroll
-        for (int k = 0; k < kMergeAhead; ++k) {
-            if (c + k > c1) break;
-            const PartialAt x = part(c + k);
-            m[k] = x.m[r];
-            l[k] = x.l[r];
+                for (int u = 0; u < TURNS; ++u)
+                    o[k][u] = *reinterpret_cast<const float4*>(
+                        x.at(r, 4 * (j0 + u * (kMergeThreads / kMergeRows))));
+            }
 #pragma unroll
-            for (int j = 0; j < V; ++j) o[k][j] = x.o[static_cast<size_t>(r) * D + lane * V + j];
+            for (int k = 0; k < kMergeAhead; ++k) {
+                if (c + k > c1) break;
+                const float f = fast_exp2(m[k] - M);
+                den = fmaf(f, l[k], den);
+#pragma unroll
+                for (int u = 0; u < TURNS; ++u) {
+                    num[u].x = fmaf(f, o[k][u].x, num[u].x);
+                    num[u].y = fmaf(f, o[k][u].y, num[u].y);
+                    num[u].z = fmaf(f, o[k][u].z, num[u].z);
+                    num[u].w = fmaf(f, o[k][u].w, num[u].w);
+                }
+            }
         }
+        const float inv = den > 0.f ? p.vscale / den : (den == 0.f ? 0.f : den);
 #pragma unroll
-        for (int k = 0; k < kMergeAhead; ++k) {
-            if (c + k > c1) break;
-            const float f = fast_exp2(m[k] - M);
-            den = fmaf(f, l[k], den);
-#pragma unroll
-            for (int j = 0; j < V; ++j) num[j] = fmaf(f, o[k][j], num[j]);
-        }
+        for (int u = 0; u < TURNS; ++u)
+            stage[i][j0 + u * (kMergeThreads / kMergeRows)] =
+                make_uint2(pack_bf16x2(num[u].x * inv, num[u].y * inv),
+                           pack_bf16x2(num[u].z * inv, num[u].w * inv));
     }
-    const float inv = den > 0.f ? p.vscale / den : (den == 0.f ? 0.f : den);
-    const int rr = row0 + r;
-    __nv_bfloat16* out = p.O + (static_cast<int64_t>(s.first + rr / p.QG) * p.Hq + g * p.QG +
-                                rr % p.QG) * D + lane * V;
-#pragma unroll
-    for (int j = 0; j < V; j += 2)
-        *reinterpret_cast<uint32_t*>(out + j) = pack_bf16x2(num[j] * inv, num[j + 1] * inv);
+    __syncthreads();
+    constexpr int CH = D / 8;   // 16-byte chunks of a row
+    const int ri = threadIdx.x / CH, c = threadIdx.x % CH;
+    if (ri < kMergeRows && chunk * kMergeRows + ri < rows) {
+        const int rr = row0 + chunk * kMergeRows + ri;
+        const int64_t to = static_cast<int64_t>(s.first + rr / p.QG) * p.Hq + g * p.QG + rr % p.QG;
+        *reinterpret_cast<uint4*>(p.O + to * D + 8 * c) =
+            *reinterpret_cast<const uint4*>(&stage[ri][2 * c]);
+    }
 }
 
 template <int D, bool kFp8, bool kHalf>

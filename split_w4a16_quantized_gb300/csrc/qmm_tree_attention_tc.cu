@@ -108,13 +108,14 @@ struct TcSmem {
     float m[2][128], l[2][128];
     float qs[2][256];                   // E4M3: the rows' scales, by stretch parity
     int16_t par[kMaxTree];
-    union alignas(16) {
-        uint32_t anc[128][kWords + 1];  // a thread's own row: ancestors and itself
-        float x[96][16];                // columns of O from other copies of the rows
-    } u[2];                             // of each group
+    // by group: 16 columns of O from the other copies of the rows (96 or 64 rows
+    // of 64 bytes, or none), then 32 rows x 32 BF16 columns of O for each warp
+    // that writes (1, 2 or 4)
+    alignas(16) float4 x[2][512];
+    uint32_t anc[256][kWords + 1];      // a thread's own row: ancestors and itself
     RunShared run;
 };
-static_assert(offsetof(TcSmem, u) % 16 == 0 && sizeof(TcSmem::u) % 32 == 0, "16-byte accesses");
+static_assert(offsetof(TcSmem, x) % 16 == 0, "16-byte accesses");
 constexpr int kSmemHead = (sizeof(TcSmem) + 1023) / 1024 * 1024;
 
 // A ring position.
@@ -444,13 +445,10 @@ __global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
                 if (k > 0 && !waits(&sm.qfree, (k - 1) & 1)) break;
                 if (k > 0) fence_proxy_async_smem();
                 const __nv_bfloat16* q0 = p.q + x.s.first * p.q_stride + x.g * p.QG * D;
-                auto row_of = [&](int r) {
-                    const int rr = x.row0 + r;
-                    return q0 + (rr / p.QG) * p.q_stride + (rr % p.QG) * D;
-                };
                 if (kFp8) {
                     for (int r = t64; r < rows; r += 64) {
-                        const __nv_bfloat16* qv = row_of(r);
+                        const int node = (x.row0 + r) / p.QG, head = x.row0 + r - node * p.QG;
+                        const __nv_bfloat16* qv = q0 + node * p.q_stride + head * D;
                         uint32_t big = 0;   // largest magnitude, as bits: NaN above all
 #pragma unroll 8
                         for (int c = 0; c < D / 8; ++c) {
@@ -502,15 +500,20 @@ __global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
                         }
                     }
                 } else {
-                    constexpr int CH = D / 8;   // 16-byte chunks of a row
+                    constexpr int CH = D / 8;        // 16-byte chunks of a row
+                    constexpr int STEP = 64 / CH;    // rows a pass
+                    const int c = t64 % CH;
                     const uint32_t dst = smem_addr(q_s);
-                    for (int i = t64; i < rows * CH; i += 64) {
-                        const int r = i / CH, c = i % CH;
-                        const __nv_bfloat16* src = row_of(r) + 8 * c;
+                    int node = (x.row0 + t64 / CH) / p.QG;
+                    int head = x.row0 + t64 / CH - node * p.QG;
+                    for (int r = t64 / CH; r < rows; r += STEP) {
+                        const __nv_bfloat16* src = q0 + node * p.q_stride + head * D + 8 * c;
                         for (int y = 0; y < copies; ++y)
                             cp_async16(dst + (r >> 7) * C::Q +
                                            tile_off<128>((r & 127) + y * (128 / copies), c),
                                        src, true);
+                        head += STEP;
+                        while (head >= p.QG) head -= p.QG, ++node;
                     }
                     cp_async_commit();
                     cp_async_wait<0>();
@@ -577,6 +580,8 @@ __global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
         const uint32_t tO = tmem + quarter + kColO;       // stream 0's; stream 1's + 128
         int base = 0;             // tiles of the run before this stretch
         int ns = 0, no = 0;       // S's and O's taken
+        int anc_b = -1, anc_row = 0;   // whose rows' ancestors stand in sm.anc
+        uint32_t* const anc = sm.anc[tid - 32 * kSoftmaxWarp0];
         for (int k = 0; next_stretch(p, run, &x); ++k) {
             const int nt = x.t1 - x.t0;
             const int rows = min(1 << p.row_shift, x.s.n * p.QG - x.row0);
@@ -588,10 +593,13 @@ __global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
             const bool warp_on = __any_sync(0xffffffffu, on);
             const int node = (x.row0 + (on ? r : 0)) / p.QG;
             const int head = x.g * p.QG + (x.row0 + (on ? r : 0)) % p.QG;
-            // ---- ancestors, where the stretch reaches the drafted slots ----
-            if (x.t1 * kTile > x.s.len) {
+            // ---- ancestors, where the stretch reaches the drafted slots: the same
+            // for all heads of a sequence ----
+            if (x.t1 * kTile > x.s.len && (x.b != anc_b || x.row0 != anc_row)) {
+                anc_b = x.b;
+                anc_row = x.row0;
                 if (p.parents) {
-                    named_bar_sync(1, 256);   // the last stretch's walks are done
+                    named_bar_sync(1, 256);   // the last walks are done
                     for (int i = tid - 32 * kSoftmaxWarp0; i < x.s.n; i += 256) {
                         const int v = p.parents[x.s.first + i];
                         sm.par[i] = static_cast<int16_t>(v >= 0 && v < i ? v : -1);
@@ -609,7 +617,7 @@ __global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
                             if (j == i >> 5) w[j] |= 1u << (i & 31);
                     }
 #pragma unroll
-                for (int j = 0; j < kWords; ++j) sm.u[s].anc[gt][j] = w[j];
+                for (int j = 0; j < kWords; ++j) anc[j] = w[j];
             }
 
             float qs = p.qscale, ref = -INFINITY, sum = 0.f;
@@ -635,7 +643,7 @@ __global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
                         uint64_t see = ~0ull;
                         const int j = j0 + h;
                         if (j + 64 > 0)
-                            see = (low_bits(-j) | bits_from(sm.u[s].anc[gt], j)) & low_bits(valid - h);
+                            see = (low_bits(-j) | bits_from(anc, j)) & low_bits(valid - h);
                         for (int q = 0; q < pieces; ++q)
                             if (!((have >> q) & 1u)) {
                                 const int lo = (q << p.box_shift) - col0 - h;
@@ -778,9 +786,11 @@ __global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
                 part.m[r] = M;
                 part.l[r] = den;
             }
-            __nv_bfloat16* out = p.O + (static_cast<int64_t>(x.s.first + node) * p.Hq + head) * D;
-            float* po = part.o + static_cast<size_t>(r) * D;
+            const int64_t row_at = static_cast<int64_t>(x.s.first + node) * p.Hq + head;
             const uint32_t o0 = both ? tO + 128 * s : tO;
+            float4* const xg = sm.x[s];
+            float4* const stage = xg + (copies > 1 ? (copies - 1) * span * 4 : 0) + (warp & 3) * 128;
+            auto swz = [](int row, int j) { return row * 4 + ((j + (row >> 1)) & 3); };
 #pragma unroll 1
             for (int c = c_lo; c < c_hi; c += 16) {
                 float y[16];
@@ -796,42 +806,55 @@ __global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
                     }
                 }
                 if (copies > 1) {   // (uniform in the group; the other copies hand over)
-                    float4* mine_x = reinterpret_cast<float4*>(sm.u[s].x[copy > 0 ? gt - span : 0]);
                     if (on && copy > 0)
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
-                            mine_x[(q + gt) & 3] = make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2],
-                                                               y[4 * q + 3]);
+                            xg[swz(gt - span, q)] =
+                                make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
                     named_bar_sync(2 + s, 128);
                     if (on && copy == 0)
-                        for (int z = 1; z < copies; ++z) {
-                            const int l = gt + z * span;
-                            const float4* in = reinterpret_cast<const float4*>(sm.u[s].x[l - span]);
+                        for (int z = 0; z < copies - 1; ++z)
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {
-                                const float4 v = in[(q + l) & 3];
+                                const float4 v = xg[swz(gt + z * span, q)];
                                 y[4 * q] += v.x;
                                 y[4 * q + 1] += v.y;
                                 y[4 * q + 2] += v.z;
                                 y[4 * q + 3] += v.w;
                             }
-                        }
                     named_bar_sync(2 + s, 128);
                 }
-                if (writes) {
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) y[q] *= inv;
-                    if (whole) {
-#pragma unroll
-                        for (int q = 0; q < 16; q += 8)
-                            *reinterpret_cast<uint4*>(out + c + q) = make_uint4(
-                                pack_bf16x2(y[q], y[q + 1]), pack_bf16x2(y[q + 2], y[q + 3]),
-                                pack_bf16x2(y[q + 4], y[q + 5]), pack_bf16x2(y[q + 6], y[q + 7]));
-                    } else {
+                if (copy == 0 && warp_on && !whole) {
+                    if (writes)
 #pragma unroll
                         for (int q = 0; q < 16; q += 4)
-                            *reinterpret_cast<float4*>(po + c + q) =
+                            *reinterpret_cast<float4*>(part.at(r, c + q)) =
                                 make_float4(y[q], y[q + 1], y[q + 2], y[q + 3]);
+                } else if (copy == 0 && warp_on) {
+                    // a warp's 32 rows x 32 columns turn in shared memory: 8 rows of
+                    // 64 bytes a store instead of 32 of 16
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) y[q] *= inv;
+                    const int half = (c >> 3) & 2;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        uint4 w = make_uint4(
+                            pack_bf16x2(y[8 * q], y[8 * q + 1]), pack_bf16x2(y[8 * q + 2], y[8 * q + 3]),
+                            pack_bf16x2(y[8 * q + 4], y[8 * q + 5]), pack_bf16x2(y[8 * q + 6], y[8 * q + 7]));
+                        *reinterpret_cast<uint4*>(&stage[swz(lane, half + q)]) = w;
+                    }
+                    if (half) {
+                        __syncwarp();
+                        const uint32_t mask = __ballot_sync(0xffffffffu, writes);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int row = q * 8 + (lane >> 2);
+                            const int64_t to = __shfl_sync(0xffffffffu, row_at, row);
+                            if ((mask >> row) & 1u)
+                                *reinterpret_cast<uint4*>(p.O + to * D + (c - 16) + 8 * (lane & 3)) =
+                                    *reinterpret_cast<const uint4*>(&stage[swz(row, lane & 3)]);
+                        }
+                        __syncwarp();
                     }
                 }
             }
