@@ -217,16 +217,6 @@ __device__ __forceinline__ bool elect_one() {
     return one != 0;
 }
 
-// Page numbers of the copies of one tile, for the thread that issues them; a
-// missing page (or a piece past the last position) is num_pages: outside the
-// map, where a copy fills zeros.
-template <int kTile>
-struct TilePages {
-    static constexpr int kMax = kTile / 8;   // pieces of the smallest pages
-    int page[kMax];
-    int have;   // one bit per piece that exists
-};
-
 // The table entries of a stretch, looked up by a warp 32 pieces at a time and
 // one batch ahead.
 template <int kTile>
@@ -243,8 +233,11 @@ struct PageWalk {
         cur = entry(p, c0 + lane);
         nxt = entry(p, c0 + 32 + lane);
     }
-    // whole warp
-    __device__ __forceinline__ TilePages<kTile> tile(const TreeParams& p, int t, int lane) {
+    // Whole warp: the page numbers of a tile's pieces into `pages` (kTile / 8 of
+    // shared memory), for the thread that issues the copies; returns one bit per
+    // piece that exists.  A missing page (or a piece past the last position) is
+    // num_pages: outside the map, where a copy fills zeros.
+    __device__ __forceinline__ uint32_t tile(const TreeParams& p, int t, int lane, int* pages) {
         const int pieces = kTile >> p.box_shift;
         if (t * pieces >= c0 + 32) {
             c0 += 32;
@@ -254,13 +247,9 @@ struct PageWalk {
         const int at = t * pieces - c0;
         const bool real = cur >= 0 && cur < p.d.num_pages;
         const uint32_t ok = __ballot_sync(0xffffffffu, real);
-        const int pg = real ? cur : p.d.num_pages;
-        TilePages<kTile> r;
-        r.have = static_cast<int>((ok >> at) & ((1u << pieces) - 1u));
-#pragma unroll
-        for (int k = 0; k < TilePages<kTile>::kMax; ++k)
-            r.page[k] = __shfl_sync(0xffffffffu, pg, (at + k) & 31);
-        return r;
+        if (lane >= at && lane < at + pieces) pages[lane - at] = real ? cur : p.d.num_pages;
+        __syncwarp();
+        return (ok >> at) & ((1u << pieces) - 1u);
     }
 };
 
@@ -268,18 +257,16 @@ struct PageWalk {
 // column blocks of `kBox` bytes (kElems values), kTile rows of a block together.
 template <int kTile, int kBoxes, int kBox, int kElems>
 __device__ __forceinline__ void copy_tile(const TreeParams& p, const CUtensorMap* map, uint64_t* bar,
-                                          uint32_t dst, const TilePages<kTile>& pg, int t,
-                                          int g) {
+                                          uint32_t dst, const int* pages, int t, int g) {
     const int pieces = kTile >> p.box_shift;
     const int slot_mask = (1 << p.d.page_shift) - 1;
-#pragma unroll
-    for (int k = 0; k < TilePages<kTile>::kMax; ++k) {
-        if (k >= pieces) break;
+#pragma unroll 1
+    for (int k = 0; k < pieces; ++k) {
         const int row = k << p.box_shift;
 #pragma unroll
         for (int x = 0; x < kBoxes; ++x)
             tma_load_4d(dst + x * (kTile * kBox) + row * kBox, map, bar, x * kElems,
-                        (t * kTile + row) & slot_mask, g, pg.page[k]);
+                        (t * kTile + row) & slot_mask, g, pages[k]);
     }
 }
 
@@ -303,9 +290,10 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return y;
 }
 
-// One launch of the tcgen05 kernel (qmm_tree_attention_tc.cu: tiles of 128
-// positions); the merge kernel is the caller's.
-constexpr int kTcTileShift = 7;
+// One launch of the tcgen05 kernel (qmm_tree_attention_tc.cu); the merge
+// kernel is the caller's.  Tiles of 64 positions for items of up to 128 rows
+// (row_shift 7, two CTAs per SM), of 128 positions for 256 (8, one).
+constexpr int kTcTileShift1 = 6, kTcTileShift2 = 7;
 int launch_tree_tc(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int D,
                    bool fp8, cudaStream_t st);
 

@@ -71,6 +71,7 @@ struct Smem {
     uint64_t full[kStages];
     uint64_t empty[kStages];
     int have[kStages];                 // pages of the stage's tile that exist, one bit a copy
+    int pages[kTile / 8];              // of the tile being copied
     float wm[kWarps][kRows];
     float wl[kWarps][kRows];
     uint32_t anc[kRows][kWords];       // ancestors (and self) of each row's token
@@ -160,22 +161,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             PageWalk<kTile> walk;
             walk.start(p, x, lane);
             for (int t = x.t0; t < x.t1; ++t, ++it) {
-                const TilePages<kTile> pg = walk.tile(p, t, lane);
+                const uint32_t have = walk.tile(p, t, lane, sm.pages);
                 const int st = it % kStages;
                 ok = it < kStages ||
                      mbar_wait_warp(&sm.empty[st], ((it / kStages) & 1) ^ 1, abort, p.status);
                 if (!ok) break;
                 if (elect_one()) {
-                    sm.have[st] = pg.have;
+                    sm.have[st] = static_cast<int>(have);
                     // the compute warps read (and may have zeroed) the stage with
                     // ordinary accesses
                     fence_proxy_async_smem();
                     mbar_arrive_expect_tx(&sm.full[st], C::STAGE);
                     constexpr int E = C::BOX / (kFp8 ? 1 : 2);
                     copy_tile<kTile, C::BOXES, C::BOX, E>(p, &kmap, &sm.full[st], ring_a + st * C::STAGE,
-                                                   pg, t, x.g);
+                                                   sm.pages, t, x.g);
                     copy_tile<kTile, C::BOXES, C::BOX, E>(p, &vmap, &sm.full[st],
-                                                   ring_a + st * C::STAGE + C::TILE, pg, t, x.g);
+                                                   ring_a + st * C::STAGE + C::TILE, sm.pages, t,
+                                                   x.g);
                 }
                 __syncwarp();
             }
@@ -693,7 +695,8 @@ struct Variant {
 };
 Variant variant(int rows) {
     if (rows <= kRows) return {false, 4, 6, kCtasPerSm, 2, 1};
-    return {true, rows <= 128 ? 7 : 8, kTcTileShift, 1, 4, 2};
+    if (rows <= 128) return {true, 7, kTcTileShift1, 2, 4, 2};
+    return {true, 8, kTcTileShift2, 1, 4, 2};
 }
 
 }  // namespace

@@ -2,43 +2,43 @@
 // the products on the 5th-generation tensor cores.
 //
 // The formulas and the work split are those of qmm_tree_attention.cu.  Here a
-// work item is up to 128 or 256 rows, the MMA's M, and a tile is 128 positions:
-//   S [128 x 128] = Q [128 x D] K^T    Q and the K tile in shared memory
-//   O [128 x D]  += P [128 x 128] V    P in tensor memory, V in shared memory
+// work item is up to 128 or 256 rows, the MMA's M once or twice, and a tile is
+// 64 or 128 positions:
+//   S [128 x tile] = Q [128 x D] K^T    Q and the K tile in shared memory
+//   O [128 x D]   += P [128 x tile] V   P in tensor memory, V in shared memory
 // with S and O accumulated in tensor memory.  Rows past the item's are computed
-// and dropped: at 128 rows a tile's products take less than half the time its
-// K and V take from HBM, so padding costs nothing where there are few rows, and
-// full tiles are what the layout is for.
+// and dropped: at 128 rows a tile's products take about half the time its K and
+// V take from HBM, so padding costs little where there are few rows.
 //
-// One CTA per SM:
-//   warp 0     copies: K and V tiles into a ring each
-//   warp 1     issues the MMAs and owns the tensor memory
-//   warps 2-3  bring the next item's q
-//   warps 4-7, 8-11  two softmax groups of 128 threads, one thread a row
-//   warps 12-15  E4M3 cache: V tiles to F16
-// Two streams of (S/P, O) keep the tensor cores and the exponentials busy at
-// the same time: while a group turns its S into P, the other stream's products
-// run.  An item of more than 128 rows gives each stream half of the rows and
-// the same tiles; an item of at most 128 gives both streams all rows and every
-// other tile, and the groups add their two states at the end.
-//   MMA order:  ... P0 V(i), Q0 K(i+1) | P1 V(i), Q1 K(i+1) ...
-// P overwrites S in place (BF16 or F16 in half the columns); the MMAs run in
-// issue order, so a group that sees S of its next tile also knows that its last
-// P V is done, and may rescale O.
+// Roles of a CTA:
+//   warp 0      copies: K and V tiles into a ring each
+//   warp 1      issues the MMAs and owns the tensor memory
+//   warps 2-3   bring the next item's q
+//   softmax groups of 128 threads, a thread a row
+//   E4M3 cache: four warps that turn V tiles into F16
+// Two buffers of S keep the tensor cores and the exponentials busy at the same
+// time: while a group turns one S into P, the products of the other run.  P
+// overwrites S in place (BF16 or F16 in half the columns).
+//   up to 128 rows: one group; two CTAs per SM, tiles of 64 positions, the
+//     buffers take the tiles in turn.   ... P0 V(i), Q K(i+2) | P1 V(i+1), ...
+//     Two CTAs, because each item ends with a few thousand clocks in which its
+//     last products drain and its output is written; the other CTA's products
+//     and copies run on meanwhile.
+//   up to 256 rows: two groups with half of the rows and an O each; one CTA per
+//     SM, tiles of 128 positions that both groups use.
+//                                       ... P0 V(i), Q0 K(i+1) | P1 V(i), ...
+//     (An MMA takes the same time for N = 64 as for 128, so that tile has half
+//     of the score MMAs; two such CTAs do not fit an SM.)
 //
 // Few rows.  An item of at most 64 (32) rows is put into the 128 twice (four
 // times).  The MMA computes all copies' scores anyway; copy c of a row takes
-// columns [c w, (c + 1) w) of the tile, w = 128 / copies, and zeros elsewhere
+// columns [c w, (c + 1) w) of the tile, w = tile / copies, and zeros elsewhere
 // in P, so a row's exponentials are spread over that many warps, which would
 // idle otherwise.  The copies' states are added at the end.
 //
 // An item's first scores need only its q and K: they are issued right behind
-// the last products of the item before, while the groups still write that
+// the last products of the item before, while the group still writes that
 // item's output.
-//
-// Why 128 positions: an MMA takes about 68 clocks for any N up to 128 (measured:
-// with 64 positions a tile the same products took 1.5 times as long), and the
-// hand-overs between the roles cost the same per tile whatever its size.
 //
 // A row's maximum is followed lazily: P = 2^(s - ref) with a reference that is
 // raised only when a score passes it by more than 8, so P stays below 2^8 and O
@@ -55,9 +55,7 @@
 // of P than two E4M3 terms give far below the maximum (a long flat tail under
 // one large weight would vanish), so V is converted to F16, exactly, and P is
 // F16.
-//
-// Tensor memory (512 columns): S/P 2 x 128, O 2 x 128.
-#include <cstddef>
+#include <algorithm>
 #include <mutex>
 #include <type_traits>
 
@@ -67,56 +65,67 @@
 namespace qmm {
 namespace {
 
-constexpr int kTile = 1 << kTcTileShift;
-constexpr int kSoftmaxWarp0 = 4, kConvWarp0 = 12;
 constexpr int kConvWarps = 4;
 constexpr int kMaxSlots = 8;        // of one ring
 constexpr int kConvSlots = 2;
-constexpr int kHave = 16;           // tiles whose page bits are kept
+constexpr int kHave = 32;           // tiles whose page bits are kept
 constexpr float kLazy = 8.f;        // log2 units a score may pass the reference by
-constexpr uint32_t kColS = 0, kColO = 256;   // stream s: + 128 s
 
-template <int D, bool kFp8>
+// kGroups: softmax groups (1: two CTAs per SM, up to 128 rows; 2: one CTA, 256).
+template <int D, bool kFp8, int kGroups>
 struct Tc {
+    static constexpr int TILE_SHIFT = kGroups == 1 ? kTcTileShift1 : kTcTileShift2;
+    static constexpr int TILE = 1 << TILE_SHIFT;             // positions
+    static constexpr int CTAS_PER_SM = kGroups == 1 ? 2 : 1;
+    static constexpr int SOFTMAX0 = 4, CONV0 = 4 + 4 * kGroups;   // first warps
+    static constexpr int WARPS = CONV0 + (kFp8 ? kConvWarps : 0);
+    static constexpr int THREADS = 32 * WARPS;
     // registers: the launch gives every thread the same share; the softmax groups
-    // hold a row of S (128 values) and take over what the others do not need
-    static constexpr int THREADS = kFp8 ? 512 : 384;
-    static constexpr int REGS_CTL = kFp8 ? 56 : 88;
-    static constexpr int REGS_SOFTMAX = kFp8 ? 200 : 208;
-    static constexpr int REGS_CONV = 56;
-    static_assert(kFp8 ? 128 * (REGS_CTL + 2 * REGS_SOFTMAX + REGS_CONV) <= THREADS * 128
-                       : 128 * (REGS_CTL + 2 * REGS_SOFTMAX) <= THREADS * 168, "registers");
+    // hold a row of S and take over what the others do not need
+    static constexpr int SHARE = 65536 / (CTAS_PER_SM * THREADS) / 8 * 8;
+    static constexpr int REGS_CTL = kFp8 ? (kGroups == 1 ? 48 : 56) : (kGroups == 1 ? 72 : 88);
+    static constexpr int REGS_CONV = kGroups == 1 ? 48 : 56;
+    static constexpr int REGS_SOFTMAX = kFp8 ? (kGroups == 1 ? 144 : 200) : (kGroups == 1 ? 184 : 208);
+    static_assert(REGS_CTL + kGroups * REGS_SOFTMAX + (kFp8 ? REGS_CONV : 0) <= SHARE * WARPS / 4,
+                  "registers");
     static constexpr int ROW = D * (kFp8 ? 1 : 2);           // bytes of a cache row
     static constexpr int BOX = ROW < 128 ? ROW : 128;        // row bytes of one copy
     static constexpr int BOXES = ROW / BOX;
-    static constexpr int SLOT = kTile * ROW;                 // a copied tile
-    static constexpr int Q = 128 * D * 2;                    // a stream's Q: BF16, or two E4M3 terms
-    static constexpr int CONV = kTile * D * 2;               // a converted V tile
+    static constexpr int SLOT = TILE * ROW;                  // a copied tile
+    static constexpr int Q = 128 * D * 2;                    // a group's Q: BF16, or two E4M3 terms
+    static constexpr int CONV = TILE * D * 2;                // a converted V tile
+    // tensor memory: S/P buffers, then an O of each group
+    static constexpr uint32_t COLS = 256 * kGroups, COL_O = 2 * TILE;
+    static_assert(2 * TILE + kGroups * D <= static_cast<int>(COLS), "tensor memory");
 };
 
+template <int kGroups>
 struct TcSmem {
     uint64_t kfull[kMaxSlots], kempty[kMaxSlots], vfull[kMaxSlots], vempty[kMaxSlots];
     uint64_t cfull[kConvSlots], cempty[kConvSlots];
-    uint64_t sfull[2];                  // S of a stream's next tile is there
-    uint64_t pready[2];                 // P is, and O may take its product
-    uint64_t ofull[2];                  // O is complete
+    uint64_t sfull[2];                  // a buffer's next S is there
+    uint64_t pready[2];                 // its P is, and O may take the product
+    uint64_t pvdone;                    // (one group) a product with V has ended
+    uint64_t ofull[2];                  // a group's O is complete
     uint64_t qready, qfree;             // an item's q is there; its products have read it
-    uint64_t odone;                     // O, m and l of an item are read by all
+    uint64_t odone;                     // an item's O has been read by all
     uint64_t drained;                   // abort: every MMA issued has ended
     uint32_t tmem;
+    int abort;
     int have[kHave];                    // pages of a tile that exist, one bit a copy
-    float m[2][128], l[2][128];
-    float qs[2][256];                   // E4M3: the rows' scales, by stretch parity
+    int pages[16];                      // of the tile being copied
+    float m[128], l[128];               // (one group) the copies' statistics
+    float qs[2][128 * kGroups];         // E4M3: the rows' scales, by stretch parity
     int16_t par[kMaxTree];
     // by group: 16 columns of O from the other copies of the rows (96 or 64 rows
     // of 64 bytes, or none), then 32 rows x 32 BF16 columns of O for each warp
     // that writes (1, 2 or 4)
-    alignas(16) float4 x[2][512];
-    uint32_t anc[256][kWords + 1];      // a thread's own row: ancestors and itself
+    alignas(16) float4 x[kGroups][512];
+    uint32_t anc[128 * kGroups][kWords];   // a thread's own row: ancestors and itself
     RunShared run;
 };
-static_assert(offsetof(TcSmem, x) % 16 == 0, "16-byte accesses");
-constexpr int kSmemHead = (sizeof(TcSmem) + 1023) / 1024 * 1024;
+template <int kGroups>
+constexpr int kSmemHead = (sizeof(TcSmem<kGroups>) + 1023) / 1024 * 1024;
 
 // A ring position.
 struct Cursor {
@@ -141,12 +150,14 @@ __device__ __forceinline__ uint64_t sdesc_k_major(uint32_t saddr) {
            (static_cast<uint64_t>((8 * kRow) >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
            (static_cast<uint64_t>(kRow == 128 ? 2 : 4) << 61);
 }
-// A V tile as B, N-major with the 128-byte swizzle: rows are positions (the
-// MMA's K), 64 values of the head wide; the next 64 values are kTile rows on
-// (leading offset), the next 8 positions 1024 bytes (stride offset).
+// A V tile of kRows positions as B, N-major with the 128-byte swizzle: rows are
+// positions (the MMA's K), 64 values of the head wide; the next 64 values are
+// kRows rows on (leading offset), the next 8 positions 1024 bytes (stride
+// offset).
+template <int kRows>
 __device__ __forceinline__ uint64_t sdesc_n_major(uint32_t saddr) {
     return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) |
-           (static_cast<uint64_t>((kTile * 128) >> 4) << 16) |
+           (static_cast<uint64_t>((kRows * 128) >> 4) << 16) |
            (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
            (static_cast<uint64_t>(2) << 61);
 }
@@ -182,6 +193,14 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
         : "r"(taddr)
         : "memory");
 }
+// 32 lanes x 8 columns.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+        : "memory");
+}
+
 template <int kRegs>
 __device__ __forceinline__ void regs_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegs));
@@ -191,12 +210,12 @@ __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegs));
 }
 
-// Offset of 16-byte chunk c of row r in a tile of 128 rows: boxes of kBox bytes
-// a row, the chunk permuted by the swizzle of that width.
-template <int kBox>
+// Offset of 16-byte chunk c of row r in a tile of kRows rows: boxes of kBox
+// bytes a row, the chunk permuted by the swizzle of that width.
+template <int kBox, int kRows>
 __device__ __forceinline__ uint32_t tile_off(int r, int c) {
     if (kBox == 128)
-        return static_cast<uint32_t>((c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+        return static_cast<uint32_t>((c >> 3) * (kRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
     return static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
@@ -227,26 +246,27 @@ struct Layout {
 // How often an item's rows stand in the 128 of a product.
 __device__ __forceinline__ int copies_of(int rows) { return rows <= 32 ? 4 : (rows <= 64 ? 2 : 1); }
 
-template <int D, bool kFp8>
-__global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
+template <int D, bool kFp8, int kGroups>
+__global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGroups>::CTAS_PER_SM)
     tree_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap, const __grid_constant__ TreeParams p,
                    const Layout lay) {
-    using C = Tc<D, kFp8>;
+    using C = Tc<D, kFp8, kGroups>;
+    constexpr int kTile = C::TILE;
+    constexpr bool kOne = kGroups == 1;
     extern __shared__ uint8_t tree_tc_smem_raw[];
     uint8_t* base_s = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(tree_tc_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    TcSmem& sm = *reinterpret_cast<TcSmem*>(base_s);
-    uint8_t* q_s = base_s + kSmemHead;
-    uint8_t* conv_s = q_s + (C::Q << (p.row_shift - 7));
+    TcSmem<kGroups>& sm = *reinterpret_cast<TcSmem<kGroups>*>(base_s);
+    uint8_t* q_s = base_s + kSmemHead<kGroups>;
+    uint8_t* conv_s = q_s + kGroups * C::Q;
     uint8_t* k_s = conv_s + (kFp8 ? kConvSlots * C::CONV : 0);
     uint8_t* v_s = k_s + lay.k_slots * C::SLOT;
-    __shared__ int abort_flag;
-    volatile int* abort = &abort_flag;
+    volatile int* abort = &sm.abort;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
-        abort_flag = 0;
+        sm.abort = 0;
         for (int i = 0; i < kMaxSlots; ++i) {
             mbar_init(&sm.kfull[i], 1);
             mbar_init(&sm.kempty[i], 1);
@@ -262,9 +282,10 @@ __global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
             mbar_init(&sm.pready[s], 4);
             mbar_init(&sm.ofull[s], 1);
         }
+        mbar_init(&sm.pvdone, 1);
         mbar_init(&sm.qready, 2);
         mbar_init(&sm.qfree, 1);
-        mbar_init(&sm.odone, 8);
+        mbar_init(&sm.odone, 4 * kGroups);
         mbar_init(&sm.drained, 1);
         mbar_fence_init();
         tma_prefetch_map(&kmap);
@@ -275,7 +296,7 @@ __global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
     // never waits for one that still needs it.
     pdl_wait();
     if (warp == 1) {
-        tmem_alloc(&sm.tmem, 512);
+        tmem_alloc(&sm.tmem, C::COLS);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -290,7 +311,7 @@ __global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
         return mbar_wait_warp(bar, phase, abort, p.status);
     };
 
-    if (warp < kSoftmaxWarp0) {
+    if (warp < C::SOFTMAX0) {
         regs_dec<C::REGS_CTL>();
         if (warp == 0) {
             // ---- copies ----
@@ -302,14 +323,14 @@ __global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
                 PageWalk<kTile> walk;
                 walk.start(p, x, lane);
                 for (int t = x.t0; t < x.t1; ++t) {
-                    const TilePages<kTile> pg = walk.tile(p, t, lane);
+                    const uint32_t have = walk.tile(p, t, lane, sm.pages);
                     if (!(ok = waits(&sm.kempty[kc.slot], kc.phase ^ 1))) break;
                     if (elect_one()) {
-                        sm.have[it % kHave] = pg.have;
+                        sm.have[it % kHave] = static_cast<int>(have);
                         mbar_arrive_expect_tx(&sm.kfull[kc.slot], C::SLOT);
                         copy_tile<kTile, C::BOXES, C::BOX, E>(p, &kmap, &sm.kfull[kc.slot],
                                                               smem_addr(k_s) + kc.slot * C::SLOT,
-                                                              pg, t, x.g);
+                                                              sm.pages, t, x.g);
                     }
                     __syncwarp();
                     ++it;
@@ -322,7 +343,7 @@ __global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
                         mbar_arrive_expect_tx(&sm.vfull[vc.slot], C::SLOT);
                         copy_tile<kTile, C::BOXES, C::BOX, E>(p, &vmap, &sm.vfull[vc.slot],
                                                               smem_addr(v_s) + vc.slot * C::SLOT,
-                                                              pg, t, x.g);
+                                                              sm.pages, t, x.g);
                     }
                     __syncwarp();
                     ++nv;
@@ -341,17 +362,18 @@ __global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
             constexpr uint32_t ipv = idesc(D, kFp8 ? 0u : 1u, true);
             const uint64_t q_desc = sdesc_k_major<C::BOX>(smem_addr(q_s));
             const uint64_t k_desc = sdesc_k_major<C::BOX>(smem_addr(k_s));
-            const uint64_t v_desc = sdesc_n_major(smem_addr(kFp8 ? conv_s : v_s));
+            const uint64_t v_desc = sdesc_n_major<kTile>(smem_addr(kFp8 ? conv_s : v_s));
             uint64_t* vfull = kFp8 ? sm.cfull : sm.vfull;
             uint64_t* vempty = kFp8 ? sm.cempty : sm.vempty;
             constexpr int VSLOT = kFp8 ? C::CONV : C::SLOT;
             const int v_slots = kFp8 ? kConvSlots : lay.v_slots;
             Cursor kc, vc;
-            int np[2] = {0, 0}, nq = 0;     // P's and Q's taken
-            int todo = 0;                   // products with this stretch's Q to come
+            int nq = 0;                     // Q's taken
+            uint32_t pphase = 0;            // phase of each buffer's P, a bit each
             bool go = true;
-            auto qk = [&](int s, bool own_q) {   // S of stream s from the K tile at kc
-                const uint64_t a = q_desc + (own_q ? (C::Q >> 4) * s : 0);
+            // S of buffer s from group g's rows and the K tile at kc
+            auto qk = [&](int s, int g) {
+                const uint64_t a = q_desc + (C::Q >> 4) * g;
                 const uint64_t b = k_desc + static_cast<uint32_t>(kc.slot * C::SLOT >> 4);
                 if (kFp8) {
                     // 32 values a step; q's two terms
@@ -359,74 +381,73 @@ __global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int k = 0; k < D / 32; ++k)
-                            umma_ss<true>(tmem + kColS + 128 * s, a + ((h * 128 * D + k * 32) >> 4),
+                            umma_ss<true>(tmem + kTile * s, a + ((h * 128 * D + k * 32) >> 4),
                                           b + ((k * 32) >> 4), iqk, h > 0 || k > 0);
                 } else {
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
-                        umma_ss<false>(tmem + kColS + 128 * s, a + off, b + off, iqk, k > 0);
-                    }
+                    for (int k = 0; k < D / 16; ++k)
+                        umma_ss<false>(tmem + kTile * s,
+                                       a + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
+                                       b + (((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4), iqk, k > 0);
                 }
                 umma_commit(&sm.sfull[s]);
                 // this thread has seen the tile's copy complete, and with it the
                 // copy warp's page bits: hand that on
                 mbar_arrive(&sm.sfull[s]);
-                if (todo == 1) umma_commit(&sm.qfree);
             };
-            auto pv = [&](int s, bool first) {
+            // O of group g (+)= P of buffer s times the V tile at vc
+            auto pv = [&](int s, int g, bool first) {
                 const uint64_t b = v_desc + static_cast<uint32_t>(vc.slot * VSLOT >> 4);
 #pragma unroll
                 for (int k = 0; k < kTile / 16; ++k)
-                    umma_bf16_tmem_a(tmem + kColO + 128 * s, tmem + kColS + 128 * s + 8 * k,
+                    umma_bf16_tmem_a(tmem + C::COL_O + D * g, tmem + kTile * s + 8 * k,
                                      b + ((k * 2048) >> 4), ipv, !first || k > 0);
             };
             while (go && next_stretch(p, run, &x)) {
                 const int nt = x.t1 - x.t0;
-                const bool both = x.s.n * p.QG - x.row0 > 128;   // two halves of the rows
-                const int step = both ? 1 : 2;
                 if (!(go = waits(&sm.qready, nq & 1))) break;
-                todo = both ? 2 * nt : nt;
-                // first S of each stream
-                for (int i = 0; i < (both ? 1 : min(nt, 2)); ++i) {
+                // the first S of each buffer
+                for (int i = 0; i < (kOne ? min(nt, 2) : 1); ++i) {
                     if (!(go = waits(&sm.kfull[kc.slot], kc.phase))) break;
                     tc_fence_after();
-                    for (int u = 0; u < (both ? 2 : 1); ++u, --todo) {
-                        if (elect_one()) {
-                            qk(both ? u : i, both);
-                            if (!both || u == 1) umma_commit(&sm.kempty[kc.slot]);
-                        }
-                        __syncwarp();
+                    if (elect_one()) {
+                        qk(i, 0);
+                        if (!kOne) qk(1, 1);
+                        umma_commit(&sm.kempty[kc.slot]);
+                        if (i + 1 == (kOne ? nt : 1) && (kOne || nt == 1)) umma_commit(&sm.qfree);
                     }
+                    __syncwarp();
                     kc.next(lay.k_slots);
                 }
                 // O is free once the last stretch's has been read
                 if (go && nq > 0) go = waits(&sm.odone, (nq - 1) & 1);
                 ++nq;
                 for (int i = 0; go && i < nt; ++i) {
-                    const bool more = i + step < nt;
-                    for (int u = 0; u < (both ? 2 : 1); ++u) {
-                        const int s = both ? u : i & 1;
-                        const bool last = !both || u == 1;   // last reader of the tiles
-                        if (!(go = waits(&sm.pready[s], np[s] & 1))) break;
-                        ++np[s];
+                    const int next = i + (kOne ? 2 : 1);   // tile of the buffer's next S
+#pragma unroll
+                    for (int u = 0; u < kGroups; ++u) {
+                        const int s = kOne ? i & 1 : u;
+                        const bool last = u == kGroups - 1;   // last reader of the tiles
+                        if (!(go = waits(&sm.pready[s], (pphase >> s) & 1))) break;
+                        pphase ^= 1u << s;
                         if (u == 0 && !(go = waits(&vfull[vc.slot], vc.phase))) break;
                         tc_fence_after();
                         if (elect_one()) {
-                            pv(s, i < step);
+                            pv(s, u, i == 0);
                             if (last) umma_commit(&vempty[vc.slot]);
-                            if (!more) umma_commit(&sm.ofull[s]);
+                            if (kOne) umma_commit(&sm.pvdone);
+                            if (i + 1 == nt) umma_commit(&sm.ofull[u]);
                         }
                         __syncwarp();
                         if (last) vc.next(v_slots);
-                        if (!more) continue;
+                        if (next >= nt) continue;
                         if (u == 0 && !(go = waits(&sm.kfull[kc.slot], kc.phase))) break;
                         if (elect_one()) {
-                            qk(s, both);
+                            qk(s, u);
                             if (last) umma_commit(&sm.kempty[kc.slot]);
+                            if (last && next + 1 == nt) umma_commit(&sm.qfree);
                         }
                         __syncwarp();
-                        --todo;
                         if (last) kc.next(lay.k_slots);
                     }
                 }
@@ -441,7 +462,7 @@ __global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
             const int t64 = tid - 64;
             for (int k = 0; next_stretch(p, run, &x); ++k) {
                 const int rows = min(1 << p.row_shift, x.s.n * p.QG - x.row0);
-                const int copies = copies_of(rows);
+                const int copies = kOne ? copies_of(rows) : 1;
                 if (k > 0 && !waits(&sm.qfree, (k - 1) & 1)) break;
                 if (k > 0) fence_proxy_async_smem();
                 const __nv_bfloat16* q0 = p.q + x.s.first * p.q_stride + x.g * p.QG * D;
@@ -491,8 +512,9 @@ __global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
                                 lo[i] = l2[0] | (l2[1] << 16);
                             }
                             uint8_t* dst = q_s + (r >> 7) * C::Q;
+#pragma unroll 1
                             for (int y = 0; y < copies; ++y) {
-                                const uint32_t o = tile_off<C::BOX>((r & 127) + y * (128 / copies), c);
+                                const uint32_t o = tile_off<C::BOX, 128>((r & 127) + y * (128 / copies), c);
                                 *reinterpret_cast<uint4*>(dst + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                                 *reinterpret_cast<uint4*>(dst + 128 * D + o) =
                                     make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -506,11 +528,13 @@ __global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
                     const uint32_t dst = smem_addr(q_s);
                     int node = (x.row0 + t64 / CH) / p.QG;
                     int head = x.row0 + t64 / CH - node * p.QG;
+#pragma unroll 2
                     for (int r = t64 / CH; r < rows; r += STEP) {
                         const __nv_bfloat16* src = q0 + node * p.q_stride + head * D + 8 * c;
+#pragma unroll 1
                         for (int y = 0; y < copies; ++y)
                             cp_async16(dst + (r >> 7) * C::Q +
-                                           tile_off<128>((r & 127) + y * (128 / copies), c),
+                                           tile_off<128, 128>((r & 127) + y * (128 / copies), c),
                                        src, true);
                         head += STEP;
                         while (head >= p.QG) head -= p.QG, ++node;
@@ -523,10 +547,13 @@ __global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
                 if (lane == 0) mbar_arrive(&sm.qready);
             }
         }
-    } else if (kFp8 && warp >= kConvWarp0) {
-        // ---- V to F16: thread = position ----
+    } else if (kFp8 && warp >= C::CONV0) {
+        // ---- V to F16: a thread takes a position, or half of one ----
         regs_dec<C::REGS_CONV>();
-        const int r = tid - 32 * kConvWarp0;
+        constexpr int SHARES = 128 / kTile;               // threads of a position
+        constexpr int CH = D / 16 / SHARES;               // 16-byte chunks of a thread
+        const int t128 = tid - 32 * C::CONV0;
+        const int r = t128 % kTile, ch0 = t128 / kTile * CH;
         Cursor vc, cc;
         bool go = true;
         while (go && next_stretch(p, run, &x)) {
@@ -536,29 +563,33 @@ __global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
                 if (!(go = waits(&sm.cempty[cc.slot], cc.phase ^ 1))) break;
                 const uint8_t* src = v_s + vc.slot * C::SLOT;
                 uint8_t* dst = conv_s + cc.slot * C::CONV;
-                uint4 in[D / 16];
 #pragma unroll
-                for (int c = 0; c < D / 16; ++c)
-                    in[c] = *reinterpret_cast<const uint4*>(src + tile_off<C::BOX>(r, c));
-                if (r >= valid) {
-                    // slots past the last position may hold anything, and 0 * NaN
-                    // is not 0
+                for (int c0 = 0; c0 < CH; c0 += 4) {
+                    constexpr int N4 = CH < 4 ? CH : 4;
+                    uint4 in[N4];
 #pragma unroll
-                    for (int c = 0; c < D / 16; ++c) in[c] = make_uint4(0, 0, 0, 0);
-                }
-#pragma unroll
-                for (int c = 0; c < D / 16; ++c) {
-                    const uint32_t w[4] = {in[c].x, in[c].y, in[c].z, in[c].w};
-                    uint32_t f[8];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        f[2 * i] = e4m3x2_to_f16x2(w[i] & 0xffffu);
-                        f[2 * i + 1] = e4m3x2_to_f16x2(w[i] >> 16);
+                    for (int c = 0; c < N4; ++c) {
+                        in[c] = *reinterpret_cast<const uint4*>(
+                            src + tile_off<C::BOX, kTile>(r, ch0 + c0 + c));
+                        // slots past the last position may hold anything, and
+                        // 0 * NaN is not 0
+                        if (r >= valid) in[c] = make_uint4(0, 0, 0, 0);
                     }
-                    *reinterpret_cast<uint4*>(dst + tile_off<128>(r, 2 * c)) =
-                        make_uint4(f[0], f[1], f[2], f[3]);
-                    *reinterpret_cast<uint4*>(dst + tile_off<128>(r, 2 * c + 1)) =
-                        make_uint4(f[4], f[5], f[6], f[7]);
+#pragma unroll
+                    for (int c = 0; c < N4; ++c) {
+                        const uint32_t w[4] = {in[c].x, in[c].y, in[c].z, in[c].w};
+                        uint32_t f[8];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            f[2 * i] = e4m3x2_to_f16x2(w[i] & 0xffffu);
+                            f[2 * i + 1] = e4m3x2_to_f16x2(w[i] >> 16);
+                        }
+                        const int o = 2 * (ch0 + c0 + c);
+                        *reinterpret_cast<uint4*>(dst + tile_off<128, kTile>(r, o)) =
+                            make_uint4(f[0], f[1], f[2], f[3]);
+                        *reinterpret_cast<uint4*>(dst + tile_off<128, kTile>(r, o + 1)) =
+                            make_uint4(f[4], f[5], f[6], f[7]);
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -573,22 +604,22 @@ __global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
     } else {
         // ---- softmax groups ----
         regs_inc<C::REGS_SOFTMAX>();
-        const int s = (warp - kSoftmaxWarp0) >> 2;
+        const int g = (warp - C::SOFTMAX0) >> 2;          // group
         const int gt = (warp & 3) * 32 + lane;            // thread of the group = tensor memory lane
-        const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t tS = tmem + quarter + kColS + 128 * s;
-        const uint32_t tO = tmem + quarter + kColO;       // stream 0's; stream 1's + 128
+        const uint32_t quarter = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t tO = quarter + C::COL_O + D * g;
         int base = 0;             // tiles of the run before this stretch
-        int ns = 0, no = 0;       // S's and O's taken
+        int no = 0;               // O's taken
+        uint32_t sphase = 0;      // phase of each buffer's S, a bit each
         int anc_b = -1, anc_row = 0;   // whose rows' ancestors stand in sm.anc
-        uint32_t* const anc = sm.anc[tid - 32 * kSoftmaxWarp0];
+        uint32_t* const anc = sm.anc[tid - 32 * C::SOFTMAX0];
         for (int k = 0; next_stretch(p, run, &x); ++k) {
             const int nt = x.t1 - x.t0;
             const int rows = min(1 << p.row_shift, x.s.n * p.QG - x.row0);
-            const bool both = rows > 128;
-            const int copies = copies_of(rows), span = 128 / copies;   // lanes, and columns, of a copy
+            const int copies = kOne ? copies_of(rows) : 1;
+            const int span = 128 / copies;                           // lanes of a copy
             const int copy = gt / span;
-            const int r = both ? gt + 128 * s : gt - copy * span;    // row of the item
+            const int r = kOne ? gt - copy * span : gt + 128 * g;    // row of the item
             const bool on = r < rows;
             const bool warp_on = __any_sync(0xffffffffu, on);
             const int node = (x.row0 + (on ? r : 0)) / p.QG;
@@ -599,12 +630,12 @@ __global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
                 anc_b = x.b;
                 anc_row = x.row0;
                 if (p.parents) {
-                    named_bar_sync(1, 256);   // the last walks are done
-                    for (int i = tid - 32 * kSoftmaxWarp0; i < x.s.n; i += 256) {
+                    named_bar_sync(1, 128 * kGroups);   // the last walks are done
+                    for (int i = tid - 32 * C::SOFTMAX0; i < x.s.n; i += 128 * kGroups) {
                         const int v = p.parents[x.s.first + i];
                         sm.par[i] = static_cast<int16_t>(v >= 0 && v < i ? v : -1);
                     }
-                    named_bar_sync(1, 256);
+                    named_bar_sync(1, 128 * kGroups);
                 }
                 uint32_t w[kWords];
 #pragma unroll
@@ -621,15 +652,16 @@ __global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
             }
 
             float qs = p.qscale, ref = -INFINITY, sum = 0.f;
-            int mine = 0;   // tiles of this stream
 
-            // One tile: NC columns from the copy's first on.
-            auto tile = [&](auto nc, int t, int at) {
+            // One tile in buffer s: NC columns from the copy's first on.
+            auto tile = [&](auto nc, int s, int t, int at) {
                 constexpr int NC = decltype(nc)::value;
                 const int col0 = copy * NC;
+                const uint32_t tS = quarter + kTile * s;
                 uint32_t v[NC];
+                if (NC < 32) tmem_ld16(tS + col0, v);
 #pragma unroll
-                for (int c = 0; c < NC; c += 32) tmem_ld32(tS + col0 + c, v + c);
+                for (int c = 0; c + 32 <= NC; c += 32) tmem_ld32(tS + col0 + c, v + c);
                 // what the row sees of the tile
                 const uint32_t have = static_cast<uint32_t>(sm.have[at % kHave]);
                 const int j0 = t * kTile + col0 - x.s.len;   // drafted token of the first position
@@ -658,24 +690,29 @@ __global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < NC; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(v[c]));
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * qs;
-                // raise the reference
-                const bool raise = top > ref + kLazy;
+                // raise the reference, row by row: a row's result must not depend
+                // on its neighbours (those past the item's rows hold anything)
+                const bool raise = on && top > ref + kLazy;
                 if (__any_sync(0xffffffffu, raise)) {
-                    const float now = fmaxf(ref, top);
-                    const float f = now == -INFINITY ? 1.f : fast_exp2(ref - now);
+                    const float f = raise ? fast_exp2(ref - top) : 1.f;
                     sum *= f;
-                    ref = now;
-                    if (mine > 0) {
-                        const uint32_t o = tO + 128 * s;
+                    if (raise) ref = top;
+                    if (t > x.t0) {
+                        // two groups: the last P V was issued before this S's
+                        // products, and is done; one group: they ran ahead of it
+                        if (kOne) {
+                            waits(&sm.pvdone, (at - 1) & 1);
+                            tc_fence_after();
+                        }
 #pragma unroll 1
                         for (int c = 0; c < D; c += 16) {
                             uint32_t w[16];
-                            tmem_ld16(o + c, w);
+                            tmem_ld16(tO + c, w);
                             tmem_ld_wait();
 #pragma unroll
                             for (int q = 0; q < 16; ++q)
                                 w[q] = __float_as_uint(__uint_as_float(w[q]) * f);
-                            tmem_st16(o + c, w);
+                            tmem_st16(tO + c, w);
                         }
                         tmem_st_wait();
                     }
@@ -686,31 +723,37 @@ __global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
                 for (int h = 0; h < NC; h += 32) {
                     uint32_t pw[16];
 #pragma unroll
-                    for (int c = 0; c < 32; c += 2) {
+                    for (int c = 0; c < (NC < 32 ? NC : 32); c += 2) {
                         const float a = fast_exp2(fmaf(__uint_as_float(v[h + c]), qs, -sub));
                         const float b = fast_exp2(fmaf(__uint_as_float(v[h + c + 1]), qs, -sub));
                         part[c / 2 & 3] += a + b;
                         pw[c / 2] = kFp8 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
                     }
-                    tmem_st16(tS + (col0 + h) / 2, pw);
+                    if (NC < 32) tmem_st8(tS + (col0 + h) / 2, pw);
+                    else tmem_st16(tS + (col0 + h) / 2, pw);
                 }
                 sum += (part[0] + part[1]) + (part[2] + part[3]);
                 if (NC < kTile) {   // the other copies' columns
                     uint32_t z[16];
 #pragma unroll
                     for (int q = 0; q < 16; ++q) z[q] = 0;
+                    constexpr int W = NC < 32 ? NC : 32;
 #pragma unroll
-                    for (int c = 0; c < kTile; c += 32)
-                        if (c < col0 || c >= col0 + NC) tmem_st16(tS + c / 2, z);
+                    for (int c = 0; c < kTile; c += W)
+                        if (c < col0 || c >= col0 + NC) {
+                            if (W < 32) tmem_st8(tS + c / 2, z);
+                            else tmem_st16(tS + c / 2, z);
+                        }
                 }
                 tmem_st_wait();
             };
 
-            for (int i = both ? 0 : s; i < nt; i += both ? 1 : 2, ++mine) {
-                if (!waits(&sm.sfull[s], ns & 1)) break;
-                ++ns;
+            for (int i = 0; i < nt; ++i) {
+                const int s = kOne ? i & 1 : g;
+                if (!waits(&sm.sfull[s], (sphase >> s) & 1)) break;
+                sphase ^= 1u << s;
                 tc_fence_after();
-                if (kFp8 && mine == 0) qs = p.qscale * sm.qs[k & 1][on ? r : 0];
+                if (kFp8 && i == 0) qs = p.qscale * sm.qs[k & 1][on ? r : 0];
                 const int t = x.t0 + i;
                 const int valid = x.s.total - t * kTile;
                 if (!kFp8 && valid < kTile) {
@@ -720,90 +763,60 @@ __global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
                     if (!waits(&sm.vfull[j % lay.v_slots], (j / lay.v_slots) & 1)) break;
                     uint8_t* v = v_s + (j % lay.v_slots) * C::SLOT;
                     for (int c = gt; c < (kTile - valid) * (C::ROW / 16); c += 128)
-                        *reinterpret_cast<uint4*>(v + tile_off<C::BOX>(valid + c / (C::ROW / 16),
-                                                                       c % (C::ROW / 16))) =
+                        *reinterpret_cast<uint4*>(
+                            v + tile_off<C::BOX, kTile>(valid + c / (C::ROW / 16), c % (C::ROW / 16))) =
                             make_uint4(0, 0, 0, 0);
                     fence_proxy_async_smem();
                 }
                 if (warp_on) {
-                    if (copies == 4) tile(std::integral_constant<int, 32>(), t, base + i);
-                    else if (copies == 2) tile(std::integral_constant<int, 64>(), t, base + i);
-                    else tile(std::integral_constant<int, 128>(), t, base + i);
+                    if (kOne && copies == 4) tile(std::integral_constant<int, kTile / 4>(), s, t, base + i);
+                    else if (kOne && copies == 2) tile(std::integral_constant<int, kTile / 2>(), s, t, base + i);
+                    else tile(std::integral_constant<int, kTile>(), s, t, base + i);
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.pready[s]);
             }
             base += nt;
-            if (mine > 0) {
-                waits(&sm.ofull[s], no & 1);
-                ++no;
-                tc_fence_after();
-            }
-            // ---- O, or the partial state.  With tiles shared out, both groups
-            // exchange their statistics and each adds half of the columns, over
-            // the two streams and then over the copies of a row ----
-            float f0 = 1.f, f1 = 0.f, M = ref, den = sum;
-            int c_lo = 0, c_hi = D;
-            bool two = false;
-            if (!both) {
-                // (a group without tiles leaves its place alone: the other one may
-                // still be reading it for the stretch before)
-                if (mine > 0) {
-                    sm.m[s][gt] = ref;
-                    sm.l[s][gt] = sum;
-                }
-                tc_fence_before();
-                named_bar_sync(1, 256);
-                tc_fence_after();
-                two = nt > 1;
+            waits(&sm.ofull[g], no & 1);
+            ++no;
+            tc_fence_after();
+            // ---- O, or the partial state, over the copies of a row ----
+            float f0 = 1.f, M = ref, den = sum;
+            if (copies > 1) {
+                sm.m[gt] = ref;
+                sm.l[gt] = sum;
+                named_bar_sync(2, 128);
+                const int first = gt & (span - 1);
                 M = -INFINITY;
-                for (int y = 0; y < copies; ++y) {
-                    M = fmaxf(M, sm.m[0][(gt & (span - 1)) + y * span]);
-                    if (two) M = fmaxf(M, sm.m[1][(gt & (span - 1)) + y * span]);
-                }
+                for (int y = 0; y < copies; ++y) M = fmaxf(M, sm.m[first + y * span]);
                 const float mf = finite_max(M);
                 den = 0.f;
-                for (int y = 0; y < copies; ++y) {
-                    const int l = (gt & (span - 1)) + y * span;
-                    const float a = fast_exp2(sm.m[0][l] - mf);
-                    den = fmaf(a, sm.l[0][l], den);
-                    if (y == copy) f0 = a;
-                    if (two) {
-                        const float c = fast_exp2(sm.m[1][l] - mf);
-                        den = fmaf(c, sm.l[1][l], den);
-                        if (y == copy) f1 = c;
-                    }
-                }
-                c_lo = s * (D / 2);
-                c_hi = c_lo + D / 2;
+                for (int y = 0; y < copies; ++y)
+                    den = fmaf(fast_exp2(sm.m[first + y * span] - mf), sm.l[first + y * span], den);
+                f0 = fast_exp2(ref - mf);
             }
             const bool whole = x.t0 == 0 && x.t1 == x.s.tiles;
             const PartialAt part = partial_at<D>(p, 2 * blockIdx.x + (x.t0 == 0 ? 1 : 0));
             const float inv = whole ? (den > 0.f ? p.vscale / den : (den == 0.f ? 0.f : den)) : 1.f;
             const bool writes = on && copy == 0 && !*abort;
-            if (writes && !whole && c_lo == 0) {
+            if (writes && !whole) {
                 part.m[r] = M;
                 part.l[r] = den;
             }
             const int64_t row_at = static_cast<int64_t>(x.s.first + node) * p.Hq + head;
-            const uint32_t o0 = both ? tO + 128 * s : tO;
-            float4* const xg = sm.x[s];
+            float4* const xg = sm.x[g];
             float4* const stage = xg + (copies > 1 ? (copies - 1) * span * 4 : 0) + (warp & 3) * 128;
             auto swz = [](int row, int j) { return row * 4 + ((j + (row >> 1)) & 3); };
 #pragma unroll 1
-            for (int c = c_lo; c < c_hi; c += 16) {
+            for (int c = 0; c < D; c += 16) {
                 float y[16];
                 if (warp_on) {
-                    uint32_t a[16], b[16];
-                    tmem_ld16(o0 + c, a);
-                    if (two) tmem_ld16(tO + 128 + c, b);
+                    uint32_t a[16];
+                    tmem_ld16(tO + c, a);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) {
-                        y[q] = __uint_as_float(a[q]) * f0;
-                        if (two) y[q] = fmaf(__uint_as_float(b[q]), f1, y[q]);
-                    }
+                    for (int q = 0; q < 16; ++q) y[q] = __uint_as_float(a[q]) * f0;
                 }
                 if (copies > 1) {   // (uniform in the group; the other copies hand over)
                     if (on && copy > 0)
@@ -811,7 +824,7 @@ __global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
                         for (int q = 0; q < 4; ++q)
                             xg[swz(gt - span, q)] =
                                 make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
-                    named_bar_sync(2 + s, 128);
+                    named_bar_sync(2, 128);
                     if (on && copy == 0)
                         for (int z = 0; z < copies - 1; ++z)
 #pragma unroll
@@ -822,7 +835,7 @@ __global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
                                 y[4 * q + 2] += v.z;
                                 y[4 * q + 3] += v.w;
                             }
-                    named_bar_sync(2 + s, 128);
+                    named_bar_sync(2, 128);
                 }
                 if (copy == 0 && warp_on && !whole) {
                     if (writes)
@@ -858,7 +871,7 @@ __global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
                     }
                 }
             }
-            // the next stretch's P V waits for all eight warps
+            // the next stretch's P V waits for all warps
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.odone);
@@ -867,24 +880,25 @@ __global__ void __launch_bounds__(Tc<D, kFp8>::THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem, 512);
+    if (warp == 1) tmem_dealloc(tmem, C::COLS);
 }
 
-template <int D, bool kFp8>
+template <int D, bool kFp8, int kGroups>
 int launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, cudaStream_t st) {
-    using C = Tc<D, kFp8>;
-    auto kern = tree_tc_kernel<D, kFp8>;
+    using C = Tc<D, kFp8, kGroups>;
+    auto kern = tree_tc_kernel<D, kFp8, kGroups>;
     static int limit = -1;
     static std::once_flag once;
     std::call_once(once, [&] { limit = set_max_dynamic_smem(reinterpret_cast<const void*>(kern)); });
-    // the rings share what Q and the converted tiles leave
-    const int fixed = 1024 + kSmemHead + (C::Q << (p.row_shift - 7)) +
-                      (kFp8 ? kConvSlots * C::CONV : 0);
-    const int slots = (limit - fixed) / C::SLOT;
+    // the rings share what Q and the converted tiles leave; two CTAs of an SM
+    // have 114 KB each, 1 KB of it the system's
+    const int room = C::CTAS_PER_SM == 1 ? limit : std::min(limit, 113 * 1024);
+    const int fixed = 1024 + kSmemHead<kGroups> + kGroups * C::Q + (kFp8 ? kConvSlots * C::CONV : 0);
+    const int slots = (room - fixed) / C::SLOT;
     if (limit < 0 || slots < 4) return cudaErrorInvalidValue;
     Layout lay;
-    lay.v_slots = slots / 2 < kMaxSlots ? slots / 2 : kMaxSlots;
-    lay.k_slots = slots - lay.v_slots < kMaxSlots ? slots - lay.v_slots : kMaxSlots;
+    lay.v_slots = std::min(slots / 2, kMaxSlots);
+    lay.k_slots = std::min(slots - lay.v_slots, kMaxSlots);
     cudaLaunchConfig_t cfg = {};
     LaunchAttrs la;
     apply_pdl(cfg, la);
@@ -895,13 +909,22 @@ int launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p
     return cudaLaunchKernelEx(&cfg, kern, kmap, vmap, p, lay);
 }
 
+template <int D, bool kFp8>
+int launch_groups(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p,
+                  cudaStream_t st) {
+    return p.row_shift == 7 ? launch<D, kFp8, 1>(kmap, vmap, p, st)
+                            : launch<D, kFp8, 2>(kmap, vmap, p, st);
+}
+
 }  // namespace
 
 int launch_tree_tc(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int D,
                    bool fp8, cudaStream_t st) {
     if (D == 128)
-        return fp8 ? launch<128, true>(kmap, vmap, p, st) : launch<128, false>(kmap, vmap, p, st);
-    return fp8 ? launch<64, true>(kmap, vmap, p, st) : launch<64, false>(kmap, vmap, p, st);
+        return fp8 ? launch_groups<128, true>(kmap, vmap, p, st)
+                   : launch_groups<128, false>(kmap, vmap, p, st);
+    return fp8 ? launch_groups<64, true>(kmap, vmap, p, st)
+               : launch_groups<64, false>(kmap, vmap, p, st);
 }
 
 }  // namespace qmm
