@@ -1182,11 +1182,13 @@ int qmm_kv_append(const qmm_kv_cache* cache, const void* q, const void* k, const
 static int check_tree(const qmm_kv_cache* c, int Hq, int T) {
     if (Hq < 1 || T < 1 || Hq % c->Hkv) return QMM_EINVAL;
     if (T > qmm::kMaxTree || Hq / c->Hkv > 64) return QMM_ESHAPE;
-    // the kernels count a sequence's units of work in 32 bits; at most this many
-    // (tiles of 64 positions and a few more, row tiles of 16, heads)
+    // the kernels count a sequence's units of work in 32 bits, and so a CTA's
+    // share of the batch's: at most this many a sequence (tiles of 64 positions
+    // and a few more, row tiles of 16, heads), over at least 64 CTAs
     const int64_t cap = static_cast<int64_t>(c->max_pages) * c->page_size;
     const int64_t rows = ceil_div(static_cast<int64_t>(T) * (Hq / c->Hkv), 16);
-    return (cap / 64 + 16) * rows * c->Hkv > INT_MAX ? QMM_ESHAPE : QMM_OK;
+    const int64_t units = (cap / 64 + 16) * rows * c->Hkv;
+    return units > INT_MAX || units * c->B > int64_t{64} * INT_MAX ? QMM_ESHAPE : QMM_OK;
 }
 
 size_t qmm_tree_attention_workspace_bytes(const qmm_kv_cache* cache, int Hq, int T, int num_sms) {

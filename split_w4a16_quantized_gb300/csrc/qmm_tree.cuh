@@ -30,6 +30,7 @@ struct TreeParams {
     int* status;
     int64_t q_stride;
     int N, T, Hq, QG, ctas;
+    uint32_t qg_inv;   // ceil(2^22 / QG)
     int row_shift;   // log2 of the query rows of a work item
     int tile_shift;  // log2 of the positions of a tile
     int min_run;     // units of the shortest run
@@ -38,6 +39,12 @@ struct TreeParams {
     float qscale;    // scale * log2(e) * k_scale
     float vscale;
 };
+
+// Token of row r of a sequence's heads: r / QG, exact for r < 2^14 and QG <= 64
+// (r (QG - 1) < 2^22).
+__device__ __forceinline__ int row_node(const TreeParams& p, int r) {
+    return static_cast<int>((static_cast<uint64_t>(r) * p.qg_inv) >> 22);
+}
 
 // ---- work split ----------------------------------------------------------------
 
@@ -99,12 +106,13 @@ struct Run {
     Seq s;            // sequence b
     int b;
     int at;           // unit within the sequence's list
-    long long left;   // units of the run still to do
+    int left;         // units of the run still to do
 };
 
 // The CTA's run: whole block of kN threads; sh: shared scratch.
-struct RunShared {
+struct RunShared {   // (s and at hold nothing where b < 0)
     long long red[32];
+    Seq s;
     int at, b;
 };
 template <int kN>
@@ -112,7 +120,11 @@ __device__ __forceinline__ Run find_run(const TreeParams& p, RunShared& sh) {
     const int per = (p.d.B + kN - 1) / kN;
     const int b0 = min(p.d.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.d.B, b0 + per);
     long long mine = 0, all;
-    for (int b = b0; b < b1; ++b) mine += units_of(p, sequence(p, b));
+    Seq s;
+    for (int b = b0; b < b1; ++b) {
+        s = sequence(p, b);
+        mine += units_of(p, s);
+    }
     if (threadIdx.x == 0) sh.b = -1;
     const long long before = block_scan<kN>(mine, sh.red, &all);
     const long long len = run_length(p, all);
@@ -121,10 +133,12 @@ __device__ __forceinline__ Run find_run(const TreeParams& p, RunShared& sh) {
         // this thread's sequences hold the start
         long long at = start - before;
         for (int b = b0; b < b1; ++b) {
-            const int u = units_of(p, sequence(p, b));
+            if (per > 1) s = sequence(p, b);
+            const int u = units_of(p, s);
             if (at < u) {
                 sh.b = b;
                 sh.at = static_cast<int>(at);
+                sh.s = s;
                 break;
             }
             at -= u;
@@ -134,8 +148,8 @@ __device__ __forceinline__ Run find_run(const TreeParams& p, RunShared& sh) {
     Run r;
     r.b = sh.b;
     r.at = sh.at;
-    r.s = sequence(p, r.b < 0 ? 0 : r.b);
-    r.left = r.b < 0 ? 0 : (all - start < len ? all - start : len);
+    r.s = sh.s;
+    r.left = r.b < 0 ? 0 : static_cast<int>(all - start < len ? all - start : len);
     return r;
 }
 
@@ -158,7 +172,7 @@ __device__ __forceinline__ bool next_stretch(const TreeParams& p, Run& r, Stretc
         x->b = r.b;
         x->g = item / x->s.row_tiles;
         x->row0 = (item - x->g * x->s.row_tiles) << p.row_shift;
-        const int u1 = r.left < units - u0 ? u0 + static_cast<int>(r.left) : units;
+        const int u1 = r.left < units - u0 ? u0 + r.left : units;
         r.at += u1 - u0;
         r.left -= u1 - u0;
         // the first `setup` units stand for the item's fixed cost: a run that

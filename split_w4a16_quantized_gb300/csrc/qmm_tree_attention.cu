@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             // drafted slots; a chain needs none ----
             int node[H];
 #pragma unroll
-            for (int h = 0; h < H; ++h) node[h] = (x.row0 + min(gr + 8 * h, rows - 1)) / p.QG;
+            for (int h = 0; h < H; ++h) node[h] = row_node(p, x.row0 + min(gr + 8 * h, rows - 1));
             if (p.parents && x.t1 * kTile > x.s.len) {
                 for (int i = tid; i < x.s.n; i += 32 * kWarps) {
                     const int v = p.parents[x.s.first + i];
@@ -695,8 +695,8 @@ struct Variant {
 };
 Variant variant(int rows) {
     if (rows <= kRows) return {false, 4, 6, kCtasPerSm, 2, 1};
-    if (rows <= 128) return {true, 7, kTcTileShift1, 2, 4, 2};
-    return {true, 8, kTcTileShift2, 1, 4, 2};
+    if (rows <= 128) return {true, 7, kTcTileShift1, 2, 6, 4};
+    return {true, 8, kTcTileShift2, 1, 6, 3};
 }
 
 }  // namespace
@@ -724,6 +724,7 @@ int launch_tree_attention(const qmm_kv_cache& c, const void* q, int64_t q_stride
     p.T = T;
     p.Hq = Hq;
     p.QG = Hq / c.Hkv;
+    p.qg_inv = ((1u << 22) + p.QG - 1) / p.QG;
     const Variant var = variant(T * p.QG);
     p.ctas = var.ctas_per_sm * num_sms;
     p.row_shift = var.row_shift;

@@ -30,12 +30,6 @@
 //     (An MMA takes the same time for N = 64 as for 128, so that tile has half
 //     of the score MMAs; two such CTAs do not fit an SM.)
 //
-// Few rows.  An item of at most 64 (32) rows is put into the 128 twice (four
-// times).  The MMA computes all copies' scores anyway; copy c of a row takes
-// columns [c w, (c + 1) w) of the tile, w = tile / copies, and zeros elsewhere
-// in P, so a row's exponentials are spread over that many warps, which would
-// idle otherwise.  The copies' states are added at the end.
-//
 // An item's first scores need only its q and K: they are issued right behind
 // the last products of the item before, while the group still writes that
 // item's output.
@@ -57,7 +51,6 @@
 // F16.
 #include <algorithm>
 #include <mutex>
-#include <type_traits>
 
 #include "qmm.h"
 #include "qmm_tree.cuh"
@@ -83,9 +76,9 @@ struct Tc {
     // registers: the launch gives every thread the same share; the softmax groups
     // hold a row of S and take over what the others do not need
     static constexpr int SHARE = 65536 / (CTAS_PER_SM * THREADS) / 8 * 8;
-    static constexpr int REGS_CTL = kFp8 ? (kGroups == 1 ? 48 : 56) : (kGroups == 1 ? 72 : 88);
-    static constexpr int REGS_CONV = kGroups == 1 ? 48 : 56;
-    static constexpr int REGS_SOFTMAX = kFp8 ? (kGroups == 1 ? 144 : 200) : (kGroups == 1 ? 184 : 208);
+    static constexpr int REGS_CTL = kFp8 ? 56 : 88;
+    static constexpr int REGS_CONV = kGroups == 1 ? 40 : 56;
+    static constexpr int REGS_SOFTMAX = kFp8 ? (kGroups == 1 ? 144 : 200) : (kGroups == 1 ? 168 : 208);
     static_assert(REGS_CTL + kGroups * REGS_SOFTMAX + (kFp8 ? REGS_CONV : 0) <= SHARE * WARPS / 4,
                   "registers");
     static constexpr int ROW = D * (kFp8 ? 1 : 2);           // bytes of a cache row
@@ -114,14 +107,10 @@ struct TcSmem {
     int abort;
     int have[kHave];                    // pages of a tile that exist, one bit a copy
     int pages[16];                      // of the tile being copied
-    float m[128], l[128];               // (one group) the copies' statistics
     float qs[2][128 * kGroups];         // E4M3: the rows' scales, by stretch parity
     int16_t par[kMaxTree];
-    // by group: 16 columns of O from the other copies of the rows (96 or 64 rows
-    // of 64 bytes, or none), then 32 rows x 32 BF16 columns of O for each warp
-    // that writes (1, 2 or 4)
-    alignas(16) float4 x[kGroups][512];
-    uint32_t anc[128 * kGroups][kWords];   // a thread's own row: ancestors and itself
+    alignas(16) uint4 stage[4 * kGroups][128];   // by warp: 32 rows x 32 BF16 columns of O
+    uint32_t anc[128 * kGroups][kWords + 1];     // a thread's own row: ancestors and itself
     RunShared run;
 };
 template <int kGroups>
@@ -193,14 +182,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
         : "r"(taddr)
         : "memory");
 }
-// 32 lanes x 8 columns.
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-        : "memory");
-}
-
 template <int kRegs>
 __device__ __forceinline__ void regs_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegs));
@@ -242,9 +223,6 @@ __device__ __forceinline__ uint64_t bits_from(const uint32_t* anc, int from) {
 struct Layout {
     int k_slots, v_slots;
 };
-
-// How often an item's rows stand in the 128 of a product.
-__device__ __forceinline__ int copies_of(int rows) { return rows <= 32 ? 4 : (rows <= 64 ? 2 : 1); }
 
 template <int D, bool kFp8, int kGroups>
 __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGroups>::CTAS_PER_SM)
@@ -462,23 +440,34 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
             const int t64 = tid - 64;
             for (int k = 0; next_stretch(p, run, &x); ++k) {
                 const int rows = min(1 << p.row_shift, x.s.n * p.QG - x.row0);
-                const int copies = kOne ? copies_of(rows) : 1;
                 if (k > 0 && !waits(&sm.qfree, (k - 1) & 1)) break;
                 if (k > 0) fence_proxy_async_smem();
                 const __nv_bfloat16* q0 = p.q + x.s.first * p.q_stride + x.g * p.QG * D;
                 if (kFp8) {
-                    for (int r = t64; r < rows; r += 64) {
-                        const int node = (x.row0 + r) / p.QG, head = x.row0 + r - node * p.QG;
-                        const __nv_bfloat16* qv = q0 + node * p.q_stride + head * D;
+                    // a lane takes 16 values, D / 16 lanes a row; the next rows'
+                    // loads are in flight while these are converted
+                    constexpr int LPR = D / 16, STEP = 64 / LPR;
+                    const int c = t64 % LPR;
+                    uint4 a, b;
+                    auto load = [&](int r) {
+                        const int node = row_node(p, x.row0 + r);
+                        const __nv_bfloat16* src =
+                            q0 + node * p.q_stride + (x.row0 + r - node * p.QG) * D + 16 * c;
+                        a = *reinterpret_cast<const uint4*>(src);
+                        b = *reinterpret_cast<const uint4*>(src + 8);
+                    };
+                    int r = t64 / LPR;
+                    if (r < rows) load(r);
+                    for (int r0 = 0; r0 < rows; r0 += STEP, r += STEP) {
+                        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                        if (r + STEP < rows) load(r + STEP);
                         uint32_t big = 0;   // largest magnitude, as bits: NaN above all
-#pragma unroll 8
-                        for (int c = 0; c < D / 8; ++c) {
-                            const uint4 v = *reinterpret_cast<const uint4*>(qv + 8 * c);
-                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                big = max(big, max((w[i] & 0x7fffu) << 16, w[i] & 0x7fff0000u));
-                        }
+                        for (int i = 0; i < 8; ++i)
+                            big = max(big, max((w[i] & 0x7fffu) << 16, w[i] & 0x7fff0000u));
+#pragma unroll
+                        for (int o = LPR / 2; o > 0; o >>= 1)
+                            big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
                         // 2^e <= big < 2^(e+1); a row that holds infinities or NaN
                         // becomes NaN (what its softmax would be)
                         int e = static_cast<int>(big >> 23) - 127;
@@ -486,39 +475,27 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                         e = big > 0 && !bad ? max(-110, min(126, e)) : 0;
                         const float up = bad ? __int_as_float(0x7fffffff)
                                              : __uint_as_float(static_cast<uint32_t>(134 - e) << 23);
-                        sm.qs[k & 1][r] = __uint_as_float(static_cast<uint32_t>(120 + e) << 23);
-#pragma unroll 2
-                        for (int c = 0; c < D / 16; ++c) {
-                            uint32_t hi[4], lo[4];
+                        uint32_t hi[4], lo[4];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint2 w = *reinterpret_cast<const uint2*>(qv + 16 * c + 4 * i);
-                                const float f[4] = {__uint_as_float(w.x << 16) * up,
-                                                    __uint_as_float(w.x & 0xffff0000u) * up,
-                                                    __uint_as_float(w.y << 16) * up,
-                                                    __uint_as_float(w.y & 0xffff0000u) * up};
-                                uint32_t h2[2], l2[2];
-#pragma unroll
-                                for (int j = 0; j < 2; ++j) {
-                                    h2[j] = __nv_cvt_float2_to_fp8x2(
-                                        make_float2(f[2 * j], f[2 * j + 1]), __NV_SATFINITE, __NV_E4M3);
-                                    const uint32_t b = e4m3x2_to_f16x2(h2[j]);
-                                    const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&b));
-                                    l2[j] = __nv_cvt_float2_to_fp8x2(
-                                        make_float2(f[2 * j] - g.x, f[2 * j + 1] - g.y), __NV_SATFINITE,
-                                        __NV_E4M3);
-                                }
-                                hi[i] = h2[0] | (h2[1] << 16);
-                                lo[i] = l2[0] | (l2[1] << 16);
-                            }
-                            uint8_t* dst = q_s + (r >> 7) * C::Q;
-#pragma unroll 1
-                            for (int y = 0; y < copies; ++y) {
-                                const uint32_t o = tile_off<C::BOX, 128>((r & 127) + y * (128 / copies), c);
-                                *reinterpret_cast<uint4*>(dst + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                                *reinterpret_cast<uint4*>(dst + 128 * D + o) =
-                                    make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                            }
+                        for (int i = 0; i < 8; ++i) {
+                            const float f0 = __uint_as_float(w[i] << 16) * up;
+                            const float f1 = __uint_as_float(w[i] & 0xffff0000u) * up;
+                            const uint32_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(f0, f1),
+                                                                         __NV_SATFINITE, __NV_E4M3);
+                            const uint32_t h = e4m3x2_to_f16x2(h2);
+                            const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&h));
+                            const uint32_t l2 = __nv_cvt_float2_to_fp8x2(
+                                make_float2(f0 - g.x, f1 - g.y), __NV_SATFINITE, __NV_E4M3);
+                            if (i % 2 == 0) hi[i / 2] = h2, lo[i / 2] = l2;
+                            else hi[i / 2] |= h2 << 16, lo[i / 2] |= l2 << 16;
+                        }
+                        if (r < rows) {
+                            uint8_t* dst = q_s + (r >> 7) * C::Q + tile_off<C::BOX, 128>(r & 127, c);
+                            *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                            *reinterpret_cast<uint4*>(dst + 128 * D) =
+                                make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                            if (c == 0)
+                                sm.qs[k & 1][r] = __uint_as_float(static_cast<uint32_t>(120 + e) << 23);
                         }
                     }
                 } else {
@@ -526,18 +503,11 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                     constexpr int STEP = 64 / CH;    // rows a pass
                     const int c = t64 % CH;
                     const uint32_t dst = smem_addr(q_s);
-                    int node = (x.row0 + t64 / CH) / p.QG;
-                    int head = x.row0 + t64 / CH - node * p.QG;
-#pragma unroll 2
                     for (int r = t64 / CH; r < rows; r += STEP) {
-                        const __nv_bfloat16* src = q0 + node * p.q_stride + head * D + 8 * c;
-#pragma unroll 1
-                        for (int y = 0; y < copies; ++y)
-                            cp_async16(dst + (r >> 7) * C::Q +
-                                           tile_off<128, 128>((r & 127) + y * (128 / copies), c),
-                                       src, true);
-                        head += STEP;
-                        while (head >= p.QG) head -= p.QG, ++node;
+                        const int node = row_node(p, x.row0 + r);
+                        cp_async16(dst + (r >> 7) * C::Q + tile_off<128, 128>(r & 127, c),
+                                   q0 + node * p.q_stride + (x.row0 + r - node * p.QG) * D + 8 * c,
+                                   true);
                     }
                     cp_async_commit();
                     cp_async_wait<0>();
@@ -616,14 +586,11 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
         for (int k = 0; next_stretch(p, run, &x); ++k) {
             const int nt = x.t1 - x.t0;
             const int rows = min(1 << p.row_shift, x.s.n * p.QG - x.row0);
-            const int copies = kOne ? copies_of(rows) : 1;
-            const int span = 128 / copies;                           // lanes of a copy
-            const int copy = gt / span;
-            const int r = kOne ? gt - copy * span : gt + 128 * g;    // row of the item
+            const int r = kOne ? gt : gt + 128 * g;   // row of the item
             const bool on = r < rows;
             const bool warp_on = __any_sync(0xffffffffu, on);
-            const int node = (x.row0 + (on ? r : 0)) / p.QG;
-            const int head = x.g * p.QG + (x.row0 + (on ? r : 0)) % p.QG;
+            const int row = x.row0 + (on ? r : 0);
+            const int node = row_node(p, row), head = x.g * p.QG + row - node * p.QG;
             // ---- ancestors, where the stretch reaches the drafted slots: the same
             // for all heads of a sequence ----
             if (x.t1 * kTile > x.s.len && (x.b != anc_b || x.row0 != anc_row)) {
@@ -637,40 +604,30 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                     }
                     named_bar_sync(1, 128 * kGroups);
                 }
-                uint32_t w[kWords];
 #pragma unroll
                 for (int j = 0; j < kWords; ++j)
-                    w[j] = p.parents ? 0u : static_cast<uint32_t>(low_bits(node + 1 - 32 * j));
+                    anc[j] = p.parents ? 0u : static_cast<uint32_t>(low_bits(node + 1 - 32 * j));
                 if (p.parents)
-                    for (int i = node; i >= 0; i = sm.par[i]) {
-#pragma unroll
-                        for (int j = 0; j < kWords; ++j)
-                            if (j == i >> 5) w[j] |= 1u << (i & 31);
-                    }
-#pragma unroll
-                for (int j = 0; j < kWords; ++j) anc[j] = w[j];
+                    for (int i = node; i >= 0; i = sm.par[i]) anc[i >> 5] |= 1u << (i & 31);
             }
 
             float qs = p.qscale, ref = -INFINITY, sum = 0.f;
 
-            // One tile in buffer s: NC columns from the copy's first on.
-            auto tile = [&](auto nc, int s, int t, int at) {
-                constexpr int NC = decltype(nc)::value;
-                const int col0 = copy * NC;
+            // One tile in buffer s; `at` counts the tiles of the run.
+            auto tile = [&](int s, int t, int at) {
                 const uint32_t tS = quarter + kTile * s;
-                uint32_t v[NC];
-                if (NC < 32) tmem_ld16(tS + col0, v);
+                uint32_t v[kTile];
 #pragma unroll
-                for (int c = 0; c + 32 <= NC; c += 32) tmem_ld32(tS + col0 + c, v + c);
+                for (int c = 0; c < kTile; c += 32) tmem_ld32(tS + c, v + c);
                 // what the row sees of the tile
                 const uint32_t have = static_cast<uint32_t>(sm.have[at % kHave]);
-                const int j0 = t * kTile + col0 - x.s.len;   // drafted token of the first position
-                const int valid = x.s.total - t * kTile - col0;
-                const bool cut = j0 + NC > 0 || have != (1u << pieces) - 1u;
+                const int j0 = t * kTile - x.s.len;   // drafted token of the first position
+                const int valid = x.s.total - t * kTile;
+                const bool cut = j0 + kTile > 0 || have != (1u << pieces) - 1u;
                 tmem_ld_wait();
                 if (cut) {
 #pragma unroll
-                    for (int h = 0; h < NC; h += 64) {
+                    for (int h = 0; h < kTile; h += 64) {
                         // history, then the ancestors
                         uint64_t see = ~0ull;
                         const int j = j0 + h;
@@ -678,17 +635,17 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                             see = (low_bits(-j) | bits_from(anc, j)) & low_bits(valid - h);
                         for (int q = 0; q < pieces; ++q)
                             if (!((have >> q) & 1u)) {
-                                const int lo = (q << p.box_shift) - col0 - h;
+                                const int lo = (q << p.box_shift) - h;
                                 see &= ~(low_bits(lo + (1 << p.box_shift)) & ~low_bits(lo));
                             }
 #pragma unroll
-                        for (int c = 0; c < (NC < 64 ? NC : 64); ++c)
+                        for (int c = 0; c < 64; ++c)
                             if (!((see >> c) & 1ull)) v[h + c] = 0xff800000u;   // -inf
                     }
                 }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < NC; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(v[c]));
+                for (int c = 0; c < kTile; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(v[c]));
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * qs;
                 // raise the reference, row by row: a row's result must not depend
                 // on its neighbours (those past the item's rows hold anything)
@@ -720,31 +677,18 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                 const float sub = finite_max(ref);
                 float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int h = 0; h < NC; h += 32) {
+                for (int h = 0; h < kTile; h += 32) {
                     uint32_t pw[16];
 #pragma unroll
-                    for (int c = 0; c < (NC < 32 ? NC : 32); c += 2) {
+                    for (int c = 0; c < 32; c += 2) {
                         const float a = fast_exp2(fmaf(__uint_as_float(v[h + c]), qs, -sub));
                         const float b = fast_exp2(fmaf(__uint_as_float(v[h + c + 1]), qs, -sub));
                         part[c / 2 & 3] += a + b;
                         pw[c / 2] = kFp8 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
                     }
-                    if (NC < 32) tmem_st8(tS + (col0 + h) / 2, pw);
-                    else tmem_st16(tS + (col0 + h) / 2, pw);
+                    tmem_st16(tS + h / 2, pw);
                 }
                 sum += (part[0] + part[1]) + (part[2] + part[3]);
-                if (NC < kTile) {   // the other copies' columns
-                    uint32_t z[16];
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) z[q] = 0;
-                    constexpr int W = NC < 32 ? NC : 32;
-#pragma unroll
-                    for (int c = 0; c < kTile; c += W)
-                        if (c < col0 || c >= col0 + NC) {
-                            if (W < 32) tmem_st8(tS + c / 2, z);
-                            else tmem_st16(tS + c / 2, z);
-                        }
-                }
                 tmem_st_wait();
             };
 
@@ -768,11 +712,7 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                             make_uint4(0, 0, 0, 0);
                     fence_proxy_async_smem();
                 }
-                if (warp_on) {
-                    if (kOne && copies == 4) tile(std::integral_constant<int, kTile / 4>(), s, t, base + i);
-                    else if (kOne && copies == 2) tile(std::integral_constant<int, kTile / 2>(), s, t, base + i);
-                    else tile(std::integral_constant<int, kTile>(), s, t, base + i);
-                }
+                if (warp_on) tile(s, t, base + i);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.pready[s]);
@@ -781,94 +721,56 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
             waits(&sm.ofull[g], no & 1);
             ++no;
             tc_fence_after();
-            // ---- O, or the partial state, over the copies of a row ----
-            float f0 = 1.f, M = ref, den = sum;
-            if (copies > 1) {
-                sm.m[gt] = ref;
-                sm.l[gt] = sum;
-                named_bar_sync(2, 128);
-                const int first = gt & (span - 1);
-                M = -INFINITY;
-                for (int y = 0; y < copies; ++y) M = fmaxf(M, sm.m[first + y * span]);
-                const float mf = finite_max(M);
-                den = 0.f;
-                for (int y = 0; y < copies; ++y)
-                    den = fmaf(fast_exp2(sm.m[first + y * span] - mf), sm.l[first + y * span], den);
-                f0 = fast_exp2(ref - mf);
-            }
+            // ---- O, or the partial state ----
             const bool whole = x.t0 == 0 && x.t1 == x.s.tiles;
-            const PartialAt part = partial_at<D>(p, 2 * blockIdx.x + (x.t0 == 0 ? 1 : 0));
-            const float inv = whole ? (den > 0.f ? p.vscale / den : (den == 0.f ? 0.f : den)) : 1.f;
-            const bool writes = on && copy == 0 && !*abort;
-            if (writes && !whole) {
-                part.m[r] = M;
-                part.l[r] = den;
-            }
-            const int64_t row_at = static_cast<int64_t>(x.s.first + node) * p.Hq + head;
-            float4* const xg = sm.x[g];
-            float4* const stage = xg + (copies > 1 ? (copies - 1) * span * 4 : 0) + (warp & 3) * 128;
-            auto swz = [](int row, int j) { return row * 4 + ((j + (row >> 1)) & 3); };
+            const bool writes = on && !*abort;
+            if (warp_on && !whole) {
+                const PartialAt part = partial_at<D>(p, 2 * blockIdx.x + (x.t0 == 0 ? 1 : 0));
+                if (writes) {
+                    part.m[r] = ref;
+                    part.l[r] = sum;
+                }
 #pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-                float y[16];
-                if (warp_on) {
-                    uint32_t a[16];
-                    tmem_ld16(tO + c, a);
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t y[32];
+                    tmem_ld32(tO + c, y);
                     tmem_ld_wait();
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) y[q] = __uint_as_float(a[q]) * f0;
-                }
-                if (copies > 1) {   // (uniform in the group; the other copies hand over)
-                    if (on && copy > 0)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            xg[swz(gt - span, q)] =
-                                make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
-                    named_bar_sync(2, 128);
-                    if (on && copy == 0)
-                        for (int z = 0; z < copies - 1; ++z)
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const float4 v = xg[swz(gt + z * span, q)];
-                                y[4 * q] += v.x;
-                                y[4 * q + 1] += v.y;
-                                y[4 * q + 2] += v.z;
-                                y[4 * q + 3] += v.w;
-                            }
-                    named_bar_sync(2, 128);
-                }
-                if (copy == 0 && warp_on && !whole) {
                     if (writes)
 #pragma unroll
-                        for (int q = 0; q < 16; q += 4)
-                            *reinterpret_cast<float4*>(part.at(r, c + q)) =
-                                make_float4(y[q], y[q + 1], y[q + 2], y[q + 3]);
-                } else if (copy == 0 && warp_on) {
-                    // a warp's 32 rows x 32 columns turn in shared memory: 8 rows of
-                    // 64 bytes a store instead of 32 of 16
+                        for (int q = 0; q < 32; q += 4)
+                            *reinterpret_cast<uint4*>(part.at(r, c + q)) =
+                                make_uint4(y[q], y[q + 1], y[q + 2], y[q + 3]);
+                }
+            } else if (warp_on) {
+                // a warp's 32 rows x 32 columns turn in shared memory: 8 rows of 64
+                // bytes a store instead of 32 of 16
+                const float inv = sum > 0.f ? p.vscale / sum : (sum == 0.f ? 0.f : sum);
+                const int64_t row_at = static_cast<int64_t>(x.s.first + node) * p.Hq + head;
+                const uint32_t mask = __ballot_sync(0xffffffffu, writes);
+                uint4* const stage = sm.stage[warp - C::SOFTMAX0];
+                auto swz = [](int row, int j) { return row * 4 + ((j + (row >> 1)) & 3); };
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t y[32];
+                    tmem_ld32(tO + c, y);
+                    tmem_ld_wait();
+                    auto pair = [&](int q) {
+                        return pack_bf16x2(__uint_as_float(y[q]) * inv, __uint_as_float(y[q + 1]) * inv);
+                    };
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) y[q] *= inv;
-                    const int half = (c >> 3) & 2;
+                    for (int q = 0; q < 4; ++q)
+                        stage[swz(lane, q)] = make_uint4(pair(8 * q), pair(8 * q + 2), pair(8 * q + 4),
+                                                         pair(8 * q + 6));
+                    __syncwarp();
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        uint4 w = make_uint4(
-                            pack_bf16x2(y[8 * q], y[8 * q + 1]), pack_bf16x2(y[8 * q + 2], y[8 * q + 3]),
-                            pack_bf16x2(y[8 * q + 4], y[8 * q + 5]), pack_bf16x2(y[8 * q + 6], y[8 * q + 7]));
-                        *reinterpret_cast<uint4*>(&stage[swz(lane, half + q)]) = w;
+                    for (int q = 0; q < 4; ++q) {
+                        const int from = q * 8 + (lane >> 2);
+                        const int64_t to = __shfl_sync(0xffffffffu, row_at, from);
+                        if ((mask >> from) & 1u)
+                            *reinterpret_cast<uint4*>(p.O + to * D + c + 8 * (lane & 3)) =
+                                stage[swz(from, lane & 3)];
                     }
-                    if (half) {
-                        __syncwarp();
-                        const uint32_t mask = __ballot_sync(0xffffffffu, writes);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const int row = q * 8 + (lane >> 2);
-                            const int64_t to = __shfl_sync(0xffffffffu, row_at, row);
-                            if ((mask >> row) & 1u)
-                                *reinterpret_cast<uint4*>(p.O + to * D + (c - 16) + 8 * (lane & 3)) =
-                                    *reinterpret_cast<const uint4*>(&stage[swz(row, lane & 3)]);
-                        }
-                        __syncwarp();
-                    }
+                    __syncwarp();
                 }
             }
             // the next stretch's P V waits for all warps
