@@ -5,11 +5,13 @@
 // Append.  Per head x of D values: y = x w / sqrt(mean(x^2) + eps), then each
 // pair (a, c) turns by its angle, (a cos - c sin, c cos + a sin).  A few
 // operations per value read and written once: the call is bound by the bytes
-// of q, k, v and the cache rows.  A head row is held by D / 8 lanes, 16 bytes
-// each, so that every access is one full 128-bit one; the partner of a value
-// in a pair sits in the same lane (interleaved pairs) or in the lane dim / 16
-// further (halves), reached by shuffles.  A lane keeps its cosines and sines
-// for all the rows it handles, and its next rows' loads are issued together.
+// of q, k, v and the cache rows, if the instructions per value are few.  A head
+// row is held by D / 8 lanes, and a lane holds four pairs: values [4 j, 4 j + 4)
+// of both halves of the rotated part, or eight neighbours where pairs are
+// neighbours or nothing turns.  So a pair never crosses lanes, the lane's four
+// cosines and sines serve all its rows, and the arithmetic runs on two values
+// an instruction (f32x2).  The first rows are asked for before the chain of
+// loads (range, length, page) that says where they go.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -25,7 +27,7 @@ namespace qmm {
 namespace {
 
 constexpr int kAppendThreads = 256;
-constexpr int kAppendRows = 4;  // head rows whose loads a lane has in flight
+constexpr int kAppendQ = 4;   // q rows whose loads a lane has in flight, beside a k and a v row
 
 struct AppendParams {
     PagedDims d;
@@ -42,18 +44,62 @@ struct AppendParams {
     float eps, k_scale, v_scale;
 };
 
-__device__ __forceinline__ void unpack8(const uint4& u, float x[8]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        x[2 * j] = __uint_as_float(w[j] << 16);
-        x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-    }
+// Two FP32 values in one register pair, and arithmetic on both at once.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 split(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
 }
 
-__device__ __forceinline__ uint4 pack8(const float x[8]) {
-    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                      pack_bf16x2(x[6], x[7]));
+// Eight BF16 values of a lane as its four pairs: a = the pairs' first values
+// (two and two), c = their partners.  Interleaved: the pairs are neighbours in
+// memory; otherwise lo and hi are the two halves' pieces.
+struct Pairs {
+    F2 a[2], c[2];
+};
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+template <bool kInter>
+__device__ __forceinline__ Pairs pairs_of(uint2 lo, uint2 hi) {
+    Pairs p;
+    if (kInter) {
+        p.a[0] = f2(bf_lo(lo.x), bf_lo(lo.y)), p.c[0] = f2(bf_hi(lo.x), bf_hi(lo.y));
+        p.a[1] = f2(bf_lo(hi.x), bf_lo(hi.y)), p.c[1] = f2(bf_hi(hi.x), bf_hi(hi.y));
+    } else {
+        p.a[0] = f2(bf_lo(lo.x), bf_hi(lo.x)), p.a[1] = f2(bf_lo(lo.y), bf_hi(lo.y));
+        p.c[0] = f2(bf_lo(hi.x), bf_hi(hi.x)), p.c[1] = f2(bf_lo(hi.y), bf_hi(hi.y));
+    }
+    return p;
+}
+// The same values in memory order: lo then hi, four each.
+template <bool kInter>
+__device__ __forceinline__ void values_of(const Pairs& p, float x[8]) {
+    const float2 a0 = split(p.a[0]), a1 = split(p.a[1]), c0 = split(p.c[0]), c1 = split(p.c[1]);
+    if (kInter) {
+        x[0] = a0.x, x[1] = c0.x, x[2] = a0.y, x[3] = c0.y;
+        x[4] = a1.x, x[5] = c1.x, x[6] = a1.y, x[7] = c1.y;
+    } else {
+        x[0] = a0.x, x[1] = a0.y, x[2] = a1.x, x[3] = a1.y;
+        x[4] = c0.x, x[5] = c0.y, x[6] = c1.x, x[7] = c1.y;
+    }
 }
 
 // x / scale to the nearest E4M3 number, at most +-448 (ties to even)
@@ -65,21 +111,45 @@ __device__ __forceinline__ uint32_t e4m3x4(const float* x, float scale) {
     return lo | (hi << 16);
 }
 
-template <int D, bool kFp8>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendParams p) {
+template <int D, bool kFp8, bool kInter>
+__global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const AppendParams p) {
     constexpr int L = D / 8;                        // lanes of a head row
     constexpr int kGroups = kAppendThreads / L;     // lane groups of the block
     pdl_trigger();
     const int lane = threadIdx.x % L;
     const int group = threadIdx.x / L;
-    const int sub = group % p.per_token;
-    const int tok = blockIdx.x * (kGroups / p.per_token) + group / p.per_token;
+    const int step = p.per_token;                   // lane groups of a token
+    const int sub = group & (step - 1);
+    const int tok = blockIdx.x * (kGroups / step) + group / step;
     pdl_wait();
     // A group's lanes leave together or not at all; the shuffles below name
     // only the group's own lanes.
     if (tok >= p.N) return;
-    const uint32_t mask = (L == 32 ? 0xffffffffu : ((1u << (L & 31)) - 1u))
-                          << ((threadIdx.x & 31) / L * L);
+    const uint32_t mask = ((1u << L) - 1u) << ((threadIdx.x & 31) / L * L);
+
+    // where the lane's two pieces of four values start
+    const bool turns = 8 * lane < p.dim;
+    const int at_lo = !kInter && turns ? 4 * lane : 8 * lane;
+    const int at_hi = !kInter && turns ? p.dim / 2 + 4 * lane : 8 * lane + 4;
+    const int Hq = p.Hq, Hkv = p.d.Hkv;
+    const __nv_bfloat16* qrow = p.q + tok * p.q_stride;
+    const __nv_bfloat16* krow = p.k + tok * p.k_stride;
+    const __nv_bfloat16* vrow = p.v + tok * p.v_stride;
+    struct In {
+        uint2 lo, hi;
+    };
+    auto load = [&](const __nv_bfloat16* row, int h) {
+        In x;
+        x.lo = __ldcs(reinterpret_cast<const uint2*>(row + h * D + at_lo));
+        x.hi = __ldcs(reinterpret_cast<const uint2*>(row + h * D + at_hi));
+        return x;
+    };
+    In qi[kAppendQ], ki, vi;
+#pragma unroll
+    for (int u = 0; u < kAppendQ; ++u)
+        if (sub + u * step < Hq) qi[u] = load(qrow, sub + u * step);
+    if (sub < Hkv) ki = load(krow, sub), vi = load(vrow, sub);
+
     int b, i;
     if (!p.cu) {
         b = tok / p.T;
@@ -95,109 +165,96 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
         i = tok - p.cu[b];
         if (i < 0) return;
     }
+    const int pos_given = p.positions ? p.positions[tok] : 0;
     const int len = cached_tokens(p.d, b);
-    const int pos = p.positions ? p.positions[tok] : len + i;
+    const int pos = p.positions ? pos_given : len + i;
     if (p.dim > 0 && (pos < 0 || pos >= p.rows)) return;
     // (len <= cap < 2^31 - 65535 and i < N: the sum is tested before it is used)
     const int64_t slot = static_cast<int64_t>(len) + i;
     const int64_t at = slot < p.d.cap ? slot_offset(p.d, b, static_cast<int>(slot)) : -1;
 
-    // the lane's cosines and sines: of pair j for its value 2j or 2j + 1
-    // (interleaved), of pair (8 lane + j) mod (dim / 2) otherwise
-    const bool turns = 8 * lane < p.dim;
-    const int half = p.dim / 16;  // lanes of half a rotated head
-    float cs[8], sn[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) cs[j] = 1.f, sn[j] = 0.f;
+    // cosines and sines of the lane's four pairs
+    F2 cs[2], sn[2], ns[2];
     if (turns) {
-        const float* row = p.cos_sin + static_cast<int64_t>(pos) * p.dim;
-        if (p.interleaved) {
-            const float4 c4 = *reinterpret_cast<const float4*>(row + 4 * lane);
-            const float4 s4 = *reinterpret_cast<const float4*>(row + p.dim / 2 + 4 * lane);
-            cs[0] = cs[1] = c4.x, cs[2] = cs[3] = c4.y, cs[4] = cs[5] = c4.z, cs[6] = cs[7] = c4.w;
-            sn[0] = sn[1] = s4.x, sn[2] = sn[3] = s4.y, sn[4] = sn[5] = s4.z, sn[6] = sn[7] = s4.w;
-        } else {
-            const float* c = row + 8 * (lane < half ? lane : lane - half);
+        const float* row = p.cos_sin + static_cast<int64_t>(pos) * p.dim + 4 * lane;
+        const float4 c4 = *reinterpret_cast<const float4*>(row);
+        const float4 s4 = *reinterpret_cast<const float4*>(row + p.dim / 2);
+        cs[0] = f2(c4.x, c4.y), cs[1] = f2(c4.z, c4.w);
+        sn[0] = f2(s4.x, s4.y), sn[1] = f2(s4.z, s4.w);
+        ns[0] = f2(-s4.x, -s4.y), ns[1] = f2(-s4.z, -s4.w);
+    }
+    // norm (weights w, or none) and rotation
+    auto turned = [&](const In& in, const __nv_bfloat16* w, float x[8]) {
+        Pairs y = pairs_of<kInter>(in.lo, in.hi);
+        if (w) {
+            const uint2 wl = __ldg(reinterpret_cast<const uint2*>(w + at_lo));
+            const uint2 wh = __ldg(reinterpret_cast<const uint2*>(w + at_hi));
+            F2 s2 = mul2(y.a[0], y.a[0]);
+            s2 = fma2(y.a[1], y.a[1], s2);
+            s2 = fma2(y.c[0], y.c[0], s2);
+            s2 = fma2(y.c[1], y.c[1], s2);
+            const float2 s1 = split(s2);
+            float ss = s1.x + s1.y;
 #pragma unroll
-            for (int j = 0; j < 8; j += 4) {
-                const float4 c4 = *reinterpret_cast<const float4*>(c + j);
-                const float4 s4 = *reinterpret_cast<const float4*>(c + p.dim / 2 + j);
-                cs[j] = c4.x, cs[j + 1] = c4.y, cs[j + 2] = c4.z, cs[j + 3] = c4.w;
-                sn[j] = s4.x, sn[j + 1] = s4.y, sn[j + 2] = s4.z, sn[j + 3] = s4.w;
+            for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
+            const float rms = rsqrtf(ss * (1.f / D) + p.eps);
+            const F2 r2 = f2(rms, rms);
+            const Pairs wp = pairs_of<kInter>(wl, wh);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                y.a[j] = mul2(mul2(y.a[j], r2), wp.a[j]);
+                y.c[j] = mul2(mul2(y.c[j], r2), wp.c[j]);
             }
+        }
+        if (turns) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const F2 a = y.a[j], c = y.c[j];
+                y.a[j] = fma2(c, ns[j], mul2(a, cs[j]));
+                y.c[j] = fma2(a, sn[j], mul2(c, cs[j]));
+            }
+        }
+        values_of<kInter>(y, x);
+    };
+
+    for (int h0 = sub; h0 < Hq; h0 += kAppendQ * step) {
+#pragma unroll
+        for (int u = 0; u < kAppendQ; ++u) {
+            const int h = h0 + u * step;
+            if (h >= Hq) break;
+            if (h0 != sub) qi[u] = load(qrow, h);
+            float x[8];
+            turned(qi[u], p.q_norm, x);
+            __nv_bfloat16* out = p.q_out + tok * p.q_out_stride + h * D;
+            *reinterpret_cast<uint2*>(out + at_lo) =
+                make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+            *reinterpret_cast<uint2*>(out + at_hi) =
+                make_uint2(pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
         }
     }
-    // the first half (even values) subtracts its partner's product
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (p.interleaved ? j % 2 == 0 : lane < half) sn[j] = -sn[j];
-    const int partner = turns && !p.interleaved ? (lane < half ? lane + half : lane - half) : lane;
-
-    // head rows of the token: Hq of q, Hkv of k, Hkv of v
-    const int Hkv = p.d.Hkv, all = p.Hq + 2 * Hkv;
-    const __nv_bfloat16* qrow = p.q + tok * p.q_stride + 8 * lane;
-    const __nv_bfloat16* krow = p.k + tok * p.k_stride + 8 * lane;
-    const __nv_bfloat16* vrow = p.v + tok * p.v_stride + 8 * lane;
-    for (int r0 = sub; r0 < all; r0 += kAppendRows * p.per_token) {
-        uint4 in[kAppendRows];
-#pragma unroll
-        for (int u = 0; u < kAppendRows; ++u) {
-            const int r = r0 + u * p.per_token;
-            if (r < all)
-                in[u] = *reinterpret_cast<const uint4*>(
-                    r < p.Hq ? qrow + r * D
-                             : (r < p.Hq + Hkv ? krow + (r - p.Hq) * D : vrow + (r - p.Hq - Hkv) * D));
+    if (at < 0) return;   // no slot: nothing is stored
+    auto store = [&](void* pool, int h, const float x[8], float scale) {
+        const int64_t e = at + h * p.d.head_stride;
+        if (kFp8) {
+            uint8_t* out = static_cast<uint8_t*>(pool) + e;
+            *reinterpret_cast<uint32_t*>(out + at_lo) = e4m3x4(x, scale);
+            *reinterpret_cast<uint32_t*>(out + at_hi) = e4m3x4(x + 4, scale);
+        } else {
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(pool) + e;
+            *reinterpret_cast<uint2*>(out + at_lo) =
+                make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+            *reinterpret_cast<uint2*>(out + at_hi) =
+                make_uint2(pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
         }
-#pragma unroll
-        for (int u = 0; u < kAppendRows; ++u) {
-            const int r = r0 + u * p.per_token;
-            if (r >= all) break;
-            const int kind = r < p.Hq ? 0 : (r < p.Hq + Hkv ? 1 : 2);
-            if (kind > 0 && at < 0) break;  // no slot: this row and the later ones store nothing
-            float x[8];
-            unpack8(in[u], x);
-            const __nv_bfloat16* w = kind == 0 ? p.q_norm : (kind == 1 ? p.k_norm : nullptr);
-            if (w) {
-                float ss = 0.f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-#pragma unroll
-                for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
-                const float rms = rsqrtf(ss * (1.f / D) + p.eps);
-                float wf[8];
-                unpack8(__ldg(reinterpret_cast<const uint4*>(w + 8 * lane)), wf);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = x[j] * rms * wf[j];
-            }
-            if (kind < 2 && p.dim > 0) {
-                float y[8];
-                if (p.interleaved) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) y[j] = x[j ^ 1];
-                } else {
-                    // (a lane past dim is its own partner)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        y[j] = __shfl_sync(mask, x[j], partner, L);
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = turns ? fmaf(y[j], sn[j], x[j] * cs[j]) : x[j];
-            }
-            if (kind == 0) {
-                *reinterpret_cast<uint4*>(p.q_out + tok * p.q_out_stride + r * D + 8 * lane) = pack8(x);
-            } else {
-                const int h = kind == 1 ? r - p.Hq : r - p.Hq - Hkv;
-                const int64_t e = at + h * p.d.head_stride + 8 * lane;
-                void* pool = kind == 1 ? p.K : p.V;
-                if (kFp8) {
-                    const float sc = kind == 1 ? p.k_scale : p.v_scale;
-                    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + e) =
-                        make_uint2(e4m3x4(x, sc), e4m3x4(x + 4, sc));
-                } else {
-                    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(pool) + e) = pack8(x);
-                }
-            }
-        }
+    };
+    for (int h = sub; h < Hkv; h += step) {
+        if (h != sub) ki = load(krow, h), vi = load(vrow, h);
+        float x[8];
+        turned(ki, p.k_norm, x);
+        store(p.K, h, x, p.k_scale);
+        const Pairs v = pairs_of<false>(vi.lo, vi.hi);
+        values_of<false>(v, x);
+        store(p.V, h, x, p.v_scale);
     }
 }
 
@@ -337,9 +394,15 @@ int launch_kv_append(const qmm_kv_cache& c, const void* q, const void* k, const 
         p.interleaved = rope->interleaved;
         p.eps = rope->eps;
     }
-    const int groups = kAppendThreads / (c.D / 8);
+    // lane groups per token: one per head row where the call is small (latency),
+    // else as few as leave kAppendQ q rows, or one k and v row, a group (bytes in
+    // flight)
+    const int groups = kAppendThreads / (c.D / 8), rows = Hq > c.Hkv ? Hq : c.Hkv;
+    const bool small = static_cast<int64_t>(N) * rows <= 4 * 152 * groups;
     p.per_token = 1;
-    while (p.per_token < groups && p.per_token < Hq + 2 * c.Hkv) p.per_token *= 2;
+    while (p.per_token < groups &&
+           (p.per_token * (small ? 1 : kAppendQ) < Hq || p.per_token < c.Hkv))
+        p.per_token *= 2;
     const int tokens = groups / p.per_token;
     cudaLaunchConfig_t cfg = {};
     LaunchAttrs la;
@@ -347,12 +410,13 @@ int launch_kv_append(const qmm_kv_cache& c, const void* q, const void* k, const 
     cfg.gridDim = dim3((N - 1) / tokens + 1, 1, 1);
     cfg.blockDim = dim3(kAppendThreads, 1, 1);
     cfg.stream = static_cast<cudaStream_t>(stream);
-    const bool fp8 = c.dtype == QMM_CACHE_E4M3;
+    const bool fp8 = c.dtype == QMM_CACHE_E4M3, inter = rope && rope->interleaved;
+    auto run = [&](auto kernel) { return static_cast<int>(cudaLaunchKernelEx(&cfg, kernel, p)); };
     if (c.D == 128)
-        return fp8 ? cudaLaunchKernelEx(&cfg, kv_append_kernel<128, true>, p)
-                   : cudaLaunchKernelEx(&cfg, kv_append_kernel<128, false>, p);
-    return fp8 ? cudaLaunchKernelEx(&cfg, kv_append_kernel<64, true>, p)
-               : cudaLaunchKernelEx(&cfg, kv_append_kernel<64, false>, p);
+        return fp8 ? (inter ? run(kv_append_kernel<128, true, true>) : run(kv_append_kernel<128, true, false>))
+                   : (inter ? run(kv_append_kernel<128, false, true>) : run(kv_append_kernel<128, false, false>));
+    return fp8 ? (inter ? run(kv_append_kernel<64, true, true>) : run(kv_append_kernel<64, true, false>))
+               : (inter ? run(kv_append_kernel<64, false, true>) : run(kv_append_kernel<64, false, false>));
 }
 
 int launch_tree_accept(const qmm_kv_cache* caches, int n, const int* tokens, const int* targets,
