@@ -26,7 +26,7 @@
 namespace qmm {
 namespace {
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;
 constexpr int kAppendQ = 4;   // q rows whose loads a lane has in flight, beside a k and a v row
 
 struct AppendParams {
@@ -112,7 +112,7 @@ __device__ __forceinline__ uint32_t e4m3x4(const float* x, float scale) {
 }
 
 template <int D, bool kFp8, bool kInter>
-__global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 8) kv_append_kernel(const AppendParams p) {
     constexpr int L = D / 8;                        // lanes of a head row
     constexpr int kGroups = kAppendThreads / L;     // lane groups of the block
     pdl_trigger();
@@ -140,8 +140,8 @@ __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const Appe
     };
     auto load = [&](const __nv_bfloat16* row, int h) {
         In x;
-        x.lo = __ldcs(reinterpret_cast<const uint2*>(row + h * D + at_lo));
-        x.hi = __ldcs(reinterpret_cast<const uint2*>(row + h * D + at_hi));
+        x.lo = __ldg(reinterpret_cast<const uint2*>(row + h * D + at_lo));
+        x.hi = __ldg(reinterpret_cast<const uint2*>(row + h * D + at_hi));
         return x;
     };
     In qi[kAppendQ], ki, vi;
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const Appe
 // ---- accepted path -----------------------------------------------------------
 
 constexpr int kAcceptThreads = 256;
-constexpr int kAcceptRows = 4;  // rows a lane group has in flight
+constexpr int kAcceptRows = 8;  // rows a lane group has in flight
 
 struct AcceptParams {
     PagedDims d;
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kAcceptThreads)
     tree_accept_kernel(const __grid_constant__ AcceptParams p) {
     __shared__ int tok[kMaxTree], tgt[kMaxTree], par[kMaxTree], path[kMaxTree];
     __shared__ int64_t src[kMaxTree], dst[kMaxTree];  // element offsets, -1: no page
-    __shared__ int count_s;
+    __shared__ int count_s, moves_s;
     const int tid = threadIdx.x, b = blockIdx.y;
     pdl_trigger();
     pdl_wait();
@@ -330,32 +330,43 @@ __global__ void __launch_bounds__(kAcceptThreads)
         // (an int holds it: len <= cap, and cap + 256 < 2^31)
         if (p.new_lens && tid == 0) p.new_lens[b] = len + count;
     }
-    for (int j = tid; j < count; j += kAcceptThreads) {
-        src[j] = slot_offset(p.d, b, len + path[j]);
-        dst[j] = slot_offset(p.d, b, len + j);
+    // the rows that move, in order
+    if (tid < 32) {
+        int moves = 0;
+        for (int j0 = 0; j0 < count; j0 += 32) {
+            const int j = j0 + tid;
+            int64_t from = -1, to = -1;
+            if (j < count && path[j] != j) {
+                from = slot_offset(p.d, b, len + path[j]);
+                to = slot_offset(p.d, b, len + j);
+            }
+            const bool moved = from >= 0 && to >= 0;
+            const uint32_t bits = __ballot_sync(0xffffffffu, moved);
+            if (moved) {
+                const int at = moves + __popc(bits & ((1u << tid) - 1u));
+                src[at] = from;
+                dst[at] = to;
+            }
+            moves += __popc(bits);
+        }
+        if (tid == 0) moves_s = moves;
     }
     __syncthreads();
+    const int moves = moves_s;
     const int lanes = p.row_bytes / 16;
     const int lane = tid % lanes;
     const int cols = 2 * p.n * p.d.Hkv;
     const int last = min(cols, (static_cast<int>(blockIdx.x) + 1) * p.per_block);
     for (int c = blockIdx.x * p.per_block + tid / lanes; c < last; c += kAcceptThreads / lanes) {
-        uint8_t* pool = p.pools[c / p.d.Hkv];
-        const int64_t head = (c % p.d.Hkv) * p.d.head_stride;
-        for (int j0 = 0; j0 < count; j0 += kAcceptRows) {
+        uint8_t* pool = p.pools[c / p.d.Hkv] + (c % p.d.Hkv) * p.d.head_stride * p.elem + 16 * lane;
+        for (int j0 = 0; j0 < moves; j0 += kAcceptRows) {
             uint4 x[kAcceptRows];
 #pragma unroll
-            for (int u = 0; u < kAcceptRows; ++u) {
-                const int j = j0 + u;
-                if (j < count && path[j] != j && src[j] >= 0 && dst[j] >= 0)
-                    x[u] = *reinterpret_cast<const uint4*>(pool + (src[j] + head) * p.elem + 16 * lane);
-            }
+            for (int u = 0; u < kAcceptRows; ++u)
+                if (j0 + u < moves) x[u] = *reinterpret_cast<const uint4*>(pool + src[j0 + u] * p.elem);
 #pragma unroll
-            for (int u = 0; u < kAcceptRows; ++u) {
-                const int j = j0 + u;
-                if (j < count && path[j] != j && src[j] >= 0 && dst[j] >= 0)
-                    *reinterpret_cast<uint4*>(pool + (dst[j] + head) * p.elem + 16 * lane) = x[u];
-            }
+            for (int u = 0; u < kAcceptRows; ++u)
+                if (j0 + u < moves) *reinterpret_cast<uint4*>(pool + dst[j0 + u] * p.elem) = x[u];
         }
     }
 }
@@ -443,9 +454,12 @@ int launch_tree_accept(const qmm_kv_cache* caches, int n, const int* tokens, con
         p.pools[2 * i] = static_cast<uint8_t*>(caches[i].K);
         p.pools[2 * i + 1] = static_cast<uint8_t*>(caches[i].V);
     }
-    // one column per lane group where that leaves the grid within 64K blocks
+    // columns per block: a block's walk and table look-ups take longer than its
+    // moves, so the blocks fill the SMs once (4 of them each) and no more
     const int64_t cols = static_cast<int64_t>(2) * n * c.Hkv;
-    p.per_block = kAcceptThreads / (p.row_bytes / 16);
+    const int groups = kAcceptThreads / (p.row_bytes / 16);
+    const int64_t share = (cols * c.B - 1) / (4 * 152) + 1;
+    p.per_block = static_cast<int>((share - 1) / groups + 1) * groups;
     while ((cols - 1) / p.per_block + 1 > 65535) p.per_block *= 2;
     cudaLaunchConfig_t cfg = {};
     LaunchAttrs la;
