@@ -1113,6 +1113,23 @@ int qmm_decode_attention(const void* q, const void* K, const void* V, const int*
 
 // ---- paged KV cache ----
 
+// check_device() and the SM count, asked of the runtime once per thread and
+// device: the calls below are short enough for its queries to show (0.5 us of
+// 3).
+static int device_ready(int* sms) {
+    thread_local int known = -1, known_sms = 0;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return QMM_ENODEV;
+    if (dev != known) {
+        int rc = check_device();
+        if (rc == QMM_OK) rc = device_sms(&known_sms);
+        if (rc != QMM_OK) return rc;
+        known = dev;
+    }
+    if (sms) *sms = known_sms;
+    return QMM_OK;
+}
+
 // A stride of a dimension of `extent` rows, in elements of e bytes: rows do
 // not overlap, start on 16 bytes, and stay within a tensor map's range.
 static bool stride_ok(int64_t stride, int extent, int D, int e) {
@@ -1172,7 +1189,7 @@ int qmm_kv_append(const qmm_kv_cache* cache, const void* q, const void* k, const
         (rope && (!aligned(rope->cos_sin, 16) || !aligned(rope->q_norm, 16) ||
                   !aligned(rope->k_norm, 16))))
         return QMM_EALIGN;
-    rc = check_device();
+    rc = device_ready(nullptr);
     if (rc != QMM_OK) return rc;
     return launched(qmm::launch_kv_append(*cache, q, k, v, q_out, N, Hq, q_stride, k_stride,
                                           v_stride, q_out_stride, cu, positions, rope, stream));
@@ -1210,10 +1227,8 @@ int qmm_tree_attention(const qmm_kv_cache* cache, const void* q, int64_t q_strid
     if (q_stride % 8 || q_stride < static_cast<int64_t>(Hq) * cache->D) return QMM_ESHAPE;
     if (!aligned(q, 16) || !aligned(O, 16) || !aligned(cu, 4) || !aligned(parents, 4))
         return QMM_EALIGN;
-    rc = check_device();
-    if (rc != QMM_OK) return rc;
     int sms = 0;
-    rc = device_sms(&sms);
+    rc = device_ready(&sms);
     if (rc != QMM_OK) return rc;
     if (!workspace ||
         ws_bytes < qmm::tree_attention_workspace(cache->D, T * (Hq / cache->Hkv), sms))
@@ -1248,7 +1263,7 @@ int qmm_tree_accept(const qmm_kv_cache* caches, int n, const int* tokens, const 
     if (!aligned(tokens, 4) || !aligned(targets, 4) || !aligned(parents, 4) || !aligned(cu, 4) ||
         !aligned(path, 4) || !aligned(count, 4) || !aligned(next, 4) || !aligned(new_lens, 4))
         return QMM_EALIGN;
-    rc = check_device();
+    rc = device_ready(nullptr);
     if (rc != QMM_OK) return rc;
     for (int i = 0; i < n && rc == QMM_OK; i += qmm::kMaxAcceptCaches)
         rc = launched(qmm::launch_tree_accept(caches + i, std::min(n - i, qmm::kMaxAcceptCaches),

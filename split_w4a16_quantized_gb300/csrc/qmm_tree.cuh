@@ -115,8 +115,44 @@ struct RunShared {   // (s and at hold nothing where b < 0)
     Seq s;
     int at, b;
 };
+// Units of the whole batch and of the sequences before b; of up to 32
+// sequences: a lane's sequence each, every warp for itself, no barrier.
+__device__ __forceinline__ long long warp_scan(long long v, long long* total) {
+    const int lane = threadIdx.x & 31;
+    long long x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    *total = __shfl_sync(0xffffffffu, x, 31);
+    return x - v;
+}
+
 template <int kN>
 __device__ __forceinline__ Run find_run(const TreeParams& p, RunShared& sh) {
+    Run r;
+    if (p.d.B <= 32) {
+        const int lane = threadIdx.x & 31;
+        Seq s = {};
+        if (lane < p.d.B) s = sequence(p, lane);
+        const int mine = lane < p.d.B ? units_of(p, s) : 0;
+        long long all;
+        const long long before = warp_scan(mine, &all);
+        const long long len = run_length(p, all), start = len * blockIdx.x;
+        const uint32_t owner = __ballot_sync(0xffffffffu, start >= before && start < before + mine);
+        r.b = owner ? __ffs(owner) - 1 : -1;
+        const int from = owner ? r.b : 0;
+        r.at = __shfl_sync(0xffffffffu, static_cast<int>(start - before), from);
+        r.s.first = __shfl_sync(0xffffffffu, s.first, from);
+        r.s.n = __shfl_sync(0xffffffffu, s.n, from);
+        r.s.len = __shfl_sync(0xffffffffu, s.len, from);
+        r.s.total = __shfl_sync(0xffffffffu, s.total, from);
+        r.s.tiles = __shfl_sync(0xffffffffu, s.tiles, from);
+        r.s.row_tiles = __shfl_sync(0xffffffffu, s.row_tiles, from);
+        r.left = r.b < 0 ? 0 : static_cast<int>(all - start < len ? all - start : len);
+        return r;
+    }
     const int per = (p.d.B + kN - 1) / kN;
     const int b0 = min(p.d.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.d.B, b0 + per);
     long long mine = 0, all;
@@ -145,7 +181,6 @@ __device__ __forceinline__ Run find_run(const TreeParams& p, RunShared& sh) {
         }
     }
     __syncthreads();
-    Run r;
     r.b = sh.b;
     r.at = sh.at;
     r.s = sh.s;

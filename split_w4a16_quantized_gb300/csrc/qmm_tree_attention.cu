@@ -567,14 +567,21 @@ __global__ void __launch_bounds__(kMergeThreads)
     const int rows = min(1 << p.row_shift, s.n * p.QG - row0);
     int c0 = 0, c1 = 0;
     if (rt < s.row_tiles && chunk * kMergeRows < rows) {
-        long long mine = 0, upto = 0, all, before;
-        for (int i = threadIdx.x; i < p.d.B; i += kMergeThreads) {
-            const int u = units_of(p, sequence(p, i));
-            mine += u;
-            if (i < b) upto += u;
+        long long all, before;
+        if (p.d.B <= 32) {
+            const int lane = threadIdx.x & 31;
+            const long long mine = lane < p.d.B ? units_of(p, sequence(p, lane)) : 0;
+            before = __shfl_sync(0xffffffffu, warp_scan(mine, &all), b);
+        } else {
+            long long mine = 0, upto = 0;
+            for (int i = threadIdx.x; i < p.d.B; i += kMergeThreads) {
+                const int u = units_of(p, sequence(p, i));
+                mine += u;
+                if (i < b) upto += u;
+            }
+            block_scan<kMergeThreads>(mine, red[0], &all);
+            block_scan<kMergeThreads>(upto, red[1], &before);
         }
-        block_scan<kMergeThreads>(mine, red[0], &all);
-        block_scan<kMergeThreads>(upto, red[1], &before);
         const long long len = run_length(p, all);
         const int units = item_units(p, s);
         const long long start = before + static_cast<long long>(g * s.row_tiles + rt) * units;

@@ -727,6 +727,7 @@ def kv_caches(caches) -> "ctypes.Array":
     arr.device = caches[0].device
     if any(c.device != arr.device for c in caches):
         raise ValueError("the caches are on different devices")
+    arr.n, arr.B, arr.ref = len(caches), caches[0].B, ctypes.addressof(arr)
     return arr
 
 
@@ -741,40 +742,56 @@ def rope(cos_sin: torch.Tensor | None = None, interleaved: bool = False,
           (k_norm, _BF16, "k_norm"))]
     r = qmm_rope(p[0], p[1], p[2], rows, dim, int(bool(interleaved)), float(eps))
     r.tensors = (cos_sin, q_norm, k_norm)
-    r.head_dims = {t.numel() for t in (q_norm, k_norm) if t is not None}
-    r.devices = {t.get_device() for t in r.tensors if t is not None}
+    dims = {t.numel() for t in (q_norm, k_norm) if t is not None}
+    devices = {t.get_device() for t in r.tensors if t is not None}
+    if len(dims) > 1 or len(devices) > 1:
+        raise ValueError("norm weights of different lengths, or tensors on different devices")
+    r.D, r.device = max(dims, default=0), max(devices, default=-1)
     r.ref = ctypes.addressof(r)
     return r
 
 
-def _on(device: int, *tensors):
-    """Every tensor on `device`, and `device` the current one: the kernels run
-    there."""
+def _elsewhere(device: int, tensors):
+    """Report the tensor that is not on `device` (or is none), or that `device`
+    is not the current one."""
     for t in tensors:
+        if t is not None and not isinstance(t, torch.Tensor):
+            raise TypeError("expected CUDA tensors")
         if t is not None and t.get_device() != device:
+            if not t.is_cuda:
+                raise TypeError("expected CUDA tensors")
             raise ValueError("a tensor is not on the cache's device")
-    if _cur_device is not None and torch.cuda.is_initialized() and _cur_device() != device:
-        raise ValueError("the cache's device is not the current one")
+    raise ValueError("the cache's device is not the current one")
 
 
-def _heads(t: torch.Tensor, D: int, name: str) -> int:
+def _current(device: int) -> bool:
+    """Whether `device`, where a tensor was found, is the current one: the
+    kernels run there."""
+    return (_cur_device or torch.cuda.current_device)() == device
+
+
+def _stream_on(device: int, stream):
+    """_stream for the current device, which is `device` and in use."""
+    return _raw_stream(device) if stream is None and _raw_stream is not None else _stream(stream)
+
+
+def _heads(t: torch.Tensor, N: int, H: int, D: int, name: str) -> int:
     """The token stride of [N, H, D] bf16 rows whose heads are contiguous."""
-    if t.dtype != torch.bfloat16 or not t.is_cuda:
-        raise TypeError("%s must be a bfloat16 CUDA tensor" % name)
     s0, s1, s2 = t.stride()
-    H = t.shape[1]
+    if t.dtype is not torch.bfloat16:
+        raise TypeError("%s must be bfloat16" % name)
     if s2 != 1 or (s1 != D and H > 1):
         raise ValueError("%s: the heads of a token must be contiguous" % name)
-    return s0 if t.shape[0] > 1 else H * D
+    return s0 if N > 1 else H * D
 
 
-def _tokens(t, N: int, name: str):
-    """Pointer of an optional int32 vector of N elements."""
-    if t is None:
-        return None
-    if t.numel() != N:
-        raise ValueError("%s must have %d elements" % (name, N))
-    return _ptr(t, _INT32, name)
+def _ints(t: torch.Tensor, N: int, name: str) -> int:
+    """Pointer of an int32 vector of N elements."""
+    if t.dtype is not torch.int32:
+        raise TypeError("%s must be int32" % name)
+    if t.numel() != N or not t.is_contiguous():
+        raise ValueError("%s must be contiguous, of %d elements" % (name, N))
+    return t.data_ptr()
 
 
 def qmm_kv_append(cache: qmm_kv_cache, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
@@ -785,28 +802,35 @@ def qmm_kv_append(cache: qmm_kv_cache, q: torch.Tensor | None, k: torch.Tensor, 
     strides free, so views of one fused projection do) behind the cached
     tokens.  q may be None (only append); q_out may be q.  positions int32 [N]
     and cu int32 [B + 1]: see qmm.h."""
-    N, Hkv, D = k.shape
-    if Hkv != cache.Hkv or D != cache.D or v.shape != k.shape:
+    device = cache.device
+    if not (k.get_device() == device == v.get_device() and _current(device) and
+            (q is None or q.get_device() == device == q_out.get_device()) and
+            (positions is None or positions.get_device() == device) and
+            (cu is None or cu.get_device() == device)):
+        _elsewhere(device, (q, k, v, q_out, positions, cu))
+    shape = k.shape
+    N, Hkv, D = shape
+    if Hkv != cache.Hkv or D != cache.D or v.shape != shape:
         raise ValueError("qmm_kv_append: inconsistent shapes")
-    Hq, qs, qos, qp, qop = 0, 0, 0, None, None
+    Hq = qs = qos = 0
+    qp = qop = None
     if q is not None:
-        Hq = q.shape[1]
-        if q_out is None or tuple(q.shape) != (N, Hq, D) or q_out.shape != q.shape:
+        shape = q.shape
+        Hq = shape[1]
+        if shape != (N, Hq, D) or q_out.shape != shape:
             raise ValueError("qmm_kv_append: inconsistent shapes")
-        qs, qos = _heads(q, D, "q"), _heads(q_out, D, "q_out")
+        qs, qos = _heads(q, N, Hq, D, "q"), _heads(q_out, N, Hq, D, "q_out")
         qp, qop = q.data_ptr(), q_out.data_ptr()
     r = None
     if rope is not None:
-        if any(d != D for d in rope.head_dims):
-            raise ValueError("qmm_kv_append: norm weights must have D elements")
-        if any(d != cache.device for d in rope.devices):
-            raise ValueError("a tensor is not on the cache's device")
+        if rope.D not in (0, D) or rope.device not in (-1, device):
+            raise ValueError("qmm_kv_append: norm weights must have D elements, and the rope's "
+                             "tensors the cache's device")
         r = rope.ref
-    _on(cache.device, q, k, v, q_out, positions, cu)
     rc = (_lib or lib()).qmm_kv_append(
-        cache.ref, qp, k.data_ptr(), v.data_ptr(), qop, N, Hq, qs, _heads(k, D, "k"),
-        _heads(v, D, "v"), qos, _tokens(cu, cache.B + 1, "cu"), _tokens(positions, N, "positions"),
-        r, _stream(stream))
+        cache.ref, qp, k.data_ptr(), v.data_ptr(), qop, N, Hq, qs, _heads(k, N, Hkv, D, "k"),
+        _heads(v, N, Hkv, D, "v"), qos, None if cu is None else _ints(cu, cache.B + 1, "cu"),
+        None if positions is None else _ints(positions, N, "positions"), r, _stream_on(device, stream))
     if rc != QMM_OK:
         raise QmmError(rc, "qmm_kv_append")
 
@@ -823,17 +847,26 @@ def qmm_tree_attention(cache: qmm_kv_cache, q: torch.Tensor, O: torch.Tensor, T:
     """O [N, Hq, D] = attention of the drafted tokens q [N, Hq, D] (at most T a
     sequence, their keys already appended) over the cache; parents int32 [N]
     gives the trees, None a chain (see qmm.h)."""
-    N, Hq, D = q.shape
-    if D != cache.D or O.shape != q.shape:
+    device = cache.device
+    if not (q.get_device() == device == O.get_device() and _current(device) and
+            (parents is None or parents.get_device() == device) and
+            (cu is None or cu.get_device() == device) and
+            (workspace is None or workspace.get_device() == device)):
+        _elsewhere(device, (q, O, parents, cu, workspace))
+    shape = q.shape
+    N, Hq, D = shape
+    if D != cache.D or O.shape != shape:
         raise ValueError("qmm_tree_attention: inconsistent shapes")
     ws, ws_bytes = None, 0
     if workspace is not None:
-        ws, ws_bytes = _ptr(workspace, (workspace.dtype,), "workspace"), workspace.nbytes
-    _on(cache.device, q, O, parents, cu, workspace)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
     rc = (_lib or lib()).qmm_tree_attention(
-        cache.ref, q.data_ptr(), _heads(q, D, "q"), _ptr(O, _BF16, "O"), N, T, Hq,
-        _tokens(cu, cache.B + 1, "cu"), _tokens(parents, N, "parents"), scale, ws, ws_bytes,
-        _stream(stream))
+        cache.ref, q.data_ptr(), _heads(q, N, Hq, D, "q"), _ptr(O, _BF16, "O"), N, T, Hq,
+        None if cu is None else _ints(cu, cache.B + 1, "cu"),
+        None if parents is None else _ints(parents, N, "parents"), scale, ws, ws_bytes,
+        _stream_on(device, stream))
     if rc != QMM_OK:
         raise QmmError(rc, "qmm_tree_attention")
 
@@ -845,15 +878,21 @@ def qmm_tree_accept(caches, tokens: torch.Tensor, targets: torch.Tensor, T: int,
     """Follow targets down the drafted trees (tokens, parents int32 [N]) and
     move the accepted rows in every cache of `caches` (kv_caches()).  path
     int32 [B, T], count, next and new_lens int32 [B] (see qmm.h)."""
-    N, B = tokens.numel(), caches[0].B
-    _on(caches.device, tokens, targets, path, count, next, new_lens, parents, cu)
-    if path.numel() != B * T:
-        raise ValueError("qmm_tree_accept: path must be [B, T]")
+    device, B = caches.device, caches.B
+    if not (tokens.get_device() == device == targets.get_device() and _current(device) and
+            path.get_device() == device == count.get_device() and
+            (next is None or next.get_device() == device) and
+            (new_lens is None or new_lens.get_device() == device) and
+            (parents is None or parents.get_device() == device) and
+            (cu is None or cu.get_device() == device)):
+        _elsewhere(device, (tokens, targets, path, count, next, new_lens, parents, cu))
+    N = tokens.numel()
     rc = (_lib or lib()).qmm_tree_accept(
-        caches, len(caches), _ptr(tokens, _INT32, "tokens"), _tokens(targets, N, "targets"),
-        _tokens(parents, N, "parents"), _tokens(cu, B + 1, "cu"), N, T, _ptr(path, _INT32, "path"),
-        _tokens(count, B, "count"), _tokens(next, B, "next"), _tokens(new_lens, B, "new_lens"),
-        _stream(stream))
+        caches.ref, caches.n, _ints(tokens, N, "tokens"), _ints(targets, N, "targets"),
+        None if parents is None else _ints(parents, N, "parents"),
+        None if cu is None else _ints(cu, B + 1, "cu"), N, T, _ints(path, B * T, "path"),
+        _ints(count, B, "count"), None if next is None else _ints(next, B, "next"),
+        None if new_lens is None else _ints(new_lens, B, "new_lens"), _stream_on(device, stream))
     if rc != QMM_OK:
         raise QmmError(rc, "qmm_tree_accept")
 
