@@ -46,6 +46,20 @@ __device__ __forceinline__ int row_node(const TreeParams& p, int r) {
     return static_cast<int>((static_cast<uint64_t>(r) * p.qg_inv) >> 22);
 }
 
+// Ask for the lengths and the page table while the kernels before this one may
+// still run: a CTA reads them one after the other before its first copy, a trip
+// to HBM each.  (Only L2 is touched: what those kernels write is seen.)
+__device__ __forceinline__ void prefetch_plan(const TreeParams& p, int tid, int threads) {
+    const int64_t at = (static_cast<int64_t>(blockIdx.x) * threads + tid) * 32;
+    const int64_t table = static_cast<int64_t>(p.d.B) * p.d.max_pages;
+    if (at < table) prefetch_l2(p.d.table + at);
+    if (at < p.d.B) {
+        prefetch_l2(p.d.lens + at);
+        if (p.cu) prefetch_l2(p.cu + at);
+    }
+    if (p.parents && at < p.N) prefetch_l2(p.parents + at);
+}
+
 // ---- work split ----------------------------------------------------------------
 
 struct Seq {
@@ -340,9 +354,9 @@ __device__ __forceinline__ float fast_exp2(float x) {
 }
 
 // One launch of the tcgen05 kernel (qmm_tree_attention_tc.cu); the merge
-// kernel is the caller's.  Tiles of 64 positions for items of up to 128 rows
-// (row_shift 7, two CTAs per SM), of 128 positions for 256 (8, one).
-constexpr int kTcTileShift1 = 6, kTcTileShift2 = 7;
+// kernel is the caller's.  Items of up to 128 rows (row_shift 7, two CTAs per
+// SM) or 256 (8, one).
+constexpr int kTcTileShift = 6;
 int launch_tree_tc(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int D,
                    bool fp8, cudaStream_t st);
 

@@ -702,8 +702,8 @@ struct Variant {
 };
 Variant variant(int rows) {
     if (rows <= kRows) return {false, 4, 6, kCtasPerSm, 2, 1};
-    if (rows <= 128) return {true, 7, kTcTileShift1, 2, 6, 4};
-    return {true, 8, kTcTileShift2, 1, 6, 3};
+    if (rows <= 128) return {true, 7, kTcTileShift, 2, 6, 4};
+    return {true, 8, kTcTileShift, 1, 6, 4};
 }
 
 }  // namespace

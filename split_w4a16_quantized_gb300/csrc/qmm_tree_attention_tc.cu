@@ -3,32 +3,29 @@
 //
 // The formulas and the work split are those of qmm_tree_attention.cu.  Here a
 // work item is up to 128 or 256 rows, the MMA's M once or twice, and a tile is
-// 64 or 128 positions:
-//   S [128 x tile] = Q [128 x D] K^T    Q and the K tile in shared memory
-//   O [128 x D]   += P [128 x tile] V   P in tensor memory, V in shared memory
+// 64 positions:
+//   S [128 x 64] = Q [128 x D] K^T    Q and the K tile in shared memory
+//   O [128 x D] += P [128 x 64] V     P in tensor memory, V in shared memory
 // with S and O accumulated in tensor memory.  Rows past the item's are computed
-// and dropped: at 128 rows a tile's products take about half the time its K and
-// V take from HBM, so padding costs little where there are few rows.
+// and dropped: at 128 rows a tile's products (630 clocks, D = 128) take half the
+// time its K and V take from HBM, so padding costs little where there are few
+// rows.
 //
 // Roles of a CTA:
 //   warp 0      copies: K and V tiles into a ring each
 //   warp 1      issues the MMAs and owns the tensor memory
 //   warps 2-3   bring the next item's q
-//   softmax groups of 128 threads, a thread a row
+//   one or two softmax groups of 128 threads, a thread a row
 //   E4M3 cache: four warps that turn V tiles into F16
-// Two buffers of S keep the tensor cores and the exponentials busy at the same
-// time: while a group turns one S into P, the products of the other run.  P
+// A group has two buffers of S: while it turns one into P, the products of the
+// other run, and with them the 480 clocks an MMA takes to be seen as done.  P
 // overwrites S in place (BF16 or F16 in half the columns).
-//   up to 128 rows: one group; two CTAs per SM, tiles of 64 positions, the
-//     buffers take the tiles in turn.   ... P0 V(i), Q K(i+2) | P1 V(i+1), ...
-//     Two CTAs, because each item ends with a few thousand clocks in which its
-//     last products drain and its output is written; the other CTA's products
-//     and copies run on meanwhile.
-//   up to 256 rows: two groups with half of the rows and an O each; one CTA per
-//     SM, tiles of 128 positions that both groups use.
-//                                       ... P0 V(i), Q0 K(i+1) | P1 V(i), ...
-//     (An MMA takes the same time for N = 64 as for 128, so that tile has half
-//     of the score MMAs; two such CTAs do not fit an SM.)
+//   MMA order of a group:  ... P(i) V(i), Q K(i+2) | P(i+1) V(i+1), Q K(i+3) ...
+//   up to 128 rows: one group, two CTAs per SM, because each item ends with a few
+//     thousand clocks in which its last products drain and its output is
+//     written; the other CTA's products and copies run on meanwhile.
+//   up to 256 rows: two groups with half of the rows each, which use the same K
+//     and V tiles; one CTA per SM.
 //
 // An item's first scores need only its q and K: they are issued right behind
 // the last products of the item before, while the group still writes that
@@ -59,16 +56,14 @@ namespace qmm {
 namespace {
 
 constexpr int kConvWarps = 4;
+constexpr int kTile = 1 << kTcTileShift;   // positions
 constexpr int kMaxSlots = 8;        // of one ring
-constexpr int kConvSlots = 2;
 constexpr int kHave = 32;           // tiles whose page bits are kept
 constexpr float kLazy = 8.f;        // log2 units a score may pass the reference by
 
 // kGroups: softmax groups (1: two CTAs per SM, up to 128 rows; 2: one CTA, 256).
 template <int D, bool kFp8, int kGroups>
 struct Tc {
-    static constexpr int TILE_SHIFT = kGroups == 1 ? kTcTileShift1 : kTcTileShift2;
-    static constexpr int TILE = 1 << TILE_SHIFT;             // positions
     static constexpr int CTAS_PER_SM = kGroups == 1 ? 2 : 1;
     static constexpr int SOFTMAX0 = 4, CONV0 = 4 + 4 * kGroups;   // first warps
     static constexpr int WARPS = CONV0 + (kFp8 ? kConvWarps : 0);
@@ -84,22 +79,25 @@ struct Tc {
     static constexpr int ROW = D * (kFp8 ? 1 : 2);           // bytes of a cache row
     static constexpr int BOX = ROW < 128 ? ROW : 128;        // row bytes of one copy
     static constexpr int BOXES = ROW / BOX;
-    static constexpr int SLOT = TILE * ROW;                  // a copied tile
+    static constexpr int SLOT = kTile * ROW;                 // a copied tile
     static constexpr int Q = 128 * D * 2;                    // a group's Q: BF16, or two E4M3 terms
-    static constexpr int CONV = TILE * D * 2;                // a converted V tile
-    // tensor memory: S/P buffers, then an O of each group
-    static constexpr uint32_t COLS = 256 * kGroups, COL_O = 2 * TILE;
-    static_assert(2 * TILE + kGroups * D <= static_cast<int>(COLS), "tensor memory");
+    static constexpr int CONV = kTile * D * 2;               // a converted V tile
+    // one converted tile where two CTAs share the SM: the next is converted
+    // while the group's softmax runs, and the ring is short
+    static constexpr int CONV_SLOTS = kFp8 ? kGroups : 0;
+    // tensor memory: two S/P buffers of each group, then an O of each
+    static constexpr uint32_t COLS = 256 * kGroups, COL_O = 2 * kTile * kGroups;
+    static_assert(kGroups * (2 * kTile + D) <= static_cast<int>(COLS), "tensor memory");
 };
 
 template <int kGroups>
 struct TcSmem {
     uint64_t kfull[kMaxSlots], kempty[kMaxSlots], vfull[kMaxSlots], vempty[kMaxSlots];
-    uint64_t cfull[kConvSlots], cempty[kConvSlots];
-    uint64_t sfull[2];                  // a buffer's next S is there
-    uint64_t pready[2];                 // its P is, and O may take the product
-    uint64_t pvdone;                    // (one group) a product with V has ended
-    uint64_t ofull[2];                  // a group's O is complete
+    uint64_t cfull[2], cempty[2];
+    uint64_t sfull[2 * kGroups];        // a buffer's next S is there
+    uint64_t pready[2 * kGroups];       // its P is, and O may take the product
+    uint64_t pvdone[kGroups];           // a group's product with V has ended
+    uint64_t ofull[kGroups];            // a group's O is complete
     uint64_t qready, qfree;             // an item's q is there; its products have read it
     uint64_t odone;                     // an item's O has been read by all
     uint64_t drained;                   // abort: every MMA issued has ended
@@ -230,15 +228,13 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                    const __grid_constant__ CUtensorMap vmap, const __grid_constant__ TreeParams p,
                    const Layout lay) {
     using C = Tc<D, kFp8, kGroups>;
-    constexpr int kTile = C::TILE;
-    constexpr bool kOne = kGroups == 1;
     extern __shared__ uint8_t tree_tc_smem_raw[];
     uint8_t* base_s = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(tree_tc_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     TcSmem<kGroups>& sm = *reinterpret_cast<TcSmem<kGroups>*>(base_s);
     uint8_t* q_s = base_s + kSmemHead<kGroups>;
     uint8_t* conv_s = q_s + kGroups * C::Q;
-    uint8_t* k_s = conv_s + (kFp8 ? kConvSlots * C::CONV : 0);
+    uint8_t* k_s = conv_s + (C::CONV_SLOTS * C::CONV);
     uint8_t* v_s = k_s + lay.k_slots * C::SLOT;
     volatile int* abort = &sm.abort;
 
@@ -251,16 +247,18 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
             mbar_init(&sm.vfull[i], 1);
             mbar_init(&sm.vempty[i], kFp8 ? kConvWarps : 1);
         }
-        for (int i = 0; i < kConvSlots; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.cfull[i], kConvWarps);
             mbar_init(&sm.cempty[i], 1);
         }
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < 2 * kGroups; ++s) {
             mbar_init(&sm.sfull[s], 2);    // the commit, and the issuing thread
             mbar_init(&sm.pready[s], 4);
-            mbar_init(&sm.ofull[s], 1);
         }
-        mbar_init(&sm.pvdone, 1);
+        for (int g = 0; g < kGroups; ++g) {
+            mbar_init(&sm.pvdone[g], 1);
+            mbar_init(&sm.ofull[g], 1);
+        }
         mbar_init(&sm.qready, 2);
         mbar_init(&sm.qfree, 1);
         mbar_init(&sm.odone, 4 * kGroups);
@@ -269,6 +267,7 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
         tma_prefetch_map(&kmap);
         tma_prefetch_map(&vmap);
     }
+    prefetch_plan(p, tid, C::THREADS);
     // Tensor memory is taken after the kernels before this one have ended, and
     // the next may start only once it is taken: a CTA that holds tensor memory
     // never waits for one that still needs it.
@@ -344,13 +343,14 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
             uint64_t* vfull = kFp8 ? sm.cfull : sm.vfull;
             uint64_t* vempty = kFp8 ? sm.cempty : sm.vempty;
             constexpr int VSLOT = kFp8 ? C::CONV : C::SLOT;
-            const int v_slots = kFp8 ? kConvSlots : lay.v_slots;
+            const int v_slots = kFp8 ? C::CONV_SLOTS : lay.v_slots;
             Cursor kc, vc;
             int nq = 0;                     // Q's taken
-            uint32_t pphase = 0;            // phase of each buffer's P, a bit each
+            uint32_t pphase = 0;            // phase of the P of buffers 0 and 1, a bit each
             bool go = true;
-            // S of buffer s from group g's rows and the K tile at kc
-            auto qk = [&](int s, int g) {
+            // S of group g's buffer `odd` from its rows and the K tile at kc
+            auto qk = [&](int odd, int g) {
+                const int s = 2 * g + odd;
                 const uint64_t a = q_desc + (C::Q >> 4) * g;
                 const uint64_t b = k_desc + static_cast<uint32_t>(kc.slot * C::SLOT >> 4);
                 if (kFp8) {
@@ -373,8 +373,9 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                 // copy warp's page bits: hand that on
                 mbar_arrive(&sm.sfull[s]);
             };
-            // O of group g (+)= P of buffer s times the V tile at vc
-            auto pv = [&](int s, int g, bool first) {
+            // O of group g (+)= P of its buffer times the V tile at vc
+            auto pv = [&](int odd, int g, bool first) {
+                const int s = 2 * g + odd;
                 const uint64_t b = v_desc + static_cast<uint32_t>(vc.slot * VSLOT >> 4);
 #pragma unroll
                 for (int k = 0; k < kTile / 16; ++k)
@@ -385,14 +386,14 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                 const int nt = x.t1 - x.t0;
                 if (!(go = waits(&sm.qready, nq & 1))) break;
                 // the first S of each buffer
-                for (int i = 0; i < (kOne ? min(nt, 2) : 1); ++i) {
+                for (int i = 0; i < min(nt, 2); ++i) {
                     if (!(go = waits(&sm.kfull[kc.slot], kc.phase))) break;
                     tc_fence_after();
                     if (elect_one()) {
-                        qk(i, 0);
-                        if (!kOne) qk(1, 1);
+#pragma unroll
+                        for (int g = 0; g < kGroups; ++g) qk(i, g);
                         umma_commit(&sm.kempty[kc.slot]);
-                        if (i + 1 == (kOne ? nt : 1) && (kOne || nt == 1)) umma_commit(&sm.qfree);
+                        if (i + 1 == nt) umma_commit(&sm.qfree);
                     }
                     __syncwarp();
                     kc.next(lay.k_slots);
@@ -401,33 +402,32 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                 if (go && nq > 0) go = waits(&sm.odone, (nq - 1) & 1);
                 ++nq;
                 for (int i = 0; go && i < nt; ++i) {
-                    const int next = i + (kOne ? 2 : 1);   // tile of the buffer's next S
+                    const int odd = i & 1;
 #pragma unroll
-                    for (int u = 0; u < kGroups; ++u) {
-                        const int s = kOne ? i & 1 : u;
-                        const bool last = u == kGroups - 1;   // last reader of the tiles
-                        if (!(go = waits(&sm.pready[s], (pphase >> s) & 1))) break;
-                        pphase ^= 1u << s;
-                        if (u == 0 && !(go = waits(&vfull[vc.slot], vc.phase))) break;
+                    for (int g = 0; g < kGroups; ++g) {
+                        const bool last = g == kGroups - 1;   // last reader of the tiles
+                        if (!(go = waits(&sm.pready[2 * g + odd], (pphase >> odd) & 1))) break;
+                        if (g == 0 && !(go = waits(&vfull[vc.slot], vc.phase))) break;
                         tc_fence_after();
                         if (elect_one()) {
-                            pv(s, u, i == 0);
+                            pv(odd, g, i == 0);
                             if (last) umma_commit(&vempty[vc.slot]);
-                            if (kOne) umma_commit(&sm.pvdone);
-                            if (i + 1 == nt) umma_commit(&sm.ofull[u]);
+                            umma_commit(&sm.pvdone[g]);
+                            if (i + 1 == nt) umma_commit(&sm.ofull[g]);
                         }
                         __syncwarp();
-                        if (last) vc.next(v_slots);
-                        if (next >= nt) continue;
-                        if (u == 0 && !(go = waits(&sm.kfull[kc.slot], kc.phase))) break;
+                        if (i + 2 >= nt) continue;
+                        if (g == 0 && !(go = waits(&sm.kfull[kc.slot], kc.phase))) break;
                         if (elect_one()) {
-                            qk(s, u);
+                            qk(odd, g);
                             if (last) umma_commit(&sm.kempty[kc.slot]);
-                            if (last && next + 1 == nt) umma_commit(&sm.qfree);
+                            if (last && i + 3 == nt) umma_commit(&sm.qfree);
                         }
                         __syncwarp();
-                        if (last) kc.next(lay.k_slots);
                     }
+                    pphase ^= 1u << odd;
+                    vc.next(v_slots);
+                    if (i + 2 < nt) kc.next(lay.k_slots);
                 }
             }
             if (!go) {  // MMAs in flight end before the tensor memory goes back
@@ -443,24 +443,48 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                 if (k > 0 && !waits(&sm.qfree, (k - 1) & 1)) break;
                 if (k > 0) fence_proxy_async_smem();
                 const __nv_bfloat16* q0 = p.q + x.s.first * p.q_stride + x.g * p.QG * D;
+                // this thread's rows, STEP apart, without a division each: a row
+                // further is D values on, a token further q_stride - QG D more
+                auto each_row = [&](int start, int step, auto&& f) {
+                    int node = row_node(p, x.row0 + start);
+                    int head = x.row0 + start - node * p.QG;
+                    const __nv_bfloat16* src = q0 + node * p.q_stride + head * D;
+                    const int dn = row_node(p, step), dh = step - dn * p.QG;
+                    const int64_t by = dn * p.q_stride + dh * D, wrap = p.q_stride - p.QG * D;
+#pragma unroll 4
+                    for (int r = start; r < rows; r += step) {
+                        f(r, src);
+                        src += by;
+                        head += dh;
+                        if (head >= p.QG) {
+                            head -= p.QG;
+                            src += wrap;
+                        }
+                    }
+                };
                 if (kFp8) {
-                    // a lane takes 16 values, D / 16 lanes a row; the next rows'
-                    // loads are in flight while these are converted
+                    // A row's BF16 values are copied to where its two E4M3 terms
+                    // will stand (as many bytes), all rows in flight together, and
+                    // turned in place: a lane takes 16 values, D / 16 lanes of a
+                    // warp a row.
                     constexpr int LPR = D / 16, STEP = 64 / LPR;
                     const int c = t64 % LPR;
-                    uint4 a, b;
-                    auto load = [&](int r) {
-                        const int node = row_node(p, x.row0 + r);
-                        const __nv_bfloat16* src =
-                            q0 + node * p.q_stride + (x.row0 + r - node * p.QG) * D + 16 * c;
-                        a = *reinterpret_cast<const uint4*>(src);
-                        b = *reinterpret_cast<const uint4*>(src + 8);
+                    auto place = [&](int r) {
+                        return q_s + (r >> 7) * C::Q + tile_off<C::BOX, 128>(r & 127, c);
                     };
-                    int r = t64 / LPR;
-                    if (r < rows) load(r);
-                    for (int r0 = 0; r0 < rows; r0 += STEP, r += STEP) {
+                    each_row(t64 / LPR, STEP, [&](int r, const __nv_bfloat16* src) {
+                        const uint32_t dst = smem_addr(place(r));
+                        cp_async16(dst, src + 16 * c, true);
+                        cp_async16(dst + 128 * D, src + 16 * c + 8, true);
+                    });
+                    cp_async_commit();
+                    cp_async_wait<0>();
+                    // (a lane turns only what it copied itself)
+                    for (int r0 = 0, r = t64 / LPR; r0 < rows; r0 += STEP, r += STEP) {
+                        uint8_t* dst = place(r < rows ? r : 0);
+                        const uint4 a = *reinterpret_cast<const uint4*>(dst);
+                        const uint4 b = *reinterpret_cast<const uint4*>(dst + 128 * D);
                         const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-                        if (r + STEP < rows) load(r + STEP);
                         uint32_t big = 0;   // largest magnitude, as bits: NaN above all
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
@@ -490,7 +514,6 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                             else hi[i / 2] |= h2 << 16, lo[i / 2] |= l2 << 16;
                         }
                         if (r < rows) {
-                            uint8_t* dst = q_s + (r >> 7) * C::Q + tile_off<C::BOX, 128>(r & 127, c);
                             *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                             *reinterpret_cast<uint4*>(dst + 128 * D) =
                                 make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -503,12 +526,10 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                     constexpr int STEP = 64 / CH;    // rows a pass
                     const int c = t64 % CH;
                     const uint32_t dst = smem_addr(q_s);
-                    for (int r = t64 / CH; r < rows; r += STEP) {
-                        const int node = row_node(p, x.row0 + r);
-                        cp_async16(dst + (r >> 7) * C::Q + tile_off<128, 128>(r & 127, c),
-                                   q0 + node * p.q_stride + (x.row0 + r - node * p.QG) * D + 8 * c,
+                    each_row(t64 / CH, STEP, [&](int r, const __nv_bfloat16* src) {
+                        cp_async16(dst + (r >> 7) * C::Q + tile_off<128, 128>(r & 127, c), src + 8 * c,
                                    true);
-                    }
+                    });
                     cp_async_commit();
                     cp_async_wait<0>();
                 }
@@ -568,7 +589,7 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                     mbar_arrive(&sm.cfull[cc.slot]);
                 }
                 vc.next(lay.v_slots);
-                cc.next(kConvSlots);
+                cc.next(C::CONV_SLOTS);
             }
         }
     } else {
@@ -586,7 +607,7 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
         for (int k = 0; next_stretch(p, run, &x); ++k) {
             const int nt = x.t1 - x.t0;
             const int rows = min(1 << p.row_shift, x.s.n * p.QG - x.row0);
-            const int r = kOne ? gt : gt + 128 * g;   // row of the item
+            const int r = gt + 128 * g;   // row of the item
             const bool on = r < rows;
             const bool warp_on = __any_sync(0xffffffffu, on);
             const int row = x.row0 + (on ? r : 0);
@@ -613,9 +634,9 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
 
             float qs = p.qscale, ref = -INFINITY, sum = 0.f;
 
-            // One tile in buffer s; `at` counts the tiles of the run.
+            // One tile in the group's buffer s; `at` counts the tiles of the run.
             auto tile = [&](int s, int t, int at) {
-                const uint32_t tS = quarter + kTile * s;
+                const uint32_t tS = quarter + kTile * (2 * g + s);
                 uint32_t v[kTile];
 #pragma unroll
                 for (int c = 0; c < kTile; c += 32) tmem_ld32(tS + c, v + c);
@@ -655,12 +676,9 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                     sum *= f;
                     if (raise) ref = top;
                     if (t > x.t0) {
-                        // two groups: the last P V was issued before this S's
-                        // products, and is done; one group: they ran ahead of it
-                        if (kOne) {
-                            waits(&sm.pvdone, (at - 1) & 1);
-                            tc_fence_after();
-                        }
+                        // (this S's products ran ahead of the last P V)
+                        waits(&sm.pvdone[g], (at - 1) & 1);
+                        tc_fence_after();
 #pragma unroll 1
                         for (int c = 0; c < D; c += 16) {
                             uint32_t w[16];
@@ -693,8 +711,8 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
             };
 
             for (int i = 0; i < nt; ++i) {
-                const int s = kOne ? i & 1 : g;
-                if (!waits(&sm.sfull[s], (sphase >> s) & 1)) break;
+                const int s = i & 1;
+                if (!waits(&sm.sfull[2 * g + s], (sphase >> s) & 1)) break;
                 sphase ^= 1u << s;
                 tc_fence_after();
                 if (kFp8 && i == 0) qs = p.qscale * sm.qs[k & 1][on ? r : 0];
@@ -715,7 +733,7 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                 if (warp_on) tile(s, t, base + i);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.pready[s]);
+                if (lane == 0) mbar_arrive(&sm.pready[2 * g + s]);
             }
             base += nt;
             waits(&sm.ofull[g], no & 1);
@@ -795,7 +813,7 @@ int launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p
     // the rings share what Q and the converted tiles leave; two CTAs of an SM
     // have 114 KB each, 1 KB of it the system's
     const int room = C::CTAS_PER_SM == 1 ? limit : std::min(limit, 113 * 1024);
-    const int fixed = 1024 + kSmemHead<kGroups> + kGroups * C::Q + (kFp8 ? kConvSlots * C::CONV : 0);
+    const int fixed = 1024 + kSmemHead<kGroups> + kGroups * C::Q + C::CONV_SLOTS * C::CONV;
     const int slots = (room - fixed) / C::SLOT;
     if (limit < 0 || slots < 4) return cudaErrorInvalidValue;
     Layout lay;
