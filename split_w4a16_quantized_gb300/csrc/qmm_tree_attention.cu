@@ -30,9 +30,10 @@
 namespace qmm {
 
 // Tiled tensor map helper (qmm_w4a16_tc.cu)
-bool encode_tiled(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* ptr,
-                  const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
-                  CUtensorMapSwizzle swizzle);
+bool encode_tiled_promoted(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* ptr,
+                           const cuuint64_t* dims, const cuuint64_t* strides,
+                           const cuuint32_t* box, CUtensorMapSwizzle swizzle,
+                           CUtensorMapL2promotion promotion);
 
 namespace {
 
@@ -756,8 +757,14 @@ int launch_tree_attention(const qmm_kv_cache& c, const void* q, int64_t q_stride
                                          : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const CUtensorMapSwizzle sw = row < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
     CUtensorMap kmap, vmap;
-    if (!encode_tiled(&kmap, type, 4, c.K, dims, strides, box, sw) ||
-        !encode_tiled(&vmap, type, 4, c.V, dims, strides, box, sw))
+    // L2 fetches what a copy reads and no neighbouring head with it: a row, where
+    // the next slot's row is not the next in memory
+    const CUtensorMapL2promotion l2 = p.d.slot_stride == c.D || row >= 256
+                                          ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                      : row == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                                   : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
+    if (!encode_tiled_promoted(&kmap, type, 4, c.K, dims, strides, box, sw, l2) ||
+        !encode_tiled_promoted(&vmap, type, 4, c.V, dims, strides, box, sw, l2))
         return cudaErrorInvalidValue;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int rc;

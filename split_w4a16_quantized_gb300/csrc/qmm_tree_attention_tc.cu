@@ -14,9 +14,8 @@
 // Roles of a CTA:
 //   warp 0      copies: K and V tiles into a ring each
 //   warp 1      issues the MMAs and owns the tensor memory
-//   warps 2-3   bring the next item's q
+//   warps 2-3   bring the next item's q; E4M3 cache: turn V tiles into F16
 //   one or two softmax groups of 128 threads, a thread a row
-//   E4M3 cache: four warps that turn V tiles into F16
 // A group has two buffers of S: while it turns one into P, the products of the
 // other run, and with them the 480 clocks an MMA takes to be seen as done.  P
 // overwrites S in place (BF16 or F16 in half the columns).
@@ -55,7 +54,7 @@
 namespace qmm {
 namespace {
 
-constexpr int kConvWarps = 4;
+constexpr int kConvWarps = 2;
 constexpr int kTile = 1 << kTcTileShift;   // positions
 constexpr int kMaxSlots = 8;        // of one ring
 constexpr int kHave = 32;           // tiles whose page bits are kept
@@ -65,26 +64,13 @@ constexpr float kLazy = 8.f;        // log2 units a score may pass the reference
 template <int D, bool kFp8, int kGroups>
 struct Tc {
     static constexpr int CTAS_PER_SM = kGroups == 1 ? 2 : 1;
-    static constexpr int SOFTMAX0 = 4, CONV0 = 4 + 4 * kGroups;   // first warps
-    static constexpr int WARPS = CONV0 + (kFp8 ? kConvWarps : 0);
-    static constexpr int THREADS = 32 * WARPS;
-    // registers: the launch gives every thread the same share; the softmax groups
-    // hold a row of S and take over what the others do not need
-    static constexpr int SHARE = 65536 / (CTAS_PER_SM * THREADS) / 8 * 8;
-    static constexpr int REGS_CTL = kFp8 ? 56 : 88;
-    static constexpr int REGS_CONV = kGroups == 1 ? 40 : 56;
-    static constexpr int REGS_SOFTMAX = kFp8 ? (kGroups == 1 ? 144 : 200) : (kGroups == 1 ? 168 : 208);
-    static_assert(REGS_CTL + kGroups * REGS_SOFTMAX + (kFp8 ? REGS_CONV : 0) <= SHARE * WARPS / 4,
-                  "registers");
+    static constexpr int SOFTMAX0 = 4;                       // first softmax warp
+    static constexpr int THREADS = 128 + 128 * kGroups;
     static constexpr int ROW = D * (kFp8 ? 1 : 2);           // bytes of a cache row
     static constexpr int BOX = ROW < 128 ? ROW : 128;        // row bytes of one copy
     static constexpr int BOXES = ROW / BOX;
     static constexpr int SLOT = kTile * ROW;                 // a copied tile
-    static constexpr int Q = 128 * D * 2;                    // a group's Q: BF16, or two E4M3 terms
     static constexpr int CONV = kTile * D * 2;               // a converted V tile
-    // one converted tile where two CTAs share the SM: the next is converted
-    // while the group's softmax runs, and the ring is short
-    static constexpr int CONV_SLOTS = kFp8 ? kGroups : 0;
     // tensor memory: two S/P buffers of each group, then an O of each
     static constexpr uint32_t COLS = 256 * kGroups, COL_O = 2 * kTile * kGroups;
     static_assert(kGroups * (2 * kTile + D) <= static_cast<int>(COLS), "tensor memory");
@@ -180,15 +166,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
         : "r"(taddr)
         : "memory");
 }
-template <int kRegs>
-__device__ __forceinline__ void regs_inc() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegs));
-}
-template <int kRegs>
-__device__ __forceinline__ void regs_dec() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegs));
-}
-
 // Offset of 16-byte chunk c of row r in a tile of kRows rows: boxes of kBox
 // bytes a row, the chunk permuted by the swizzle of that width.
 template <int kBox, int kRows>
@@ -218,8 +195,11 @@ __device__ __forceinline__ uint64_t bits_from(const uint32_t* anc, int from) {
     return bits << lead;
 }
 
+// Shared memory of a launch.  q_rows: rows kept of a group's Q (32, 64 or 128:
+// the products read 128, and what follows stands for the rest, which nobody
+// looks at).
 struct Layout {
-    int k_slots, v_slots;
+    int q_rows, conv_slots, k_slots, v_slots;
 };
 
 template <int D, bool kFp8, int kGroups>
@@ -233,8 +213,9 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
         (reinterpret_cast<uintptr_t>(tree_tc_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     TcSmem<kGroups>& sm = *reinterpret_cast<TcSmem<kGroups>*>(base_s);
     uint8_t* q_s = base_s + kSmemHead<kGroups>;
-    uint8_t* conv_s = q_s + kGroups * C::Q;
-    uint8_t* k_s = conv_s + (C::CONV_SLOTS * C::CONV);
+    const int q_box = lay.q_rows * C::BOX, q_bytes = lay.q_rows * D * 2;   // BF16, or two E4M3 terms
+    uint8_t* conv_s = q_s + kGroups * q_bytes;
+    uint8_t* k_s = conv_s + lay.conv_slots * C::CONV;
     uint8_t* v_s = k_s + lay.k_slots * C::SLOT;
     volatile int* abort = &sm.abort;
 
@@ -284,12 +265,14 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
     Run run = find_run<C::THREADS>(p, sm.run);
     const int pieces = kTile >> p.box_shift;
     Stretch x;
+    // (test_wait answers in 60 clocks where the phase is complete, as it mostly
+    // is; try_wait takes 170)
     auto waits = [&](uint64_t* bar, int phase) {
-        return mbar_wait_warp(bar, phase, abort, p.status);
+        return __all_sync(0xffffffffu, mbar_probe(bar, phase)) ||
+               mbar_wait_warp(bar, phase, abort, p.status);
     };
 
     if (warp < C::SOFTMAX0) {
-        regs_dec<C::REGS_CTL>();
         if (warp == 0) {
             // ---- copies ----
             constexpr int E = C::BOX / (kFp8 ? 1 : 2);
@@ -343,7 +326,7 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
             uint64_t* vfull = kFp8 ? sm.cfull : sm.vfull;
             uint64_t* vempty = kFp8 ? sm.cempty : sm.vempty;
             constexpr int VSLOT = kFp8 ? C::CONV : C::SLOT;
-            const int v_slots = kFp8 ? C::CONV_SLOTS : lay.v_slots;
+            const int v_slots = kFp8 ? lay.conv_slots : lay.v_slots;
             Cursor kc, vc;
             int nq = 0;                     // Q's taken
             uint32_t pphase = 0;            // phase of the P of buffers 0 and 1, a bit each
@@ -351,7 +334,7 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
             // S of group g's buffer `odd` from its rows and the K tile at kc
             auto qk = [&](int odd, int g) {
                 const int s = 2 * g + odd;
-                const uint64_t a = q_desc + (C::Q >> 4) * g;
+                const uint64_t a = q_desc + static_cast<uint32_t>((q_bytes >> 4) * g);
                 const uint64_t b = k_desc + static_cast<uint32_t>(kc.slot * C::SLOT >> 4);
                 if (kFp8) {
                     // 32 values a step; q's two terms
@@ -359,13 +342,14 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int k = 0; k < D / 32; ++k)
-                            umma_ss<true>(tmem + kTile * s, a + ((h * 128 * D + k * 32) >> 4),
+                            umma_ss<true>(tmem + kTile * s,
+                                          a + static_cast<uint32_t>((h * q_box + k * 32) >> 4),
                                           b + ((k * 32) >> 4), iqk, h > 0 || k > 0);
                 } else {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
                         umma_ss<false>(tmem + kTile * s,
-                                       a + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
+                                       a + static_cast<uint32_t>(((k >> 2) * q_box + (k & 3) * 32) >> 4),
                                        b + (((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4), iqk, k > 0);
                 }
                 umma_commit(&sm.sfull[s]);
@@ -403,31 +387,46 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                 ++nq;
                 for (int i = 0; go && i < nt; ++i) {
                     const int odd = i & 1;
+                    const bool more = i + 2 < nt;   // the buffer gets another S
+                    bool k_here = false;
 #pragma unroll
                     for (int g = 0; g < kGroups; ++g) {
                         const bool last = g == kGroups - 1;   // last reader of the tiles
                         if (!(go = waits(&sm.pready[2 * g + odd], (pphase >> odd) & 1))) break;
-                        if (g == 0 && !(go = waits(&vfull[vc.slot], vc.phase))) break;
+                        if (g == 0) {
+                            if (!(go = waits(&vfull[vc.slot], vc.phase))) break;
+                            // K has come by now, as a rule: then everything is issued
+                            // in one go (a block of its own costs 200 clocks, and this
+                            // thread is what few-row items wait for)
+                            k_here = more && __all_sync(0xffffffffu,
+                                                        mbar_probe(&sm.kfull[kc.slot], kc.phase));
+                        }
                         tc_fence_after();
                         if (elect_one()) {
                             pv(odd, g, i == 0);
                             if (last) umma_commit(&vempty[vc.slot]);
                             umma_commit(&sm.pvdone[g]);
                             if (i + 1 == nt) umma_commit(&sm.ofull[g]);
+                            if (k_here) {
+                                qk(odd, g);
+                                if (last) umma_commit(&sm.kempty[kc.slot]);
+                                if (last && i + 3 == nt) umma_commit(&sm.qfree);
+                            }
                         }
                         __syncwarp();
-                        if (i + 2 >= nt) continue;
-                        if (g == 0 && !(go = waits(&sm.kfull[kc.slot], kc.phase))) break;
-                        if (elect_one()) {
-                            qk(odd, g);
-                            if (last) umma_commit(&sm.kempty[kc.slot]);
-                            if (last && i + 3 == nt) umma_commit(&sm.qfree);
+                        if (more && !k_here) {
+                            if (g == 0 && !(go = waits(&sm.kfull[kc.slot], kc.phase))) break;
+                            if (elect_one()) {
+                                qk(odd, g);
+                                if (last) umma_commit(&sm.kempty[kc.slot]);
+                                if (last && i + 3 == nt) umma_commit(&sm.qfree);
+                            }
+                            __syncwarp();
                         }
-                        __syncwarp();
                     }
                     pphase ^= 1u << odd;
                     vc.next(v_slots);
-                    if (i + 2 < nt) kc.next(lay.k_slots);
+                    if (more) kc.next(lay.k_slots);
                 }
             }
             if (!go) {  // MMAs in flight end before the tensor memory goes back
@@ -436,9 +435,11 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                 mbar_wait_warp(&sm.drained, 0, nullptr, p.status);
             }
         } else {
-            // ---- q of each item to shared memory, all its copies ----
+            // ---- q of each item to shared memory, then its V tiles to F16 ----
             const int t64 = tid - 64;
-            for (int k = 0; next_stretch(p, run, &x); ++k) {
+            Cursor vc, cc;
+            bool go = true;
+            for (int k = 0; go && next_stretch(p, run, &x); ++k) {
                 const int rows = min(1 << p.row_shift, x.s.n * p.QG - x.row0);
                 if (k > 0 && !waits(&sm.qfree, (k - 1) & 1)) break;
                 if (k > 0) fence_proxy_async_smem();
@@ -470,12 +471,12 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                     constexpr int LPR = D / 16, STEP = 64 / LPR;
                     const int c = t64 % LPR;
                     auto place = [&](int r) {
-                        return q_s + (r >> 7) * C::Q + tile_off<C::BOX, 128>(r & 127, c);
+                        return q_s + (r >> 7) * q_bytes + tile_off<C::BOX, 128>(r & 127, c);
                     };
                     each_row(t64 / LPR, STEP, [&](int r, const __nv_bfloat16* src) {
                         const uint32_t dst = smem_addr(place(r));
                         cp_async16(dst, src + 16 * c, true);
-                        cp_async16(dst + 128 * D, src + 16 * c + 8, true);
+                        cp_async16(dst + q_box, src + 16 * c + 8, true);
                     });
                     cp_async_commit();
                     cp_async_wait<0>();
@@ -483,7 +484,7 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                     for (int r0 = 0, r = t64 / LPR; r0 < rows; r0 += STEP, r += STEP) {
                         uint8_t* dst = place(r < rows ? r : 0);
                         const uint4 a = *reinterpret_cast<const uint4*>(dst);
-                        const uint4 b = *reinterpret_cast<const uint4*>(dst + 128 * D);
+                        const uint4 b = *reinterpret_cast<const uint4*>(dst + q_box);
                         const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
                         uint32_t big = 0;   // largest magnitude, as bits: NaN above all
 #pragma unroll
@@ -515,7 +516,7 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                         }
                         if (r < rows) {
                             *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                            *reinterpret_cast<uint4*>(dst + 128 * D) =
+                            *reinterpret_cast<uint4*>(dst + q_box) =
                                 make_uint4(lo[0], lo[1], lo[2], lo[3]);
                             if (c == 0)
                                 sm.qs[k & 1][r] = __uint_as_float(static_cast<uint32_t>(120 + e) << 23);
@@ -527,8 +528,9 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                     const int c = t64 % CH;
                     const uint32_t dst = smem_addr(q_s);
                     each_row(t64 / CH, STEP, [&](int r, const __nv_bfloat16* src) {
-                        cp_async16(dst + (r >> 7) * C::Q + tile_off<128, 128>(r & 127, c), src + 8 * c,
-                                   true);
+                        cp_async16(dst + (r >> 7) * q_bytes + (c >> 3) * q_box +
+                                       tile_off<128, 128>(r & 127, c & 7),
+                                   src + 8 * c, true);
                     });
                     cp_async_commit();
                     cp_async_wait<0>();
@@ -536,65 +538,53 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.qready);
-            }
-        }
-    } else if (kFp8 && warp >= C::CONV0) {
-        // ---- V to F16: a thread takes a position, or half of one ----
-        regs_dec<C::REGS_CONV>();
-        constexpr int SHARES = 128 / kTile;               // threads of a position
-        constexpr int CH = D / 16 / SHARES;               // 16-byte chunks of a thread
-        const int t128 = tid - 32 * C::CONV0;
-        const int r = t128 % kTile, ch0 = t128 / kTile * CH;
-        Cursor vc, cc;
-        bool go = true;
-        while (go && next_stretch(p, run, &x)) {
-            for (int t = x.t0; t < x.t1; ++t) {
-                const int valid = x.s.total - t * kTile;
-                if (!(go = waits(&sm.vfull[vc.slot], vc.phase))) break;
-                if (!(go = waits(&sm.cempty[cc.slot], cc.phase ^ 1))) break;
-                const uint8_t* src = v_s + vc.slot * C::SLOT;
-                uint8_t* dst = conv_s + cc.slot * C::CONV;
+                // a thread takes a position
+                for (int t = x.t0; kFp8 && t < x.t1; ++t) {
+                    const int valid = x.s.total - t * kTile;
+                    if (!(go = waits(&sm.vfull[vc.slot], vc.phase))) break;
+                    if (!(go = waits(&sm.cempty[cc.slot], cc.phase ^ 1))) break;
+                    const uint8_t* src = v_s + vc.slot * C::SLOT;
+                    uint8_t* dst = conv_s + cc.slot * C::CONV;
 #pragma unroll
-                for (int c0 = 0; c0 < CH; c0 += 4) {
-                    constexpr int N4 = CH < 4 ? CH : 4;
-                    uint4 in[N4];
+                    for (int c0 = 0; c0 < D / 16; c0 += 4) {
+                        uint4 in[4];
 #pragma unroll
-                    for (int c = 0; c < N4; ++c) {
-                        in[c] = *reinterpret_cast<const uint4*>(
-                            src + tile_off<C::BOX, kTile>(r, ch0 + c0 + c));
-                        // slots past the last position may hold anything, and
-                        // 0 * NaN is not 0
-                        if (r >= valid) in[c] = make_uint4(0, 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int c = 0; c < N4; ++c) {
-                        const uint32_t w[4] = {in[c].x, in[c].y, in[c].z, in[c].w};
-                        uint32_t f[8];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            f[2 * i] = e4m3x2_to_f16x2(w[i] & 0xffffu);
-                            f[2 * i + 1] = e4m3x2_to_f16x2(w[i] >> 16);
+                        for (int c = 0; c < 4; ++c) {
+                            in[c] = *reinterpret_cast<const uint4*>(
+                                src + tile_off<C::BOX, kTile>(t64, c0 + c));
+                            // slots past the last position may hold anything, and
+                            // 0 * NaN is not 0
+                            if (t64 >= valid) in[c] = make_uint4(0, 0, 0, 0);
                         }
-                        const int o = 2 * (ch0 + c0 + c);
-                        *reinterpret_cast<uint4*>(dst + tile_off<128, kTile>(r, o)) =
-                            make_uint4(f[0], f[1], f[2], f[3]);
-                        *reinterpret_cast<uint4*>(dst + tile_off<128, kTile>(r, o + 1)) =
-                            make_uint4(f[4], f[5], f[6], f[7]);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t w[4] = {in[c].x, in[c].y, in[c].z, in[c].w};
+                            uint32_t f[8];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                f[2 * i] = e4m3x2_to_f16x2(w[i] & 0xffffu);
+                                f[2 * i + 1] = e4m3x2_to_f16x2(w[i] >> 16);
+                            }
+                            const int o = 2 * (c0 + c);
+                            *reinterpret_cast<uint4*>(dst + tile_off<128, kTile>(t64, o)) =
+                                make_uint4(f[0], f[1], f[2], f[3]);
+                            *reinterpret_cast<uint4*>(dst + tile_off<128, kTile>(t64, o + 1)) =
+                                make_uint4(f[4], f[5], f[6], f[7]);
+                        }
                     }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&sm.vempty[vc.slot]);
+                        mbar_arrive(&sm.cfull[cc.slot]);
+                    }
+                    vc.next(lay.v_slots);
+                    cc.next(lay.conv_slots);
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&sm.vempty[vc.slot]);
-                    mbar_arrive(&sm.cfull[cc.slot]);
-                }
-                vc.next(lay.v_slots);
-                cc.next(C::CONV_SLOTS);
             }
         }
     } else {
         // ---- softmax groups ----
-        regs_inc<C::REGS_SOFTMAX>();
         const int g = (warp - C::SOFTMAX0) >> 2;          // group
         const int gt = (warp & 3) * 32 + lane;            // thread of the group = tensor memory lane
         const uint32_t quarter = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
@@ -813,10 +803,14 @@ int launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p
     // the rings share what Q and the converted tiles leave; two CTAs of an SM
     // have 114 KB each, 1 KB of it the system's
     const int room = C::CTAS_PER_SM == 1 ? limit : std::min(limit, 113 * 1024);
-    const int fixed = 1024 + kSmemHead<kGroups> + kGroups * C::Q + C::CONV_SLOTS * C::CONV;
-    const int slots = (room - fixed) / C::SLOT;
-    if (limit < 0 || slots < 4) return cudaErrorInvalidValue;
     Layout lay;
+    const int rows = p.T * p.QG;
+    lay.q_rows = kGroups == 2 || rows > 64 ? 128 : (rows > 32 ? 64 : 32);
+    const int fixed = 1024 + kSmemHead<kGroups> + kGroups * lay.q_rows * D * 2;
+    // two converted tiles where that leaves three slots to either ring
+    lay.conv_slots = kFp8 ? ((room - fixed - 2 * C::CONV) / C::SLOT >= 6 ? 2 : 1) : 0;
+    const int slots = (room - fixed - lay.conv_slots * C::CONV) / C::SLOT;
+    if (limit < 0 || slots < 4) return cudaErrorInvalidValue;
     lay.v_slots = std::min(slots / 2, kMaxSlots);
     lay.k_slots = std::min(slots - lay.v_slots, kMaxSlots);
     cudaLaunchConfig_t cfg = {};
@@ -824,7 +818,8 @@ int launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p
     apply_pdl(cfg, la);
     cfg.gridDim = dim3(p.ctas, 1, 1);
     cfg.blockDim = dim3(C::THREADS, 1, 1);
-    cfg.dynamicSmemBytes = fixed + static_cast<size_t>(lay.k_slots + lay.v_slots) * C::SLOT;
+    cfg.dynamicSmemBytes = fixed + static_cast<size_t>(lay.conv_slots) * C::CONV +
+                           static_cast<size_t>(lay.k_slots + lay.v_slots) * C::SLOT;
     cfg.stream = st;
     return cudaLaunchKernelEx(&cfg, kern, kmap, vmap, p, lay);
 }

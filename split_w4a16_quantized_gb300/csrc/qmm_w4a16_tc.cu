@@ -80,15 +80,22 @@ bool encode_2d(CUtensorMap* map, CUtensorMapDataType type, const void* ptr, uint
 }
 
 // rank-dimensional tiled map (dims[0] innermost; strides in bytes of dims 1..)
-bool encode_tiled(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* ptr,
-                  const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
-                  CUtensorMapSwizzle swizzle) {
+bool encode_tiled_promoted(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* ptr,
+                           const cuuint64_t* dims, const cuuint64_t* strides,
+                           const cuuint32_t* box, CUtensorMapSwizzle swizzle,
+                           CUtensorMapL2promotion promotion) {
     auto fn = tensor_map_encoder();
     if (!fn) return false;
     const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
     return fn(map, type, static_cast<cuuint32_t>(rank), const_cast<void*>(ptr), dims, strides, box,
-              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promotion,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool encode_tiled(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* ptr,
+                  const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+                  CUtensorMapSwizzle swizzle) {
+    return encode_tiled_promoted(map, type, rank, ptr, dims, strides, box, swizzle,
+                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 int* tc_status_ptr() {
