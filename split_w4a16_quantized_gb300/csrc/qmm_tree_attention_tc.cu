@@ -175,6 +175,12 @@ __device__ __forceinline__ uint32_t tile_off(int r, int c) {
     return static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 __device__ __forceinline__ uint64_t low_bits(int n) {
     return n <= 0 ? 0ull : (n >= 64 ? ~0ull : (1ull << n) - 1ull);
 }
@@ -656,8 +662,9 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                 }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < kTile; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(v[c]));
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * qs;
+                for (int c = 0; c < kTile; c += 2)
+                    mx[c / 2 & 3] = max3(mx[c / 2 & 3], __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+                const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * qs;
                 // raise the reference, row by row: a row's result must not depend
                 // on its neighbours (those past the item's rows hold anything)
                 const bool raise = on && top > ref + kLazy;
@@ -683,20 +690,23 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                     }
                 }
                 const float sub = finite_max(ref);
-                float part[4] = {0.f, 0.f, 0.f, 0.f};
+                const F2 q2 = f2(qs, qs), s2 = f2(-sub, -sub);
+                F2 part[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
                 for (int h = 0; h < kTile; h += 32) {
                     uint32_t pw[16];
 #pragma unroll
                     for (int c = 0; c < 32; c += 2) {
-                        const float a = fast_exp2(fmaf(__uint_as_float(v[h + c]), qs, -sub));
-                        const float b = fast_exp2(fmaf(__uint_as_float(v[h + c + 1]), qs, -sub));
-                        part[c / 2 & 3] += a + b;
+                        const float2 y = split(fma2(
+                            f2(__uint_as_float(v[h + c]), __uint_as_float(v[h + c + 1])), q2, s2));
+                        const float a = fast_exp2(y.x), b = fast_exp2(y.y);
+                        part[c / 2 & 1] = add2(part[c / 2 & 1], f2(a, b));
                         pw[c / 2] = kFp8 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
                     }
                     tmem_st16(tS + h / 2, pw);
                 }
-                sum += (part[0] + part[1]) + (part[2] + part[3]);
+                const float2 more = split(add2(part[0], part[1]));
+                sum += more.x + more.y;
                 tmem_st_wait();
             };
 
