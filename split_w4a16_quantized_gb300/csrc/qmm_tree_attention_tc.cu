@@ -15,7 +15,8 @@
 //   warp 0      copies: K and V tiles into a ring each
 //   warp 1      issues the MMAs and owns the tensor memory
 //   warps 2-3   bring the next item's q; E4M3 cache: turn V tiles into F16
-//   one or two softmax groups of 128 threads, a thread a row
+//   one or two softmax groups of 128 threads, a thread a row; E4M3 cache: turn
+//     their rows of q into two terms first
 // A group has two buffers of S: while it turns one into P, the products of the
 // other run, and with them the 480 clocks an MMA takes to be seen as done.  P
 // overwrites S in place (BF16 or F16 in half the columns).
@@ -84,14 +85,14 @@ struct TcSmem {
     uint64_t pready[2 * kGroups];       // its P is, and O may take the product
     uint64_t pvdone[kGroups];           // a group's product with V has ended
     uint64_t ofull[kGroups];            // a group's O is complete
-    uint64_t qready, qfree;             // an item's q is there; its products have read it
+    uint64_t qraw;                      // E4M3: an item's q is there, as BF16
+    uint64_t qready, qfree;             // q is there; the item's products have read it
     uint64_t odone;                     // an item's O has been read by all
     uint64_t drained;                   // abort: every MMA issued has ended
     uint32_t tmem;
     int abort;
     int have[kHave];                    // pages of a tile that exist, one bit a copy
     int pages[16];                      // of the tile being copied
-    float qs[2][128 * kGroups];         // E4M3: the rows' scales, by stretch parity
     int16_t par[kMaxTree];
     alignas(16) uint4 stage[4 * kGroups][128];   // by warp: 32 rows x 32 BF16 columns of O
     uint32_t anc[128 * kGroups][kWords + 1];     // a thread's own row: ancestors and itself
@@ -246,7 +247,8 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
             mbar_init(&sm.pvdone[g], 1);
             mbar_init(&sm.ofull[g], 1);
         }
-        mbar_init(&sm.qready, 2);
+        mbar_init(&sm.qraw, 2);
+        mbar_init(&sm.qready, kFp8 ? 4 * kGroups : 2);
         mbar_init(&sm.qfree, 1);
         mbar_init(&sm.odone, 4 * kGroups);
         mbar_init(&sm.drained, 1);
@@ -280,44 +282,49 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
 
     if (warp < C::SOFTMAX0) {
         if (warp == 0) {
-            // ---- copies ----
-            constexpr int E = C::BOX / (kFp8 ? 1 : 2);
+            // ---- copies: one thread waits and issues (a vote or a block of its own
+            // for each would cost 200 clocks, a sixth of a tile's time) ----
             Cursor kc, vc;
-            int it = 0, nv = 0;   // tiles of K and of V issued
+            int nk = 0, nv = 0;   // of the issuing thread: tiles of K and of V
+            int it = 0;           // tiles
+            int zeroed = 0;       // (BF16) V slots until one that was zeroed in part comes round
+            auto wait_one = [&](uint64_t* bar, int phase) {
+                return mbar_probe(bar, phase) || mbar_wait(bar, phase, abort, p.status);
+            };
             bool ok = true;
             while (ok && next_stretch(p, run, &x)) {
                 PageWalk<kTile> walk;
                 walk.start(p, x, lane);
-                for (int t = x.t0; t < x.t1; ++t) {
+                for (int t = x.t0; t < x.t1; ++t, ++it) {
                     const uint32_t have = walk.tile(p, t, lane, sm.pages);
-                    if (!(ok = waits(&sm.kempty[kc.slot], kc.phase ^ 1))) break;
                     if (elect_one()) {
-                        sm.have[it % kHave] = static_cast<int>(have);
-                        mbar_arrive_expect_tx(&sm.kfull[kc.slot], C::SLOT);
-                        copy_tile<kTile, C::BOXES, C::BOX, E>(p, &kmap, &sm.kfull[kc.slot],
-                                                              smem_addr(k_s) + kc.slot * C::SLOT,
-                                                              sm.pages, t, x.g);
+                        if (wait_one(&sm.kempty[kc.slot], kc.phase ^ 1)) {
+                            sm.have[it % kHave] = static_cast<int>(have);
+                            mbar_arrive_expect_tx(&sm.kfull[kc.slot], C::SLOT);
+                            copy_tile<kTile, C::BOXES, C::BOX, C::BOX / (kFp8 ? 1 : 2)>(p, &kmap, &sm.kfull[kc.slot],
+                                                     smem_addr(k_s) + kc.slot * C::SLOT, sm.pages, t,
+                                                     x.g);
+                            ++nk;
+                            if (wait_one(&sm.vempty[vc.slot], vc.phase ^ 1)) {
+                                // the slot was converted from with ordinary loads, or
+                                // zeroed in part with ordinary stores
+                                if (kFp8 || zeroed > 0) fence_proxy_async_smem();
+                                mbar_arrive_expect_tx(&sm.vfull[vc.slot], C::SLOT);
+                                copy_tile<kTile, C::BOXES, C::BOX, C::BOX / (kFp8 ? 1 : 2)>(p, &vmap, &sm.vfull[vc.slot],
+                                                         smem_addr(v_s) + vc.slot * C::SLOT, sm.pages,
+                                                         t, x.g);
+                                ++nv;
+                            }
+                        }
                     }
-                    __syncwarp();
-                    ++it;
+                    zeroed = (t + 1) * kTile > x.s.total ? lay.v_slots : max(0, zeroed - 1);
                     kc.next(lay.k_slots);
-                    if (!(ok = waits(&sm.vempty[vc.slot], vc.phase ^ 1))) break;
-                    if (elect_one()) {
-                        // the slot was converted from with ordinary loads, or perhaps
-                        // zeroed in part with ordinary stores
-                        fence_proxy_async_smem();
-                        mbar_arrive_expect_tx(&sm.vfull[vc.slot], C::SLOT);
-                        copy_tile<kTile, C::BOXES, C::BOX, E>(p, &vmap, &sm.vfull[vc.slot],
-                                                              smem_addr(v_s) + vc.slot * C::SLOT,
-                                                              sm.pages, t, x.g);
-                    }
-                    __syncwarp();
-                    ++nv;
                     vc.next(lay.v_slots);
+                    if (!(ok = !__any_sync(0xffffffffu, *abort))) break;
                 }
             }
-            if (!ok) {  // let the copies in flight land before the CTA exits
-                for (int j = max(0, it - lay.k_slots); j < it; ++j)
+            if (!ok && elect_one()) {  // let the copies in flight land before the CTA exits
+                for (int j = max(0, nk - lay.k_slots); j < nk; ++j)
                     mbar_wait(&sm.kfull[j % lay.k_slots], (j / lay.k_slots) & 1, nullptr, p.status);
                 for (int j = max(0, nv - lay.v_slots); j < nv; ++j)
                     mbar_wait(&sm.vfull[j % lay.v_slots], (j / lay.v_slots) & 1, nullptr, p.status);
@@ -471,9 +478,8 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                 };
                 if (kFp8) {
                     // A row's BF16 values are copied to where its two E4M3 terms
-                    // will stand (as many bytes), all rows in flight together, and
-                    // turned in place: a lane takes 16 values, D / 16 lanes of a
-                    // warp a row.
+                    // will stand (as many bytes): the softmax threads turn them in
+                    // place.
                     constexpr int LPR = D / 16, STEP = 64 / LPR;
                     const int c = t64 % LPR;
                     auto place = [&](int r) {
@@ -486,48 +492,6 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                     });
                     cp_async_commit();
                     cp_async_wait<0>();
-                    // (a lane turns only what it copied itself)
-                    for (int r0 = 0, r = t64 / LPR; r0 < rows; r0 += STEP, r += STEP) {
-                        uint8_t* dst = place(r < rows ? r : 0);
-                        const uint4 a = *reinterpret_cast<const uint4*>(dst);
-                        const uint4 b = *reinterpret_cast<const uint4*>(dst + q_box);
-                        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-                        uint32_t big = 0;   // largest magnitude, as bits: NaN above all
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            big = max(big, max((w[i] & 0x7fffu) << 16, w[i] & 0x7fff0000u));
-#pragma unroll
-                        for (int o = LPR / 2; o > 0; o >>= 1)
-                            big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
-                        // 2^e <= big < 2^(e+1); a row that holds infinities or NaN
-                        // becomes NaN (what its softmax would be)
-                        int e = static_cast<int>(big >> 23) - 127;
-                        const bool bad = e >= 128;
-                        e = big > 0 && !bad ? max(-110, min(126, e)) : 0;
-                        const float up = bad ? __int_as_float(0x7fffffff)
-                                             : __uint_as_float(static_cast<uint32_t>(134 - e) << 23);
-                        uint32_t hi[4], lo[4];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float f0 = __uint_as_float(w[i] << 16) * up;
-                            const float f1 = __uint_as_float(w[i] & 0xffff0000u) * up;
-                            const uint32_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(f0, f1),
-                                                                         __NV_SATFINITE, __NV_E4M3);
-                            const uint32_t h = e4m3x2_to_f16x2(h2);
-                            const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&h));
-                            const uint32_t l2 = __nv_cvt_float2_to_fp8x2(
-                                make_float2(f0 - g.x, f1 - g.y), __NV_SATFINITE, __NV_E4M3);
-                            if (i % 2 == 0) hi[i / 2] = h2, lo[i / 2] = l2;
-                            else hi[i / 2] |= h2 << 16, lo[i / 2] |= l2 << 16;
-                        }
-                        if (r < rows) {
-                            *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                            *reinterpret_cast<uint4*>(dst + q_box) =
-                                make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                            if (c == 0)
-                                sm.qs[k & 1][r] = __uint_as_float(static_cast<uint32_t>(120 + e) << 23);
-                        }
-                    }
                 } else {
                     constexpr int CH = D / 8;        // 16-byte chunks of a row
                     constexpr int STEP = 64 / CH;    // rows a pass
@@ -543,7 +507,7 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.qready);
+                if (lane == 0) mbar_arrive(kFp8 ? &sm.qraw : &sm.qready);
                 // a thread takes a position
                 for (int t = x.t0; kFp8 && t < x.t1; ++t) {
                     const int valid = x.s.total - t * kTile;
@@ -608,6 +572,61 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
             const bool warp_on = __any_sync(0xffffffffu, on);
             const int row = x.row0 + (on ? r : 0);
             const int node = row_node(p, row), head = x.g * p.QG + row - node * p.QG;
+            // ---- E4M3: the row of q as two terms ----
+            float qs = p.qscale;
+            if (kFp8) {
+                if (waits(&sm.qraw, k & 1) && on) {
+                    uint8_t* const row_s = q_s + g * q_bytes;
+                    uint32_t big = 0;   // largest magnitude, as bits: NaN above all
+#pragma unroll 4
+                    for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint4 w = *reinterpret_cast<const uint4*>(
+                                row_s + h * q_box + tile_off<C::BOX, 128>(gt, c));
+                            big = max(big, max(max((w.x & 0x7fffu) << 16, w.x & 0x7fff0000u),
+                                               max((w.y & 0x7fffu) << 16, w.y & 0x7fff0000u)));
+                            big = max(big, max(max((w.z & 0x7fffu) << 16, w.z & 0x7fff0000u),
+                                               max((w.w & 0x7fffu) << 16, w.w & 0x7fff0000u)));
+                        }
+                    // 2^e <= big < 2^(e+1); a row that holds infinities or NaN
+                    // becomes NaN (what its softmax would be)
+                    int e = static_cast<int>(big >> 23) - 127;
+                    const bool bad = e >= 128;
+                    e = big > 0 && !bad ? max(-110, min(126, e)) : 0;
+                    const float up = bad ? __int_as_float(0x7fffffff)
+                                         : __uint_as_float(static_cast<uint32_t>(134 - e) << 23);
+                    qs *= __uint_as_float(static_cast<uint32_t>(120 + e) << 23);
+                    // the first term is the value cut to 4 significant bits, the
+                    // second the 4 bits that were cut off
+#pragma unroll 1
+                    for (int c = 0; c < D / 16; ++c) {
+                        uint4* const at = reinterpret_cast<uint4*>(row_s + tile_off<C::BOX, 128>(gt, c));
+                        uint4* const at2 = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(at) + q_box);
+                        const uint4 a = *at, b = *at2;
+                        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                        uint32_t t[2][4];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float f0 = __uint_as_float(w[i] << 16) * up;
+                            const float f1 = __uint_as_float(w[i] & 0xffff0000u) * up;
+                            const float h0 = __uint_as_float(__float_as_uint(f0) & 0xfff00000u);
+                            const float h1 = __uint_as_float(__float_as_uint(f1) & 0xfff00000u);
+                            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(h0, h1),
+                                                                         __NV_SATFINITE, __NV_E4M3);
+                            const uint32_t lo = __nv_cvt_float2_to_fp8x2(
+                                make_float2(f0 - h0, f1 - h1), __NV_SATFINITE, __NV_E4M3);
+                            if (i % 2 == 0) t[0][i / 2] = hi, t[1][i / 2] = lo;
+                            else t[0][i / 2] |= hi << 16, t[1][i / 2] |= lo << 16;
+                        }
+                        *at = make_uint4(t[0][0], t[0][1], t[0][2], t[0][3]);
+                        *at2 = make_uint4(t[1][0], t[1][1], t[1][2], t[1][3]);
+                    }
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.qready);
+            }
             // ---- ancestors, where the stretch reaches the drafted slots: the same
             // for all heads of a sequence ----
             if (x.t1 * kTile > x.s.len && (x.b != anc_b || x.row0 != anc_row)) {
@@ -628,7 +647,7 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                     for (int i = node; i >= 0; i = sm.par[i]) anc[i >> 5] |= 1u << (i & 31);
             }
 
-            float qs = p.qscale, ref = -INFINITY, sum = 0.f;
+            float ref = -INFINITY, sum = 0.f;
 
             // One tile in the group's buffer s; `at` counts the tiles of the run.
             auto tile = [&](int s, int t, int at) {
@@ -715,7 +734,6 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                 if (!waits(&sm.sfull[2 * g + s], (sphase >> s) & 1)) break;
                 sphase ^= 1u << s;
                 tc_fence_after();
-                if (kFp8 && i == 0) qs = p.qscale * sm.qs[k & 1][on ? r : 0];
                 const int t = x.t0 + i;
                 const int valid = x.s.total - t * kTile;
                 if (!kFp8 && valid < kTile) {
@@ -817,8 +835,9 @@ int launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p
     const int rows = p.T * p.QG;
     lay.q_rows = kGroups == 2 || rows > 64 ? 128 : (rows > 32 ? 64 : 32);
     const int fixed = 1024 + kSmemHead<kGroups> + kGroups * lay.q_rows * D * 2;
-    // two converted tiles where that leaves three slots to either ring
-    lay.conv_slots = kFp8 ? ((room - fixed - 2 * C::CONV) / C::SLOT >= 6 ? 2 : 1) : 0;
+    // two converted tiles where that leaves two slots to either ring (32 sequences
+    // of 32 tokens, 128 rows: 112 us, with one tile and three slots 119)
+    lay.conv_slots = kFp8 ? ((room - fixed - 2 * C::CONV) / C::SLOT >= 4 ? 2 : 1) : 0;
     const int slots = (room - fixed - lay.conv_slots * C::CONV) / C::SLOT;
     if (limit < 0 || slots < 4) return cudaErrorInvalidValue;
     lay.v_slots = std::min(slots / 2, kMaxSlots);
