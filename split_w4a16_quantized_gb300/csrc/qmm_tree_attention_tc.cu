@@ -275,6 +275,9 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
     Stretch x;
     // (test_wait answers in 60 clocks where the phase is complete, as it mostly
     // is; try_wait takes 170)
+    auto wait_one = [&](uint64_t* bar, int phase) {
+        return mbar_probe(bar, phase) || mbar_wait(bar, phase, abort, p.status);
+    };
     auto waits = [&](uint64_t* bar, int phase) {
         return __all_sync(0xffffffffu, mbar_probe(bar, phase)) ||
                mbar_wait_warp(bar, phase, abort, p.status);
@@ -288,9 +291,6 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
             int nk = 0, nv = 0;   // of the issuing thread: tiles of K and of V
             int it = 0;           // tiles
             int zeroed = 0;       // (BF16) V slots until one that was zeroed in part comes round
-            auto wait_one = [&](uint64_t* bar, int phase) {
-                return mbar_probe(bar, phase) || mbar_wait(bar, phase, abort, p.status);
-            };
             bool ok = true;
             while (ok && next_stretch(p, run, &x)) {
                 PageWalk<kTile> walk;
@@ -379,74 +379,79 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                     umma_bf16_tmem_a(tmem + C::COL_O + D * g, tmem + kTile * s + 8 * k,
                                      b + ((k * 2048) >> 4), ipv, !first || k > 0);
             };
-            while (go && next_stretch(p, run, &x)) {
-                const int nt = x.t1 - x.t0;
-                if (!(go = waits(&sm.qready, nq & 1))) break;
-                // the first S of each buffer
-                for (int i = 0; i < min(nt, 2); ++i) {
-                    if (!(go = waits(&sm.kfull[kc.slot], kc.phase))) break;
-                    tc_fence_after();
-                    if (elect_one()) {
-#pragma unroll
-                        for (int g = 0; g < kGroups; ++g) qk(i, g);
-                        umma_commit(&sm.kempty[kc.slot]);
-                        if (i + 1 == nt) umma_commit(&sm.qfree);
-                    }
-                    __syncwarp();
-                    kc.next(lay.k_slots);
-                }
-                // O is free once the last stretch's has been read
-                if (go && nq > 0) go = waits(&sm.odone, (nq - 1) & 1);
-                ++nq;
-                for (int i = 0; go && i < nt; ++i) {
-                    const int odd = i & 1;
-                    const bool more = i + 2 < nt;   // the buffer gets another S
-                    bool k_here = false;
-#pragma unroll
-                    for (int g = 0; g < kGroups; ++g) {
-                        const bool last = g == kGroups - 1;   // last reader of the tiles
-                        if (!(go = waits(&sm.pready[2 * g + odd], (pphase >> odd) & 1))) break;
-                        if (g == 0) {
-                            if (!(go = waits(&vfull[vc.slot], vc.phase))) break;
-                            // K has come by now, as a rule: then everything is issued
-                            // in one go (a block of its own costs 200 clocks, and this
-                            // thread is what few-row items wait for)
-                            k_here = more && __all_sync(0xffffffffu,
-                                                        mbar_probe(&sm.kfull[kc.slot], kc.phase));
-                        }
+            // Two groups: one thread waits and issues, because a vote or an issuing
+            // block of its own after each wait costs 200 clocks, in which the tensor
+            // cores run dry (16 sequences of 64 tokens: 130 us, with votes 141).  One
+            // group: the other CTA's products fill those gaps, and both CTAs' are
+            // through sooner when a tile's are issued in one go by the whole warp (32
+            // sequences of 16 tokens, E4M3: 86 us, one thread 91).
+            constexpr bool kAlone = kGroups == 2;
+            auto wait = [&](uint64_t* bar, int phase) {
+                return kAlone ? wait_one(bar, phase) : waits(bar, phase);
+            };
+            auto issue = [&](auto&& f) {
+                if (kAlone || elect_one()) f();
+                if (!kAlone) __syncwarp();
+            };
+            if (!kAlone || elect_one()) {
+                while (go && next_stretch(p, run, &x)) {
+                    const int nt = x.t1 - x.t0;
+                    if (!(go = wait(&sm.qready, nq & 1))) break;
+                    // the first S of each buffer
+                    for (int i = 0; i < min(nt, 2); ++i) {
+                        if (!(go = wait(&sm.kfull[kc.slot], kc.phase))) break;
                         tc_fence_after();
-                        if (elect_one()) {
-                            pv(odd, g, i == 0);
-                            if (last) umma_commit(&vempty[vc.slot]);
-                            umma_commit(&sm.pvdone[g]);
-                            if (i + 1 == nt) umma_commit(&sm.ofull[g]);
-                            if (k_here) {
-                                qk(odd, g);
-                                if (last) umma_commit(&sm.kempty[kc.slot]);
-                                if (last && i + 3 == nt) umma_commit(&sm.qfree);
-                            }
-                        }
-                        __syncwarp();
-                        if (more && !k_here) {
-                            if (g == 0 && !(go = waits(&sm.kfull[kc.slot], kc.phase))) break;
-                            if (elect_one()) {
-                                qk(odd, g);
-                                if (last) umma_commit(&sm.kempty[kc.slot]);
-                                if (last && i + 3 == nt) umma_commit(&sm.qfree);
-                            }
-                            __syncwarp();
-                        }
+                        issue([&] {
+#pragma unroll
+                            for (int g = 0; g < kGroups; ++g) qk(i, g);
+                            umma_commit(&sm.kempty[kc.slot]);
+                            if (i + 1 == nt) umma_commit(&sm.qfree);
+                        });
+                        kc.next(lay.k_slots);
                     }
-                    pphase ^= 1u << odd;
-                    vc.next(v_slots);
-                    if (more) kc.next(lay.k_slots);
+                    // O is free once the last stretch's has been read
+                    if (go && nq > 0) go = wait(&sm.odone, (nq - 1) & 1);
+                    ++nq;
+                    for (int i = 0; go && i < nt; ++i) {
+                        const int odd = i & 1;
+                        const bool more = i + 2 < nt;   // the buffer gets another S
+                        auto next_s = [&](int g) {
+                            qk(odd, g);
+                            if (g == kGroups - 1) umma_commit(&sm.kempty[kc.slot]);
+                            if (g == kGroups - 1 && i + 3 == nt) umma_commit(&sm.qfree);
+                        };
+#pragma unroll
+                        for (int g = 0; g < kGroups; ++g) {
+                            if (!(go = wait(&sm.pready[2 * g + odd], (pphase >> odd) & 1))) break;
+                            if (g == 0 && !(go = wait(&vfull[vc.slot], vc.phase))) break;
+                            // K has come by now, as a rule
+                            const bool k_here =
+                                !kAlone && more &&
+                                __all_sync(0xffffffffu, mbar_probe(&sm.kfull[kc.slot], kc.phase));
+                            tc_fence_after();
+                            issue([&] {
+                                pv(odd, g, i == 0);
+                                if (g == kGroups - 1) umma_commit(&vempty[vc.slot]);
+                                umma_commit(&sm.pvdone[g]);
+                                if (i + 1 == nt) umma_commit(&sm.ofull[g]);
+                                if (k_here) next_s(g);
+                            });
+                            if (more && !k_here) {
+                                if (g == 0 && !(go = wait(&sm.kfull[kc.slot], kc.phase))) break;
+                                issue([&] { next_s(g); });
+                            }
+                        }
+                        pphase ^= 1u << odd;
+                        vc.next(v_slots);
+                        if (more) kc.next(lay.k_slots);
+                    }
+                }
+                if (!go) {  // MMAs in flight end before the tensor memory goes back
+                    issue([&] { umma_commit(&sm.drained); });
+                    mbar_wait(&sm.drained, 0, nullptr, p.status);
                 }
             }
-            if (!go) {  // MMAs in flight end before the tensor memory goes back
-                if (elect_one()) umma_commit(&sm.drained);
-                __syncwarp();
-                mbar_wait_warp(&sm.drained, 0, nullptr, p.status);
-            }
+            __syncwarp();
         } else {
             // ---- q of each item to shared memory, then its V tiles to F16 ----
             const int t64 = tid - 64;
