@@ -598,10 +598,7 @@ __global__ void __launch_bounds__(kMergeThreads)
     const int j0 = threadIdx.x / kMergeRows;
     if (r < rows) {
         auto part = [&](int c) { return partial_at<D>(p, 2 * c + (c == c0 ? 1 : 0)); };
-        float M = -INFINITY;
-#pragma unroll 4
-        for (int c = c0; c <= c1; ++c) M = fmaxf(M, part(c).m[r]);
-        M = finite_max(M);
+        float M = -INFINITY;   // running: a pass of its own would cost a latency
         float4 num[TURNS];
         float den = 0.f;
 #pragma unroll
@@ -611,7 +608,8 @@ __global__ void __launch_bounds__(kMergeThreads)
             float4 o[kMergeAhead][TURNS];
 #pragma unroll
             for (int k = 0; k < kMergeAhead; ++k) {
-                if (c + k > c1) break;
+                m[k] = -INFINITY;
+                if (c + k > c1) continue;
                 const PartialAt x = part(c + k);
                 m[k] = x.m[r];
                 l[k] = x.l[r];
@@ -620,10 +618,23 @@ __global__ void __launch_bounds__(kMergeThreads)
                     o[k][u] = *reinterpret_cast<const float4*>(
                         x.at(r, 4 * (j0 + u * (kMergeThreads / kMergeRows))));
             }
+            float top = M;
+#pragma unroll
+            for (int k = 0; k < kMergeAhead; ++k) top = fmaxf(top, m[k]);
+            const float sub = finite_max(top), old = fast_exp2(M - sub);
+            M = top;
+            den *= old;
+#pragma unroll
+            for (int u = 0; u < TURNS; ++u) {
+                num[u].x *= old;
+                num[u].y *= old;
+                num[u].z *= old;
+                num[u].w *= old;
+            }
 #pragma unroll
             for (int k = 0; k < kMergeAhead; ++k) {
                 if (c + k > c1) break;
-                const float f = fast_exp2(m[k] - M);
+                const float f = fast_exp2(m[k] - sub);
                 den = fmaf(f, l[k], den);
 #pragma unroll
                 for (int u = 0; u < TURNS; ++u) {
