@@ -647,8 +647,9 @@ int qmm_decode_attention(const void *q, const void *K, const void *V, const int 
  *   table  device int32 [B, max_pages]: slot s of sequence b is row
  *          s % page_size of page table[b, s / page_size].  An entry outside
  *          [0, num_pages) is no page: nothing is written there and attention
- *          leaves its positions out.  No page may hold slots of two
- *          sequences that a call writes.
+ *          leaves its positions out.  A slot that a call writes may not be
+ *          reached from a second place of the table (a history that several
+ *          sequences share is only read).
  *   lens   device int32 [B]: the tokens already in the cache (values outside
  *          [0, max_pages * page_size] are clamped).  The calls' new tokens
  *          take slots lens[b], lens[b] + 1, ...; slots past the table's end
@@ -656,7 +657,8 @@ int qmm_decode_attention(const void *q, const void *K, const void *V, const int 
  *   dtype  QMM_CACHE_BF16, or QMM_CACHE_E4M3: a stored value stands for
  *          k_scale (v_scale) times its E4M3 number.  k_scale and v_scale are
  *          positive and finite; 1 for BF16.
- * D is 64 or 128; page_size a power of two from 8 to 65536. */
+ * D is 64 or 128; page_size a power of two from 8 to 65536.  The pools, K's
+ * and V's and those of several caches, do not overlap. */
 enum { QMM_CACHE_BF16 = 0, QMM_CACHE_E4M3 = 1 };
 typedef struct {
     void *K, *V;       /* device */
@@ -697,8 +699,7 @@ typedef struct {
  *        alone when there is a rotation: no q_out row, nothing stored.
  *   q and q_out may be NULL with Hq = 0 (only append); q_out may be q itself
  *   (same stride), and overlaps no other input.  rope may be NULL.
- * A sequence's new slots may not repeat another's pages.  lens is not
- * changed.  One launch.  Returns QMM_OK, QMM_EINVAL, QMM_ESHAPE, QMM_EALIGN,
+ * lens is not changed.  One launch.  Returns QMM_OK, QMM_EINVAL, QMM_ESHAPE, QMM_EALIGN,
  * QMM_ENODEV or QMM_ECUDA. */
 int qmm_kv_append(const qmm_kv_cache *cache, const void *q, const void *k, const void *v,
                   void *q_out, int N, int Hq, int64_t q_stride, int64_t k_stride,
@@ -710,7 +711,8 @@ int qmm_kv_append(const qmm_kv_cache *cache, const void *q, const void *k, const
  *   q     BF16 [N, Hq, D], token stride q_stride (elements, a multiple of 8),
  *         heads contiguous; Hq a multiple of Hkv, at most 64 query heads per
  *         KV head
- *   O     BF16 [N, Hq, D], contiguous; rows of no sequence are left alone
+ *   O     BF16 [N, Hq, D], contiguous; rows of no sequence are left alone.
+ *         Overlaps nothing that the call reads
  *   cu    as in qmm_kv_append; NULL: T tokens each and N = B * T.  A range of
  *         more than T tokens counts as its first T.
  *   parents  device int32 [N], nullable: the parent of token i within its
@@ -729,6 +731,10 @@ int qmm_kv_append(const qmm_kv_cache *cache, const void *q, const void *k, const
  *         split over the history.  Calls that may overlap on the GPU need
  *         workspaces of their own.  Nothing is kept in it between calls.
  * The result does not depend on timing: the same call gives the same bits.
+ * QMM_ESHAPE also where the tables are so long that the work split's 32-bit
+ * counts would not hold them: with s = max_pages * page_size,
+ * (s / 64 + 16) * ceil(T Hq / (16 Hkv)) * Hkv above 2^31 - 1, or B times it above
+ * 64 (2^31 - 1).
  * Returns QMM_OK, QMM_EINVAL, QMM_ESHAPE, QMM_EALIGN, QMM_ENODEV,
  * QMM_EWORKSPACE or QMM_ECUDA. */
 int qmm_tree_attention(const qmm_kv_cache *cache, const void *q, int64_t q_stride, void *O, int N,

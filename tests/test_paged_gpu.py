@@ -334,6 +334,175 @@ def test_attention_two_streams_and_graph(n):
     assert not torch.equal(O.view(torch.int16), want.view(torch.int16))
 
 
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("e4m3", 128), ("bf16", 64), ("e4m3", 64)])
+@pytest.mark.parametrize("rows", [15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256])
+def test_attention_row_borders(rows, dtype, D):
+    """One query head per KV head: as many rows as tokens, on both sides of each
+    border between kernels, tiles and shared-memory layouts."""
+    _check_attention(Problem([150, 0, 64], [rows, 1, rows - 1], 2, D, 32, dtype, seed=rows), 2)
+
+
+@pytest.mark.parametrize("D,dtype", [(128, "bf16"), (64, "e4m3")])
+def test_attention_most_rows(D, dtype):
+    """256 tokens of 64 query heads per KV head."""
+    _check_attention(Problem([70], [256], 1, D, 64, dtype), 64)
+
+
+def test_attention_thousands_of_sequences():
+    rng = np.random.default_rng(6)
+    lens = [int(v) for v in rng.integers(0, 20, 4097)]
+    _check_attention(Problem(lens, [1] * 4097, 1, 64, 8, seed=4), 2, "none")
+    _check_attention(Problem(lens, [3] * 4097, 1, 64, 8, "e4m3", seed=4), 8, "tree")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [3, 12, 40, 90])
+def test_attention_values_that_are_not_numbers_stay_in_their_rows(n, dtype):
+    """Rows of q with infinities, NaN, zeros, the type's largest and smallest
+    values: what the formula makes NaN is, and every other row is what it is
+    without them, bit for bit."""
+    pb = Problem([130, 5], [n, n], 2, 128, 16, dtype)
+    rng = np.random.default_rng(n)
+    q = torch.from_numpy(rng.standard_normal((pb.N, 8, 128))).bfloat16()
+    par = np.concatenate([_tree(rng, n, "tree") for _ in range(2)]).astype(np.int32)
+    clean = _run_attention(pb, q.cuda(), par).cpu()
+    bad = q.clone()
+    bad[0, 0, 3] = float("nan")
+    bad[0, 1, 100] = float("inf")
+    bad[1, 5, 0] = float("-inf")
+    bad[n + 1, 7] = 0.0
+    bad[n + 2, 6] = 2.0 ** -133            # BF16's smallest
+    got = _run_attention(pb, bad.cuda(), par).cpu()
+    touched = torch.zeros((pb.N, 8), dtype=torch.bool)
+    for r, h in ((0, 0), (0, 1), (1, 5)):
+        touched[r, h] = True
+        assert not torch.isfinite(got[r, h].float()).any()
+    for r, h in ((n + 1, 7), (n + 2, 6)):
+        touched[r, h] = True
+    O, A, S = _attention64(pb, torch.nan_to_num(bad, 0, 0, 0), par, 1 / math.sqrt(128))
+    lim = _limit(pb, O, A, S, n, 128)
+    for r, h in ((n + 1, 7), (n + 2, 6)):
+        assert ((got[r, h].double() - O[r, h]).abs() <= lim[r, h]).all()
+    assert torch.equal(got[~touched].view(torch.int16), clean[~touched].view(torch.int16))
+
+
+@pytest.mark.parametrize("how", ["kv by head", "kv by row", "padded rows"])
+@pytest.mark.parametrize("n", [2, 30])
+def test_attention_of_pools_with_gaps(n, how):
+    """K and V woven into one allocation, and rows with space behind them."""
+    pb = Problem([70, 9], [n, n], 2, 64, 16)
+    want = _check_attention(pb, 8)
+    P = pb.K.shape[0]
+    if how == "kv by head":
+        both = torch.full((P, 2, 2, 16, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+        K, V = both[:, 0], both[:, 1]
+    elif how == "kv by row":
+        both = torch.full((P, 2, 16, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+        K, V = both[..., :64], both[..., 64:]
+    else:
+        K, V = (torch.full((P, 2, 16, 72), float("nan"), dtype=torch.bfloat16,
+                           device="cuda")[..., :64] for _ in range(2))
+    K.copy_(pb.K), V.copy_(pb.V)
+    pb.K, pb.V = K, V
+    pb.bind()
+    got = _check_attention(pb, 8)
+    assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+
+
+def test_one_page_of_one_head_in_a_view():
+    """Dimensions of one row: their strides mean nothing."""
+    pb = Problem([3], [4], 1, 128, 8, spare=0, width=1)
+    want = _check_attention(pb, 2)
+    for strides in ((8, 0, 128, 1), (0, 24, 128, 1)):
+        odd = [x.as_strided((1, 1, 8, 128), strides) for x in (pb.K, pb.V)]
+        pb.cache = Q.kv_cache(odd[0], odd[1], pb.d_table, pb.d_lens)
+        got = _check_attention(pb, 2)
+        assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_two_graphs_with_workspaces_of_their_own(n):
+    """Captured calls replayed side by side, over and over, keep their results."""
+    pbs = [Problem([700, 31], [n, n], 2, 128, 16, seed=s) for s in (1, 2)]
+    rng = np.random.default_rng(3)
+    par = np.concatenate([_tree(rng, n, "tree") for _ in range(2)]).astype(np.int32)
+    d_par = _dev(par)
+    runs = []
+    for pb in pbs:
+        q = torch.from_numpy(rng.standard_normal((pb.N, 8, 128))).bfloat16().cuda()
+        want = _run_attention(pb, q, par)
+        O = torch.zeros_like(q)
+        ws = torch.empty(Q.qmm_tree_attention_workspace_bytes(pb.cache, 8, n), dtype=torch.uint8,
+                         device="cuda")
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(3):
+                Q.qmm_tree_attention(pb.cache, q, O, n, parents=d_par, workspace=ws)
+        runs.append((g, O, want, torch.cuda.Stream(), q, ws))
+    for _ in range(10):
+        for g, _, _, st, _, _ in runs:
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for _, O, want, _, _, _ in runs:
+        assert torch.equal(O.view(torch.int16), want.view(torch.int16))
+
+
+def test_pools_beyond_32_bits():
+    """Pages whose offsets pass 2^32 bytes and 2^31 values: append, attention and
+    the accepted path reach them and nothing else."""
+    B, n, Hkv, page, D = 2, 6, 8, 64, 128
+    pages = 40000                                   # of 128 KB: 5.2 GB a pool
+    free, _ = torch.cuda.mem_get_info()
+    if free < 16 << 30:
+        pytest.skip("needs 11 GB")
+    small = Problem([90, 10], [n, n], Hkv, D, page, seed=8)
+    K, V = (torch.empty((pages, Hkv, page, D), dtype=torch.bfloat16, device="cuda")
+            for _ in range(2))
+    far = np.array([[pages - 1, pages - 3], [pages - 2, 5]], np.int32)
+    for pool, src in ((K, small.K), (V, small.V)):
+        pool[pages - 8:] = 0
+        pool[:8] = 0
+        for b in range(B):
+            for i in range(2):
+                if small.table[b, i] >= 0:
+                    pool[int(far[b, i])] = src[int(small.table[b, i])]
+    rng = np.random.default_rng(9)
+    x = [torch.from_numpy(rng.standard_normal((B * n, Hkv, D))).bfloat16().cuda() for _ in range(2)]
+    q = torch.from_numpy(rng.standard_normal((B * n, 16, D))).bfloat16().cuda()
+    par = np.concatenate([_tree(rng, n, "tree") for _ in range(B)]).astype(np.int32)
+    tok = np.arange(B * n, dtype=np.int32)
+    path = [0, 2, 3, 5]
+    for b in range(B):                              # the chain 0, 2, 3, 5 is accepted
+        for a, c in zip(path, path[1:]):
+            par[b * n + c] = a
+    tgt = np.full(B * n, -1, np.int32)
+    for b in range(B):
+        for a, c in zip(path, path[1:]):
+            tgt[b * n + a] = tok[b * n + c]
+    got = []
+    for k, v, table in ((small.K, small.V, small.d_table[:, :2].contiguous()), (K, V, _dev(far))):
+        cache = Q.kv_cache(k, v, table, small.d_lens)
+        Q.qmm_kv_append(cache, None, x[0], x[1])
+        O = torch.empty_like(q)
+        ws = torch.empty(Q.qmm_tree_attention_workspace_bytes(cache, 16, n), dtype=torch.uint8,
+                         device="cuda")
+        Q.qmm_tree_attention(cache, q, O, n, parents=_dev(par), workspace=ws)
+        out = [torch.empty((B, n), dtype=torch.int32, device="cuda"),
+               torch.empty(B, dtype=torch.int32, device="cuda")]
+        Q.qmm_tree_accept(Q.kv_caches([cache]), _dev(tok), _dev(tgt), n, out[0], out[1],
+                          parents=_dev(par))
+        torch.cuda.synchronize()
+        assert out[1].tolist() == [4, 4] and out[0][:, :4].tolist() == [path, path]
+        rows = [pool[int(table[b, s // page]), :, s % page]
+                for pool in (k, v) for b in range(B)
+                for s in range(small.lens[b], small.lens[b] + 4)]
+        got.append((O, torch.stack(rows)))
+    for a, b in zip(*got):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
 # ---- append ---------------------------------------------------------------------
 
 def _cos_sin(rows, dim, base=1e4):
