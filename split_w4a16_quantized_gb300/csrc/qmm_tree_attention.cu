@@ -114,7 +114,8 @@ __device__ __forceinline__ void mma16816(float d[4], const uint32_t a[4], uint32
 //     E4M3 cache: the values are exact in F16, so the products run in F16; a
 //     row of q is scaled by a power of two to a maximum in [1, 2) first, so
 //     rounding it to F16 (11 bits, 2^-25 absolute) loses nothing of its 8 bits
-//     but what lies 2^-17 below the row's maximum, and P is one F16 term.
+//     but what lies 2^-17 below the row's maximum, and P is one F16 term,
+//     times 2^15: weights down to 2^-29 of the largest keep 11 bits.
 //   - When a stretch ends the 4 states are merged: each warp collects a quarter
 //     of the columns from the other three.
 // Every wait is bounded (1 s): a wait that runs out sets the status word and
@@ -362,10 +363,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                         const float mf = finite_max(mn);
                         corr[h] = fast_exp2(m_run[h] - mf);
                         m_run[h] = mn;
+                        const float by = mf - (kFp8 ? 15.f : 0.f);
                         float rs = 0.f;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            pw[h][e] = fast_exp2(v[e] - mf);
+                            pw[h][e] = fast_exp2(v[e] - by);
                             rs += pw[h][e];
                         }
                         l_run[h] = l_run[h] * corr[h] + rs;

@@ -45,7 +45,7 @@
 // of the row's maximum and to 2^-17 of that maximum below.  P V needs more bits
 // of P than two E4M3 terms give far below the maximum (a long flat tail under
 // one large weight would vanish), so V is converted to F16, exactly, and P is
-// F16.
+// F16, times 2^7: at most 2^15, and 11 bits down to 2^-21 of the reference.
 #include <algorithm>
 #include <mutex>
 
@@ -60,6 +60,7 @@ constexpr int kTile = 1 << kTcTileShift;   // positions
 constexpr int kMaxSlots = 8;        // of one ring
 constexpr int kHave = 32;           // tiles whose page bits are kept
 constexpr float kLazy = 8.f;        // log2 units a score may pass the reference by
+constexpr float kLift = 7.f;        // log2 of the factor on F16 weights
 
 // kGroups: softmax groups (1: two CTAs per SM, up to 128 rows; 2: one CTA, 256).
 template <int D, bool kFp8, int kGroups>
@@ -713,7 +714,7 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                         tmem_st_wait();
                     }
                 }
-                const float sub = finite_max(ref);
+                const float sub = finite_max(ref) - (kFp8 ? kLift : 0.f);
                 const F2 q2 = f2(qs, qs), s2 = f2(-sub, -sub);
                 F2 part[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll

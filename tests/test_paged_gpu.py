@@ -386,6 +386,30 @@ def test_attention_values_that_are_not_numbers_stay_in_their_rows(n, dtype):
     assert torch.equal(got[~touched].view(torch.int16), clean[~touched].view(torch.int16))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 2, 9, 40])
+def test_attention_small_weights_keep_their_bits(n, dtype):
+    """One key takes all but 2^-15 of the weight and has no V: the output is
+    what weights of 2^-23.5 each make of the others."""
+    pb = Problem([300], [n], 2, 128, 16, dtype, seed=11)
+    for pool, vals in ((pb.K, pb.values[0][0]), (pb.V, pb.values[1][0])):
+        if vals is pb.values[0][0]:
+            vals.zero_()
+            vals[0, :, 0] = 448 * pb.scales[0] if pb.fp8 else 5.625
+        else:
+            vals[0] = 0
+        for s in range(300 + n):
+            row = vals[s] / (pb.scales[0] if vals is pb.values[0][0] else pb.scales[1])
+            pool[int(pb.table[0, s // 16]), :, s % 16] = row.float().to(pool.dtype).cuda()
+    q = torch.zeros((n, 8, 128), dtype=torch.bfloat16)
+    q[:, :, 0] = 2.90625                    # 2.90625 * 5.6 = 16.3 = 23.5 log2 units
+    parents = np.arange(-1, n - 1).astype(np.int32)
+    got = _run_attention(pb, q.cuda(), parents, 1.0).cpu().double()
+    O, A, S = _attention64(pb, q, parents, 1.0)
+    lim = _limit(pb, O, A, S, n, 128)
+    assert ((got - O).abs() <= lim).all(), ((got - O).abs() / lim).max()
+
+
 @pytest.mark.parametrize("how", ["kv by head", "kv by row", "padded rows"])
 @pytest.mark.parametrize("n", [2, 30])
 def test_attention_of_pools_with_gaps(n, how):
