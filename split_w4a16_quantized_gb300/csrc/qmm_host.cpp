@@ -1201,7 +1201,7 @@ static int check_tree(const qmm_kv_cache* c, int Hq, int T) {
     if (T > qmm::kMaxTree || Hq / c->Hkv > 64) return QMM_ESHAPE;
     // the kernels count a sequence's units of work in 32 bits, and so a CTA's
     // share of the batch's: at most this many a sequence (tiles of 64 positions
-    // and a few more, row tiles of 16, heads), over at least 64 CTAs
+    // and a few more, row tiles of 8 alone or 128 counted as 16 each, heads), over at least 64 CTAs
     const int64_t cap = static_cast<int64_t>(c->max_pages) * c->page_size;
     const int64_t rows = ceil_div(static_cast<int64_t>(T) * (Hq / c->Hkv), 16);
     const int64_t units = (cap / 64 + 16) * rows * c->Hkv;

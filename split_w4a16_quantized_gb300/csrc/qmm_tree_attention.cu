@@ -38,7 +38,7 @@ bool encode_tiled_promoted(CUtensorMap* map, CUtensorMapDataType type, int rank,
 namespace {
 
 constexpr int kTile = 64;      // positions per tile
-constexpr int kRows = 16;      // query rows per work item
+constexpr int kRows = 8;       // query rows per work item
 constexpr int kWarps = 4;      // compute warps
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kKeys = kTile / kWarps;   // positions per compute warp
@@ -102,10 +102,14 @@ __device__ __forceinline__ void mma16816(float d[4], const uint32_t a[4], uint32
 
 // ---- the kernel -------------------------------------------------------------
 //
-// CTA: 4 compute warps and one copy warp, as the contiguous decode kernel.
+// Up to 8 query rows per KV head (plain decode): half of an m16n8k16 fragment.
+// CTA: 4 compute warps and one copy warp, as the contiguous decode kernel.  Bound
+// by HBM where there is enough to read (32 sequences of 1024 to 8192 positions,
+// BF16: 78 us, 5.8 TB/s), by start-up and the merge's launch where there is not
+// (one of 1000: 9 us for both).
 //   - The copy warp loads tiles of 64 positions into a 3-stage ring, one 4-D
-//     copy per page piece and 128-byte column block, each by its own lane.  A
-//     lane looks up one table entry of the next 32 pieces at a time.  A
+//     copy per page piece and 128-byte column block.  A lane looks up one table
+//     entry of the next 32 pieces at a time, one lane issues the copies.  A
 //     missing page (or a piece past the last position) is copied from outside
 //     the map, which fills zeros; the stage's bits tell the compute warps.
 //   - Compute warp w takes positions 16w .. 16w+15 of a tile and keeps its own
@@ -120,14 +124,13 @@ __device__ __forceinline__ void mma16816(float d[4], const uint32_t a[4], uint32
 //     of the columns from the other three.
 // Every wait is bounded (1 s): a wait that runs out sets the status word and
 // the CTA winds down after its copies in flight have landed.
-template <int D, bool kFp8, bool kHalf>   // kHalf: at most 8 rows are in use
+template <int D, bool kFp8>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     tree_attn_kernel(const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap,
                      const __grid_constant__ TreeParams p) {
     using C = Cfg<D, kFp8>;
     constexpr int KS = C::KS, NB = C::NB, NQ = NB / kWarps;
-    constexpr int H = kHalf ? 1 : 2;   // row halves: rows gr and gr + 8
     extern __shared__ uint8_t tree_smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(tree_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -199,9 +202,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             const int rows = min(kRows, x.s.n * p.QG - x.row0);
             // ---- ancestors of the rows' tokens, where the stretch reaches the
             // drafted slots; a chain needs none ----
-            int node[H];
-#pragma unroll
-            for (int h = 0; h < H; ++h) node[h] = row_node(p, x.row0 + min(gr + 8 * h, rows - 1));
+            const bool on = gr < rows;
+            const int row = x.row0 + min(gr, rows - 1);
+            const int node = row_node(p, row), head = x.g * p.QG + row - node * p.QG;
             if (p.parents && x.t1 * kTile > x.s.len) {
                 for (int i = tid; i < x.s.n; i += 32 * kWarps) {
                     const int v = p.parents[x.s.first + i];
@@ -225,15 +228,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             // ---- A operand of S: rows of q, k = head dims ----
             // E4M3: dims 4 tq .. 4 tq + 3 of each 16 take the fragment's two
             // column pairs, as the 8-bit keys' loads lay them out.
-            uint32_t qa[KS][2 * H];
-            float qs[H];
-#pragma unroll
-            for (int h = 0; h < H; ++h) {
-                const int r = x.row0 + gr + 8 * h;
-                const bool on = gr + 8 * h < rows;
-                const __nv_bfloat16* qv =
-                    p.q + (on ? (x.s.first + r / p.QG) * p.q_stride + (x.g * p.QG + r % p.QG) * D : 0);
-                float big = 0.f;
+            // (rows 8 .. 15 of the fragment are zeros)
+            uint32_t qa[KS][2];
+            float qs = p.qscale, big = 0.f;
+            {
+                const __nv_bfloat16* qv = p.q + (x.s.first + node) * p.q_stride + head * D;
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
                     uint32_t lo, hi;
@@ -245,8 +244,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                         lo = *reinterpret_cast<const uint32_t*>(qv + ks * 16 + 2 * tq);
                         hi = *reinterpret_cast<const uint32_t*>(qv + ks * 16 + 8 + 2 * tq);
                     }
-                    qa[ks][h] = on ? lo : 0u;
-                    qa[ks][H + h] = on ? hi : 0u;
+                    qa[ks][0] = on ? lo : 0u;
+                    qa[ks][1] = on ? hi : 0u;
                     if (kFp8) {
                         const uint32_t a = lo & 0x7fff7fffu, c = hi & 0x7fff7fffu;
                         big = fmaxf(big, fmaxf(fmaxf(__uint_as_float(a << 16),
@@ -255,7 +254,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                                                      __uint_as_float(c & 0xffff0000u))));
                     }
                 }
-                qs[h] = p.qscale;
                 if (kFp8) {
                     big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
                     big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
@@ -264,25 +262,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     int e = static_cast<int>(__float_as_uint(big) >> 23) - 127;
                     e = big > 0.f && e < 128 ? max(-126, min(126, e)) : 0;
                     const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                    qs[h] *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+                    qs *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const uint32_t v = qa[ks][i * H + h];
-                            qa[ks][i * H + h] = pack_f16x2(__uint_as_float(v << 16) * down,
+                            const uint32_t v = qa[ks][i];
+                            qa[ks][i] = pack_f16x2(__uint_as_float(v << 16) * down,
                                                            __uint_as_float(v & 0xffff0000u) * down);
                         }
                 }
             }
-            float o[NB][2 * H];
+            float o[NB][2];
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                for (int i = 0; i < 2 * H; ++i) o[nb][i] = 0.f;
-            float m_run[H], l_run[H];   // l_run: this lane's share of the row's sum
-#pragma unroll
-            for (int h = 0; h < H; ++h) m_run[h] = -INFINITY, l_run[h] = 0.f;
+            for (int nb = 0; nb < NB; ++nb) o[nb][0] = o[nb][1] = 0.f;
+            float m_run = -INFINITY, l_run = 0.f;   // l_run: this lane's share of the row's sum
 
             for (int t = x.t0; t < x.t1; ++t, ++it) {
                 const int st = it % kStages;
@@ -316,8 +310,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
                                 const int ks = 2 * k2 + i;
-                                const uint32_t a[4] = {qa[ks][0], H == 2 ? qa[ks][H - 1] : 0u,
-                                                       qa[ks][H], H == 2 ? qa[ks][2 * H - 1] : 0u};
+                                const uint32_t a[4] = {qa[ks][0], 0u, qa[ks][1], 0u};
 #pragma unroll
                                 for (int nb = 0; nb < 2; ++nb)
                                     mma16816<true>(sc[nb], a, e4m3x2_to_f16x2(kf[2 * i + nb] & 0xffffu),
@@ -330,64 +323,54 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                         for (int ks = 0; ks < KS; ++ks) {
                             uint32_t kf[4];
                             ldmatrix_x4(kf, kt + C::off(kb + (mj >> 1) * 8 + mr, 2 * ks + (mj & 1)));
-                            const uint32_t a[4] = {qa[ks][0], H == 2 ? qa[ks][H - 1] : 0u, qa[ks][H],
-                                                   H == 2 ? qa[ks][2 * H - 1] : 0u};
+                            const uint32_t a[4] = {qa[ks][0], 0u, qa[ks][1], 0u};
                             mma16816<false>(sc[0], a, kf[0], kf[1]);
                             mma16816<false>(sc[1], a, kf[2], kf[3]);
                         }
                     }
                     // online softmax of each row over the 16 positions
-                    float pw[H][4], corr[H];
+                    float v[4];
 #pragma unroll
-                    for (int h = 0; h < H; ++h) {
-                        float v[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) v[e] = sc[e >> 1][2 * h + (e & 1)] * qs[h];
-                        if (!plain) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int k = (e >> 1) * 8 + 2 * tq + (e & 1);
-                                const int j = pos0 + k - x.s.len;   // drafted token, >= 0
-                                bool see = k < valid && ((have >> ((kb + k) >> p.box_shift)) & 1u);
-                                if (see && j >= 0)
-                                    see = p.parents
-                                              ? (sm.anc[min(gr + 8 * h, rows - 1)][j >> 5] >> (j & 31)) & 1u
-                                              : j <= node[h];
-                                if (!see) v[e] = -INFINITY;
-                            }
-                        }
-                        float mx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                        const float mn = fmaxf(m_run[h], mx);
-                        const float mf = finite_max(mn);
-                        corr[h] = fast_exp2(m_run[h] - mf);
-                        m_run[h] = mn;
-                        const float by = mf - (kFp8 ? 15.f : 0.f);
-                        float rs = 0.f;
+                    for (int e = 0; e < 4; ++e) v[e] = sc[e >> 1][e & 1] * qs;
+                    if (!plain) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            pw[h][e] = fast_exp2(v[e] - by);
-                            rs += pw[h][e];
+                            const int k = (e >> 1) * 8 + 2 * tq + (e & 1);
+                            const int j = pos0 + k - x.s.len;   // drafted token, >= 0
+                            bool see = k < valid && ((have >> ((kb + k) >> p.box_shift)) & 1u);
+                            if (see && j >= 0)
+                                see = p.parents ? (sm.anc[min(gr, rows - 1)][j >> 5] >> (j & 31)) & 1u
+                                                : j <= node;
+                            if (!see) v[e] = -INFINITY;
                         }
-                        l_run[h] = l_run[h] * corr[h] + rs;
                     }
+                    float mx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    const float mn = fmaxf(m_run, mx), mf = finite_max(mn);
+                    const float corr = fast_exp2(m_run - mf), by = mf - (kFp8 ? 15.f : 0.f);
+                    m_run = mn;
+                    float pw[4], rs = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        pw[e] = fast_exp2(v[e] - by);
+                        rs += pw[e];
+                    }
+                    l_run = l_run * corr + rs;
                     // P as the A operand of P V (rows, k = positions)
                     uint32_t ph[4] = {0, 0, 0, 0}, pl[4] = {0, 0, 0, 0};
 #pragma unroll
-                    for (int h = 0; h < H; ++h)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float a = pw[h][2 * i], c = pw[h][2 * i + 1];
-                            if (kFp8) {
-                                ph[2 * i + h] = pack_f16x2(a, c);
-                            } else {
-                                const uint32_t w = pack_bf16x2(a, c);
-                                ph[2 * i + h] = w;
-                                pl[2 * i + h] = pack_bf16x2(a - __uint_as_float(w << 16),
-                                                            c - __uint_as_float(w & 0xffff0000u));
-                            }
+                    for (int i = 0; i < 2; ++i) {
+                        const float a = pw[2 * i], c = pw[2 * i + 1];
+                        if (kFp8) {
+                            ph[2 * i] = pack_f16x2(a, c);
+                        } else {
+                            const uint32_t w = pack_bf16x2(a, c);
+                            ph[2 * i] = w;
+                            pl[2 * i] = pack_bf16x2(a - __uint_as_float(w << 16),
+                                                    c - __uint_as_float(w & 0xffff0000u));
                         }
+                    }
                     // o = o * corr + P V
 #pragma unroll
                     for (int db = 0; db < NB / 2; ++db) {
@@ -410,12 +393,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
                                     for (int n = 0; n < 2; ++n) {
                                         float* acc = o[2 * (db + i) + n];
-                                        float d4[4] = {acc[0] * corr[0], acc[1] * corr[0],
-                                                       H == 2 ? acc[2 * H - 2] * corr[H - 1] : 0.f,
-                                                       H == 2 ? acc[2 * H - 1] * corr[H - 1] : 0.f};
+                                        float d4[4] = {acc[0] * corr, acc[1] * corr, 0.f, 0.f};
                                         mma16816<true>(d4, ph, vf[2 * n], vf[2 * n + 1]);
-#pragma unroll
-                                        for (int q = 0; q < 2 * H; ++q) acc[q] = d4[q];
+                                        acc[0] = d4[0], acc[1] = d4[1];
                                     }
                                 }
                             }
@@ -425,13 +405,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
                             for (int n = 0; n < 2; ++n) {
                                 float* acc = o[2 * db + n];
-                                float d4[4] = {acc[0] * corr[0], acc[1] * corr[0],
-                                               H == 2 ? acc[2 * H - 2] * corr[H - 1] : 0.f,
-                                               H == 2 ? acc[2 * H - 1] * corr[H - 1] : 0.f};
+                                float d4[4] = {acc[0] * corr, acc[1] * corr, 0.f, 0.f};
                                 mma16816<false>(d4, ph, vf[2 * n], vf[2 * n + 1]);
                                 mma16816<false>(d4, pl, vf[2 * n], vf[2 * n + 1]);
-#pragma unroll
-                                for (int q = 0; q < 2 * H; ++q) acc[q] = d4[q];
+                                acc[0] = d4[0], acc[1] = d4[1];
                             }
                         }
                     }
@@ -442,37 +419,29 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
             // ---- merge the warps' states; warp w ends with columns
             // [w D/4, (w + 1) D/4) of every row ----
-#pragma unroll
-            for (int h = 0; h < H; ++h) {
-                l_run[h] += __shfl_xor_sync(0xffffffffu, l_run[h], 1);
-                l_run[h] += __shfl_xor_sync(0xffffffffu, l_run[h], 2);
-                if (tq == 0) {
-                    sm.wm[warp][gr + 8 * h] = m_run[h];
-                    sm.wl[warp][gr + 8 * h] = l_run[h];
-                }
+            l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
+            l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
+            if (tq == 0) {
+                sm.wm[warp][gr] = m_run;
+                sm.wl[warp][gr] = l_run;
             }
             named_bar_sync(1, 32 * kWarps);
-            float M[H], den[H], fac[H];
+            float M = -INFINITY, den = 0.f;
 #pragma unroll
-            for (int h = 0; h < H; ++h) {
-                M[h] = -INFINITY;
-                den[h] = 0.f;
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.wm[w][gr]);
+            const float mf = finite_max(M);
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) M[h] = fmaxf(M[h], sm.wm[w][gr + 8 * h]);
-                const float mf = finite_max(M[h]);
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w)
-                    den[h] = fmaf(fast_exp2(sm.wm[w][gr + 8 * h] - mf), sm.wl[w][gr + 8 * h], den[h]);
-                fac[h] = fast_exp2(m_run[h] - mf);
-            }
-            float acc[NQ][2 * H];
+            for (int w = 0; w < kWarps; ++w)
+                den = fmaf(fast_exp2(sm.wm[w][gr] - mf), sm.wl[w][gr], den);
+            const float fac = fast_exp2(m_run - mf);
+            float acc[NQ][2];
 #pragma unroll
             for (int qq = 0; qq < kWarps; ++qq)
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                    for (int i = 0; i < 2 * H; ++i) {
-                        o[qq * NQ + n][i] *= fac[i >> 1];
+                    for (int i = 0; i < 2; ++i) {
+                        o[qq * NQ + n][i] *= fac;
                         if (qq == warp) acc[n][i] = o[qq * NQ + n][i];
                     }
             // round i: warp w hands columns of warp (w + i) % 4 over
@@ -484,20 +453,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     if (qq == to)
 #pragma unroll
                         for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                            for (int h = 0; h < H; ++h)
-                                *reinterpret_cast<float2*>(&sm.ex[to][gr + 8 * h][n * 8 + 2 * tq]) =
-                                    make_float2(o[qq * NQ + n][2 * h], o[qq * NQ + n][2 * h + 1]);
+                            *reinterpret_cast<float2*>(&sm.ex[to][gr][n * 8 + 2 * tq]) =
+                                make_float2(o[qq * NQ + n][0], o[qq * NQ + n][1]);
                 named_bar_sync(1, 32 * kWarps);
 #pragma unroll
-                for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                    for (int h = 0; h < H; ++h) {
-                        const float2 v =
-                            *reinterpret_cast<const float2*>(&sm.ex[warp][gr + 8 * h][n * 8 + 2 * tq]);
-                        acc[n][2 * h] += v.x;
-                        acc[n][2 * h + 1] += v.y;
-                    }
+                for (int n = 0; n < NQ; ++n) {
+                    const float2 v =
+                        *reinterpret_cast<const float2*>(&sm.ex[warp][gr][n * 8 + 2 * tq]);
+                    acc[n][0] += v.x;
+                    acc[n][1] += v.y;
+                }
                 named_bar_sync(1, 32 * kWarps);
             }
             // (the other warps may not have seen the flag yet: this one goes on to
@@ -505,22 +470,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             if (*abort) continue;
             // ---- O, or the partial state ----
             const bool whole = x.t0 == 0 && x.t1 == x.s.tiles;
-            const int slot = 2 * blockIdx.x + (x.t0 == 0 ? 1 : 0);
-            const PartialAt part = partial_at<D>(p, slot);
-#pragma unroll
-            for (int h = 0; h < H; ++h) {
-                const int r = gr + 8 * h;
-                if (r >= rows) continue;
-                const float inv = whole ? (den[h] > 0.f ? p.vscale / den[h]
-                                                        : (den[h] == 0.f ? 0.f : den[h]))
-                                        : 1.f;
+            const PartialAt part = partial_at<D>(p, 2 * blockIdx.x + (x.t0 == 0 ? 1 : 0));
+            if (on) {
+                const float inv =
+                    whole ? (den > 0.f ? p.vscale / den : (den == 0.f ? 0.f : den)) : 1.f;
                 if (!whole && warp == 0 && tq == 0) {
-                    part.m[r] = M[h];
-                    part.l[r] = den[h];
+                    part.m[gr] = M;
+                    part.l[gr] = den;
                 }
-                const int rr = x.row0 + r;
-                __nv_bfloat16* out = p.O + (static_cast<int64_t>(x.s.first + rr / p.QG) * p.Hq +
-                                            x.g * p.QG + rr % p.QG) * D;
+                __nv_bfloat16* out =
+                    p.O + (static_cast<int64_t>(x.s.first + node) * p.Hq + head) * D;
 #pragma unroll
                 for (int n = 0; n < NQ; n += kFp8 ? 2 : 1) {
                     // columns: BF16 8 n + 2 tq + {0, 1}; E4M3 n-blocks 2i (even
@@ -528,22 +487,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     const int c = (warp * NQ + n) * 8 + (kFp8 ? 4 : 2) * tq;
                     if (kFp8) {
                         const int n1 = n + 1 < NQ ? n + 1 : n;
-                        const float4 v = make_float4(acc[n][2 * h] * inv, acc[n1][2 * h] * inv,
-                                                     acc[n][2 * h + 1] * inv, acc[n1][2 * h + 1] * inv);
+                        const float4 v = make_float4(acc[n][0] * inv, acc[n1][0] * inv,
+                                                     acc[n][1] * inv, acc[n1][1] * inv);
                         if (whole)
                             *reinterpret_cast<uint2*>(out + c) =
                                 make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
                         else
-                            *reinterpret_cast<float4*>(part.at(r, c)) = v;
+                            *reinterpret_cast<float4*>(part.at(gr, c)) = v;
                     } else {
-                        const float2 v = make_float2(acc[n][2 * h] * inv, acc[n][2 * h + 1] * inv);
+                        const float2 v = make_float2(acc[n][0] * inv, acc[n][1] * inv);
                         if (whole)
                             *reinterpret_cast<uint32_t*>(out + c) = pack_bf16x2(v.x, v.y);
                         else
-                            *reinterpret_cast<float2*>(part.at(r, c)) = v;
+                            *reinterpret_cast<float2*>(part.at(gr, c)) = v;
                     }
                 }
             }
+            __syncwarp();
         }
     }
     __syncthreads();
@@ -665,10 +625,10 @@ __global__ void __launch_bounds__(kMergeThreads)
     }
 }
 
-template <int D, bool kFp8, bool kHalf>
+template <int D, bool kFp8>
 int launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, cudaStream_t st) {
     using C = Cfg<D, kFp8>;
-    auto kern = tree_attn_kernel<D, kFp8, kHalf>;
+    auto kern = tree_attn_kernel<D, kFp8>;
     const size_t smem = 1024 + static_cast<size_t>(kStages) * C::STAGE + sizeof(Smem<D>);
     static int ok = -1;
     static std::once_flag once;
@@ -701,21 +661,23 @@ int launch_merge(const TreeParams& p, int D, cudaStream_t st) {
                     : cudaLaunchKernelEx(&cfg, tree_merge_kernel<64>, p, row_tiles, chunks);
 }
 
-template <int D, bool kFp8>
-int launch_rows(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p,
-                cudaStream_t st) {
-    return p.T * p.QG <= 8 ? launch<D, kFp8, true>(kmap, vmap, p, st)
-                           : launch<D, kFp8, false>(kmap, vmap, p, st);
-}
-
 // The kernel for `rows` query rows per KV head, its rows per work item, CTAs
-// per SM and shortest run.
+// per SM, shortest run and an item's fixed units.  Measured on both sides of each
+// border with 32 sequences of 500 to 16000 positions, D = 128 (us), unless said:
+//   8 rows: this file's kernel.  4 rows of one sequence of 1000: 9.6, the
+//     tcgen05 kernel 12.2 (its start and drain are longer); 64 sequences of 1000
+//     to 4000, E4M3: 73 and 81, BF16: 99 and 98.
+//   9 to 128 rows: tcgen05, one group.  16 rows: 105, E4M3 77, with both row halves
+//     of this file's fragments in use 132 and 113.  128 rows: 123, E4M3 109, with
+//     two groups of a single CTA per SM 127 and 140.
+//   more: two groups of 128 rows that share the K and V tiles.  256 rows: 143,
+//     E4M3 173; one group that reads them twice 212 and 204.
 struct Variant {
     bool tc;
     int row_shift, tile_shift, ctas_per_sm, min_run, setup;
 };
 Variant variant(int rows) {
-    if (rows <= kRows) return {false, 4, 6, kCtasPerSm, 2, 1};
+    if (rows <= kRows) return {false, 3, 6, kCtasPerSm, 2, 1};
     if (rows <= 128) return {true, 7, kTcTileShift, 2, 6, 4};
     return {true, 8, kTcTileShift, 1, 6, 4};
 }
@@ -784,11 +746,11 @@ int launch_tree_attention(const qmm_kv_cache& c, const void* q, int64_t q_stride
     if (var.tc)
         rc = launch_tree_tc(kmap, vmap, p, c.D, fp8, st);
     else if (c.D == 128)
-        rc = fp8 ? launch_rows<128, true>(kmap, vmap, p, st)
-                 : launch_rows<128, false>(kmap, vmap, p, st);
+        rc = fp8 ? launch<128, true>(kmap, vmap, p, st)
+                 : launch<128, false>(kmap, vmap, p, st);
     else
-        rc = fp8 ? launch_rows<64, true>(kmap, vmap, p, st)
-                 : launch_rows<64, false>(kmap, vmap, p, st);
+        rc = fp8 ? launch<64, true>(kmap, vmap, p, st)
+                 : launch<64, false>(kmap, vmap, p, st);
     return rc == cudaSuccess ? launch_merge(p, c.D, st) : rc;
 }
 

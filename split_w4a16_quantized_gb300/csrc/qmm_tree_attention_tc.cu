@@ -1,4 +1,4 @@
-// Tree attention for more than 16 query rows per KV head (qmm_tree_attention):
+// Tree attention for more than 8 query rows per KV head (qmm_tree_attention):
 // the products on the 5th-generation tensor cores.
 //
 // The formulas and the work split are those of qmm_tree_attention.cu.  Here a
@@ -18,7 +18,7 @@
 //   one or two softmax groups of 128 threads, a thread a row; E4M3 cache: turn
 //     their rows of q into two terms first
 // A group has two buffers of S: while it turns one into P, the products of the
-// other run, and with them the 480 clocks an MMA takes to be seen as done.  P
+// other run, and with them the 130 to 480 clocks a commit takes to be seen.  P
 // overwrites S in place (BF16 or F16 in half the columns).
 //   MMA order of a group:  ... P(i) V(i), Q K(i+2) | P(i+1) V(i+1), Q K(i+3) ...
 //   up to 128 rows: one group, two CTAs per SM, because each item ends with a few
@@ -38,6 +38,20 @@
 // cache) whatever its scale.  One BF16 term of P, where the kernel for few rows
 // keeps two: the second would double the P V products, and its error is that of
 // rounding the output.
+//
+// What bounds it (152 SMs; a tile is 64 positions, D = 128).
+//   BF16, up to 128 rows: HBM; 32 sequences of 16 tokens (64 rows), 500 to 16000
+//     positions: 112 us, 5.5 TB/s.  Short ones: the start (5 us to the first
+//     scores: plan, table, copy) and the merge; 8 of 8 tokens, 1500 to 4000:
+//     26 us, floor 12.6.
+//   BF16, 256 rows: the tensor cores with the hand-overs between their issue and
+//     the softmax; 16 sequences of 64 tokens, 8000 positions: 124 to 130 us, 1.05
+//     PFLOP/s.  An SM's products need 1,270 clocks a tile, 620 a group (measured
+//     alone and beside the softmax's tensor-memory traffic), of about 2,000.
+//   E4M3, up to 128 rows: shared memory.  The products read q again for every
+//     tile (two terms, 32 KB) and V is converted through it (8 KB read, 16
+//     written, 16 read): with K and the copies 104 KB, 830 clocks of an SM's
+//     bandwidth a tile, of 930; 32 sequences of 16 tokens: 85 us, 3.6 TB/s.
 //
 // E4M3 cache.  Q K^T runs on the 8-bit keys as they are: a BF16 number has 8
 // significant bits, so a row of q, scaled by a power of two to a maximum in
