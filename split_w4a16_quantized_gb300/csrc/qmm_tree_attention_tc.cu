@@ -41,13 +41,13 @@
 //
 // What bounds it (152 SMs; a tile is 64 positions, D = 128).
 //   BF16, up to 128 rows: HBM; 32 sequences of 16 tokens (64 rows), 500 to 16000
-//     positions: 112 us, 5.5 TB/s.  Short ones: the start (5 us to the first
+//     positions: 106 us, 5.8 TB/s.  Short ones: the start (5 us to the first
 //     scores: plan, table, copy) and the merge; 8 of 8 tokens, 1500 to 4000:
-//     26 us, floor 12.6.
+//     24 us, floor 12.6.
 //   BF16, 256 rows: the tensor cores with the hand-overs between their issue and
-//     the softmax; 16 sequences of 64 tokens, 8000 positions: 124 to 130 us, 1.05
-//     PFLOP/s.  An SM's products need 1,270 clocks a tile, 620 a group (measured
-//     alone and beside the softmax's tensor-memory traffic), of about 2,000.
+//     the softmax; 16 sequences of 64 tokens, 8000 positions: 118 us, 1.15
+//     PFLOP/s.  An SM's products need 1,240 clocks a tile, 620 a group (measured
+//     alone and beside the softmax's tensor-memory traffic), of about 1,900.
 //   E4M3, up to 128 rows: shared memory.  The products read q again for every
 //     tile (two terms, 32 KB) and V is converted through it (8 KB read, 16
 //     written, 16 read): with K and the copies 104 KB, 830 clocks of an SM's
@@ -107,7 +107,7 @@ struct TcSmem {
     uint32_t tmem;
     int abort;
     int have[kHave];                    // pages of a tile that exist, one bit a copy
-    int pages[16];                      // of the tile being copied
+    int pages[2][16];                   // of the tiles being copied
     int16_t par[kMaxTree];
     alignas(16) uint4 stage[4 * kGroups][128];   // by warp: 32 rows x 32 BF16 columns of O
     uint32_t anc[128 * kGroups][kWords + 1];     // a thread's own row: ancestors and itself
@@ -302,40 +302,51 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
         if (warp == 0) {
             // ---- copies: one thread waits and issues (a vote or a block of its own
             // for each would cost 200 clocks, a sixth of a tile's time) ----
+            // K runs a tile ahead of V, as the products want them (8 sequences of 8
+            // tokens: 24.3 us, in step 26.4); not where V has yet to be converted
+            // (E4M3, 32 of 16 tokens: in step 86, ahead 91).
+            constexpr int kLead = kFp8 ? 0 : 1;
             Cursor kc, vc;
             int nk = 0, nv = 0;   // of the issuing thread: tiles of K and of V
-            int it = 0;           // tiles
+            int it = 0;           // tiles of K
             int zeroed = 0;       // (BF16) V slots until one that was zeroed in part comes round
             bool ok = true;
+            auto copy = [&](const CUtensorMap* map, uint64_t* bar, uint8_t* slot, int t) {
+                mbar_arrive_expect_tx(bar, C::SLOT);
+                copy_tile<kTile, C::BOXES, C::BOX, C::BOX / (kFp8 ? 1 : 2)>(
+                    p, map, bar, smem_addr(slot), sm.pages[t & 1], t, x.g);
+            };
             while (ok && next_stretch(p, run, &x)) {
                 PageWalk<kTile> walk;
                 walk.start(p, x, lane);
-                for (int t = x.t0; t < x.t1; ++t, ++it) {
-                    const uint32_t have = walk.tile(p, t, lane, sm.pages);
+                for (int t = x.t0 - kLead; ok && t < x.t1; ++t) {
+                    const bool more = t + kLead < x.t1;
+                    uint32_t have = 0;
+                    if (more) have = walk.tile(p, t + kLead, lane, sm.pages[(t + kLead) & 1]);
                     if (elect_one()) {
-                        if (wait_one(&sm.kempty[kc.slot], kc.phase ^ 1)) {
+                        bool go = true;
+                        if (more && (go = wait_one(&sm.kempty[kc.slot], kc.phase ^ 1))) {
                             sm.have[it % kHave] = static_cast<int>(have);
-                            mbar_arrive_expect_tx(&sm.kfull[kc.slot], C::SLOT);
-                            copy_tile<kTile, C::BOXES, C::BOX, C::BOX / (kFp8 ? 1 : 2)>(p, &kmap, &sm.kfull[kc.slot],
-                                                     smem_addr(k_s) + kc.slot * C::SLOT, sm.pages, t,
-                                                     x.g);
+                            copy(&kmap, &sm.kfull[kc.slot], k_s + kc.slot * C::SLOT, t + kLead);
                             ++nk;
-                            if (wait_one(&sm.vempty[vc.slot], vc.phase ^ 1)) {
-                                // the slot was converted from with ordinary loads, or
-                                // zeroed in part with ordinary stores
-                                if (kFp8 || zeroed > 0) fence_proxy_async_smem();
-                                mbar_arrive_expect_tx(&sm.vfull[vc.slot], C::SLOT);
-                                copy_tile<kTile, C::BOXES, C::BOX, C::BOX / (kFp8 ? 1 : 2)>(p, &vmap, &sm.vfull[vc.slot],
-                                                         smem_addr(v_s) + vc.slot * C::SLOT, sm.pages,
-                                                         t, x.g);
-                                ++nv;
-                            }
+                        }
+                        if (go && t >= x.t0 && wait_one(&sm.vempty[vc.slot], vc.phase ^ 1)) {
+                            // the slot was converted from with ordinary loads, or
+                            // zeroed in part with ordinary stores
+                            if (kFp8 || zeroed > 0) fence_proxy_async_smem();
+                            copy(&vmap, &sm.vfull[vc.slot], v_s + vc.slot * C::SLOT, t);
+                            ++nv;
                         }
                     }
-                    zeroed = (t + 1) * kTile > x.s.total ? lay.v_slots : max(0, zeroed - 1);
-                    kc.next(lay.k_slots);
-                    vc.next(lay.v_slots);
-                    if (!(ok = !__any_sync(0xffffffffu, *abort))) break;
+                    if (more) {
+                        kc.next(lay.k_slots);
+                        ++it;
+                    }
+                    if (t >= x.t0) {
+                        zeroed = (t + 1) * kTile > x.s.total ? lay.v_slots : max(0, zeroed - 1);
+                        vc.next(lay.v_slots);
+                    }
+                    ok = !__any_sync(0xffffffffu, *abort);
                 }
             }
             if (!ok && elect_one()) {  // let the copies in flight land before the CTA exits

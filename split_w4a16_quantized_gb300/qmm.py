@@ -722,6 +722,8 @@ def kv_cache(K: torch.Tensor, V: torch.Tensor, table: torch.Tensor, lens: torch.
 
 def kv_caches(caches) -> "ctypes.Array":
     """The layers' caches as the array qmm_tree_accept takes."""
+    if not len(caches):
+        raise ValueError("at least one cache")
     arr = (qmm_kv_cache * len(caches))(*caches)
     arr.tensors = [c.tensors for c in caches]
     arr.device = caches[0].device
