@@ -527,6 +527,96 @@ def test_pools_beyond_32_bits():
         assert torch.equal(a.view(torch.int16), b.view(torch.int16))
 
 
+@pytest.mark.parametrize("T", [4, 40])
+def test_attention_ranges_without_tokens_and_longer_than_T(T):
+    pb = Problem([20, 30], [T + 3, T], 2, 64, 16)
+    q = torch.randn((pb.N, 4, 64), device="cuda").bfloat16()
+    ws = torch.empty(Q.qmm_tree_attention_workspace_bytes(pb.cache, 4, T), dtype=torch.uint8,
+                     device="cuda")
+    O = torch.full_like(q, 7.0)
+    Q.qmm_tree_attention(pb.cache, q, O, T, cu=_dev(np.zeros(3, np.int32)), workspace=ws)
+    torch.cuda.synchronize()
+    assert (O == 7.0).all()
+    Q.qmm_tree_attention(pb.cache, q, O, T, cu=_dev(pb.cu), workspace=ws)
+    want = torch.full_like(q, 7.0)          # the first T of the first sequence, a chain
+    cu = np.array([0, T, T], np.int32)
+    Q.qmm_tree_attention(pb.cache, q, want, T, cu=_dev(cu), workspace=ws)
+    torch.cuda.synchronize()
+    assert (O[T:T + 3] == 7.0).all() and not (O[T + 3:] == 7.0).any()
+    assert torch.equal(O[:T].view(torch.int16), want[:T].view(torch.int16))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lens,n", [(0, 3), (5, 7), (0, 20), (3, 40), (8, 200)])
+def test_attention_more_tokens_than_slots(lens, n, dtype):
+    """A chain that runs past the table's one page: the tokens there see what
+    exists."""
+    pb = Problem([lens], [8 - lens], 2, 64, 8, dtype, width=1)
+    rng = np.random.default_rng(n)
+    pb.n, pb.cu, pb.N, pb.T = [n], np.array([0, n], np.int32), n, n
+    q = torch.from_numpy(rng.standard_normal((n, 8, 64))).bfloat16()
+    pb.uniform = True
+    got = [_run_attention(pb, q.cuda(), par).cpu().double()
+           for par in (None, np.arange(-1, n - 1))]
+    assert torch.equal(*got)
+    K, V = pb.values[0][0], pb.values[1][0]
+    for i in range(n):
+        m = min(lens + i + 1, 8)
+        s = torch.einsum("hgd,lhd->hgl", q[i].double().view(2, 4, 64), K[:m]) / 8
+        want = torch.einsum("hgl,lhd->hgd", s.softmax(-1), V[:m]).reshape(8, 64)
+        # O's rounding, the weights' and (64 + 2) 2^-24 of |q k| / 8 < 32 each in exp
+        lim = (2 * BF16_HALF + 2 * 66 * F32_HALF * 32 + 1024 * F32_HALF) * V[:m].abs().max()
+        assert (got[0][i] - want).abs().max() <= lim
+
+
+def test_calls_from_several_threads():
+    """Host threads with a stream and a workspace each, all kernels at once."""
+    import threading
+    jobs, errors = [], []
+    for t, (n, dtype) in enumerate([(1, "bf16"), (8, "e4m3"), (40, "bf16"), (2, "e4m3")]):
+        pb = Problem([300, 40], [n] * 2, 2, 128, 16, dtype, seed=t)
+        q = torch.randn((pb.N, 8, 128), device="cuda").bfloat16()
+        par = np.concatenate([np.arange(-1, n - 1)] * 2).astype(np.int32)
+        want = _run_attention(pb, q, par)
+        ws = torch.empty(Q.qmm_tree_attention_workspace_bytes(pb.cache, 8, n), dtype=torch.uint8,
+                         device="cuda")
+        jobs.append((pb, q, _dev(par), want, torch.zeros_like(q), ws, torch.cuda.Stream(), n))
+    torch.cuda.synchronize()
+
+    def work(pb, q, par, want, O, ws, stream, n):
+        try:
+            for _ in range(100):
+                Q.qmm_tree_attention(pb.cache, q, O, n, parents=par, workspace=ws,
+                                     stream=stream.cuda_stream)
+            stream.synchronize()
+        except Exception as e:                                  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for _, _, _, want, O, _, _, _ in jobs:
+        assert torch.equal(O.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("n", [1, 12, 80])
+def test_attention_without_programmatic_launch(n):
+    pb = Problem([500, 3], [n] * 2, 2, 128, 16)
+    q = torch.randn((pb.N, 8, 128), device="cuda").bfloat16()
+    want = _run_attention(pb, q, None)
+    torch.cuda.synchronize()
+    Q.qmm_set_pdl(0)
+    try:
+        got = _run_attention(pb, q, None)
+        torch.cuda.synchronize()
+    finally:
+        Q.qmm_set_pdl(1)
+    assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+
+
 # ---- append ---------------------------------------------------------------------
 
 def _cos_sin(rows, dim, base=1e4):
