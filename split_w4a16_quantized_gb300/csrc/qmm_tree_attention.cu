@@ -671,21 +671,28 @@ int launch_merge(const TreeParams& p, int D, cudaStream_t st) {
 //     of this file's fragments in use 132 and 113.  128 rows: 123, E4M3 109, with
 //     two groups of a single CTA per SM 127 and 140.
 //   more: two groups of 128 rows that share the K and V tiles.  256 rows: 143,
-//     E4M3 173; one group that reads them twice 212 and 204.
+//     E4M3 154; one group that reads them twice 212 and 204.
+// Shortest run: 6 units of the tcgen05 kernel (one sequence of 8 tokens behind 1000
+// positions: 3 10.9, 6 11.7, 12 14.9; two of 16 behind 1000 to 4000: 17.3, 15.9,
+// 17.1), 2 of this one (one token behind 1000: 1 11.0, 2 9.7, 4 10.5).
+// Fixed units (what an item costs beside its tiles, in tiles: its q, drain and
+// output): 4, with an E4M3 cache, whose tiles are cheaper and whose q has to be
+// turned, 8 (256 rows: 2 191, 4 174, 8 154, 12 158; BF16, 64 ragged sequences of up to
+// 5 tokens, D = 64: 2 125, 4 121, 8 124).
 struct Variant {
     bool tc;
     int row_shift, tile_shift, ctas_per_sm, min_run, setup;
 };
-Variant variant(int rows) {
+Variant variant(int rows, bool fp8) {
     if (rows <= kRows) return {false, 3, 6, kCtasPerSm, 2, 1};
-    if (rows <= 128) return {true, 7, kTcTileShift, 2, 6, 4};
-    return {true, 8, kTcTileShift, 1, 6, 4};
+    if (rows <= 128) return {true, 7, kTcTileShift, 2, 6, fp8 ? 8 : 4};
+    return {true, 8, kTcTileShift, 1, 6, fp8 ? 8 : 4};
 }
 
 }  // namespace
 
 size_t tree_attention_workspace(int D, int rows, int num_sms) {
-    const Variant v = variant(rows);
+    const Variant v = variant(rows, false);   // (the same for either type)
     return (static_cast<size_t>(2 * v.ctas_per_sm * num_sms) << v.row_shift) * (D + 2) *
            sizeof(float);
 }
@@ -708,7 +715,7 @@ int launch_tree_attention(const qmm_kv_cache& c, const void* q, int64_t q_stride
     p.Hq = Hq;
     p.QG = Hq / c.Hkv;
     p.qg_inv = ((1u << 22) + p.QG - 1) / p.QG;
-    const Variant var = variant(T * p.QG);
+    const Variant var = variant(T * p.QG, c.dtype == QMM_CACHE_E4M3);
     p.ctas = var.ctas_per_sm * num_sms;
     p.row_shift = var.row_shift;
     p.tile_shift = var.tile_shift;

@@ -51,7 +51,7 @@
 //   E4M3, up to 128 rows: shared memory.  The products read q again for every
 //     tile (two terms, 32 KB) and V is converted through it (8 KB read, 16
 //     written, 16 read): with K and the copies 104 KB, 830 clocks of an SM's
-//     bandwidth a tile, of 930; 32 sequences of 16 tokens: 85 us, 3.6 TB/s.
+//     bandwidth a tile, of 910; 32 sequences of 16 tokens: 83 us, 3.7 TB/s.
 //
 // E4M3 cache.  Q K^T runs on the 8-bit keys as they are: a BF16 number has 8
 // significant bits, so a row of q, scaled by a power of two to a maximum in
