@@ -720,8 +720,9 @@ int qmm_kv_append(const qmm_kv_cache *cache, const void *q, const void *k, const
  *         chain (parent i - 1).
  * Token i attends to slots 0 .. lens[b]-1 and lens[b] + j for j = i and every
  * ancestor j of i:  O = sum_l softmax_l(scale * q . K_l) V_l, scores, softmax
- * and sums in FP32, the weights rounded once for the product with V.  scale <= 0
- * means 1/sqrt(D).  A token that sees no position (none of its pages exists)
+ * and sums in FP32, the weights rounded once for the product with V.  For an
+ * E4M3 cache, values of q below 2^-9 of the largest of their head are rounded to
+ * 2^-17 of it.  scale <= 0 means 1/sqrt(D).  A token that sees no position (none of its pages exists)
  * gets zeros.  Positions out of sight do not enter the sums, whatever their
  * slots hold, except that a drafted token's V row must be finite where some
  * other token of its sequence does not see it.
