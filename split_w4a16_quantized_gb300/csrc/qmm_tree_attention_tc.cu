@@ -304,8 +304,9 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
             // for each would cost 200 clocks, a sixth of a tile's time) ----
             // K runs a tile ahead of V, as the products want them (8 sequences of 8
             // tokens: 24.3 us, in step 26.4); not where V has yet to be converted
-            // (E4M3, 32 of 16 tokens: in step 86, ahead 91).
-            constexpr int kLead = kFp8 ? 0 : 1;
+            // (E4M3, 32 of 16 tokens: in step 86, ahead 91) or tiles are half as
+            // large (D = 64, 64 ragged of up to 5: in step 118, ahead 122).
+            constexpr int kLead = kFp8 || D == 64 ? 0 : 1;
             Cursor kc, vc;
             int nk = 0, nv = 0;   // of the issuing thread: tiles of K and of V
             int it = 0;           // tiles of K
