@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
     const uint32_t tmem = sm.tmem;
     Run run = find_run<C::THREADS>(p, sm.run);
     const int pieces = kTile >> p.box_shift;
-    Stretch x;
+    Stretch x = {};
     // (test_wait answers in 60 clocks where the phase is complete, as it mostly
     // is; try_wait takes 170)
     auto wait_one = [&](uint64_t* bar, int phase) {
