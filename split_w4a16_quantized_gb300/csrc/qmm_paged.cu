@@ -11,7 +11,9 @@
 // neighbours or nothing turns.  So a pair never crosses lanes, the lane's four
 // cosines and sines serve all its rows, and the arithmetic runs on two values
 // an instruction (f32x2).  The first rows are asked for before the chain of
-// loads (range, length, page) that says where they go.
+// loads (range, length, page) that says where they go.  16384 tokens of 32 q and 8
+// k and v heads, D = 128: 78 us, 5.3 TB/s (a plain copy of as many bytes: 68); one
+// token: 3.1 us in a graph, latency.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -380,9 +382,10 @@ int launch_kv_append(const qmm_kv_cache& c, const void* q, const void* k, const 
         p.interleaved = rope->interleaved;
         p.eps = rope->eps;
     }
-    // lane groups per token: one per head row where the call is small (latency),
-    // else as few as leave kAppendQ q rows, or one k and v row, a group (bytes in
-    // flight)
+    // lane groups per token: one per head row where the call is small (latency:
+    // one token of 8 heads 2.4 us, with fewer groups 3.0), else as few as leave
+    // kAppendQ q rows, or one k and v row, a group (bytes in flight: 2452 tokens of
+    // 24 heads, D = 64: 5.4 us, with a group a row 6.8)
     const int groups = kAppendThreads / (c.D / 8), rows = Hq > c.Hkv ? Hq : c.Hkv;
     const bool small = static_cast<int64_t>(N) * rows <= 4 * 152 * groups;
     p.per_token = 1;
@@ -430,7 +433,8 @@ int launch_tree_accept(const qmm_kv_cache* caches, int n, const int* tokens, con
         p.pools[2 * i + 1] = static_cast<uint8_t*>(caches[i].V);
     }
     // columns per block: a block's walk and table look-ups take longer than its
-    // moves, so the blocks fill the SMs once (4 of them each) and no more
+    // moves, so the blocks fill the SMs once (4 of them each) and no more (64
+    // sequences, 36 layers: 13.9 us; 2 blocks an SM 17.9, 8 15.6)
     const int64_t cols = static_cast<int64_t>(2) * n * c.Hkv;
     const int groups = kAcceptThreads / (p.row_bytes / 16);
     const int64_t share = (cols * c.B - 1) / (4 * 152) + 1;
