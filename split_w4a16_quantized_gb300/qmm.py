@@ -802,8 +802,10 @@ def qmm_kv_append(cache: qmm_kv_cache, q: torch.Tensor | None, k: torch.Tensor, 
                   stream=None) -> None:
     """Rotate q [N, Hq, D] into q_out and append k, v [N, Hkv, D] (bf16; token
     strides free, so views of one fused projection do) behind the cached
-    tokens.  q may be None (only append); q_out may be q.  positions int32 [N]
-    and cu int32 [B + 1]: see qmm.h."""
+    tokens.  q and q_out may both be None (only append); q_out may be q.
+    positions int32 [N] and cu int32 [B + 1]: see qmm.h."""
+    if (q is None) != (q_out is None):
+        raise ValueError("qmm_kv_append: q and q_out come together")
     device = cache.device
     if not (k.get_device() == device == v.get_device() and _current(device) and
             (q is None or q.get_device() == device == q_out.get_device()) and

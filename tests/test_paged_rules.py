@@ -58,3 +58,16 @@ def test_unused_strides_through_the_host_only_entry():
     assert nb(num_pages=2, page_stride=3, Hkv=1, head_stride=-5) == 0
     assert nb(num_pages=1, page_stride=3, Hkv=2, head_stride=-5) == 0
     assert nb(num_pages=1, page_stride=3, Hkv=2, head_stride=16 * 128) > 0
+
+
+@pytest.mark.parametrize("which", ["q alone", "q_out alone"])
+def test_append_takes_q_and_q_out_together(which):
+    """Either both or neither, said before anything is asked of the tensors."""
+    c = _cache()
+    c.device = 0
+    x = torch.zeros((4, 8, 128), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="q and q_out"):
+        Q.qmm_kv_append(c, x if which == "q alone" else None, x, x,
+                        None if which == "q alone" else x)
+    with pytest.raises(ValueError, match="q and q_out"):
+        Q.qmm_kv_append(c, *((x, x, x) if which == "q alone" else (None, x, x, x)))
