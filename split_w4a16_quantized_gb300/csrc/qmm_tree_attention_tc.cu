@@ -629,8 +629,9 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                     const float up = bad ? __int_as_float(0x7fffffff)
                                          : __uint_as_float(static_cast<uint32_t>(134 - e) << 23);
                     qs *= __uint_as_float(static_cast<uint32_t>(120 + e) << 23);
-                    // the first term is the value cut to 4 significant bits, the
-                    // second the 4 bits that were cut off
+                    // the first term is the value rounded to 4 significant bits, the
+                    // second what is left of it (at most 4 bits), both to a
+                    // multiple of E4M3's smallest, 2^-9
 #pragma unroll 1
                     for (int c = 0; c < D / 16; ++c) {
                         uint4* const at = reinterpret_cast<uint4*>(row_s + tile_off<C::BOX, 128>(gt, c));
@@ -642,12 +643,12 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                         for (int i = 0; i < 8; ++i) {
                             const float f0 = __uint_as_float(w[i] << 16) * up;
                             const float f1 = __uint_as_float(w[i] & 0xffff0000u) * up;
-                            const float h0 = __uint_as_float(__float_as_uint(f0) & 0xfff00000u);
-                            const float h1 = __uint_as_float(__float_as_uint(f1) & 0xfff00000u);
-                            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(h0, h1),
+                            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f0, f1),
                                                                          __NV_SATFINITE, __NV_E4M3);
+                            const uint32_t back = e4m3x2_to_f16x2(hi);
+                            const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&back));
                             const uint32_t lo = __nv_cvt_float2_to_fp8x2(
-                                make_float2(f0 - h0, f1 - h1), __NV_SATFINITE, __NV_E4M3);
+                                make_float2(f0 - h.x, f1 - h.y), __NV_SATFINITE, __NV_E4M3);
                             if (i % 2 == 0) t[0][i / 2] = hi, t[1][i / 2] = lo;
                             else t[0][i / 2] |= hi << 16, t[1][i / 2] |= lo << 16;
                         }

@@ -1,0 +1,66 @@
+"""Paged-cache calls on a GB300 at the borders of their numbers and their memory."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from split_w4a16_quantized_gb300 import qmm as Q
+from test_paged_gpu import BF16_HALF, F16_HALF, F32_HALF, Problem, _attention64, _dev, \
+    _run_attention, _tree
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _status():
+    yield
+    torch.cuda.synchronize()
+    assert Q.qmm_kernel_status(clear=True) == 0
+
+
+def _set_rows(pb, pool, values):
+    """One sequence's rows: values [lens + n, Hkv, D] of what its cache stores."""
+    for s in range(len(values)):
+        (pb.K, pb.V)[pool][int(pb.table[0, s // pb.page]), :, s % pb.page] = \
+            values[s].float().to(pb.K.dtype).cuda()
+    pb.values[pool][0] = values.double() * pb.scales[pool]
+
+
+# ---- values of q far below the largest of their head -----------------------------
+
+@pytest.mark.parametrize("n,D", [(1, 128), (12, 128), (12, 64), (80, 128)])
+def test_small_values_of_q_beside_a_large_one(n, D):
+    """E4M3 cache: q holds one value of 128, where the keys are zero, and one small
+    value c elsewhere, where they are +-448: scores are all made of c.  c is held
+    to 2^-17 of the row's largest value, and exactly from 2^-9 of it on."""
+    pb = Problem([96], [n], 2, D, 16, "e4m3", seed=2, k_scale=2.0 ** -10, v_scale=2.0 ** -6)
+    rng = np.random.default_rng(n)
+    sign = np.where(np.arange(96 + n) % 2 == 0, 1.0, -1.0)
+    k = torch.from_numpy(np.broadcast_to(448.0 * sign[:, None, None], (96 + n, 2, D)).copy())
+    k[:, :, 0] = 0
+    v = torch.from_numpy(np.broadcast_to(64.0 * sign[:, None, None], (96 + n, 2, D)).copy())
+    _set_rows(pb, 0, k)
+    _set_rows(pb, 1, v)
+    # 8-bit significands 2^-12 to 2^-1; among them 0.0097046, whose 4 leading bits
+    # alone lie between two E4M3 numbers
+    c = rng.integers(128, 256, (n, 4)) * 2.0 ** (-7 - rng.integers(1, 12, (n, 4)))
+    c[0, 0] = 159 * 2.0 ** -14
+    q = torch.from_numpy(np.broadcast_to(c[:, :, None], (n, 4, D)).copy()).bfloat16()
+    assert (q[:, :, 1].double().numpy() == c).all()
+    q[:, :, 0] = 128.0
+    parents = np.arange(-1, n - 1).astype(np.int32)
+    # scale such that c's allowed error moves a score by 0.05
+    worst = (D - 1) * 448 * 2.0 ** -10                 # |key| of a score, as stored
+    scale = 0.05 / (worst * 128 * 2.0 ** -17)
+    got = _run_attention(pb, q.cuda(), parents, scale).cpu().double()
+    O, _, S = _attention64(pb, q, parents, scale)
+    # each score off by delta at most (c's rounding, 0 from 2^-9 on, and FP32:
+    # (D + 2) 2^-24 of sum |q k|): weights by a factor within exp(+-delta), and as
+    # |V| = 1, sum p |v - O| = 1 - O^2 takes it to O.  Second order: delta^2.
+    # Then F16 weights, sums below 2^-24 * 1024, and O's own rounding.
+    small = torch.from_numpy(c) < 128 * 2.0 ** -9
+    delta = (torch.where(small, 0.05, 0.0) + 2 * (D + 2) * F32_HALF * S)[..., None]
+    lim = BF16_HALF * O.abs() + (1 - O * O) * delta + delta ** 2 + F16_HALF + 1024 * F32_HALF
+    off = (got - O).abs()
+    assert (off <= lim).all(), (off / lim).max()
