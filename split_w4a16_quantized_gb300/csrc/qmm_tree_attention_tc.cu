@@ -625,7 +625,7 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                     // becomes NaN (what its softmax would be)
                     int e = static_cast<int>(big >> 23) - 127;
                     const bool bad = e >= 128;
-                    e = big > 0 && !bad ? max(-110, min(126, e)) : 0;
+                    e = big > 0 && !bad ? max(-110, e) : 0;
                     const float up = bad ? __int_as_float(0x7fffffff)
                                          : __uint_as_float(static_cast<uint32_t>(134 - e) << 23);
                     qs *= __uint_as_float(static_cast<uint32_t>(120 + e) << 23);

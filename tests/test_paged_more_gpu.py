@@ -64,3 +64,28 @@ def test_small_values_of_q_beside_a_large_one(n, D):
     lim = BF16_HALF * O.abs() + (1 - O * O) * delta + delta ** 2 + F16_HALF + 1024 * F32_HALF
     off = (got - O).abs()
     assert (off <= lim).all(), (off / lim).max()
+
+
+@pytest.mark.parametrize("n,D", [(1, 128), (12, 128), (12, 64), (80, 128)])
+def test_largest_values_of_q(n, D):
+    """E4M3 cache, values of q in the last binade that BF16 has: 249 and -223 times
+    2^120 against the same key, so that the score is made of their difference."""
+    ks = 2.0 ** -60
+    pb = Problem([96], [n], 2, D, 16, "e4m3", seed=2, k_scale=ks, v_scale=2.0 ** -6)
+    sign = np.where(np.arange(96 + n) % 2 == 0, 1.0, -1.0)
+    k = torch.zeros((96 + n, 2, D), dtype=torch.float64)
+    k[:, :, 3] = k[:, :, D - 7] = torch.from_numpy(2.0 ** -6 * sign)[:, None]
+    _set_rows(pb, 0, k)
+    _set_rows(pb, 1, torch.from_numpy(64.0 * sign)[:, None, None].expand(96 + n, 2, D))
+    q = torch.zeros((n, 4, D), dtype=torch.float64)
+    q[:, :, 3], q[:, :, D - 7] = 249 * 2.0 ** 120, -223 * 2.0 ** 120
+    q = q.bfloat16()
+    parents = np.arange(-1, n - 1).astype(np.int32)
+    scale = 0.5 / (26 * 2.0 ** 114 * ks)
+    got = _run_attention(pb, q.cuda(), parents, scale).cpu().double()
+    O, _, S = _attention64(pb, q, parents, scale)
+    # as above, without a rounding of q: every value has 8 bits
+    delta = (2 * (D + 2) * F32_HALF * S)[..., None]
+    lim = BF16_HALF * O.abs() + (1 - O * O) * delta + delta ** 2 + F16_HALF + 1024 * F32_HALF
+    off = (got - O).abs()
+    assert (off <= lim).all(), (off / lim).max()
