@@ -346,6 +346,12 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 // Maximum that every later exp2 can subtract: 0 while nothing is visible.
 __device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0.f : m; }
 
+// A positive factor on scores, kept from 0 and infinity (0 times a masked score
+// is NaN, and so is infinity times a score of 0).
+__device__ __forceinline__ float finite_factor(float x) {
+    return fminf(fmaxf(x, __uint_as_float(1u)), __uint_as_float(0x7f7fffffu));
+}
+
 // 2^x, one instruction (ex2.approx: 2 ulp, results below 2^-126 are 0).
 __device__ __forceinline__ float fast_exp2(float x) {
     float y;

@@ -22,6 +22,8 @@
 // a CTA, and the merge kernel adds them in run order: the bits do not depend
 // on timing.  Equal runs keep every SM busy to the end whatever the lengths,
 // and the workspace is two states per CTA whatever the batch.
+#include <algorithm>
+#include <limits>
 #include <mutex>
 
 #include "qmm.h"
@@ -262,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     int e = static_cast<int>(__float_as_uint(big) >> 23) - 127;
                     e = big > 0.f && e < 128 ? max(-126, min(126, e)) : 0;
                     const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                    qs *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+                    qs = finite_factor(qs * __uint_as_float(static_cast<uint32_t>(127 + e) << 23));
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
@@ -724,7 +726,12 @@ int launch_tree_attention(const qmm_kv_cache& c, const void* q, int64_t q_stride
     p.min_run = var.min_run;
     p.setup = var.setup;
     p.box_shift = p.d.page_shift < p.tile_shift ? p.d.page_shift : p.tile_shift;
-    p.qscale = scale * 1.4426950408889634f * c.k_scale;  // log2(e): exp2 of the scaled score
+    // log2(e): exp2 of the scaled score.  Neither 0 nor infinity, whatever scale and
+    // k_scale: times a masked score (-inf) or a score of 0 those would be NaN.
+    const double factor = static_cast<double>(scale) * 1.4426950408889634 * c.k_scale;
+    p.qscale = static_cast<float>(
+        std::min(std::max(factor, static_cast<double>(std::numeric_limits<float>::denorm_min())),
+                 static_cast<double>(std::numeric_limits<float>::max())));
     p.vscale = c.v_scale;
     // K and V as [pages, heads, slots, D], copied a page piece and 128 bytes of
     // columns at a time

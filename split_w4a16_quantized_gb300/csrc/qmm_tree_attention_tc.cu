@@ -628,7 +628,7 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                     e = big > 0 && !bad ? max(-110, e) : 0;
                     const float up = bad ? __int_as_float(0x7fffffff)
                                          : __uint_as_float(static_cast<uint32_t>(134 - e) << 23);
-                    qs *= __uint_as_float(static_cast<uint32_t>(120 + e) << 23);
+                    qs = finite_factor(qs * __uint_as_float(static_cast<uint32_t>(120 + e) << 23));
                     // the first term is the value rounded to 4 significant bits, the
                     // second what is left of it (at most 4 bits), both to a
                     // multiple of E4M3's smallest, 2^-9

@@ -6,8 +6,8 @@ import pytest
 import torch
 
 from split_w4a16_quantized_gb300 import qmm as Q
-from test_paged_gpu import BF16_HALF, F16_HALF, F32_HALF, Problem, _attention64, _dev, \
-    _run_attention, _tree
+from test_paged_gpu import BF16_HALF, F16_HALF, F32_HALF, Problem, _attention64, _check_attention, \
+    _dev, _run_attention, _tree
 
 pytestmark = pytest.mark.gpu
 
@@ -89,3 +89,30 @@ def test_largest_values_of_q(n, D):
     lim = BF16_HALF * O.abs() + (1 - O * O) * delta + delta ** 2 + F16_HALF + 1024 * F32_HALF
     off = (got - O).abs()
     assert (off <= lim).all(), (off / lim).max()
+
+
+# ---- factors on the scores at the ends of FP32 ------------------------------------
+
+@pytest.mark.parametrize("n", [1, 12, 80])
+def test_score_factors_below_fp32(n):
+    """scale * k_scale below FP32's smallest number: every visible position weighs
+    the same, and masked ones nothing.  The same where a row of q makes it so."""
+    keys = 20 * torch.from_numpy(np.random.default_rng(n).standard_normal((100 + n, 2, 128)))
+    for k_scale, scale, q_scale in ((1e-30, 1e-20, 2.0), (1e-12, 0.0, 1e-34), (1.0, 1e-45, 2.0)):
+        dtype = "bf16" if k_scale == 1.0 else "e4m3"
+        pb = Problem([100], [n], 2, 128, 16, dtype, k_scale=k_scale)
+        _set_rows(pb, 0, keys.float().to(pb.K.dtype).float())
+        got = _check_attention(pb, 8, "star", scale=scale, q_scale=q_scale)
+        assert torch.isfinite(got.float()).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 12, 80])
+def test_score_factors_above_fp32(n, dtype):
+    """scale * log2(e) * k_scale past FP32's largest number, and keys of zero: all
+    scores are 0."""
+    pb = Problem([100], [n], 2, 128, 16, dtype, k_scale=1e10)
+    _set_rows(pb, 0, torch.zeros((100 + n, 2, 128)))
+    assert torch.isfinite(_check_attention(pb, 8, "tree", scale=3e38).float()).all()
+    if dtype == "e4m3":
+        _check_attention(pb, 8, "tree", scale=1e20, q_scale=1e37)
