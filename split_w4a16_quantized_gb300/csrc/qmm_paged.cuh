@@ -65,14 +65,26 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
     return r;
 }
 
+// A value of lens or cu.  kFromL2: at GPU scope, past this SM's L1, for a kernel
+// that reads it before its own dependency wait.
+template <bool kFromL2>
+__device__ __forceinline__ int plan_value(const int* at) {
+    if (!kFromL2) return *at;
+    int v;
+    asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(at));
+    return v;
+}
+
 // Tokens in the cache of sequence b before the call.
+template <bool kFromL2 = false>
 __device__ __forceinline__ int cached_tokens(const PagedDims& d, int b) {
-    const int len = d.lens[b];
+    const int len = plan_value<kFromL2>(d.lens + b);
     return len < 0 ? 0 : (len > d.cap ? d.cap : len);
 }
 
 // New tokens of sequence b: rows [first, first + n).  cu's values are the
 // caller's device data, so they are clamped to the N rows there are.
+template <bool kFromL2 = false>
 __device__ __forceinline__ void token_range(const int* cu, int N, int T, int b, int* first,
                                             int* n) {
     if (!cu) {
@@ -80,7 +92,7 @@ __device__ __forceinline__ void token_range(const int* cu, int N, int T, int b, 
         *n = T;
         return;
     }
-    int a = cu[b], e = cu[b + 1];
+    int a = plan_value<kFromL2>(cu + b), e = plan_value<kFromL2>(cu + b + 1);
     a = a < 0 ? 0 : (a > N ? N : a);
     e = e < a ? a : (e > N ? N : e);
     *first = a;

@@ -69,10 +69,11 @@ struct Seq {
     int row_tiles;
 };
 
+template <bool kFromL2 = false>
 __device__ __forceinline__ Seq sequence(const TreeParams& p, int b) {
     Seq s;
-    token_range(p.cu, p.N, p.T, b, &s.first, &s.n);
-    s.len = cached_tokens(p.d, b);
+    token_range<kFromL2>(p.cu, p.N, p.T, b, &s.first, &s.n);
+    s.len = cached_tokens<kFromL2>(p.d, b);
     s.total = s.len + s.n < p.d.cap ? s.len + s.n : p.d.cap;
     s.tiles = (s.total + (1 << p.tile_shift) - 1) >> p.tile_shift;
     s.row_tiles = (s.n * p.QG + (1 << p.row_shift) - 1) >> p.row_shift;

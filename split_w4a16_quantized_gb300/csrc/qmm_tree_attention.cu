@@ -514,11 +514,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 // The items that a run border cuts: O = sum_c 2^(m_c - M) o_c / sum_c
 // 2^(m_c - M) l_c over the runs c that hold a stretch, in ascending c.  One
 // block per item and 16 of its rows: a thread takes a row and every 16th (D =
-// 128; 64: 8th) group of 4 columns.  The plan is worked out while the attention
-// kernel still runs: that kernel lets this one start only after everything
-// before it has ended, so lens and cu are final.  Bound by latency: one trip to the
-// states, 2 to 3 us behind the attention kernel of a small call; 16 sequences of 64
-// tokens (two states of most of 32768 rows, 33 MB): 20 us alone with a cold L2.
+// 128; 64: 8th) group of 4 columns.  Up to 256 sequences, a thread's one each, the
+// plan is worked out while the attention kernel still runs (one token behind 1000:
+// 9.4 us, behind the wait 10.0; 8 sequences of 8: 23.8 and 25.2).  That kernel's
+// threads let this one start only after their own wait for everything before it, so
+// lens and cu are final in L2, and are read there, not through an L1 that may hold
+// older lines.  More sequences: behind the wait and through L1, where a block's many
+// values come from (1024 of one token: 206 us, ahead from L2 214).  Bound by latency:
+// one trip to the states, 2 to 3 us behind the attention kernel of a small call; 16
+// sequences of 64 tokens (two states of most of 32768 rows, 33 MB): 20 us alone with
+// a cold L2.
 constexpr int kMergeThreads = 256;
 constexpr int kMergeRows = 16;
 constexpr int kMergeAhead = 4;   // states whose loads a thread has in flight
@@ -526,20 +531,43 @@ template <int D>
 __global__ void __launch_bounds__(kMergeThreads)
     tree_merge_kernel(const __grid_constant__ TreeParams p, int max_row_tiles, int chunks) {
     __shared__ long long red[2][kMergeThreads / 32];
+    __shared__ Seq own;
     __shared__ __align__(16) uint2 stage[kMergeRows][D / 4 + 2];   // BF16 rows, padded by 16 bytes
     const int chunk = blockIdx.x % chunks, item = blockIdx.x / chunks;
     const int rt = item % max_row_tiles, g = item / max_row_tiles, b = blockIdx.y;
-    const Seq s = sequence(p, b);
+    const bool ahead = p.d.B <= kMergeThreads;
+    if (!ahead) {
+        pdl_trigger();
+        pdl_wait();
+    }
     const int row0 = rt << p.row_shift;
-    const int rows = min(1 << p.row_shift, s.n * p.QG - row0);
-    int c0 = 0, c1 = 0;
-    if (rt < s.row_tiles && chunk * kMergeRows < rows) {
-        long long all, before;
-        if (p.d.B <= 32) {
-            const int lane = threadIdx.x & 31;
-            const long long mine = lane < p.d.B ? units_of(p, sequence(p, lane)) : 0;
-            before = __shfl_sync(0xffffffffu, warp_scan(mine, &all), b);
-        } else {
+    auto has_rows = [&](const Seq& x) {
+        return rt < x.row_tiles && chunk * kMergeRows < min(1 << p.row_shift, x.n * p.QG - row0);
+    };
+    Seq s;
+    long long all = 0, before = 0;
+    if (p.d.B <= 32) {
+        const int lane = threadIdx.x & 31;
+        s = sequence<true>(p, min(lane, p.d.B - 1));
+        const long long mine = lane < p.d.B ? units_of(p, s) : 0;
+        before = __shfl_sync(0xffffffffu, warp_scan(mine, &all), b);
+        s.first = __shfl_sync(0xffffffffu, s.first, b);
+        s.n = __shfl_sync(0xffffffffu, s.n, b);
+        s.tiles = __shfl_sync(0xffffffffu, s.tiles, b);
+        s.row_tiles = __shfl_sync(0xffffffffu, s.row_tiles, b);
+    } else if (ahead) {
+        long long mine = 0;
+        if (threadIdx.x < p.d.B) {
+            s = sequence<true>(p, threadIdx.x);
+            mine = units_of(p, s);
+            if (threadIdx.x == b) own = s;
+        }
+        block_scan<kMergeThreads>(mine, red[0], &all);
+        block_scan<kMergeThreads>(threadIdx.x < b ? mine : 0, red[1], &before);
+        s = own;
+    } else {
+        s = sequence(p, b);
+        if (has_rows(s)) {   // (the same for the whole block)
             long long mine = 0, upto = 0;
             for (int i = threadIdx.x; i < p.d.B; i += kMergeThreads) {
                 const int u = units_of(p, sequence(p, i));
@@ -549,14 +577,20 @@ __global__ void __launch_bounds__(kMergeThreads)
             block_scan<kMergeThreads>(mine, red[0], &all);
             block_scan<kMergeThreads>(upto, red[1], &before);
         }
+    }
+    const int rows = min(1 << p.row_shift, s.n * p.QG - row0);
+    int c0 = 0, c1 = 0;
+    if (has_rows(s)) {
         const long long len = run_length(p, all);
         const int units = item_units(p, s);
         const long long start = before + static_cast<long long>(g * s.row_tiles + rt) * units;
         c0 = static_cast<int>((start + p.setup) / len);
         c1 = static_cast<int>((start + units - 1) / len);
     }
-    pdl_trigger();
-    pdl_wait();
+    if (ahead) {
+        pdl_trigger();
+        pdl_wait();
+    }
     if (c0 == c1) return;
     constexpr int GROUPS = D / 4;
     constexpr int TURNS = GROUPS / (kMergeThreads / kMergeRows);   // column groups of a thread

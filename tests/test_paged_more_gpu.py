@@ -116,3 +116,47 @@ def test_score_factors_above_fp32(n, dtype):
     assert torch.isfinite(_check_attention(pb, 8, "tree", scale=3e38).float()).all()
     if dtype == "e4m3":
         _check_attention(pb, 8, "tree", scale=1e20, q_scale=1e37)
+
+
+# ---- lengths that change between calls in flight -----------------------------------
+
+@pytest.mark.parametrize("n", [1, 3, 12])
+@pytest.mark.parametrize("B", [3, 40, 300])
+def test_lengths_written_right_before_the_call(B, n):
+    """Calls back to back on one stream, each behind a kernel that writes its
+    lengths (and, every other time, ranges): both kernels of a call see those."""
+    rng = np.random.default_rng(B + n)
+    pb = Problem([400 if B < 100 else 60] * B, [n] * B, 2, 64, 16, seed=B)
+    q = torch.from_numpy(rng.standard_normal((pb.N, 8, 64))).bfloat16().cuda()
+    ws = torch.empty(Q.qmm_tree_attention_workspace_bytes(pb.cache, 8, n), dtype=torch.uint8,
+                     device="cuda")
+    d_lens, d_cu = torch.zeros_like(pb.d_lens), torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    cache = Q.kv_cache(pb.K, pb.V, pb.d_table, d_lens)
+    # one token a sequence and no child: accept writes new_lens = lens + 1
+    one = torch.zeros(B, dtype=torch.int32, device="cuda")
+    path, count = torch.zeros((B, 1), dtype=torch.int32, device="cuda"), torch.zeros_like(one)
+    sets = []
+    for _ in range(5):
+        base = _dev(rng.integers(0, pb.lens[0], B).astype(np.int32))
+        sets.append((base, Q.kv_caches([Q.kv_cache(pb.K, pb.V, pb.d_table, base)]),
+                     _dev(np.concatenate([[0], np.cumsum(rng.integers(0, n + 1, B))]).astype(np.int32))))
+
+    def call(i, O):
+        base, caches, cu = sets[i % 5]
+        if i % 2:
+            d_cu.copy_(cu)
+        Q.qmm_tree_accept(caches, one, one, 1, path, count, new_lens=d_lens)
+        Q.qmm_tree_attention(cache, q, O, n, cu=d_cu if i % 2 else None, workspace=ws)
+
+    want = [torch.full_like(q, 7.0) for _ in range(10)]
+    for i, O in enumerate(want):
+        call(i, O)
+        torch.cuda.synchronize()
+        assert torch.equal(d_lens, sets[i % 5][0] + 1)
+    got = [torch.full_like(q, 7.0) for _ in range(200)]
+    torch.cuda.synchronize()
+    for i, O in enumerate(got):
+        call(i, O)
+    torch.cuda.synchronize()
+    for i, O in enumerate(got):
+        assert torch.equal(O.view(torch.int16), want[i % 10].view(torch.int16)), i
