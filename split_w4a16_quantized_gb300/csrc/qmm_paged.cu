@@ -115,10 +115,12 @@ __global__ void __launch_bounds__(kAppendThreads, 8) kv_append_kernel(const Appe
     struct In {
         uint2 lo, hi;
     };
+    // (ordinary loads: q_out may be q, and the read-only path is not for memory
+    // that the kernel writes)
     auto load = [&](const __nv_bfloat16* row, int h) {
         In x;
-        x.lo = __ldg(reinterpret_cast<const uint2*>(row + h * D + at_lo));
-        x.hi = __ldg(reinterpret_cast<const uint2*>(row + h * D + at_hi));
+        x.lo = *reinterpret_cast<const uint2*>(row + h * D + at_lo);
+        x.hi = *reinterpret_cast<const uint2*>(row + h * D + at_hi);
         return x;
     };
     In qi[kAppendQ], ki, vi;
@@ -195,11 +197,15 @@ __global__ void __launch_bounds__(kAppendThreads, 8) kv_append_kernel(const Appe
     };
 
     for (int h0 = sub; h0 < Hq; h0 += kAppendQ * step) {
+        if (h0 != sub) {
+#pragma unroll
+            for (int u = 0; u < kAppendQ; ++u)
+                if (h0 + u * step < Hq) qi[u] = load(qrow, h0 + u * step);
+        }
 #pragma unroll
         for (int u = 0; u < kAppendQ; ++u) {
             const int h = h0 + u * step;
             if (h >= Hq) break;
-            if (h0 != sub) qi[u] = load(qrow, h);
             float x[8];
             turned(qi[u], p.q_norm, x);
             __nv_bfloat16* out = p.q_out + tok * p.q_out_stride + h * D;

@@ -160,3 +160,31 @@ def test_lengths_written_right_before_the_call(B, n):
     torch.cuda.synchronize()
     for i, O in enumerate(got):
         assert torch.equal(O.view(torch.int16), want[i % 10].view(torch.int16)), i
+
+
+# ---- append in place -------------------------------------------------------------
+
+@pytest.mark.parametrize("N,Hq,Hkv,D", [(5, 8, 2, 128), (700, 8, 2, 64), (900, 200, 4, 128),
+                                        (300, 333, 1, 64)])
+def test_append_in_place_equals_out_of_place(N, Hq, Hkv, D):
+    """q_out = q, from fewer heads than a lane group holds at once to many times
+    that: the same q and the same cache as with an output of its own."""
+    rng = np.random.default_rng(N)
+    x = torch.from_numpy(rng.standard_normal((N, Hq + 2 * Hkv, D))).bfloat16().cuda()
+    ang = np.arange(N)[:, None] * 1e4 ** (-np.arange(0, D, 2) / D)
+    cs = torch.from_numpy(np.concatenate([np.cos(ang), np.sin(ang)], 1)).float().cuda()
+    w = torch.from_numpy(1 + 0.2 * rng.standard_normal(D)).bfloat16().cuda()
+    rope = Q.rope(cs, q_norm=w, k_norm=w)
+    got = []
+    for in_place in (False, True):
+        pages = -(-N // 16)
+        pools = [torch.zeros((pages, Hkv, 16, D), dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+        cache = Q.kv_cache(*pools, torch.arange(pages, dtype=torch.int32, device="cuda")[None],
+                           torch.zeros(1, dtype=torch.int32, device="cuda"))
+        y = x.clone()
+        out = y[:, :Hq] if in_place else torch.empty((N, Hq, D), dtype=torch.bfloat16, device="cuda")
+        Q.qmm_kv_append(cache, y[:, :Hq], y[:, Hq:Hq + Hkv], y[:, Hq + Hkv:], out, rope=rope)
+        assert torch.equal(y[:, Hq:], x[:, Hq:]) and (in_place or torch.equal(y, x))
+        got.append([t.contiguous().view(torch.int16) for t in (out, *pools)])
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
