@@ -362,9 +362,9 @@ __device__ __forceinline__ float fast_exp2(float x) {
 
 // One launch of the tcgen05 kernel (qmm_tree_attention_tc.cu); the merge
 // kernel is the caller's.  Items of up to 128 rows (row_shift 7, two CTAs per
-// SM) or 256 (8, one).
+// SM) or 256 (8, one); device: the current one.
 constexpr int kTcTileShift = 6;
 int launch_tree_tc(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int D,
-                   bool fp8, cudaStream_t st);
+                   bool fp8, int device, cudaStream_t st);
 
 }  // namespace qmm

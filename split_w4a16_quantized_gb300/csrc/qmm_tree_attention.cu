@@ -24,9 +24,9 @@
 // and the workspace is two states per CTA whatever the batch.
 #include <algorithm>
 #include <limits>
-#include <mutex>
 
 #include "qmm.h"
+#include "qmm_per_device.h"
 #include "qmm_tree.cuh"
 
 namespace qmm {
@@ -664,17 +664,17 @@ __global__ void __launch_bounds__(kMergeThreads)
 }
 
 template <int D, bool kFp8>
-int launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, cudaStream_t st) {
+int launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int device,
+           cudaStream_t st) {
     using C = Cfg<D, kFp8>;
     auto kern = tree_attn_kernel<D, kFp8>;
     const size_t smem = 1024 + static_cast<size_t>(kStages) * C::STAGE + sizeof(Smem<D>);
-    static int ok = -1;
-    static std::once_flag once;
-    std::call_once(once, [&] {
-        ok = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  static_cast<int>(smem)) == cudaSuccess;
-    });
-    if (ok != 1) return cudaErrorInvalidValue;
+    static PerDevice<bool> opted_in;
+    if (!opted_in.get(device, [&] {
+            return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        static_cast<int>(smem)) == cudaSuccess;
+        }))
+        return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     LaunchAttrs la;
     apply_pdl(cfg, la);
@@ -739,6 +739,8 @@ int launch_tree_attention(const qmm_kv_cache& c, const void* q, int64_t q_stride
                           int T, int Hq, const int* cu, const int* parents, float scale,
                           float* ws, int num_sms, void* stream) {
     TreeParams p = {};
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) return cudaErrorInvalidDevice;
     p.status = tc_status_ptr();
     if (!p.status) return cudaErrorInvalidSymbol;
     p.d = paged_dims(c);
@@ -795,13 +797,13 @@ int launch_tree_attention(const qmm_kv_cache& c, const void* q, int64_t q_stride
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int rc;
     if (var.tc)
-        rc = launch_tree_tc(kmap, vmap, p, c.D, fp8, st);
+        rc = launch_tree_tc(kmap, vmap, p, c.D, fp8, device, st);
     else if (c.D == 128)
-        rc = fp8 ? launch<128, true>(kmap, vmap, p, st)
-                 : launch<128, false>(kmap, vmap, p, st);
+        rc = fp8 ? launch<128, true>(kmap, vmap, p, device, st)
+                 : launch<128, false>(kmap, vmap, p, device, st);
     else
-        rc = fp8 ? launch<64, true>(kmap, vmap, p, st)
-                 : launch<64, false>(kmap, vmap, p, st);
+        rc = fp8 ? launch<64, true>(kmap, vmap, p, device, st)
+                 : launch<64, false>(kmap, vmap, p, device, st);
     return rc == cudaSuccess ? launch_merge(p, c.D, st) : rc;
 }
 

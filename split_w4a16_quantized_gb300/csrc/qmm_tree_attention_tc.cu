@@ -61,9 +61,9 @@
 // one large weight would vanish), so V is converted to F16, exactly, and P is
 // F16, times 2^7: at most 2^15, and 11 bits down to 2^-21 of the reference.
 #include <algorithm>
-#include <mutex>
 
 #include "qmm.h"
+#include "qmm_per_device.h"
 #include "qmm_tree.cuh"
 
 namespace qmm {
@@ -855,12 +855,13 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
 }
 
 template <int D, bool kFp8, int kGroups>
-int launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, cudaStream_t st) {
+int launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int device,
+           cudaStream_t st) {
     using C = Tc<D, kFp8, kGroups>;
     auto kern = tree_tc_kernel<D, kFp8, kGroups>;
-    static int limit = -1;
-    static std::once_flag once;
-    std::call_once(once, [&] { limit = set_max_dynamic_smem(reinterpret_cast<const void*>(kern)); });
+    static PerDevice<int> limits;
+    const int limit =
+        limits.get(device, [&] { return set_max_dynamic_smem(reinterpret_cast<const void*>(kern)); });
     // the rings share what Q and the converted tiles leave; two CTAs of an SM
     // have 114 KB each, 1 KB of it the system's
     const int room = C::CTAS_PER_SM == 1 ? limit : std::min(limit, 113 * 1024);
@@ -887,21 +888,21 @@ int launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p
 }
 
 template <int D, bool kFp8>
-int launch_groups(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p,
+int launch_groups(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int device,
                   cudaStream_t st) {
-    return p.row_shift == 7 ? launch<D, kFp8, 1>(kmap, vmap, p, st)
-                            : launch<D, kFp8, 2>(kmap, vmap, p, st);
+    return p.row_shift == 7 ? launch<D, kFp8, 1>(kmap, vmap, p, device, st)
+                            : launch<D, kFp8, 2>(kmap, vmap, p, device, st);
 }
 
 }  // namespace
 
 int launch_tree_tc(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int D,
-                   bool fp8, cudaStream_t st) {
+                   bool fp8, int device, cudaStream_t st) {
     if (D == 128)
-        return fp8 ? launch_groups<128, true>(kmap, vmap, p, st)
-                   : launch_groups<128, false>(kmap, vmap, p, st);
-    return fp8 ? launch_groups<64, true>(kmap, vmap, p, st)
-               : launch_groups<64, false>(kmap, vmap, p, st);
+        return fp8 ? launch_groups<128, true>(kmap, vmap, p, device, st)
+                   : launch_groups<128, false>(kmap, vmap, p, device, st);
+    return fp8 ? launch_groups<64, true>(kmap, vmap, p, device, st)
+               : launch_groups<64, false>(kmap, vmap, p, device, st);
 }
 
 }  // namespace qmm

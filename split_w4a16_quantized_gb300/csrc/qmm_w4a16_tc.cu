@@ -44,6 +44,7 @@
 
 #include "qmm_device.cuh"
 #include "qmm_internal.h"
+#include "qmm_per_device.h"
 #include "qmm_sm100.cuh"
 
 namespace qmm {
@@ -99,13 +100,13 @@ bool encode_tiled(CUtensorMap* map, CUtensorMapDataType type, int rank, const vo
 }
 
 int* tc_status_ptr() {
-    static int* ptr = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
+    static PerDevice<int*> ptrs;
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) return nullptr;
+    return ptrs.get(device, [] {
         void* p = nullptr;
-        if (cudaGetSymbolAddress(&p, g_tc_status) == cudaSuccess) ptr = static_cast<int*>(p);
+        return cudaGetSymbolAddress(&p, g_tc_status) == cudaSuccess ? static_cast<int*>(p) : nullptr;
     });
-    return ptr;
 }
 
 

@@ -71,3 +71,49 @@ def test_append_takes_q_and_q_out_together(which):
                         None if which == "q alone" else x)
     with pytest.raises(ValueError, match="q and q_out"):
         Q.qmm_kv_append(c, *((x, x, x) if which == "q alone" else (None, x, x, x)))
+
+
+PER_DEVICE = r"""
+#include <cstdio>
+#include <thread>
+#include <vector>
+#include <atomic>
+#include "qmm_per_device.h"
+static std::atomic<int> made[100];
+static qmm::PerDevice<int> values;
+static int value(int device) {   // 0 stands for a device that refused
+    return values.get(device, [=] { ++made[device]; return device == 3 ? 0 : 1000 + device; });
+}
+int main() {
+    std::vector<std::thread> threads;
+    std::atomic<int> wrong{0};
+    for (int t = 0; t < 8; ++t)
+        threads.emplace_back([&, t] {
+            for (int i = 0; i < 500; ++i) {
+                const int d = (i * 7 + t) % 66;
+                wrong += value(d) != (d == 3 ? 0 : 1000 + d);
+            }
+        });
+    for (auto& t : threads) t.join();
+    int once = 0;
+    for (int d = 0; d < 64; ++d) once += made[d] == 1;
+    std::printf("%d %d %d\n", wrong.load(), once, made[64] > 1 && made[65] > 1);
+}
+"""
+
+
+def test_what_belongs_to_a_device_is_asked_once_for_each(tmp_path):
+    """The shared-memory opt-in of a kernel and the status word's address: a second
+    device gets its own, from whichever thread, and no launch asks twice."""
+    import shutil
+    import subprocess
+    src, exe = tmp_path / "per_device.cpp", tmp_path / "per_device"
+    src.write_text(PER_DEVICE)
+    csrc = os.path.join(os.path.dirname(HERE), "split_w4a16_quantized_gb300", "csrc")
+    subprocess.run([shutil.which("g++"), "-std=c++17", "-O1", "-pthread", "-I", csrc, str(src),
+                    "-o", str(exe)], check=True)
+    out = subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout
+    assert out.split() == ["0", "64", "1"]
+    for name in ("qmm_tree_attention.cu", "qmm_tree_attention_tc.cu"):
+        text = open(os.path.join(csrc, name)).read()
+        assert "PerDevice" in text and "once_flag" not in text, name
