@@ -188,3 +188,126 @@ def test_append_in_place_equals_out_of_place(N, Hq, Hkv, D):
         got.append([t.contiguous().view(torch.int16) for t in (out, *pools)])
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+# ---- memory around the buffers ----------------------------------------------------
+
+class Guarded:
+    """Buffers of exact size inside larger ones whose rest holds a pattern."""
+    PAD = 1 << 16
+
+    def __init__(self):
+        self.all = []
+
+    def like(self, t, fill=None):
+        """A copy of t (or its shape and type, filled) with guards on both sides."""
+        n = t.numel() * t.element_size()
+        raw = torch.full((n + 2 * self.PAD,), 0xA5, dtype=torch.uint8, device="cuda")
+        view = raw[self.PAD:self.PAD + n].view(t.dtype).view(t.shape)
+        view.copy_(t) if fill is None else view.fill_(fill)
+        self.all.append((raw, n))
+        return view
+
+    def check(self):
+        torch.cuda.synchronize()
+        for raw, n in self.all:
+            assert (raw[:self.PAD] == 0xA5).all() and (raw[self.PAD + n:] == 0xA5).all()
+
+
+def _guarded_cache(pb, g):
+    """pb's cache with guards around its pools, table and lengths."""
+    nhd = pb.K.stride(2) > pb.K.stride(1)
+    pools = []
+    for t in (pb.K, pb.V):
+        base = t.transpose(1, 2) if nhd else t
+        assert base.is_contiguous()
+        base = g.like(base.view(torch.uint8)).view(t.dtype).view(base.shape)
+        pools.append(base.transpose(1, 2) if nhd else base)
+    return pools, Q.kv_cache(*pools, g.like(pb.d_table), g.like(pb.d_lens), *pb.scales)
+
+
+@pytest.mark.parametrize("cu", [[0, 99, 3, 12], [0, 4, 8, 2 ** 31 - 1], [12, 8, 4, 0],
+                                [0, 12, 12, 12], [3, 5, 5, 9]])
+@pytest.mark.parametrize("T", [4, 12])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_ranges_out_of_order_write_only_their_rows(cu, T, dtype):
+    """cu is device data: its values are clamped.  Rows of no range, slots of no
+    token and everything around the buffers stay as they were."""
+    pb = Problem([30, 14, 47], [4, 4, 4], 2, 64, 16, dtype)
+    N, g = 12, Guarded()
+    (K, V), cache = _guarded_cache(pb, g)
+    d_cu = g.like(_dev(np.array(cu, np.int64).astype(np.int32)))
+    q = g.like(torch.randn((N, 8, 64), device="cuda").bfloat16())
+    O, q_out = g.like(q, 7.0), g.like(q, 7.0)
+    k, v = (g.like(torch.randn((N, 2, 64), device="cuda").bfloat16()) for _ in range(2))
+    nb = Q.qmm_tree_attention_workspace_bytes(cache, 8, T)
+    ws = g.like(torch.empty(nb, dtype=torch.uint8, device="cuda"), 0xFF)
+    bits = torch.int8 if dtype == "e4m3" else torch.int16
+    old = [t.contiguous().view(bits).clone() for t in (K, V)]
+    Q.qmm_tree_attention(cache, q, O, T, cu=d_cu, workspace=ws)
+    g.check()
+    rows = set()
+    for b in range(3):
+        a = min(max(cu[b], 0), N)
+        e = min(max(cu[b + 1], a), N)
+        rows |= set(range(a, min(e, a + T)))
+    for r in range(N):
+        assert bool((O[r] == 7.0).all()) == (r not in rows), r
+    assert all(torch.equal(t.contiguous().view(bits), o) for t, o in zip((K, V), old))
+    Q.qmm_kv_append(cache, q, k, v, q_out, cu=d_cu)
+    g.check()
+    want = [o.clone() for o in old]
+    written = set()
+    for t in range(N):
+        b = sum(c <= t for c in cu[1:])
+        if b < 3 and t >= cu[b]:
+            written.add(t)
+            s = pb.lens[b] + t - cu[b]
+            if s < pb.width * 16 and 0 <= pb.table[b, s // 16] < K.shape[0]:
+                for w, x, pool, sc in zip(want, (k, v), (K, V), pb.scales):
+                    y = (x[t].float() / sc).clamp(-448, 448) if dtype == "e4m3" else x[t]
+                    w[int(pb.table[b, s // 16]), :, s % 16] = y.to(pool.dtype).view(bits)
+    for r in range(N):
+        assert torch.equal(q_out[r], q[r]) if r in written else (q_out[r] == 7.0).all(), r
+    assert all(torch.equal(t.contiguous().view(bits), w) for t, w in zip((K, V), want))
+
+
+@pytest.mark.parametrize("lens,n,Hq,Hkv,D,page,dtype,layout", [
+    ([70, 3], [1, 1], 8, 2, 128, 16, "bf16", "hnd"),
+    ([70, 3], [2, 2], 8, 2, 64, 8, "e4m3", "nhd"),
+    ([70, 0, 9], [5, 0, 9], 6, 2, 128, 16, "bf16", "nhd"),
+    ([70, 0, 9], [5, 0, 9], 6, 2, 128, 64, "e4m3", "hnd"),
+    ([300, 64], [70, 90], 9, 3, 64, 32, "bf16", "hnd"),
+    ([300, 64], [70, 90], 9, 3, 128, 32, "e4m3", "nhd"),
+    ([3000], [256], 8, 1, 128, 16, "bf16", "hnd"),
+])
+def test_a_step_between_guards(lens, n, Hq, Hkv, D, page, dtype, layout):
+    """Append, attention and accept with every buffer of exactly its size."""
+    pb, g = Problem(lens, n, Hkv, D, page, dtype, layout, spare=0, width=None), Guarded()
+    rng = np.random.default_rng(len(lens))
+    (K, V), cache = _guarded_cache(pb, g)
+    N, B, T = pb.N, pb.B, pb.T
+    cu = None if pb.uniform else g.like(_dev(pb.cu))
+    q = g.like(torch.randn((N, Hq, D), device="cuda").bfloat16())
+    k, v = (g.like(torch.randn((N, Hkv, D), device="cuda").bfloat16()) for _ in range(2))
+    q_out, O = g.like(q, 7.0), g.like(q, float("nan"))
+    rows = max(lens) + max(n)
+    ang = np.arange(rows)[:, None] * 1e4 ** (-np.arange(0, D, 2) / D)
+    cs = g.like(torch.from_numpy(np.concatenate([np.cos(ang), np.sin(ang)], 1)).float())
+    w = g.like(torch.ones(D, device="cuda").bfloat16())
+    pos = g.like(_dev(np.concatenate([a + np.arange(m) for a, m in zip(lens, n)]).astype(np.int32)))
+    par = g.like(_dev(np.concatenate([_tree(rng, m, "tree") for m in n]).astype(np.int32)))
+    tok, tgt = (g.like(_dev(rng.integers(0, 2, N).astype(np.int32))) for _ in range(2))
+    ws = g.like(torch.empty(Q.qmm_tree_attention_workspace_bytes(cache, Hq, T), dtype=torch.uint8,
+                            device="cuda"), 0xFF)
+    path = g.like(torch.empty((B, T), dtype=torch.int32, device="cuda"), 99)
+    count, nxt, new = (g.like(torch.empty(B, dtype=torch.int32, device="cuda"), 99) for _ in range(3))
+    before = [t.clone() for t in (q, k, v, cs, w, pos, par, tok, tgt)]
+    Q.qmm_kv_append(cache, q, k, v, q_out, rope=Q.rope(cs, q_norm=w, k_norm=w), positions=pos, cu=cu)
+    Q.qmm_tree_attention(cache, q_out, O, T, parents=par, cu=cu, workspace=ws)
+    Q.qmm_tree_accept(Q.kv_caches([cache]), tok, tgt, T, path, count, nxt, new, parents=par, cu=cu)
+    g.check()
+    assert torch.isfinite(O.float()).all() and not (q_out == 7.0).all(-1).any()
+    assert all(torch.equal(a, b) for a, b in zip(before, (q, k, v, cs, w, pos, par, tok, tgt)))
+    for t in (path, count, nxt, new):
+        assert not (t == 99).any()
