@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kAppendThreads, 8) kv_append_kernel(const Appe
         for (int o = L / 2; o > 0; o >>= 1) before += __shfl_xor_sync(mask, before, o);
         if (before >= p.d.B) return;
         b = before;
-        i = tok - p.cu[b];
+        i = tok - max(p.cu[b], 0);   // clamped as token_range does
         if (i < 0) return;
     }
     const int pos_given = p.positions ? p.positions[tok] : 0;

@@ -227,7 +227,8 @@ def _guarded_cache(pb, g):
 
 
 @pytest.mark.parametrize("cu", [[0, 99, 3, 12], [0, 4, 8, 2 ** 31 - 1], [12, 8, 4, 0],
-                                [0, 12, 12, 12], [3, 5, 5, 9]])
+                                [0, 12, 12, 12], [3, 5, 5, 9], [-5, 4, 8, 12],
+                                [-2 ** 31, -2 ** 31, 2, 30]])
 @pytest.mark.parametrize("T", [4, 12])
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 def test_ranges_out_of_order_write_only_their_rows(cu, T, dtype):
@@ -262,7 +263,7 @@ def test_ranges_out_of_order_write_only_their_rows(cu, T, dtype):
         b = sum(c <= t for c in cu[1:])
         if b < 3 and t >= cu[b]:
             written.add(t)
-            s = pb.lens[b] + t - cu[b]
+            s = pb.lens[b] + t - max(cu[b], 0)
             if s < pb.width * 16 and 0 <= pb.table[b, s // 16] < K.shape[0]:
                 for w, x, pool, sc in zip(want, (k, v), (K, V), pb.scales):
                     y = (x[t].float() / sc).clamp(-448, 448) if dtype == "e4m3" else x[t]
