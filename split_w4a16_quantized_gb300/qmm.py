@@ -700,7 +700,9 @@ def kv_cache(K: torch.Tensor, V: torch.Tensor, table: torch.Tensor, lens: torch.
         raise TypeError("K and V must be CUDA tensors")
     if K.dtype not in _CACHE_DTYPES or V.dtype != K.dtype:
         raise TypeError("K and V must both be bfloat16 or float8_e4m3fn")
-    if K.dim() != 4 or V.shape != K.shape or V.stride() != K.stride():
+    # (a dimension of one row has no stride to compare)
+    if K.dim() != 4 or V.shape != K.shape or any(
+            a != b and n > 1 for a, b, n in zip(K.stride(), V.stride(), K.shape)):
         raise ValueError("K and V must be [num_pages, Hkv, page_size, D] with equal strides")
     if K.stride(3) != 1:
         raise ValueError("a cache row's values must be contiguous")

@@ -312,3 +312,15 @@ def test_a_step_between_guards(lens, n, Hq, Hkv, D, page, dtype, layout):
     assert all(torch.equal(a, b) for a, b in zip(before, (q, k, v, cs, w, pos, par, tok, tgt)))
     for t in (path, count, nxt, new):
         assert not (t == 99).any()
+
+
+def test_strides_of_one_row_may_differ_between_k_and_v():
+    """One page of one head: only the strides of the slots have to agree."""
+    pb = Problem([3], [4], 1, 128, 8, spare=0, width=1)
+    want = _check_attention(pb, 2)
+    V = pb.V.as_strided((1, 1, 8, 128), (8, 24, 128, 1))
+    pb.cache = Q.kv_cache(pb.K, V, pb.d_table, pb.d_lens)
+    assert torch.equal(_check_attention(pb, 2).view(torch.int16), want.view(torch.int16))
+    wide = torch.zeros((1, 1, 8, 256), dtype=torch.bfloat16, device="cuda")[..., :128]
+    with pytest.raises(ValueError, match="equal strides"):
+        Q.kv_cache(pb.K, wide, pb.d_table, pb.d_lens)
