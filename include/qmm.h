@@ -758,8 +758,9 @@ size_t qmm_tree_attention_workspace_bytes(const qmm_kv_cache *cache, int Hq, int
  *                tokens)
  *   next         device int32 [B], nullable: targets of the last one kept, the
  *                next step's token 0; -1 for a sequence without tokens
- *   new_lens     device int32 [B], nullable: lens[b] + count[b]; not lens
- *                itself
+ *   new_lens     device int32 [B], nullable: lens[b] + count[b]
+ *   These four overlap neither one another nor what the call reads (lens and
+ *   the table among it): QMM_EINVAL.
  *   caches       host, n of them (one per layer), all with the same table,
  *                lens, sizes, strides and dtype: slot lens[b] + j takes the K
  *                and V rows of slot lens[b] + path[j], j < count[b], in every

@@ -1239,6 +1239,16 @@ int qmm_tree_attention(const qmm_kv_cache* cache, const void* q, int64_t q_strid
                                                static_cast<float*>(workspace), sms, stream));
 }
 
+// An array of n ints from p (NULL: none).
+struct Ints {
+    const int* p;
+    int64_t n;
+};
+static bool overlap(const Ints& a, const Ints& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return x && y && x < y + 4 * static_cast<uintptr_t>(b.n) && y < x + 4 * static_cast<uintptr_t>(a.n);
+}
+
 int qmm_tree_accept(const qmm_kv_cache* caches, int n, const int* tokens, const int* targets,
                     const int* parents, const int* cu, int N, int T, int* path, int* count,
                     int* next, int* new_lens, void* stream) {
@@ -1263,6 +1273,17 @@ int qmm_tree_accept(const qmm_kv_cache* caches, int n, const int* tokens, const 
     if (!aligned(tokens, 4) || !aligned(targets, 4) || !aligned(parents, 4) || !aligned(cu, 4) ||
         !aligned(path, 4) || !aligned(count, 4) || !aligned(next, 4) || !aligned(new_lens, 4))
         return QMM_EALIGN;
+    // several blocks walk a sequence and read what one of them would overwrite
+    const int64_t B = caches[0].B;
+    const Ints out[] = {{path, B * T}, {count, B}, {next, B}, {new_lens, B}};
+    const Ints in[] = {{tokens, N}, {targets, N}, {parents, N}, {cu, B + 1}, {caches[0].lens, B},
+                       {caches[0].table, B * caches[0].max_pages}};
+    for (const Ints& o : out) {
+        for (const Ints& i : in)
+            if (overlap(o, i)) return QMM_EINVAL;
+        for (const Ints* other = out; other != &o; ++other)
+            if (overlap(o, *other)) return QMM_EINVAL;
+    }
     rc = device_ready(nullptr);
     if (rc != QMM_OK) return rc;
     for (int i = 0; i < n && rc == QMM_OK; i += qmm::kMaxAcceptCaches)

@@ -117,3 +117,27 @@ def test_what_belongs_to_a_device_is_asked_once_for_each(tmp_path):
     for name in ("qmm_tree_attention.cu", "qmm_tree_attention_tc.cu"):
         text = open(os.path.join(csrc, name)).read()
         assert "PerDevice" in text and "once_flag" not in text, name
+
+
+# tokens, targets, parents, cu, lens, table; path, count, next, new_lens: B = 4,
+# T = 2, N = 8, 20 pages a sequence
+READ = dict(tokens=(1 << 20, 8), targets=(2 << 20, 8), parents=(3 << 20, 8), cu=(4 << 20, 5),
+            lens=(5 << 20, 4), table=(6 << 20, 80))
+WRITTEN = dict(path=(7 << 20, 8), count=(8 << 20, 4), next=(9 << 20, 4), new_lens=(10 << 20, 4))
+
+
+@pytest.mark.parametrize("out", list(WRITTEN))
+@pytest.mark.parametrize("other", list(READ) + list(WRITTEN))
+def test_accept_refuses_outputs_over_what_it_reads(out, other):
+    """Each output against each input and each other output, overlapping by one
+    value on either side."""
+    if out == other:
+        return
+    at, n = (READ | WRITTEN)[other]
+    for place in (at, at + 4 * (n - 1), at - 4 * (WRITTEN[out][1] - 1)):
+        p = {k: v[0] for k, v in (READ | WRITTEN).items()}
+        p[out] = place
+        arr = (Q.qmm_kv_cache * 1)(_cache(lens=p["lens"], table=p["table"], K=1 << 30, V=2 << 30))
+        assert Q.lib().qmm_tree_accept(arr, 1, p["tokens"], p["targets"], p["parents"], p["cu"], 8, 2,
+                                       p["path"], p["count"], p["next"], p["new_lens"],
+                                       None) == Q.QMM_EINVAL
