@@ -656,7 +656,7 @@ int qmm_decode_attention(const void *q, const void *K, const void *V, const int 
  *          do not exist.
  *   dtype  QMM_CACHE_BF16, or QMM_CACHE_E4M3: a stored value stands for
  *          k_scale (v_scale) times its E4M3 number.  k_scale and v_scale are
- *          positive and finite; 1 for BF16.
+ *          positive and finite; 1 for BF16 (QMM_EINVAL otherwise).
  * D is 64 or 128; page_size a power of two from 8 to 65536.  The pools, K's
  * and V's and those of several caches, do not overlap. */
 enum { QMM_CACHE_BF16 = 0, QMM_CACHE_E4M3 = 1 };

@@ -1141,7 +1141,8 @@ static int check_cache(const qmm_kv_cache* c) {
     if (!c || !c->K || !c->V || !c->table || !c->lens || c->B < 1 || c->num_pages < 1 ||
         c->page_size < 1 || c->max_pages < 1 || c->Hkv < 1 ||
         (c->dtype != QMM_CACHE_BF16 && c->dtype != QMM_CACHE_E4M3) || !(c->k_scale > 0.f) ||
-        !(c->v_scale > 0.f) || !std::isfinite(c->k_scale) || !std::isfinite(c->v_scale))
+        !(c->v_scale > 0.f) || !std::isfinite(c->k_scale) || !std::isfinite(c->v_scale) ||
+        (c->dtype == QMM_CACHE_BF16 && (c->k_scale != 1.f || c->v_scale != 1.f)))
         return QMM_EINVAL;
     const int e = c->dtype == QMM_CACHE_E4M3 ? 1 : 2;
     if ((c->D != 64 && c->D != 128) || c->page_size < 8 || c->page_size > 65536 ||

@@ -141,3 +141,19 @@ def test_accept_refuses_outputs_over_what_it_reads(out, other):
         assert Q.lib().qmm_tree_accept(arr, 1, p["tokens"], p["targets"], p["parents"], p["cu"], 8, 2,
                                        p["path"], p["count"], p["next"], p["new_lens"],
                                        None) == Q.QMM_EINVAL
+
+
+@pytest.mark.parametrize("scales", [(0.5, 1.0), (1.0, 2.0)])
+def test_a_bf16_cache_has_no_scales(scales):
+    """Append stores BF16 values as they are, so attention must not scale them."""
+    bf16, e4m3 = (_cache(dtype=d, k_scale=scales[0], v_scale=scales[1])
+                  for d in (Q.QMM_CACHE_BF16, Q.QMM_CACHE_E4M3))
+    nb = Q.lib().qmm_tree_attention_workspace_bytes
+    assert nb(ctypes.byref(bf16), 32, 1, 152) == 0 and nb(ctypes.byref(e4m3), 32, 1, 152) > 0
+    p = [(20 + i) << 20 for i in range(8)]
+    assert Q.lib().qmm_kv_append(ctypes.byref(bf16), None, PTR, PTR, None, 4, 0, 0, 1024, 1024, 0,
+                                 None, None, None, None) == Q.QMM_EINVAL
+    assert Q.lib().qmm_tree_attention(ctypes.byref(bf16), PTR, 4096, PTR, 4, 1, 32, None, None, 0.0,
+                                      PTR, 1 << 30, None) == Q.QMM_EINVAL
+    assert Q.lib().qmm_tree_accept((Q.qmm_kv_cache * 1)(bf16), 1, p[0], p[1], None, None, 4, 1, p[2],
+                                   p[3], p[4], p[5], None) == Q.QMM_EINVAL
