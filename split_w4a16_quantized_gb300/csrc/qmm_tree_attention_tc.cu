@@ -36,22 +36,30 @@
 // is rescaled a few times per item instead of every tile.  The result is the
 // same but for rounding: sums are FP32, P is rounded to BF16 (F16 for an E4M3
 // cache) whatever its scale.  One BF16 term of P, where the kernel for few rows
-// keeps two: the second would double the P V products, and its error is that of
-// rounding the output.
+// keeps two: its error is that of rounding the output (RMS 0.0022 of the outputs'
+// RMS, with the second term 0.0017), and the second term would double the P V
+// products: 16 sequences of 64 tokens 166 us instead of 128, 64 ragged ones of up to
+// 5 tokens, D = 64, 142 instead of 118, 8 of 8 tokens 25.5 instead of 24.1.
 //
-// What bounds it (152 SMs; a tile is 64 positions, D = 128).
+// What bounds it (152 SMs; a tile is 64 positions, D = 128; clocks a tile are those
+// that 8000 more positions add to a history of 4000, 19 sequences of 8 KV heads).
 //   BF16, up to 128 rows: HBM; 32 sequences of 16 tokens (64 rows), 500 to 16000
 //     positions: 106 us, 5.8 TB/s.  Short ones: the start (5 us to the first
 //     scores: plan, table, copy) and the merge; 8 of 8 tokens, 1500 to 4000:
 //     24 us, floor 12.6.
 //   BF16, 256 rows: the tensor cores with the hand-overs between their issue and
-//     the softmax; 16 sequences of 64 tokens, 8000 positions: 118 us, 1.15
-//     PFLOP/s.  An SM's products need 1,240 clocks a tile, 620 a group (measured
-//     alone and beside the softmax's tensor-memory traffic), of about 1,900.
+//     the softmax; 16 sequences of 64 tokens, 8000 positions: 122 to 129 us with the
+//     merge, 1.05 to 1.11 PFLOP/s.  1,580 clocks a tile, of which an SM's products
+//     need 1,240, 620 a group (measured alone and beside the softmax's tensor-memory
+//     traffic); starting and ending takes as long as 20 tiles.
 //   E4M3, up to 128 rows: shared memory.  The products read q again for every
 //     tile (two terms, 32 KB) and V is converted through it (8 KB read, 16
 //     written, 16 read): with K and the copies 104 KB, 830 clocks of an SM's
-//     bandwidth a tile, of 910; 32 sequences of 16 tokens: 83 us, 3.7 TB/s.
+//     bandwidth a tile, of 900; 32 sequences of 16 tokens: 83 us, 3.7 TB/s.
+//   E4M3, 256 rows: 1,660 clocks a tile, more than BF16's; 32 sequences of 64 tokens,
+//     500 to 16000 positions: 153 us, floor 81.  The tensor pipe is active in 47 % of
+//     the clocks and 1.8 instructions are issued a clock: neither is full, the two
+//     groups and the conversion of V wait for one another.
 //
 // E4M3 cache.  Q K^T runs on the 8-bit keys as they are: a BF16 number has 8
 // significant bits, so a row of q, scaled by a power of two to a maximum in
