@@ -720,12 +720,15 @@ int qmm_kv_append(const qmm_kv_cache *cache, const void *q, const void *k, const
  *         chain (parent i - 1).
  * Token i attends to slots 0 .. lens[b]-1 and lens[b] + j for j = i and every
  * ancestor j of i:  O = sum_l softmax_l(scale * q . K_l) V_l, scores, softmax
- * and sums in FP32, the weights rounded once for the product with V.  For an
- * E4M3 cache, values of q below 2^-9 of the largest of their head are rounded to
- * 2^-17 of it.  scale <= 0 means 1/sqrt(D).  A token that sees no position (none of its pages exists)
- * gets zeros.  Positions out of sight do not enter the sums, whatever their
- * slots hold, except that a drafted token's V row must be finite where some
- * other token of its sequence does not see it.
+ * and sums in FP32, the weights rounded once for the product with V: to BF16 (two
+ * terms of it for up to 8 query rows per KV head), or for an E4M3 cache to F16, where
+ * a weight below 2^-21 of the largest is held to 2^-32 of it.  For an E4M3 cache,
+ * values of q below 2^-9 of the largest of their head are rounded to 2^-17 of it.
+ * scale <= 0 means 1/sqrt(D).  A token that sees no position (none of its pages
+ * exists) gets zeros.  Positions out of sight do not enter the sums, whatever their
+ * slots hold, except that a drafted token's V row must be finite where some other
+ * token of its sequence does not see it (the tokens that fill up a padded batch among
+ * them: give such a batch ranges instead).
  *   T     1 .. 256
  *   workspace  device, 16-byte aligned, ws_bytes at least
  *         qmm_tree_attention_workspace_bytes: partial states of the work
