@@ -13,6 +13,7 @@
 
 #include "qmm.h"
 #include "qmm_internal.h"
+#include "qmm_paged_host.h"
 
 namespace {
 

@@ -25,6 +25,7 @@
 #include "qmm_device.cuh"
 #include "qmm_internal.h"
 #include "qmm_paged.cuh"
+#include "qmm_paged_host.h"
 
 namespace qmm {
 namespace {

@@ -15,6 +15,7 @@
 #include "qmm_device.cuh"
 #include "qmm_internal.h"
 #include "qmm_paged.cuh"
+#include "qmm_paged_host.h"
 #include "qmm_sm100.cuh"
 
 namespace qmm {
