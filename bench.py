@@ -101,6 +101,22 @@ def tc_source_hash(sources=TC_SOURCES):
     return h.hexdigest()[:16]
 
 
+def as_table(rows):
+    """Dicts as one list of their keys and a list of values each (None where a dict
+    lacks the key)."""
+    columns = list(dict.fromkeys(k for r in rows for k in r))
+    return {"columns": columns, "rows": [[r.get(k) for k in columns] for r in rows]}
+
+
+def json_line(out):
+    """The result as one line of JSON, short enough to be read whole from the end
+    of a log (under 16 KB): the two long tables name their columns once."""
+    sweep = out["split_vs_control"]
+    return json.dumps({**out, "per_call": as_table(out["per_call"]),
+                       "split_vs_control": {"summary": sweep["summary"], **as_table(sweep["rows"])}},
+                      separators=(",", ":"))
+
+
 def policy_desc():
     from split_w4a16_quantized_gb300 import qmm as Q
     parts = []
@@ -1295,7 +1311,7 @@ def main():
     if rank == 0 and world == 1 and not args.no_cpu_baseline:
         out["cpu_baseline"] = cpu_baseline(wl.host)
     if rank == 0:
-        print(json.dumps(out), flush=True)
+        print(json_line(out), flush=True)
     if world > 1:
         import torch.distributed as dist
         dist.destroy_process_group()
