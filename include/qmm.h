@@ -706,6 +706,27 @@ int qmm_kv_append(const qmm_kv_cache *cache, const void *q, const void *k, const
                   int64_t v_stride, int64_t q_out_stride, const int *cu, const int *positions,
                   const qmm_rope *rope, void *stream);
 
+/* Positions of several axes, as prompts with images and video have them (time,
+ * height, width): pair j of a head turns by the position of axis[j], so
+ * consecutive runs of axis make sections, and 0, 1, 2, 0, 1, 2, ... axes in turn.
+ *   axes  positions of a token, 1 .. 8
+ *   axis  axis[j] < axes for each pair j < dim / 2; the others are not looked at */
+typedef struct {
+    int axes;
+    uint8_t axis[64];
+} qmm_rope_axes;
+
+/* qmm_kv_append with a position for each axis: positions is device int32
+ * [axes, N], and rope and its rotation (dim > 0) are given.  A token any of whose
+ * positions is outside [0, rows) is left alone.  With one axis the results are
+ * qmm_kv_append's, bit for bit.  QMM_EINVAL also where positions, rope or axes is
+ * NULL, dim is 0, or an axis is out of range; everything else as there. */
+int qmm_kv_append_axes(const qmm_kv_cache *cache, const void *q, const void *k, const void *v,
+                       void *q_out, int N, int Hq, int64_t q_stride, int64_t k_stride,
+                       int64_t v_stride, int64_t q_out_stride, const int *cu,
+                       const int *positions, const qmm_rope *rope, const qmm_rope_axes *axes,
+                       void *stream);
+
 /* Attention of up to T drafted tokens per sequence over the cache, which
  * already holds their keys and values at slots lens[b] + i (qmm_kv_append).
  *   q     BF16 [N, Hq, D], token stride q_stride (elements, a multiple of 8),
@@ -750,6 +771,48 @@ int qmm_tree_attention(const qmm_kv_cache *cache, const void *q, int64_t q_strid
  * arguments.  Host only. */
 size_t qmm_tree_attention_workspace_bytes(const qmm_kv_cache *cache, int Hq, int T, int num_sms);
 
+/* Prefixes that several sequences of a batch share (a system prompt, a document),
+ * whose pages are in the cache's pools.
+ *   table  device int32 [G, max_pages]: slot s of prefix g is row s % page_size of page
+ *          table[g, s / page_size]; an entry outside [0, num_pages) is no page
+ *   lens   device int32 [G]: tokens of each prefix (clamped to [0, max_pages *
+ *          page_size])
+ *   first  device int32 [G + 1], ascending: sequences first[g] .. first[g+1]-1 of the
+ *          batch share prefix g (clamped to [0, B]); the others have none */
+typedef struct {
+    const int *table; /* device */
+    const int *lens;  /* device */
+    const int *first; /* device */
+    int G, max_pages;
+} qmm_prefix;
+
+/* qmm_tree_attention where each token also sees the whole prefix of its sequence, in
+ * front of the sequence's own slots: the cache's table and lens, and the slots that
+ * qmm_kv_append writes, hold only what follows the prefix (positions of their own:
+ * those count the prefix too).  A prefix's keys and values are read once for 128 query
+ * rows per KV head, not once for each of its sequences.
+ * The arguments, checks and results are qmm_tree_attention's, but:
+ *   - the weights are rounded once, to BF16 (F16 for an E4M3 cache), for any number of
+ *     rows;
+ *   - cu has to ascend without gaps within a prefix's sequences, and their ranges to be
+ *     of at most T tokens, for all of them to see it;
+ *   - the workspace is qmm_prefix_attention_workspace_bytes, which grows with N;
+ *   - QMM_EINVAL also for a NULL prefix or array, G or max_pages below 1; QMM_ESHAPE for
+ *     G above 65535, N Hq above 2^31 - 1, a prefix table of more than 2^31 - 65536 slots,
+ *     or (s / 64 + 16) * (ceil(N Hq / (128 Hkv)) + G) * Hkv above 2^31 - 1, s being its
+ *     slots; QMM_EALIGN for arrays that are not 4-byte aligned.
+ * Two launches. */
+int qmm_prefix_attention(const qmm_kv_cache *cache, const qmm_prefix *prefix, const void *q,
+                         int64_t q_stride, void *O, int N, int T, int Hq, const int *cu,
+                         const int *parents, float scale, void *workspace, size_t ws_bytes,
+                         void *stream);
+
+/* Workspace bytes of qmm_prefix_attention for this cache and N tokens, whatever the
+ * lengths and prefixes.  num_sms <= 0 queries the device.  0 for invalid arguments.
+ * Host only. */
+size_t qmm_prefix_attention_workspace_bytes(const qmm_kv_cache *cache, int Hq, int N, int T,
+                                            int num_sms);
+
 /* Greedy verification of a drafted tree.  Token 0 of a sequence is its last
  * sampled token and always stays; from token i the walk goes on to the first
  * child c (parents[c] == i, lowest c) with tokens[c] == targets[i], the
@@ -774,6 +837,67 @@ size_t qmm_tree_attention_workspace_bytes(const qmm_kv_cache *cache, int Hq, int
 int qmm_tree_accept(const qmm_kv_cache *caches, int n, const int *tokens, const int *targets,
                     const int *parents, const int *cu, int N, int T, int *path, int *count,
                     int *next, int *new_lens, void *stream);
+
+/* qmm_tree_attention of a chain (parents NULL: one token per sequence is plain decode, a
+ * prompt's last tokens are a window on it) that also adds up the weight each slot
+ * receives, for qmm_kv_evict.  With p[i, h, s] the softmax weight of slot s for token i
+ * and query head h of a sequence's KV head g, and s < lens[b] + n_b (its n_b tokens among
+ * them):
+ *   mass[b, g, s] = sum over i and the heads h of g of p[i, h, s], in FP32,
+ *                 + decay * mass[b, g, s] for s < lens[b]
+ * Slots of the call's own tokens start at 0, whatever stood there, and those behind them
+ * are left alone.  The weights are the softmax's own, not as rounded for the product
+ * with V.  A slot without a page, and every slot of a sequence without tokens, keeps
+ * decay times its sum.
+ *   mass   device FP32 [B, Hkv, mass_stride], 16-byte aligned, mass_stride a multiple of
+ *          4 and at least max_pages * page_size.  Overlaps nothing else of the call
+ *   decay  0 or more, finite; with 0 the old sums are not read
+ * The other arguments, O and the errors are qmm_tree_attention's.  The workspace is
+ * qmm_scored_attention_workspace_bytes, which grows with the table and the batch.  The
+ * result does not depend on timing.  Three launches. */
+int qmm_scored_attention(const qmm_kv_cache *cache, const void *q, int64_t q_stride, void *O,
+                         int N, int T, int Hq, const int *cu, float scale, float *mass,
+                         int64_t mass_stride, float decay, void *workspace, size_t ws_bytes,
+                         void *stream);
+
+/* Workspace bytes of qmm_scored_attention for this cache, whatever the lengths.
+ * num_sms <= 0 queries the device.  0 for invalid arguments.  Host only. */
+size_t qmm_scored_attention_workspace_bytes(const qmm_kv_cache *cache, int Hq, int T,
+                                            int num_sms);
+
+/* Eviction by the weight that each slot has received from the queries so far.
+ * In each cache (one per layer), sequence and KV head, of the first len = lens[b]
+ * slots those of a budget stay:
+ *   len <= keep: all of them.  Otherwise the first `sinks`, the last `recent`, and
+ *   of those between the keep - sinks - recent with the largest weights, the lowest
+ *   slots among equal ones (+0 and -0 are equal; NaN is below everything).
+ * The K and V rows that stay come to slots 0 .. keep-1, and what stood behind them may
+ * be overwritten by the next tokens.  With line = keep - recent: a slot below the line
+ * that stays keeps its place; the evicted slots below it take, in ascending order, the
+ * slots between the line and len - recent that stay; slot line + i takes the recent
+ * slot len - recent + i.  So the last `recent` slots are the newest tokens, in order, at
+ * every later eviction as well; the order of the others says nothing about their age.
+ * Keys keep the rotation that they were stored with: later tokens are appended with
+ * positions of their own (qmm_kv_append's default, the cached length, no longer is the
+ * token's position).
+ *   caches     host, n of them, as in qmm_tree_accept; n may be 1 .. 1024
+ *   mass       device FP32 [n, B, Hkv, mass_stride], mass_stride at least max_pages *
+ *              page_size: the weight of each slot (qmm_scored_attention).  Layers are
+ *              layer_stride values apart (at least B * Hkv * mass_stride; not looked at
+ *              for n = 1).  Both strides multiples of 4, the pointers 16-byte aligned
+ *   mass_out   as mass, which it may be (no other overlap): the first min(len, keep)
+ *              weights of each column, moved as the rows are; the rest is left alone
+ *   keep       1 or more; sinks, recent  0 or more, together at most keep
+ *   kept       device int32 [n, B, Hkv, keep]: the slot whose rows stand in slot j now;
+ *              -1 from min(len, keep) on
+ *   new_lens   device int32 [B]: min(lens[b], keep).  lens is not changed
+ *   mass_out, kept and new_lens overlap neither one another nor what the call reads:
+ *   QMM_EINVAL.
+ * A row whose page is missing on either side is not moved.  Two launches per 64 caches.
+ * Returns QMM_OK, QMM_EINVAL, QMM_ESHAPE, QMM_EALIGN, QMM_ENODEV or QMM_ECUDA. */
+int qmm_kv_evict(const qmm_kv_cache *caches, int n, const float *mass, float *mass_out,
+                 int64_t layer_stride, int64_t mass_stride, int keep, int sinks, int recent,
+                 int *kept, int *new_lens, void *stream);
 
 /* ---- streaming host activations through the matmul ----------------------
  *

@@ -1165,10 +1165,11 @@ static bool ranges_ok(const int* cu, int N, int B, int T) {
     return T > 0 ? static_cast<int64_t>(B) * T == N : N % B == 0;
 }
 
-int qmm_kv_append(const qmm_kv_cache* cache, const void* q, const void* k, const void* v,
+// qmm_kv_append, and qmm_kv_append_axes (with_axes).
+static int append(const qmm_kv_cache* cache, const void* q, const void* k, const void* v,
                   void* q_out, int N, int Hq, int64_t q_stride, int64_t k_stride,
                   int64_t v_stride, int64_t q_out_stride, const int* cu, const int* positions,
-                  const qmm_rope* rope, void* stream) {
+                  const qmm_rope* rope, const qmm_rope_axes* axes, bool with_axes, void* stream) {
     int rc = check_cache(cache);
     if (rc == QMM_EINVAL) return rc;
     if (!k || !v || Hq < 0 || (Hq > 0) != (q != nullptr) || (Hq > 0) != (q_out != nullptr) ||
@@ -1178,6 +1179,13 @@ int qmm_kv_append(const qmm_kv_cache* cache, const void* q, const void* k, const
                  (rope->interleaved != 0 && rope->interleaved != 1) ||
                  ((rope->q_norm || rope->k_norm) && !(rope->eps >= 0.f && std::isfinite(rope->eps)))))
         return QMM_EINVAL;
+    if (with_axes) {
+        // (a pair's axis is looked at only where the pair exists)
+        if (!axes || !positions || !rope || rope->dim < 1 || axes->axes < 1 || axes->axes > 8)
+            return QMM_EINVAL;
+        for (int j = 0; j < std::min(rope->dim / 2, 64); ++j)
+            if (axes->axis[j] >= axes->axes) return QMM_EINVAL;
+    }
     if (rc != QMM_OK) return rc;
     const int D = cache->D;
     const int64_t kw = static_cast<int64_t>(cache->Hkv) * D, qw = static_cast<int64_t>(Hq) * D;
@@ -1194,7 +1202,24 @@ int qmm_kv_append(const qmm_kv_cache* cache, const void* q, const void* k, const
     rc = device_ready(nullptr);
     if (rc != QMM_OK) return rc;
     return launched(qmm::launch_kv_append(*cache, q, k, v, q_out, N, Hq, q_stride, k_stride,
-                                          v_stride, q_out_stride, cu, positions, rope, stream));
+                                          v_stride, q_out_stride, cu, positions, rope, axes, stream));
+}
+
+int qmm_kv_append(const qmm_kv_cache* cache, const void* q, const void* k, const void* v,
+                  void* q_out, int N, int Hq, int64_t q_stride, int64_t k_stride,
+                  int64_t v_stride, int64_t q_out_stride, const int* cu, const int* positions,
+                  const qmm_rope* rope, void* stream) {
+    return append(cache, q, k, v, q_out, N, Hq, q_stride, k_stride, v_stride, q_out_stride, cu,
+                  positions, rope, nullptr, false, stream);
+}
+
+int qmm_kv_append_axes(const qmm_kv_cache* cache, const void* q, const void* k, const void* v,
+                       void* q_out, int N, int Hq, int64_t q_stride, int64_t k_stride,
+                       int64_t v_stride, int64_t q_out_stride, const int* cu,
+                       const int* positions, const qmm_rope* rope, const qmm_rope_axes* axes,
+                       void* stream) {
+    return append(cache, q, k, v, q_out, N, Hq, q_stride, k_stride, v_stride, q_out_stride, cu,
+                  positions, rope, axes, true, stream);
 }
 
 // Sizes of a tree attention call; QMM_OK, QMM_EINVAL or QMM_ESHAPE.
@@ -1241,19 +1266,69 @@ int qmm_tree_attention(const qmm_kv_cache* cache, const void* q, int64_t q_strid
                                                static_cast<float*>(workspace), sms, stream));
 }
 
-// An array of n ints from p (NULL: none).
-struct Ints {
-    const int* p;
+// The sizes of a call with shared prefixes beside those of check_tree.
+static int check_prefix(const qmm_kv_cache* c, const qmm_prefix* pre, int Hq, int N) {
+    if (pre->max_pages < 1 || pre->G < 1 || N < 1) return QMM_EINVAL;
+    const int64_t cap = static_cast<int64_t>(pre->max_pages) * c->page_size;
+    if (pre->G > 65535 || cap > 0x7fff0000LL || static_cast<int64_t>(N) * Hq > INT_MAX)
+        return QMM_ESHAPE;
+    // units of work in 32 bits, as in check_tree: row tiles of 128 rows, a last one of
+    // each prefix in part
+    const int64_t tiles = ceil_div(static_cast<int64_t>(N) * (Hq / c->Hkv), 128) + pre->G;
+    return cap / 64 + 16 > INT_MAX / c->Hkv / tiles ? QMM_ESHAPE : QMM_OK;
+}
+
+size_t qmm_prefix_attention_workspace_bytes(const qmm_kv_cache* cache, int Hq, int N, int T,
+                                            int num_sms) {
+    if (check_cache(cache) != QMM_OK || check_tree(cache, Hq, T) != QMM_OK || N < 1 ||
+        static_cast<int64_t>(N) * Hq > INT_MAX)
+        return 0;
+    if (num_sms <= 0 && device_sms(&num_sms) != QMM_OK) return 0;
+    return qmm::prefix_attention_workspace(cache->D, static_cast<int64_t>(N) * Hq, num_sms);
+}
+
+int qmm_prefix_attention(const qmm_kv_cache* cache, const qmm_prefix* prefix, const void* q,
+                         int64_t q_stride, void* O, int N, int T, int Hq, const int* cu,
+                         const int* parents, float scale, void* workspace, size_t ws_bytes,
+                         void* stream) {
+    int rc = check_cache(cache);
+    if (rc == QMM_EINVAL) return rc;
+    if (!prefix || !prefix->table || !prefix->lens || !prefix->first || prefix->max_pages < 1 ||
+        prefix->G < 1 || !q || !O || T < 1 || Hq < 1 || Hq % cache->Hkv || !std::isfinite(scale) ||
+        !ranges_ok(cu, N, cache->B, T))
+        return QMM_EINVAL;
+    if (rc == QMM_OK) rc = check_tree(cache, Hq, T);
+    if (rc == QMM_OK) rc = check_prefix(cache, prefix, Hq, N);
+    if (rc != QMM_OK) return rc;
+    if (q_stride % 8 || q_stride < static_cast<int64_t>(Hq) * cache->D) return QMM_ESHAPE;
+    if (!aligned(q, 16) || !aligned(O, 16) || !aligned(cu, 4) || !aligned(parents, 4) ||
+        !aligned(prefix->table, 4) || !aligned(prefix->lens, 4) || !aligned(prefix->first, 4))
+        return QMM_EALIGN;
+    int sms = 0;
+    rc = device_ready(&sms);
+    if (rc != QMM_OK) return rc;
+    if (!workspace || ws_bytes < qmm::prefix_attention_workspace(
+                                     cache->D, static_cast<int64_t>(N) * Hq, sms))
+        return QMM_EWORKSPACE;
+    if (!aligned(workspace, 16)) return QMM_EALIGN;
+    const float sc = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(cache->D));
+    return launched(qmm::launch_prefix_attention(*cache, *prefix, q, q_stride, O, N, T, Hq, cu,
+                                                 parents, sc, static_cast<float*>(workspace), sms,
+                                                 stream));
+}
+
+// An array of n 32-bit values from p (NULL: none).
+struct Words {
+    const void* p;
     int64_t n;
 };
-static bool overlap(const Ints& a, const Ints& b) {
+static bool overlap(const Words& a, const Words& b) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
     return x && y && x < y + 4 * static_cast<uintptr_t>(b.n) && y < x + 4 * static_cast<uintptr_t>(a.n);
 }
 
-int qmm_tree_accept(const qmm_kv_cache* caches, int n, const int* tokens, const int* targets,
-                    const int* parents, const int* cu, int N, int T, int* path, int* count,
-                    int* next, int* new_lens, void* stream) {
+// check_cache for the n caches of one call, which differ in their pools alone.
+static int check_caches(const qmm_kv_cache* caches, int n) {
     if (!caches || n < 1 || n > 1024) return QMM_EINVAL;
     int rc = QMM_OK;
     for (int i = 0; i < n; ++i) {
@@ -1267,6 +1342,14 @@ int qmm_tree_accept(const qmm_kv_cache* caches, int n, const int* tokens, const 
             a.max_pages != b.max_pages || a.Hkv != b.Hkv || a.D != b.D || a.dtype != b.dtype)
             return QMM_EINVAL;
     }
+    return rc;
+}
+
+int qmm_tree_accept(const qmm_kv_cache* caches, int n, const int* tokens, const int* targets,
+                    const int* parents, const int* cu, int N, int T, int* path, int* count,
+                    int* next, int* new_lens, void* stream) {
+    int rc = check_caches(caches, n);
+    if (rc == QMM_EINVAL) return rc;
     if (!tokens || !targets || !path || !count || T < 1 || new_lens == caches[0].lens ||
         !ranges_ok(cu, N, caches[0].B, T))
         return QMM_EINVAL;
@@ -1277,13 +1360,13 @@ int qmm_tree_accept(const qmm_kv_cache* caches, int n, const int* tokens, const 
         return QMM_EALIGN;
     // several blocks walk a sequence and read what one of them would overwrite
     const int64_t B = caches[0].B;
-    const Ints out[] = {{path, B * T}, {count, B}, {next, B}, {new_lens, B}};
-    const Ints in[] = {{tokens, N}, {targets, N}, {parents, N}, {cu, B + 1}, {caches[0].lens, B},
+    const Words out[] = {{path, B * T}, {count, B}, {next, B}, {new_lens, B}};
+    const Words in[] = {{tokens, N}, {targets, N}, {parents, N}, {cu, B + 1}, {caches[0].lens, B},
                        {caches[0].table, B * caches[0].max_pages}};
-    for (const Ints& o : out) {
-        for (const Ints& i : in)
+    for (const Words& o : out) {
+        for (const Words& i : in)
             if (overlap(o, i)) return QMM_EINVAL;
-        for (const Ints* other = out; other != &o; ++other)
+        for (const Words* other = out; other != &o; ++other)
             if (overlap(o, *other)) return QMM_EINVAL;
     }
     rc = device_ready(nullptr);
@@ -1292,6 +1375,85 @@ int qmm_tree_accept(const qmm_kv_cache* caches, int n, const int* tokens, const 
         rc = launched(qmm::launch_tree_accept(caches + i, std::min(n - i, qmm::kMaxAcceptCaches),
                                               tokens, targets, parents, cu, N, T, path, count, next,
                                               new_lens, i == 0, stream));
+    return rc;
+}
+
+// Weights of the slots, [B, Hkv, mass_stride]: QMM_OK, QMM_EINVAL, QMM_ESHAPE or QMM_EALIGN.
+static int check_mass(const qmm_kv_cache& c, const float* mass, int64_t mass_stride) {
+    if (!mass) return QMM_EINVAL;
+    if (mass_stride < static_cast<int64_t>(c.max_pages) * c.page_size || mass_stride % 4 ||
+        mass_stride >= int64_t{1} << 38)
+        return QMM_ESHAPE;
+    return aligned(mass, 16) ? QMM_OK : QMM_EALIGN;
+}
+
+size_t qmm_scored_attention_workspace_bytes(const qmm_kv_cache* cache, int Hq, int T,
+                                            int num_sms) {
+    if (check_cache(cache) != QMM_OK || check_tree(cache, Hq, T) != QMM_OK) return 0;
+    if (num_sms <= 0 && device_sms(&num_sms) != QMM_OK) return 0;
+    return qmm::scored_attention_workspace(*cache, T, Hq, num_sms);
+}
+
+int qmm_scored_attention(const qmm_kv_cache* cache, const void* q, int64_t q_stride, void* O, int N,
+                         int T, int Hq, const int* cu, float scale, float* mass,
+                         int64_t mass_stride, float decay, void* workspace, size_t ws_bytes,
+                         void* stream) {
+    int rc = check_cache(cache);
+    if (rc == QMM_EINVAL) return rc;
+    if (!q || !O || !mass || T < 1 || Hq < 1 || Hq % cache->Hkv || !std::isfinite(scale) ||
+        !(decay >= 0.f && std::isfinite(decay)) || !ranges_ok(cu, N, cache->B, T))
+        return QMM_EINVAL;
+    if (rc == QMM_OK) rc = check_tree(cache, Hq, T);
+    if (rc == QMM_OK) rc = check_mass(*cache, mass, mass_stride);
+    if (rc != QMM_OK) return rc;
+    if (q_stride % 8 || q_stride < static_cast<int64_t>(Hq) * cache->D) return QMM_ESHAPE;
+    if (!aligned(q, 16) || !aligned(O, 16) || !aligned(cu, 4)) return QMM_EALIGN;
+    int sms = 0;
+    rc = device_ready(&sms);
+    if (rc != QMM_OK) return rc;
+    if (!workspace || ws_bytes < qmm::scored_attention_workspace(*cache, T, Hq, sms))
+        return QMM_EWORKSPACE;
+    if (!aligned(workspace, 16)) return QMM_EALIGN;
+    const float sc = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(cache->D));
+    return launched(qmm::launch_scored_attention(*cache, q, q_stride, O, N, T, Hq, cu, sc, mass,
+                                                 mass_stride, decay,
+                                                 static_cast<float*>(workspace), sms, stream));
+}
+
+int qmm_kv_evict(const qmm_kv_cache* caches, int n, const float* mass, float* mass_out,
+                 int64_t layer_stride, int64_t mass_stride, int keep, int sinks, int recent,
+                 int* kept, int* new_lens, void* stream) {
+    int rc = check_caches(caches, n);
+    if (rc == QMM_EINVAL) return rc;
+    if (!mass || !mass_out || !kept || !new_lens || keep < 1 || sinks < 0 || recent < 0 ||
+        static_cast<int64_t>(sinks) + recent > keep)
+        return QMM_EINVAL;
+    if (rc != QMM_OK) return rc;
+    const qmm_kv_cache& c = caches[0];
+    rc = check_mass(c, mass, mass_stride);
+    if (rc != QMM_OK) return rc;
+    const int64_t rows = static_cast<int64_t>(c.B) * c.Hkv;
+    if (n > 1 && (layer_stride % 4 || layer_stride < rows * mass_stride ||
+                  layer_stride >= int64_t{1} << 48))
+        return QMM_ESHAPE;
+    if (!aligned(mass_out, 16) || !aligned(kept, 4) || !aligned(new_lens, 4)) return QMM_EALIGN;
+    // what one block writes another may yet read; a column's own weights are read first
+    const int64_t cap = static_cast<int64_t>(c.max_pages) * c.page_size;
+    const int64_t words = (n > 1 ? (n - 1) * layer_stride : 0) + (rows - 1) * mass_stride + cap;
+    const Words out[] = {{kept, n * rows * keep}, {new_lens, c.B}, {mass_out, words}};
+    const Words in[] = {{mass_out == mass ? nullptr : mass, words}, {c.lens, c.B},
+                        {c.table, static_cast<int64_t>(c.B) * c.max_pages}};
+    for (const Words& o : out) {
+        for (const Words& i : in)
+            if (overlap(o, i)) return QMM_EINVAL;
+        for (const Words* other = out; other != &o; ++other)
+            if (overlap(o, *other)) return QMM_EINVAL;
+    }
+    rc = device_ready(nullptr);
+    for (int i = 0; i < n && rc == QMM_OK; i += qmm::kMaxEvictCaches)
+        rc = launched(qmm::launch_kv_evict(caches + i, std::min(n - i, qmm::kMaxEvictCaches), i,
+                                           mass, mass_out, layer_stride, mass_stride, keep, sinks,
+                                           recent, kept, new_lens, stream));
     return rc;
 }
 

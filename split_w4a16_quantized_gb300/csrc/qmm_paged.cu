@@ -15,11 +15,16 @@
 // k and v heads, D = 128: 77 us, 5.3 TB/s (a plain copy of as many bytes: 68); into an
 // E4M3 cache 83 us, floor 56 (each stored value is divided by its scale); one token:
 // 3.1 us in a graph, latency.
+//
+// Positions of several axes (qmm_kv_append_axes): pair j turns by the position of
+// axis[j], so a lane's four pairs may take their cosines and sines from four rows of
+// the table.  A lane holds the position of one axis and the others ask it for theirs.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "qmm.h"
 #include "qmm_device.cuh"
@@ -46,6 +51,8 @@ struct AppendParams {
     int per_token;  // lane groups that share a token
     int rows, dim, interleaved;
     float eps, k_scale, v_scale;
+    int axes;            // positions of a token, [axes][N]
+    uint32_t axis4[16];  // axis of each pair, a byte each: those of lane l's four pairs
 };
 
 // Eight BF16 values of a lane as its four pairs: a = the pairs' first values
@@ -90,7 +97,7 @@ __device__ __forceinline__ uint32_t e4m3x4(const float* x, float scale) {
     return lo | (hi << 16);
 }
 
-template <int D, bool kFp8, bool kInter>
+template <int D, bool kFp8, bool kInter, bool kAxes>
 __global__ void __launch_bounds__(kAppendThreads, 8) kv_append_kernel(const AppendParams p) {
     constexpr int L = D / 8;                        // lanes of a head row
     constexpr int kGroups = kAppendThreads / L;     // lane groups of the block
@@ -146,17 +153,36 @@ __global__ void __launch_bounds__(kAppendThreads, 8) kv_append_kernel(const Appe
         i = tok - max(p.cu[b], 0);   // clamped as token_range does
         if (i < 0) return;
     }
-    const int pos_given = p.positions ? p.positions[tok] : 0;
+    int pos_given = 0;   // kAxes: of axis `lane`
+    if (kAxes) {
+        if (lane < p.axes) pos_given = p.positions[static_cast<int64_t>(lane) * p.N + tok];
+    } else if (p.positions) {
+        pos_given = p.positions[tok];
+    }
     const int len = cached_tokens(p.d, b);
-    const int pos = p.positions ? pos_given : len + i;
-    if (p.dim > 0 && (pos < 0 || pos >= p.rows)) return;
+    const int pos = kAxes || p.positions ? pos_given : len + i;
+    const bool off_table = p.dim > 0 && (pos < 0 || pos >= p.rows);
+    if (kAxes ? __any_sync(mask, off_table) : off_table) return;
     // (len <= cap < 2^31 - 65535 and i < N: the sum is tested before it is used)
     const int64_t slot = static_cast<int64_t>(len) + i;
     const int64_t at = slot < p.d.cap ? slot_offset(p.d, b, static_cast<int>(slot)) : -1;
 
     // cosines and sines of the lane's four pairs
     F2 cs[2], sn[2], ns[2];
-    if (turns) {
+    if (kAxes) {
+        const uint32_t axis = p.axis4[lane];
+        float c[4], s[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int at_axis = __shfl_sync(mask, pos, (axis >> (8 * j)) & 0xffu, L);
+            const float* row = p.cos_sin + static_cast<int64_t>(at_axis) * p.dim + 4 * lane + j;
+            c[j] = turns ? row[0] : 0.f;
+            s[j] = turns ? row[p.dim / 2] : 0.f;
+        }
+        cs[0] = f2(c[0], c[1]), cs[1] = f2(c[2], c[3]);
+        sn[0] = f2(s[0], s[1]), sn[1] = f2(s[2], s[3]);
+        ns[0] = f2(-s[0], -s[1]), ns[1] = f2(-s[2], -s[3]);
+    } else if (turns) {
         const float* row = p.cos_sin + static_cast<int64_t>(pos) * p.dim + 4 * lane;
         const float4 c4 = *reinterpret_cast<const float4*>(row);
         const float4 s4 = *reinterpret_cast<const float4*>(row + p.dim / 2);
@@ -361,7 +387,7 @@ __global__ void __launch_bounds__(kAcceptThreads)
 int launch_kv_append(const qmm_kv_cache& c, const void* q, const void* k, const void* v,
                      void* q_out, int N, int Hq, int64_t q_stride, int64_t k_stride,
                      int64_t v_stride, int64_t q_out_stride, const int* cu, const int* positions,
-                     const qmm_rope* rope, void* stream) {
+                     const qmm_rope* rope, const qmm_rope_axes* axes, void* stream) {
     AppendParams p = {};
     p.d = paged_dims(c);
     p.q = static_cast<const __nv_bfloat16*>(q);
@@ -390,6 +416,11 @@ int launch_kv_append(const qmm_kv_cache& c, const void* q, const void* k, const 
         p.interleaved = rope->interleaved;
         p.eps = rope->eps;
     }
+    if (axes) {
+        p.axes = axes->axes;
+        for (int j = 0; j < rope->dim / 2; ++j)
+            p.axis4[j / 4] |= static_cast<uint32_t>(axes->axis[j]) << (8 * (j % 4));
+    }
     // lane groups per token: one per head row where the call is small (latency:
     // one token of 8 heads 2.4 us, with fewer groups 3.0), else as few as leave
     // kAppendQ q rows, or one k and v row, a group (bytes in flight: 2452 tokens of
@@ -409,11 +440,17 @@ int launch_kv_append(const qmm_kv_cache& c, const void* q, const void* k, const 
     cfg.stream = static_cast<cudaStream_t>(stream);
     const bool fp8 = c.dtype == QMM_CACHE_E4M3, inter = rope && rope->interleaved;
     auto run = [&](auto kernel) { return static_cast<int>(cudaLaunchKernelEx(&cfg, kernel, p)); };
-    if (c.D == 128)
-        return fp8 ? (inter ? run(kv_append_kernel<128, true, true>) : run(kv_append_kernel<128, true, false>))
-                   : (inter ? run(kv_append_kernel<128, false, true>) : run(kv_append_kernel<128, false, false>));
-    return fp8 ? (inter ? run(kv_append_kernel<64, true, true>) : run(kv_append_kernel<64, true, false>))
-               : (inter ? run(kv_append_kernel<64, false, true>) : run(kv_append_kernel<64, false, false>));
+    auto pick = [&](auto d, auto with_axes) {
+        constexpr int D = decltype(d)::value;
+        constexpr bool A = decltype(with_axes)::value;
+        return fp8 ? (inter ? run(kv_append_kernel<D, true, true, A>) : run(kv_append_kernel<D, true, false, A>))
+                   : (inter ? run(kv_append_kernel<D, false, true, A>) : run(kv_append_kernel<D, false, false, A>));
+    };
+    using D128 = std::integral_constant<int, 128>;
+    using D64 = std::integral_constant<int, 64>;
+    if (axes)
+        return c.D == 128 ? pick(D128{}, std::true_type{}) : pick(D64{}, std::true_type{});
+    return c.D == 128 ? pick(D128{}, std::false_type{}) : pick(D64{}, std::false_type{});
 }
 
 int launch_tree_accept(const qmm_kv_cache* caches, int n, const int* tokens, const int* targets,

@@ -22,6 +22,15 @@ namespace qmm {
 
 constexpr int kWords = kMaxTree / 32;  // ancestor bits of a token
 
+// Prefixes that runs of sequences share (qmm_prefix_attention): each is an entry of
+// its own in the list of work, in front of the sequences, whose query rows are those
+// of all its sequences.
+struct SharedPrefixes {
+    const int *table, *lens, *first;
+    int G, max_pages, cap;
+    float* direct;   // states of items that one run holds (DirectAt)
+};
+
 struct TreeParams {
     PagedDims d;
     const __nv_bfloat16* q;
@@ -39,11 +48,16 @@ struct TreeParams {
     int box_shift;   // log2 of the positions of one copy: min(page, tile)
     float qscale;    // scale * log2(e) * k_scale
     float vscale;
+    float* lse;      // (nullable) [B][T][Hq] log2 of a row's sum of 2^score, as stat_of
+    float lift;      // log2 of the factor on the weights that the sums hold
+    SharedPrefixes pre;
 };
 
 // Token of row r of a sequence's heads: r / QG, exact for r < 2^14 and QG <= 64
-// (r (QG - 1) < 2^22).
+// (r (QG - 1) < 2^22).  A shared prefix may have more rows.
+template <bool kShared = false>
 __device__ __forceinline__ int row_node(const TreeParams& p, int r) {
+    if (kShared) return r / p.QG;
     return static_cast<int>((static_cast<uint64_t>(r) * p.qg_inv) >> 22);
 }
 
@@ -59,6 +73,13 @@ __device__ __forceinline__ void prefetch_plan(const TreeParams& p, int tid, int 
         if (p.cu) prefetch_l2(p.cu + at);
     }
     if (p.parents && at < p.N) prefetch_l2(p.parents + at);
+    if (p.pre.G > 0) {
+        if (at < static_cast<int64_t>(p.pre.G) * p.pre.max_pages) prefetch_l2(p.pre.table + at);
+        if (at < p.pre.G) {
+            prefetch_l2(p.pre.lens + at);
+            prefetch_l2(p.pre.first + at);
+        }
+    }
 }
 
 // ---- work split ----------------------------------------------------------------
@@ -70,8 +91,49 @@ struct Seq {
     int row_tiles;
 };
 
-template <bool kFromL2 = false>
+// Entries of the list: the sequences, behind the shared prefixes where there are any.
+template <bool kShared>
+__device__ __forceinline__ int entries(const TreeParams& p) {
+    return kShared ? p.pre.G + p.d.B : p.d.B;
+}
+
+// Sequences [b0, b1) of prefix g (the caller's device data, so clamped).
+template <bool kFromL2>
+__device__ __forceinline__ void group_range(const TreeParams& p, int g, int* b0, int* b1) {
+    const int a = plan_value<kFromL2>(p.pre.first + g), e = plan_value<kFromL2>(p.pre.first + g + 1);
+    *b0 = a < 0 ? 0 : (a > p.d.B ? p.d.B : a);
+    *b1 = e < *b0 ? *b0 : (e > p.d.B ? p.d.B : e);
+}
+
+// Prefix g as an entry: its rows are the tokens of its sequences, all of which see all
+// of it.
+template <bool kFromL2>
+__device__ __forceinline__ Seq shared_prefix(const TreeParams& p, int g) {
+    Seq s;
+    int b0, b1;
+    group_range<kFromL2>(p, g, &b0, &b1);
+    if (p.cu) {
+        const int a = plan_value<kFromL2>(p.cu + b0), e = plan_value<kFromL2>(p.cu + b1);
+        s.first = a < 0 ? 0 : (a > p.N ? p.N : a);
+        s.n = (e < s.first ? s.first : (e > p.N ? p.N : e)) - s.first;
+    } else {
+        s.first = b0 * p.T;
+        s.n = (b1 - b0) * p.T;
+    }
+    const int len = plan_value<kFromL2>(p.pre.lens + g);
+    s.len = b0 == b1 || len < 0 ? 0 : (len > p.pre.cap ? p.pre.cap : len);
+    s.total = s.len;
+    s.tiles = (s.total + (1 << p.tile_shift) - 1) >> p.tile_shift;
+    s.row_tiles = s.total > 0 ? (s.n * p.QG + (1 << p.row_shift) - 1) >> p.row_shift : 0;
+    return s;
+}
+
+template <bool kFromL2 = false, bool kShared = false>
 __device__ __forceinline__ Seq sequence(const TreeParams& p, int b) {
+    if (kShared) {
+        if (b < p.pre.G) return shared_prefix<kFromL2>(p, b);
+        b -= p.pre.G;
+    }
     Seq s;
     token_range<kFromL2>(p.cu, p.N, p.T, b, &s.first, &s.n);
     s.len = cached_tokens<kFromL2>(p.d, b);
@@ -145,14 +207,15 @@ __device__ __forceinline__ long long warp_scan(long long v, long long* total) {
     return x - v;
 }
 
-template <int kN>
+template <int kN, bool kShared = false>
 __device__ __forceinline__ Run find_run(const TreeParams& p, RunShared& sh) {
     Run r;
-    if (p.d.B <= 32) {
+    const int count = entries<kShared>(p);
+    if (count <= 32) {
         const int lane = threadIdx.x & 31;
         Seq s = {};
-        if (lane < p.d.B) s = sequence(p, lane);
-        const int mine = lane < p.d.B ? units_of(p, s) : 0;
+        if (lane < count) s = sequence<false, kShared>(p, lane);
+        const int mine = lane < count ? units_of(p, s) : 0;
         long long all;
         const long long before = warp_scan(mine, &all);
         const long long len = run_length(p, all), start = len * blockIdx.x;
@@ -169,12 +232,12 @@ __device__ __forceinline__ Run find_run(const TreeParams& p, RunShared& sh) {
         r.left = r.b < 0 ? 0 : static_cast<int>(all - start < len ? all - start : len);
         return r;
     }
-    const int per = (p.d.B + kN - 1) / kN;
-    const int b0 = min(p.d.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.d.B, b0 + per);
+    const int per = (count + kN - 1) / kN;
+    const int b0 = min(count, static_cast<int>(threadIdx.x) * per), b1 = min(count, b0 + per);
     long long mine = 0, all;
     Seq s;
     for (int b = b0; b < b1; ++b) {
-        s = sequence(p, b);
+        s = sequence<false, kShared>(p, b);
         mine += units_of(p, s);
     }
     if (threadIdx.x == 0) sh.b = -1;
@@ -185,7 +248,7 @@ __device__ __forceinline__ Run find_run(const TreeParams& p, RunShared& sh) {
         // this thread's sequences hold the start
         long long at = start - before;
         for (int b = b0; b < b1; ++b) {
-            if (per > 1) s = sequence(p, b);
+            if (per > 1) s = sequence<false, kShared>(p, b);
             const int u = units_of(p, s);
             if (at < u) {
                 sh.b = b;
@@ -210,12 +273,13 @@ struct Stretch {
     int b, g, row0;    // sequence, KV head, first row
     int t0, t1;        // tiles
 };
+template <bool kShared = false>
 __device__ __forceinline__ bool next_stretch(const TreeParams& p, Run& r, Stretch* x) {
     while (r.left > 0) {
         while (r.at >= units_of(p, r.s)) {
             r.at -= units_of(p, r.s);
-            if (++r.b >= p.d.B) return false;   // (not reached: the run ends with the list)
-            r.s = sequence(p, r.b);
+            if (++r.b >= entries<kShared>(p)) return false;   // (not reached: the run ends with the list)
+            r.s = sequence<false, kShared>(p, r.b);
         }
         x->s = r.s;
         const int units = item_units(p, x->s);
@@ -259,6 +323,17 @@ __device__ __forceinline__ PartialAt partial_at(const TreeParams& p, int slot) {
     return a;
 }
 
+// Where the state of an item that one run holds lies, with shared prefixes: row
+// (token, head) of the sequences' own part (0) or of the prefixes' (1).
+struct DirectAt {
+    float *m, *l, *o;   // o: the row's D values
+};
+template <int D>
+__device__ __forceinline__ DirectAt direct_at(const TreeParams& p, int part, int64_t row) {
+    const int64_t rows = static_cast<int64_t>(p.N) * p.Hq, r = part * rows + row;
+    return {p.pre.direct + r, p.pre.direct + 2 * rows + r, p.pre.direct + 4 * rows + r * D};
+}
+
 // 4-D tile load (c0 innermost), completion counted on `bar` in bytes.
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint64_t* bar,
                                             int c0, int c1, int c2, int c3) {
@@ -291,9 +366,13 @@ struct PageWalk {
     __device__ __forceinline__ int entry(const TreeParams& p, int c) const {
         return c < c_end ? row[(c << p.box_shift) >> p.d.page_shift] : -1;
     }
+    template <bool kShared = false>
     __device__ __forceinline__ void start(const TreeParams& p, const Stretch& x, int lane) {
         c_end = (x.s.total + (1 << p.box_shift) - 1) >> p.box_shift;   // pieces that hold positions
-        row = p.d.table + static_cast<int64_t>(x.b) * p.d.max_pages;
+        if (kShared && x.b < p.pre.G)
+            row = p.pre.table + static_cast<int64_t>(x.b) * p.pre.max_pages;
+        else
+            row = p.d.table + static_cast<int64_t>(x.b - (kShared ? p.pre.G : 0)) * p.d.max_pages;
         c0 = x.t0 * (kTile >> p.box_shift);
         cur = entry(p, c0 + lane);
         nxt = entry(p, c0 + 32 + lane);
@@ -354,6 +433,16 @@ __device__ __forceinline__ float finite_factor(float x) {
     return fminf(fmaxf(x, __uint_as_float(1u)), __uint_as_float(0x7f7fffffu));
 }
 
+// log2 of the sum of 2^score of a row with maximum (or reference) m and sum l of
+// weights lifted by 2^lift; infinity for a row that sees nothing, whose weights are 0.
+__device__ __forceinline__ float stat_of(const TreeParams& p, float m, float l) {
+    return l == 0.f ? INFINITY : m + (log2f(l) - p.lift);
+}
+// Where it goes: row `node`, `head` of sequence b.
+__device__ __forceinline__ float* stat_at(const TreeParams& p, int b, int node, int head) {
+    return p.lse + (static_cast<int64_t>(b) * p.T + node) * p.Hq + head;
+}
+
 // 2^x, one instruction (ex2.approx: 2 ulp, results below 2^-126 are 0).
 __device__ __forceinline__ float fast_exp2(float x) {
     float y;
@@ -361,11 +450,27 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return y;
 }
 
+// scale log2(e) k_scale, for exp2 of the scaled score.  Neither 0 nor infinity, whatever
+// scale and k_scale: times a masked score (-inf) or a score of 0 those would be NaN.
+float score_factor(const qmm_kv_cache& c, float scale);
+
+// A launch's parameters and the maps of its K and V (qmm_tree_attention.cu); returns a
+// cudaError_t.
+int tree_setup(const qmm_kv_cache& c, const void* q, int64_t q_stride, void* O, int N, int T, int Hq,
+               const int* cu, const int* parents, float scale, float* ws, int ctas, int row_shift,
+               int tile_shift, int min_run, int setup, TreeParams* out, CUtensorMap* kmap,
+               CUtensorMap* vmap);
+
 // One launch of the tcgen05 kernel (qmm_tree_attention_tc.cu); the merge
 // kernel is the caller's.  Items of up to 128 rows (row_shift 7, two CTAs per
 // SM) or 256 (8, one); device: the current one.
 constexpr int kTcTileShift = 6;
+constexpr float kTcLift = 7.f;   // log2 of its factor on F16 weights
 int launch_tree_tc(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int D,
                    bool fp8, int device, cudaStream_t st);
+// The same with shared prefixes (p.pre), items of up to 128 rows: every item leaves a
+// state, and the merge is the caller's (qmm_prefix_attention.cu).
+int launch_prefix_tc(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int D,
+                     bool fp8, int device, cudaStream_t st);
 
 }  // namespace qmm

@@ -46,6 +46,7 @@ constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kKeys = kTile / kWarps;   // positions per compute warp
 constexpr int kStages = 3;
 constexpr int kCtasPerSm = 2;
+constexpr float kLift = 15.f;  // log2 of the factor on F16 weights
 
 // ---- shared memory tiles ----------------------------------------------------
 
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                     const float mn = fmaxf(m_run, mx), mf = finite_max(mn);
-                    const float corr = fast_exp2(m_run - mf), by = mf - (kFp8 ? 15.f : 0.f);
+                    const float corr = fast_exp2(m_run - mf), by = mf - (kFp8 ? kLift : 0.f);
                     m_run = mn;
                     float pw[4], rs = 0.f;
 #pragma unroll
@@ -483,6 +484,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     part.m[gr] = M;
                     part.l[gr] = den;
                 }
+                if (whole && p.lse && warp == 0 && tq == 0)
+                    *stat_at(p, x.b, node, head) = stat_of(p, M, den);
                 __nv_bfloat16* out =
                     p.O + (static_cast<int64_t>(x.s.first + node) * p.Hq + head) * D;
 #pragma unroll
@@ -649,6 +652,10 @@ __global__ void __launch_bounds__(kMergeThreads)
             }
         }
         const float inv = den > 0.f ? p.vscale / den : (den == 0.f ? 0.f : den);
+        if (p.lse && j0 == 0) {
+            const int node = (row0 + r) / p.QG;
+            *stat_at(p, b, node, g * p.QG + row0 + r - node * p.QG) = stat_of(p, M, den);
+        }
 #pragma unroll
         for (int u = 0; u < TURNS; ++u)
             stage[i][j0 + u * (kMergeThreads / kMergeRows)] =
@@ -738,12 +745,18 @@ size_t tree_attention_workspace(int D, int rows, int num_sms) {
            sizeof(float);
 }
 
-int launch_tree_attention(const qmm_kv_cache& c, const void* q, int64_t q_stride, void* O, int N,
-                          int T, int Hq, const int* cu, const int* parents, float scale,
-                          float* ws, int num_sms, void* stream) {
+float score_factor(const qmm_kv_cache& c, float scale) {
+    const double factor = static_cast<double>(scale) * 1.4426950408889634 * c.k_scale;
+    return static_cast<float>(
+        std::min(std::max(factor, static_cast<double>(std::numeric_limits<float>::denorm_min())),
+                 static_cast<double>(std::numeric_limits<float>::max())));
+}
+
+int tree_setup(const qmm_kv_cache& c, const void* q, int64_t q_stride, void* O, int N, int T, int Hq,
+               const int* cu, const int* parents, float scale, float* ws, int ctas, int row_shift,
+               int tile_shift, int min_run, int setup, TreeParams* out, CUtensorMap* kmap,
+               CUtensorMap* vmap) {
     TreeParams p = {};
-    int device = 0;
-    if (cudaGetDevice(&device) != cudaSuccess) return cudaErrorInvalidDevice;
     p.status = tc_status_ptr();
     if (!p.status) return cudaErrorInvalidSymbol;
     p.d = paged_dims(c);
@@ -758,19 +771,13 @@ int launch_tree_attention(const qmm_kv_cache& c, const void* q, int64_t q_stride
     p.Hq = Hq;
     p.QG = Hq / c.Hkv;
     p.qg_inv = ((1u << 22) + p.QG - 1) / p.QG;
-    const Variant var = variant(T * p.QG, c.dtype == QMM_CACHE_E4M3);
-    p.ctas = var.ctas_per_sm * num_sms;
-    p.row_shift = var.row_shift;
-    p.tile_shift = var.tile_shift;
-    p.min_run = var.min_run;
-    p.setup = var.setup;
+    p.ctas = ctas;
+    p.row_shift = row_shift;
+    p.tile_shift = tile_shift;
+    p.min_run = min_run;
+    p.setup = setup;
     p.box_shift = p.d.page_shift < p.tile_shift ? p.d.page_shift : p.tile_shift;
-    // log2(e): exp2 of the scaled score.  Neither 0 nor infinity, whatever scale and
-    // k_scale: times a masked score (-inf) or a score of 0 those would be NaN.
-    const double factor = static_cast<double>(scale) * 1.4426950408889634 * c.k_scale;
-    p.qscale = static_cast<float>(
-        std::min(std::max(factor, static_cast<double>(std::numeric_limits<float>::denorm_min())),
-                 static_cast<double>(std::numeric_limits<float>::max())));
+    p.qscale = score_factor(c, scale);
     p.vscale = c.v_scale;
     // K and V as [pages, heads, slots, D], copied a page piece and 128 bytes of
     // columns at a time
@@ -786,7 +793,6 @@ int launch_tree_attention(const qmm_kv_cache& c, const void* q, int64_t q_stride
     const CUtensorMapDataType type = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                          : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const CUtensorMapSwizzle sw = row < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
-    CUtensorMap kmap, vmap;
     // L2 fetches what a copy reads and no neighbouring head with it: a row, where
     // the next slot's row is not the next in memory (E4M3, pages of [slot, head], 32
     // sequences of 16 tokens: 83.6 us, with 256 bytes 86.2; D = 64 65.4 and 68.8)
@@ -794,9 +800,28 @@ int launch_tree_attention(const qmm_kv_cache& c, const void* q, int64_t q_stride
                                           ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
                                       : row == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
                                                    : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
-    if (!encode_tiled_promoted(&kmap, type, 4, c.K, dims, strides, box, sw, l2) ||
-        !encode_tiled_promoted(&vmap, type, 4, c.V, dims, strides, box, sw, l2))
+    if (!encode_tiled_promoted(kmap, type, 4, c.K, dims, strides, box, sw, l2) ||
+        !encode_tiled_promoted(vmap, type, 4, c.V, dims, strides, box, sw, l2))
         return cudaErrorInvalidValue;
+    *out = p;
+    return cudaSuccess;
+}
+
+int launch_tree_attention(const qmm_kv_cache& c, const void* q, int64_t q_stride, void* O, int N,
+                          int T, int Hq, const int* cu, const int* parents, float scale,
+                          float* ws, int num_sms, void* stream, float* lse) {
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) return cudaErrorInvalidDevice;
+    const bool fp8 = c.dtype == QMM_CACHE_E4M3;
+    const Variant var = variant(T * (Hq / c.Hkv), fp8);
+    TreeParams p;
+    CUtensorMap kmap, vmap;
+    const int err = tree_setup(c, q, q_stride, O, N, T, Hq, cu, parents, scale, ws,
+                               var.ctas_per_sm * num_sms, var.row_shift, var.tile_shift,
+                               var.min_run, var.setup, &p, &kmap, &vmap);
+    if (err != cudaSuccess) return err;
+    p.lse = lse;
+    p.lift = fp8 ? (var.tc ? kTcLift : kLift) : 0.f;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int rc;
     if (var.tc)

@@ -82,7 +82,6 @@ constexpr int kTile = 1 << kTcTileShift;   // positions
 constexpr int kMaxSlots = 8;        // of one ring
 constexpr int kHave = 32;           // tiles whose page bits are kept
 constexpr float kLazy = 8.f;        // log2 units a score may pass the reference by
-constexpr float kLift = 7.f;        // log2 of the factor on F16 weights
 
 // kGroups: softmax groups (1: two CTAs per SM, up to 128 rows; 2: one CTA, 256).
 template <int D, bool kFp8, int kGroups>
@@ -232,7 +231,8 @@ struct Layout {
     int q_rows, conv_slots, k_slots, v_slots;
 };
 
-template <int D, bool kFp8, int kGroups>
+// kShared: with shared prefixes in the list of work; every item leaves a state.
+template <int D, bool kFp8, int kGroups, bool kShared>
 __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGroups>::CTAS_PER_SM)
     tree_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap, const __grid_constant__ TreeParams p,
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
     tc_fence_after();
     pdl_trigger();
     const uint32_t tmem = sm.tmem;
-    Run run = find_run<C::THREADS>(p, sm.run);
+    Run run = find_run<C::THREADS, kShared>(p, sm.run);
     const int pieces = kTile >> p.box_shift;
     Stretch x = {};
     // (test_wait answers in 60 clocks where the phase is complete, as it mostly
@@ -325,9 +325,9 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                 copy_tile<kTile, C::BOXES, C::BOX, C::BOX / (kFp8 ? 1 : 2)>(
                     p, map, bar, smem_addr(slot), sm.pages[t & 1], t, x.g);
             };
-            while (ok && next_stretch(p, run, &x)) {
+            while (ok && next_stretch<kShared>(p, run, &x)) {
                 PageWalk<kTile> walk;
-                walk.start(p, x, lane);
+                walk.template start<kShared>(p, x, lane);
                 for (int t = x.t0 - kLead; ok && t < x.t1; ++t) {
                     const bool more = t + kLead < x.t1;
                     uint32_t have = 0;
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                 if (!kAlone) __syncwarp();
             };
             if (!kAlone || elect_one()) {
-                while (go && next_stretch(p, run, &x)) {
+                while (go && next_stretch<kShared>(p, run, &x)) {
                     const int nt = x.t1 - x.t0;
                     if (!(go = wait(&sm.qready, nq & 1))) break;
                     // the first S of each buffer
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
             const int t64 = tid - 64;
             Cursor vc, cc;
             bool go = true;
-            for (int k = 0; go && next_stretch(p, run, &x); ++k) {
+            for (int k = 0; go && next_stretch<kShared>(p, run, &x); ++k) {
                 const int rows = min(1 << p.row_shift, x.s.n * p.QG - x.row0);
                 if (k > 0 && !waits(&sm.qfree, (k - 1) & 1)) break;
                 if (k > 0) fence_proxy_async_smem();
@@ -500,10 +500,10 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                 // this thread's rows, STEP apart, without a division each: a row
                 // further is D values on, a token further q_stride - QG D more
                 auto each_row = [&](int start, int step, auto&& f) {
-                    int node = row_node(p, x.row0 + start);
+                    int node = row_node<kShared>(p, x.row0 + start);
                     int head = x.row0 + start - node * p.QG;
                     const __nv_bfloat16* src = q0 + node * p.q_stride + head * D;
-                    const int dn = row_node(p, step), dh = step - dn * p.QG;
+                    const int dn = row_node<kShared>(p, step), dh = step - dn * p.QG;
                     const int64_t by = dn * p.q_stride + dh * D, wrap = p.q_stride - p.QG * D;
 #pragma unroll 4
                     for (int r = start; r < rows; r += step) {
@@ -604,14 +604,14 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
         uint32_t sphase = 0;      // phase of each buffer's S, a bit each
         int anc_b = -1, anc_row = 0;   // whose rows' ancestors stand in sm.anc
         uint32_t* const anc = sm.anc[tid - 32 * C::SOFTMAX0];
-        for (int k = 0; next_stretch(p, run, &x); ++k) {
+        for (int k = 0; next_stretch<kShared>(p, run, &x); ++k) {
             const int nt = x.t1 - x.t0;
             const int rows = min(1 << p.row_shift, x.s.n * p.QG - x.row0);
             const int r = gt + 128 * g;   // row of the item
             const bool on = r < rows;
             const bool warp_on = __any_sync(0xffffffffu, on);
             const int row = x.row0 + (on ? r : 0);
-            const int node = row_node(p, row), head = x.g * p.QG + row - node * p.QG;
+            const int node = row_node<kShared>(p, row), head = x.g * p.QG + row - node * p.QG;
             // ---- E4M3: the row of q as two terms ----
             float qs = p.qscale;
             if (kFp8) {
@@ -670,7 +670,8 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
             }
             // ---- ancestors, where the stretch reaches the drafted slots: the same
             // for all heads of a sequence ----
-            if (x.t1 * kTile > x.s.len && (x.b != anc_b || x.row0 != anc_row)) {
+            if (x.t1 * kTile > x.s.len && (x.b != anc_b || x.row0 != anc_row) &&
+                !(kShared && x.b < p.pre.G)) {
                 anc_b = x.b;
                 anc_row = x.row0;
                 if (p.parents) {
@@ -749,7 +750,7 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                         tmem_st_wait();
                     }
                 }
-                const float sub = finite_max(ref) - (kFp8 ? kLift : 0.f);
+                const float sub = finite_max(ref) - (kFp8 ? kTcLift : 0.f);
                 const F2 q2 = f2(qs, qs), s2 = f2(-sub, -sub);
                 F2 part[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
@@ -818,10 +819,29 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                             *reinterpret_cast<uint4*>(part.at(r, c + q)) =
                                 make_uint4(y[q], y[q + 1], y[q + 2], y[q + 3]);
                 }
+            } else if (kShared) {
+                const DirectAt at = direct_at<D>(
+                    p, x.b < p.pre.G, static_cast<int64_t>(x.s.first + node) * p.Hq + head);
+                if (writes) {
+                    *at.m = ref;
+                    *at.l = sum;
+                }
+#pragma unroll 1
+                for (int c = 0; warp_on && c < D; c += 32) {
+                    uint32_t y[32];
+                    tmem_ld32(tO + c, y);
+                    tmem_ld_wait();
+                    if (writes)
+#pragma unroll
+                        for (int q = 0; q < 32; q += 4)
+                            *reinterpret_cast<uint4*>(at.o + c + q) =
+                                make_uint4(y[q], y[q + 1], y[q + 2], y[q + 3]);
+                }
             } else if (warp_on) {
                 // a warp's 32 rows x 32 columns turn in shared memory: 8 rows of 64
                 // bytes a store instead of 32 of 16
                 const float inv = sum > 0.f ? p.vscale / sum : (sum == 0.f ? 0.f : sum);
+                if (p.lse && writes) *stat_at(p, x.b, node, head) = stat_of(p, ref, sum);
                 const int64_t row_at = static_cast<int64_t>(x.s.first + node) * p.Hq + head;
                 const uint32_t mask = __ballot_sync(0xffffffffu, writes);
                 uint4* const stage = sm.stage[warp - C::SOFTMAX0];
@@ -862,11 +882,11 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
     if (warp == 1) tmem_dealloc(tmem, C::COLS);
 }
 
-template <int D, bool kFp8, int kGroups>
+template <int D, bool kFp8, int kGroups, bool kShared>
 int launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int device,
            cudaStream_t st) {
     using C = Tc<D, kFp8, kGroups>;
-    auto kern = tree_tc_kernel<D, kFp8, kGroups>;
+    auto kern = tree_tc_kernel<D, kFp8, kGroups, kShared>;
     static PerDevice<int> limits;
     const int limit =
         limits.get(device, [&] { return set_max_dynamic_smem(reinterpret_cast<const void*>(kern)); });
@@ -874,7 +894,7 @@ int launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p
     // have 114 KB each, 1 KB of it the system's
     const int room = C::CTAS_PER_SM == 1 ? limit : std::min(limit, 113 * 1024);
     Layout lay;
-    const int rows = p.T * p.QG;
+    const int rows = (kShared ? p.N : p.T) * p.QG;
     lay.q_rows = kGroups == 2 || rows > 64 ? 128 : (rows > 32 ? 64 : 32);
     const int fixed = 1024 + kSmemHead<kGroups> + kGroups * lay.q_rows * D * 2;
     // two converted tiles where that leaves two slots to either ring (32 sequences
@@ -898,8 +918,8 @@ int launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p
 template <int D, bool kFp8>
 int launch_groups(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int device,
                   cudaStream_t st) {
-    return p.row_shift == 7 ? launch<D, kFp8, 1>(kmap, vmap, p, device, st)
-                            : launch<D, kFp8, 2>(kmap, vmap, p, device, st);
+    return p.row_shift == 7 ? launch<D, kFp8, 1, false>(kmap, vmap, p, device, st)
+                            : launch<D, kFp8, 2, false>(kmap, vmap, p, device, st);
 }
 
 }  // namespace
@@ -911,6 +931,15 @@ int launch_tree_tc(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeP
                    : launch_groups<128, false>(kmap, vmap, p, device, st);
     return fp8 ? launch_groups<64, true>(kmap, vmap, p, device, st)
                : launch_groups<64, false>(kmap, vmap, p, device, st);
+}
+
+int launch_prefix_tc(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int D,
+                     bool fp8, int device, cudaStream_t st) {
+    if (D == 128)
+        return fp8 ? launch<128, true, 1, true>(kmap, vmap, p, device, st)
+                   : launch<128, false, 1, true>(kmap, vmap, p, device, st);
+    return fp8 ? launch<64, true, 1, true>(kmap, vmap, p, device, st)
+               : launch<64, false, 1, true>(kmap, vmap, p, device, st);
 }
 
 }  // namespace qmm

@@ -98,6 +98,17 @@ class qmm_rope(ctypes.Structure):
                 ("interleaved", ctypes.c_int), ("eps", ctypes.c_float)]
 
 
+class qmm_rope_axes(ctypes.Structure):
+    """Axis of each rotated pair of qmm_kv_append_axes (see qmm.h); rope_axes() builds it."""
+    _fields_ = [("axes", ctypes.c_int), ("axis", ctypes.c_uint8 * 64)]
+
+
+class qmm_prefix(ctypes.Structure):
+    """Prefixes shared by runs of sequences (see qmm.h); prefix() builds it."""
+    _fields_ = [("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("first", ctypes.c_void_p),
+                ("G", ctypes.c_int), ("max_pages", ctypes.c_int)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -160,6 +171,14 @@ _SIGS = {
     "qmm_kv_append": (_I, [_P, _P, _P, _P, _P, _I, _I, _L, _L, _L, _L, _P, _P, _P, _P]),
     "qmm_tree_attention": (_I, [_P, _P, _L, _P, _I, _I, _I, _P, _P, ctypes.c_float, _P, _SZ, _P]),
     "qmm_tree_attention_workspace_bytes": (_SZ, [_P, _I, _I, _I]),
+    "qmm_kv_append_axes": (_I, [_P, _P, _P, _P, _P, _I, _I, _L, _L, _L, _L, _P, _P, _P, _P, _P]),
+    "qmm_kv_evict": (_I, [_P, _I, _P, _P, _L, _L, _I, _I, _I, _P, _P, _P]),
+    "qmm_prefix_attention": (_I, [_P, _P, _P, _L, _P, _I, _I, _I, _P, _P, ctypes.c_float, _P,
+                                  _SZ, _P]),
+    "qmm_prefix_attention_workspace_bytes": (_SZ, [_P, _I, _I, _I, _I]),
+    "qmm_scored_attention": (_I, [_P, _P, _L, _P, _I, _I, _I, _P, ctypes.c_float, _P, _L,
+                                  ctypes.c_float, _P, _SZ, _P]),
+    "qmm_scored_attention_workspace_bytes": (_SZ, [_P, _I, _I, _I]),
     "qmm_tree_accept": (_I, [_P, _I, _P, _P, _P, _P, _I, _I, _P, _P, _P, _P, _P]),
     "qmm_overlap_schedule": (_I, [_I, _I, ctypes.POINTER(ctypes.c_double),
                                   ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_double),
@@ -798,16 +817,22 @@ def _ints(t: torch.Tensor, N: int, name: str) -> int:
     return t.data_ptr()
 
 
-def qmm_kv_append(cache: qmm_kv_cache, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
-                  q_out: torch.Tensor | None = None, rope: qmm_rope | None = None,
-                  positions: torch.Tensor | None = None, cu: torch.Tensor | None = None,
-                  stream=None) -> None:
-    """Rotate q [N, Hq, D] into q_out and append k, v [N, Hkv, D] (bf16; token
-    strides free, so views of one fused projection do) behind the cached
-    tokens.  q and q_out may both be None (only append); q_out may be q.
-    positions int32 [N] and cu int32 [B + 1]: see qmm.h."""
+def rope_axes(axis_of_pair, axes: int | None = None) -> qmm_rope_axes:
+    """The axis (0 .. axes - 1) that each rotated pair of a head turns by, one for
+    each of the rope's dim / 2 pairs (qmm_kv_append_axes); axes: the positions of a
+    token, None for as many as the pairs name."""
+    axis = [int(a) for a in axis_of_pair]
+    axes = max(axis, default=0) + 1 if axes is None else int(axes)
+    if not 1 <= len(axis) <= 64 or not 1 <= axes <= 8 or min(axis) < 0 or max(axis) >= axes:
+        raise ValueError("rope_axes: 1 to 64 pairs, 1 to 8 axes, each pair's among them")
+    r = qmm_rope_axes(axes, (ctypes.c_uint8 * 64)(*axis))
+    r.pairs, r.ref = len(axis), ctypes.addressof(r)
+    return r
+
+
+def _append(name: str, cache: qmm_kv_cache, q, k, v, q_out, rope, positions, cu, stream, axes=None):
     if (q is None) != (q_out is None):
-        raise ValueError("qmm_kv_append: q and q_out come together")
+        raise ValueError("%s: q and q_out come together" % name)
     device = cache.device
     if not (k.get_device() == device == v.get_device() and _current(device) and
             (q is None or q.get_device() == device == q_out.get_device()) and
@@ -817,28 +842,57 @@ def qmm_kv_append(cache: qmm_kv_cache, q: torch.Tensor | None, k: torch.Tensor, 
     shape = k.shape
     N, Hkv, D = shape
     if Hkv != cache.Hkv or D != cache.D or v.shape != shape:
-        raise ValueError("qmm_kv_append: inconsistent shapes")
+        raise ValueError("%s: inconsistent shapes" % name)
     Hq = qs = qos = 0
     qp = qop = None
     if q is not None:
         shape = q.shape
         Hq = shape[1]
         if shape != (N, Hq, D) or q_out.shape != shape:
-            raise ValueError("qmm_kv_append: inconsistent shapes")
+            raise ValueError("%s: inconsistent shapes" % name)
         qs, qos = _heads(q, N, Hq, D, "q"), _heads(q_out, N, Hq, D, "q_out")
         qp, qop = q.data_ptr(), q_out.data_ptr()
     r = None
     if rope is not None:
         if rope.D not in (0, D) or rope.device not in (-1, device):
-            raise ValueError("qmm_kv_append: norm weights must have D elements, and the rope's "
-                             "tensors the cache's device")
+            raise ValueError("%s: norm weights must have D elements, and the rope's "
+                             "tensors the cache's device" % name)
         r = rope.ref
-    rc = (_lib or lib()).qmm_kv_append(
-        cache.ref, qp, k.data_ptr(), v.data_ptr(), qop, N, Hq, qs, _heads(k, N, Hkv, D, "k"),
-        _heads(v, N, Hkv, D, "v"), qos, None if cu is None else _ints(cu, cache.B + 1, "cu"),
-        None if positions is None else _ints(positions, N, "positions"), r, _stream_on(device, stream))
+    args = (cache.ref, qp, k.data_ptr(), v.data_ptr(), qop, N, Hq, qs, _heads(k, N, Hkv, D, "k"),
+            _heads(v, N, Hkv, D, "v"), qos, None if cu is None else _ints(cu, cache.B + 1, "cu"))
+    if axes is None:
+        rc = (_lib or lib()).qmm_kv_append(
+            *args, None if positions is None else _ints(positions, N, "positions"), r,
+            _stream_on(device, stream))
+    else:
+        rc = (_lib or lib()).qmm_kv_append_axes(*args, _ints(positions, axes.axes * N, "positions"),
+                                                r, axes.ref, _stream_on(device, stream))
     if rc != QMM_OK:
-        raise QmmError(rc, "qmm_kv_append")
+        raise QmmError(rc, name)
+
+
+def qmm_kv_append(cache: qmm_kv_cache, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
+                  q_out: torch.Tensor | None = None, rope: qmm_rope | None = None,
+                  positions: torch.Tensor | None = None, cu: torch.Tensor | None = None,
+                  stream=None) -> None:
+    """Rotate q [N, Hq, D] into q_out and append k, v [N, Hkv, D] (bf16; token
+    strides free, so views of one fused projection do) behind the cached
+    tokens.  q and q_out may both be None (only append); q_out may be q.
+    positions int32 [N] and cu int32 [B + 1]: see qmm.h."""
+    _append("qmm_kv_append", cache, q, k, v, q_out, rope, positions, cu, stream)
+
+
+def qmm_kv_append_axes(cache: qmm_kv_cache, q: torch.Tensor | None, k: torch.Tensor,
+                       v: torch.Tensor, positions: torch.Tensor, axes: qmm_rope_axes,
+                       rope: qmm_rope, q_out: torch.Tensor | None = None,
+                       cu: torch.Tensor | None = None, stream=None) -> None:
+    """qmm_kv_append with positions int32 [axes, N], one of each axis: pair j of a
+    head turns by positions[axis_of_pair[j]] (rope_axes; see qmm.h)."""
+    if axes.pairs * 2 != rope.dim:
+        raise ValueError("qmm_kv_append_axes: an axis for each of the rope's dim / 2 pairs")
+    if positions.dim() != 2 or positions.shape[0] != axes.axes or positions.shape[1] != k.shape[0]:
+        raise ValueError("qmm_kv_append_axes: positions must be [axes, N]")
+    _append("qmm_kv_append_axes", cache, q, k, v, q_out, rope, positions, cu, stream, axes)
 
 
 def qmm_tree_attention_workspace_bytes(cache: qmm_kv_cache, Hq: int, T: int,
@@ -877,6 +931,61 @@ def qmm_tree_attention(cache: qmm_kv_cache, q: torch.Tensor, O: torch.Tensor, T:
         raise QmmError(rc, "qmm_tree_attention")
 
 
+def prefix(table: torch.Tensor, lens: torch.Tensor, first: torch.Tensor) -> qmm_prefix:
+    """Prefixes that runs of a batch's sequences share: table int32 [G, max_pages],
+    lens int32 [G], first int32 [G + 1] (sequences first[g] .. first[g + 1] - 1 share
+    prefix g).  Checked once here; the tensors are kept alive by the result."""
+    for t, n in ((table, "table"), (lens, "lens"), (first, "first")):
+        _dev(t, _INT32, n)
+    if table.dim() != 2 or tuple(lens.shape) != (table.shape[0],) or \
+            tuple(first.shape) != (table.shape[0] + 1,):
+        raise ValueError("table must be [G, max_pages], lens [G] and first [G + 1]")
+    if len({t.get_device() for t in (table, lens, first)}) != 1:
+        raise ValueError("the prefixes' tensors are on different devices")
+    p = qmm_prefix(table.data_ptr(), lens.data_ptr(), first.data_ptr(), *table.shape)
+    p.tensors = (table, lens, first)
+    p.device = table.get_device()
+    p.ref = ctypes.addressof(p)
+    return p
+
+
+def qmm_prefix_attention_workspace_bytes(cache: qmm_kv_cache, Hq: int, N: int, T: int,
+                                         num_sms: int = 0) -> int:
+    return int(lib().qmm_prefix_attention_workspace_bytes(ctypes.byref(cache), Hq, N, T, num_sms))
+
+
+def qmm_prefix_attention(cache: qmm_kv_cache, prefix: qmm_prefix, q: torch.Tensor,
+                         O: torch.Tensor, T: int, parents: torch.Tensor | None = None,
+                         cu: torch.Tensor | None = None, scale: float = 0.0,
+                         workspace: torch.Tensor | None = None, stream=None) -> None:
+    """qmm_tree_attention of a batch whose sequences also see the prefix that they
+    share (prefix()), in front of their own slots (see qmm.h)."""
+    device = cache.device
+    if not (q.get_device() == device == O.get_device() and _current(device) and
+            (parents is None or parents.get_device() == device) and
+            (cu is None or cu.get_device() == device) and
+            (workspace is None or workspace.get_device() == device)):
+        _elsewhere(device, (q, O, parents, cu, workspace))
+    if prefix.device != device:
+        raise ValueError("the prefixes are not on the cache's device")
+    shape = q.shape
+    N, Hq, D = shape
+    if D != cache.D or O.shape != shape:
+        raise ValueError("qmm_prefix_attention: inconsistent shapes")
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    rc = (_lib or lib()).qmm_prefix_attention(
+        cache.ref, prefix.ref, q.data_ptr(), _heads(q, N, Hq, D, "q"), _ptr(O, _BF16, "O"), N, T,
+        Hq, None if cu is None else _ints(cu, cache.B + 1, "cu"),
+        None if parents is None else _ints(parents, N, "parents"), scale, ws, ws_bytes,
+        _stream_on(device, stream))
+    if rc != QMM_OK:
+        raise QmmError(rc, "qmm_prefix_attention")
+
+
 def qmm_tree_accept(caches, tokens: torch.Tensor, targets: torch.Tensor, T: int,
                     path: torch.Tensor, count: torch.Tensor, next: torch.Tensor | None = None,
                     new_lens: torch.Tensor | None = None, parents: torch.Tensor | None = None,
@@ -901,6 +1010,81 @@ def qmm_tree_accept(caches, tokens: torch.Tensor, targets: torch.Tensor, T: int,
         None if new_lens is None else _ints(new_lens, B, "new_lens"), _stream_on(device, stream))
     if rc != QMM_OK:
         raise QmmError(rc, "qmm_tree_accept")
+
+
+def _mass(t: torch.Tensor, layers: int, cache: qmm_kv_cache, name: str):
+    """Layer and row strides of weights [layers, B, Hkv, S] (one layer: [B, Hkv, S]
+    too), S at least the slots of a sequence's table."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not torch.float32:
+        raise TypeError("%s must be float32" % name)
+    if layers == 1 and len(shape) == 3:
+        shape, stride = (1, *shape), (0, *stride)
+    if len(shape) != 4 or shape[:3] != (layers, cache.B, cache.Hkv) or \
+            shape[3] < cache.max_pages * cache.page_size:
+        raise ValueError("%s must be [layers, B, Hkv, S], S at least max_pages * page_size" % name)
+    # (a dimension of one row has no stride)
+    row = stride[2] if cache.Hkv > 1 else (stride[1] if cache.B > 1 else (shape[3] + 3) // 4 * 4)
+    if stride[3] != 1 or (cache.B > 1 and stride[1] != cache.Hkv * row):
+        raise ValueError("%s: a layer's rows must be evenly spaced, their values contiguous" % name)
+    return stride[0] if layers > 1 else cache.B * cache.Hkv * row, row
+
+
+def qmm_scored_attention_workspace_bytes(cache: qmm_kv_cache, Hq: int, T: int,
+                                         num_sms: int = 0) -> int:
+    return int(lib().qmm_scored_attention_workspace_bytes(ctypes.byref(cache), Hq, T, num_sms))
+
+
+def qmm_scored_attention(cache: qmm_kv_cache, q: torch.Tensor, O: torch.Tensor, T: int,
+                         mass: torch.Tensor, decay: float = 1.0, cu: torch.Tensor | None = None,
+                         scale: float = 0.0, workspace: torch.Tensor | None = None,
+                         stream=None) -> None:
+    """qmm_tree_attention of a chain that also adds each slot's softmax weights to
+    mass, float32 [B, Hkv, S], whose old sums count `decay` times (see qmm.h)."""
+    device = cache.device
+    if not (q.get_device() == device == O.get_device() and _current(device) and
+            mass.get_device() == device and (cu is None or cu.get_device() == device) and
+            (workspace is None or workspace.get_device() == device)):
+        _elsewhere(device, (q, O, mass, cu, workspace))
+    shape = q.shape
+    N, Hq, D = shape
+    if D != cache.D or O.shape != shape:
+        raise ValueError("qmm_scored_attention: inconsistent shapes")
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    rc = (_lib or lib()).qmm_scored_attention(
+        cache.ref, q.data_ptr(), _heads(q, N, Hq, D, "q"), _ptr(O, _BF16, "O"), N, T, Hq,
+        None if cu is None else _ints(cu, cache.B + 1, "cu"), scale, mass.data_ptr(),
+        _mass(mass, 1, cache, "mass")[1], decay, ws, ws_bytes, _stream_on(device, stream))
+    if rc != QMM_OK:
+        raise QmmError(rc, "qmm_scored_attention")
+
+
+def qmm_kv_evict(caches, mass: torch.Tensor, keep: int, kept: torch.Tensor,
+                 new_lens: torch.Tensor, sinks: int = 0, recent: int = 0,
+                 mass_out: torch.Tensor | None = None, stream=None) -> None:
+    """Bring every sequence of `caches` (kv_caches()) back to `keep` slots: the
+    first `sinks`, the last `recent` and the heaviest others by mass, float32 [n,
+    B, Hkv, S], whose values move along into mass_out (None: mass itself).  kept
+    int32 [n, B, Hkv, keep] and new_lens int32 [B] are written (see qmm.h)."""
+    device, B, n = caches.device, caches.B, caches.n
+    mass_out = mass if mass_out is None else mass_out
+    if not (mass.get_device() == device == mass_out.get_device() and _current(device) and
+            kept.get_device() == device == new_lens.get_device()):
+        _elsewhere(device, (mass, mass_out, kept, new_lens))
+    c = caches[0]
+    strides = _mass(mass, n, c, "mass")
+    if mass_out is not mass and _mass(mass_out, n, c, "mass_out") != strides:
+        raise ValueError("qmm_kv_evict: mass and mass_out must have the same strides")
+    rc = (_lib or lib()).qmm_kv_evict(
+        caches.ref, n, mass.data_ptr(), mass_out.data_ptr(), *strides, keep, sinks, recent,
+        _ints(kept, n * B * c.Hkv * keep, "kept"), _ints(new_lens, B, "new_lens"),
+        _stream_on(device, stream))
+    if rc != QMM_OK:
+        raise QmmError(rc, "qmm_kv_evict")
 
 
 # ---- split-KV decode attention ---------------------------------------------
