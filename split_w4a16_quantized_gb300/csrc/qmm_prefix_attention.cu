@@ -16,7 +16,7 @@
 #include <algorithm>
 
 #include "qmm.h"
-#include "qmm_tree.cuh"
+#include "qmm_tree_merge.cuh"
 
 namespace qmm {
 namespace {
@@ -25,54 +25,6 @@ constexpr int kRowShift = 7;
 constexpr int kCtasPerSm = 2;
 constexpr int kMergeThreads = 256;
 constexpr int kMergeRows = 16;
-constexpr int kMergeAhead = 4;   // states whose loads a thread has in flight
-
-// Runs that hold a stretch of an item: [c0, c1].
-struct Runs {
-    int c0, c1;
-};
-__device__ __forceinline__ Runs runs_of(const TreeParams& p, const Seq& s, long long before,
-                                        int item, long long len) {
-    const int units = item_units(p, s);
-    const long long start = before + static_cast<long long>(item) * units;
-    return {static_cast<int>((start + p.setup) / len), static_cast<int>((start + units - 1) / len)};
-}
-
-// A row's running state: the largest maximum so far, the sum and TURNS groups of 4
-// columns.
-template <int TURNS>
-struct Acc {
-    float M = -INFINITY, den = 0.f;
-    float4 num[TURNS];
-    // K states at once: their maxima m, sums l and columns o, as many as `real`
-    template <int K>
-    __device__ __forceinline__ void add(const float* m, const float* l, const float4 (*o)[TURNS],
-                                        int real) {
-        float top = M;
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (k < real) top = fmaxf(top, m[k]);
-        const float sub = finite_max(top), old = fast_exp2(M - sub);
-        M = top;
-        den *= old;
-#pragma unroll
-        for (int u = 0; u < TURNS; ++u) {
-            num[u].x *= old, num[u].y *= old;
-            num[u].z *= old, num[u].w *= old;
-        }
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            if (k >= real) break;
-            const float f = fast_exp2(m[k] - sub);
-            den = fmaf(f, l[k], den);
-#pragma unroll
-            for (int u = 0; u < TURNS; ++u) {
-                num[u].x = fmaf(f, o[k][u].x, num[u].x), num[u].y = fmaf(f, o[k][u].y, num[u].y);
-                num[u].z = fmaf(f, o[k][u].z, num[u].z), num[u].w = fmaf(f, o[k][u].w, num[u].w);
-            }
-        }
-    }
-};
 
 // A block takes 16 query rows of a sequence's KV head, a thread a row and every 16th
 // (D = 128; 64: 8th) group of 4 columns.
@@ -123,8 +75,6 @@ __global__ void __launch_bounds__(kMergeThreads)
     if (r < rows) {
         const int node = r / p.QG, head = g * p.QG + r - node * p.QG;
         Acc<TURNS> acc;
-#pragma unroll
-        for (int u = 0; u < TURNS; ++u) acc.num[u] = make_float4(0.f, 0.f, 0.f, 0.f);
         // the states of one entry's item that holds the row (row `at` of the entry)
         auto take = [&](const Seq& e, long long before, int at, int part) {
             const int rt = at >> p.row_shift, in = at & ((1 << p.row_shift) - 1);
@@ -139,27 +89,13 @@ __global__ void __launch_bounds__(kMergeThreads)
                 acc.template add<1>(x.m, x.l, o, 1);
                 return;
             }
-            for (int k0 = c.c0; k0 <= c.c1; k0 += kMergeAhead) {
-                float m[kMergeAhead], l[kMergeAhead];
-                float4 o[kMergeAhead][TURNS];
-#pragma unroll
-                for (int k = 0; k < kMergeAhead; ++k) {
-                    if (k0 + k > c.c1) continue;
-                    const PartialAt x = partial_at<D>(p, 2 * (k0 + k) + (k0 + k == c.c0 ? 1 : 0));
-                    m[k] = x.m[in];
-                    l[k] = x.l[in];
-#pragma unroll
-                    for (int u = 0; u < TURNS; ++u)
-                        o[k][u] = *reinterpret_cast<const float4*>(x.at(in, 4 * (j0 + u * JUMP)));
-                }
-                acc.template add<kMergeAhead>(m, l, o, c.c1 - k0 + 1);
-            }
+            acc.template add_runs<D>(p, c, in, j0, JUMP);
         };
         take(s, before_own, r, 0);
         const int64_t at = static_cast<int64_t>(s.first - pre.first + node) * p.QG + r - node * p.QG;
         if (pre.row_tiles > 0 && at >= 0 && at < static_cast<int64_t>(pre.n) * p.QG)
             take(pre, before_grp, static_cast<int>(at), 1);
-        const float inv = acc.den > 0.f ? p.vscale / acc.den : (acc.den == 0.f ? 0.f : acc.den);
+        const float inv = acc.inverse(p.vscale);
 #pragma unroll
         for (int u = 0; u < TURNS; ++u)
             stage[i][j0 + u * JUMP] =

@@ -3,12 +3,15 @@
 //   mass[b, g, s] = decay mass[b, g, s] + sum over tokens i and heads h of g of
 //                   2^(score(i, h, s) - lse(i, h))
 //
-// with scores in log2 units and lse = log2 sum_s 2^score, which tree attention leaves
-// for every row beside its output.  The weights are known only once a row's whole
-// history has been seen, so the scores are formed again from K behind the attention
-// kernels: a thread a position, which holds its key and goes through the query rows.
+// with scores in log2 units and lse = log2 sum_s 2^score.  The weights are known only
+// once a row's whole history has been seen, so there are two passes over the scores:
+//   up to 8 query rows per KV head (plain decode): the attention kernel leaves the scores,
+//     4 bytes a row and position beside the 4 D of K and V, and the merge kernel's other
+//     blocks add the weights up;
+//   more rows: the scores are formed again from K, behind attention and merge, which leave
+//     each row's lse.
 #include "qmm.h"
-#include "qmm_tree.cuh"
+#include "qmm_tree_merge.cuh"
 
 namespace qmm {
 namespace {
@@ -105,11 +108,237 @@ __global__ void __launch_bounds__(kMassThreads)
     }
 }
 
+// ---- up to 8 rows ----
+//
+// One launch behind the attention kernel.  Blocks of the first B Hkv finish an output
+// each: a thread a row and a few groups of 4 columns.  The others take equal runs of the
+// batch's chunks of positions: a warp a row for its lse, from the states or, where one
+// run held the item, from the attention kernel; then a thread 4 positions of a chunk.
+constexpr int kFinishThreads = 256;
+constexpr int kChunk = 4 * kFinishThreads;
+
+struct FinishParams {
+    TreeParams t;
+    float* mass;
+    int64_t mass_stride;
+    float decay;
+    int outputs;   // blocks that finish an output
+};
+
+__device__ __forceinline__ int chunks_of(const Seq& s) {
+    return (s.total + kChunk - 1) / kChunk;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kFinishThreads)
+    scored_finish_kernel(const __grid_constant__ FinishParams p) {
+    __shared__ long long red[3][kFinishThreads / 32];
+    __shared__ __align__(16) uint2 stage[1 << kFewRowShift][D / 4 + 2];
+    __shared__ float lse_s[1 << kFewRowShift];
+    __shared__ long long before_s, chunk_s;
+    __shared__ int b_s;
+    const TreeParams& t = p.t;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const bool adds = static_cast<int>(blockIdx.x) >= p.outputs;
+    // The batch's units of work and chunks.  Read from L2 ahead of the wait: the attention
+    // kernel's threads let this one start only behind their own wait for everything before.
+    const int per = (t.d.B + kFinishThreads - 1) / kFinishThreads;
+    const int b0 = min(t.d.B, tid * per), b1 = min(t.d.B, b0 + per);
+    long long units = 0, chunks = 0, all_units, all_chunks;
+    Seq s = {};
+    for (int b = b0; b < b1; ++b) {
+        s = sequence<true>(t, b);
+        units += units_of(t, s);
+        chunks += static_cast<long long>(chunks_of(s)) * t.d.Hkv;
+    }
+    if (tid == 0) b_s = -1;
+    const long long u0 = block_scan<kFinishThreads>(units, red[0], &all_units);
+    const long long c0 = block_scan<kFinishThreads>(chunks, red[1], &all_chunks);
+    const long long run = run_length(t, all_units);
+    const long long adders = gridDim.x - p.outputs;
+    const long long share = adders > 0 ? (all_chunks + adders - 1) / adders : 0;
+    const long long start = adds ? share * (blockIdx.x - p.outputs) : 0;
+    {   // the sequence that this block starts in, and the units before it
+        const int want = adds ? -1 : static_cast<int>(blockIdx.x) / t.d.Hkv;
+        long long u = u0, c = c0;
+        for (int b = b0; b < b1; ++b) {
+            if (per > 1) s = sequence<true>(t, b);
+            const long long mine = static_cast<long long>(chunks_of(s)) * t.d.Hkv;
+            if (adds ? start >= c && start < c + mine : b == want) {
+                b_s = b;
+                before_s = u;
+                chunk_s = start - c;
+            }
+            u += units_of(t, s);
+            c += mine;
+        }
+    }
+    __syncthreads();
+    int b = b_s;
+    long long before = before_s;
+    pdl_trigger();
+    pdl_wait();
+    if (b < 0) return;
+    s = sequence<true>(t, b);
+    if (!adds) {
+        const int g = blockIdx.x % t.d.Hkv;
+        const int rows = s.n * t.QG;
+        if (rows == 0) return;
+        const Runs c = runs_of(t, s, before, g, run);
+        if (c.c0 == c.c1) return;   // written by the attention kernel
+        constexpr int ROWS = 1 << kFewRowShift, JUMP = kFinishThreads / ROWS;
+        constexpr int TURNS = D / 4 / JUMP > 0 ? D / 4 / JUMP : 1;
+        const int i = tid % ROWS, j0 = tid / ROWS;
+        if (i < rows && j0 < D / 4) {
+            Acc<TURNS> acc;
+            acc.template add_runs<D>(t, c, i, j0, JUMP);
+            const float inv = acc.inverse(t.vscale);
+#pragma unroll
+            for (int u = 0; u < TURNS; ++u)
+                stage[i][j0 + u * JUMP] =
+                    make_uint2(pack_bf16x2(acc.num[u].x * inv, acc.num[u].y * inv),
+                               pack_bf16x2(acc.num[u].z * inv, acc.num[u].w * inv));
+        }
+        __syncthreads();
+        constexpr int CH = D / 8;   // 16-byte chunks of a row
+        const int ri = tid / CH, ch = tid % CH;
+        if (ri < rows) {
+            const int node = ri / t.QG;
+            const int64_t to = static_cast<int64_t>(s.first + node) * t.Hq + g * t.QG + ri - node * t.QG;
+            *reinterpret_cast<uint4*>(t.O + to * D + 8 * ch) =
+                *reinterpret_cast<const uint4*>(&stage[ri][2 * ch]);
+        }
+        return;
+    }
+    // ---- weights ----
+    long long left = all_chunks - start < share ? all_chunks - start : share;
+    long long at = chunk_s;
+    const int all_rows = t.T * t.QG;
+    while (left > 0) {
+        while (at >= static_cast<long long>(chunks_of(s)) * t.d.Hkv) {
+            at -= static_cast<long long>(chunks_of(s)) * t.d.Hkv;
+            before += units_of(t, s);
+            if (++b >= t.d.B) return;   // (not reached: the run ends with the list)
+            s = sequence<true>(t, b);
+        }
+        const int per_head = chunks_of(s);
+        const int g = static_cast<int>(at / per_head), k0 = static_cast<int>(at - static_cast<long long>(g) * per_head);
+        const int k1 = static_cast<int>(left < per_head - k0 ? k0 + left : per_head);
+        at += k1 - k0;
+        left -= k1 - k0;
+        const int rows = s.n * t.QG;
+        const int total = s.total;
+        // each row's lse
+        __syncthreads();
+        if (warp < rows) {
+            const Runs c = runs_of(t, s, before, g, run);
+            const int node = warp / t.QG;
+            if (c.c0 == c.c1) {
+                if (lane == 0) lse_s[warp] = *stat_at(t, b, node, g * t.QG + warp - node * t.QG);
+            } else {
+                float M = -INFINITY, den = 0.f;
+                for (int k = c.c0 + lane; k <= c.c1; k += 32) {
+                    const PartialAt x = partial_at<D>(t, 2 * k + (k == c.c0 ? 1 : 0));
+                    const float m = x.m[warp], l = x.l[warp];
+                    const float top = fmaxf(M, m), sub = finite_max(top);
+                    den = fmaf(den, fast_exp2(M - sub), fast_exp2(m - sub) * l);
+                    M = top;
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    const float m = __shfl_xor_sync(0xffffffffu, M, o);
+                    const float l = __shfl_xor_sync(0xffffffffu, den, o);
+                    const float top = fmaxf(M, m), sub = finite_max(top);
+                    den = fmaf(den, fast_exp2(M - sub), fast_exp2(m - sub) * l);
+                    M = top;
+                }
+                if (lane == 0) lse_s[warp] = stat_of(t, M, den);
+            }
+        }
+        __syncthreads();
+        const int64_t col = static_cast<int64_t>(b) * t.d.Hkv + g;
+        const float* scores = t.scores + col * all_rows * t.score_stride;
+        float* mass = p.mass + col * p.mass_stride;
+        for (int k = k0; k < k1; ++k) {
+            const int64_t pos = static_cast<int64_t>(k) * kChunk + 4 * tid;
+            if (pos >= total) continue;
+            float w[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int r = 0; r < rows; ++r) {
+                const float4 v = *reinterpret_cast<const float4*>(scores + r * t.score_stride + pos);
+                const float lse = lse_s[r];
+                w[0] += fast_exp2(v.x - lse), w[1] += fast_exp2(v.y - lse);
+                w[2] += fast_exp2(v.z - lse), w[3] += fast_exp2(v.w - lse);
+            }
+            if (p.decay != 0.f) {   // (a multiple of 4 slots is the caller's: cap and strides are)
+                const float4 old = *reinterpret_cast<const float4*>(mass + pos);
+                if (pos < s.len) w[0] = fmaf(p.decay, old.x, w[0]);
+                if (pos + 1 < s.len) w[1] = fmaf(p.decay, old.y, w[1]);
+                if (pos + 2 < s.len) w[2] = fmaf(p.decay, old.z, w[2]);
+                if (pos + 3 < s.len) w[3] = fmaf(p.decay, old.w, w[3]);
+            }
+            if (pos + 3 < total)
+                *reinterpret_cast<float4*>(mass + pos) = make_float4(w[0], w[1], w[2], w[3]);
+            else
+                for (int i = 0; i < 4 && pos + i < total; ++i) mass[pos + i] = w[i];
+        }
+    }
+}
+
+size_t scores_floats(const qmm_kv_cache& c, int rows) {
+    const int64_t cap = static_cast<int64_t>(c.max_pages) * c.page_size;
+    const int64_t stride = (cap + (1 << kFewTileShift) - 1) >> kFewTileShift << kFewTileShift;
+    return static_cast<size_t>(c.B) * c.Hkv * rows * stride;
+}
+
 }  // namespace
 
+// Behind the attention's states: lse [B][T][Hq], and the scores for few rows.
+static size_t lse_floats(const qmm_kv_cache& c, int T, int Hq) {
+    return (static_cast<size_t>(c.B) * T * Hq + 3) / 4 * 4;
+}
+
 size_t scored_attention_workspace(const qmm_kv_cache& c, int T, int Hq, int num_sms) {
-    return tree_attention_workspace(c.D, T * (Hq / c.Hkv), num_sms) +
-           static_cast<size_t>(c.B) * T * Hq * sizeof(float);
+    const int rows = T * (Hq / c.Hkv);
+    return tree_attention_workspace(c.D, rows, num_sms) +
+           (lse_floats(c, T, Hq) + (rows <= 1 << kFewRowShift ? scores_floats(c, rows) : 0)) *
+               sizeof(float);
+}
+
+static int launch_few_rows(const qmm_kv_cache& c, const void* q, int64_t q_stride, void* O, int N,
+                           int T, int Hq, const int* cu, float scale, float* mass,
+                           int64_t mass_stride, float decay, float* ws, float* lse, int num_sms,
+                           void* stream) {
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) return cudaErrorInvalidDevice;
+    const bool fp8 = c.dtype == QMM_CACHE_E4M3;
+    FinishParams p = {};
+    CUtensorMap kmap, vmap;
+    int rc = tree_setup(c, q, q_stride, O, N, T, Hq, cu, nullptr, scale, ws,
+                        kFewCtasPerSm * num_sms, kFewRowShift, kFewTileShift, kFewMinRun, kFewSetup,
+                        &p.t, &kmap, &vmap);
+    if (rc != cudaSuccess) return rc;
+    p.t.lse = lse;
+    p.t.lift = fp8 ? kFewLift : 0.f;
+    p.t.scores = lse + lse_floats(c, T, Hq);
+    p.t.score_stride = (static_cast<int64_t>(p.t.d.cap) + (1 << kFewTileShift) - 1) >>
+                       kFewTileShift << kFewTileShift;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    rc = launch_tree_scores(kmap, vmap, p.t, c.D, fp8, device, st);
+    if (rc != cudaSuccess) return rc;
+    p.mass = mass;
+    p.mass_stride = mass_stride;
+    p.decay = decay;
+    p.outputs = c.B * c.Hkv;
+    const int64_t chunks = (static_cast<int64_t>(p.t.d.cap) + kChunk - 1) / kChunk * p.outputs;
+    const int64_t adders = chunks < 4 * num_sms ? chunks : 4 * num_sms;
+    cudaLaunchConfig_t cfg = {};
+    LaunchAttrs la;
+    apply_pdl(cfg, la);
+    cfg.gridDim = dim3(static_cast<unsigned>(p.outputs + adders), 1, 1);
+    cfg.blockDim = dim3(kFinishThreads, 1, 1);
+    cfg.stream = st;
+    return c.D == 128 ? cudaLaunchKernelEx(&cfg, scored_finish_kernel<128>, p)
+                      : cudaLaunchKernelEx(&cfg, scored_finish_kernel<64>, p);
 }
 
 int launch_scored_attention(const qmm_kv_cache& c, const void* q, int64_t q_stride, void* O, int N,
@@ -117,6 +346,9 @@ int launch_scored_attention(const qmm_kv_cache& c, const void* q, int64_t q_stri
                             int64_t mass_stride, float decay, float* ws, int num_sms,
                             void* stream) {
     float* lse = ws + tree_attention_workspace(c.D, T * (Hq / c.Hkv), num_sms) / sizeof(float);
+    if (T * (Hq / c.Hkv) <= 1 << kFewRowShift)
+        return launch_few_rows(c, q, q_stride, O, N, T, Hq, cu, scale, mass, mass_stride, decay, ws,
+                               lse, num_sms, stream);
     const int rc = launch_tree_attention(c, q, q_stride, O, N, T, Hq, cu, nullptr, scale, ws,
                                          num_sms, stream, lse);
     if (rc != cudaSuccess) return rc;

@@ -50,6 +50,8 @@ struct TreeParams {
     float vscale;
     float* lse;      // (nullable) [B][T][Hq] log2 of a row's sum of 2^score, as stat_of
     float lift;      // log2 of the factor on the weights that the sums hold
+    float* scores;   // [B][Hkv][T QG][score_stride]: each row's scores, for up to 8 rows
+    int64_t score_stride;
     SharedPrefixes pre;
 };
 
@@ -468,7 +470,13 @@ constexpr int kTcTileShift = 6;
 constexpr float kTcLift = 7.f;   // log2 of its factor on F16 weights
 int launch_tree_tc(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int D,
                    bool fp8, int device, cudaStream_t st);
-// The same with shared prefixes (p.pre), items of up to 128 rows: every item leaves a
+// One launch of the kernel for up to 8 rows (qmm_tree_attention.cu) that also leaves
+// each row's scores in p.scores; the merge is the caller's.
+constexpr int kFewRowShift = 3, kFewTileShift = 6, kFewCtasPerSm = 2, kFewMinRun = 2, kFewSetup = 1;
+constexpr float kFewLift = 15.f;   // log2 of its factor on F16 weights
+int launch_tree_scores(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int D,
+                       bool fp8, int device, cudaStream_t st);
+// The tcgen05 kernel with shared prefixes (p.pre), items of up to 128 rows: every item leaves a
 // state, and the merge is the caller's (qmm_prefix_attention.cu).
 int launch_prefix_tc(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int D,
                      bool fp8, int device, cudaStream_t st);

@@ -39,14 +39,13 @@ bool encode_tiled_promoted(CUtensorMap* map, CUtensorMapDataType type, int rank,
 
 namespace {
 
-constexpr int kTile = 64;      // positions per tile
-constexpr int kRows = 8;       // query rows per work item
+constexpr int kTile = 1 << kFewTileShift;   // positions per tile
+constexpr int kRows = 1 << kFewRowShift;    // query rows per work item
 constexpr int kWarps = 4;      // compute warps
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kKeys = kTile / kWarps;   // positions per compute warp
 constexpr int kStages = 3;
-constexpr int kCtasPerSm = 2;
-constexpr float kLift = 15.f;  // log2 of the factor on F16 weights
+constexpr int kCtasPerSm = kFewCtasPerSm;
 
 // ---- shared memory tiles ----------------------------------------------------
 
@@ -130,7 +129,9 @@ __device__ __forceinline__ void mma16816(float d[4], const uint32_t a[4], uint32
 //     of the columns from the other three.
 // Every wait is bounded (1 s): a wait that runs out sets the status word and
 // the CTA winds down after its copies in flight have landed.
-template <int D, bool kFp8>
+// kScores: the scores go to p.scores, and the lse of an item's rows to p.lse, as well: one more store of 8 bytes for two of them
+// (32 rows of 1024 to 8192 positions: the kernel 84 us, without 78).
+template <int D, bool kFp8, bool kScores>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     tree_attn_kernel(const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap,
@@ -282,6 +283,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             float o[NB][2];
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) o[nb][0] = o[nb][1] = 0.f;
+            float* const score_row =
+                kScores ? p.scores + ((static_cast<int64_t>(x.b) * p.d.Hkv + x.g) * (p.T * p.QG) +
+                                      row) * p.score_stride
+                        : nullptr;
             float m_run = -INFINITY, l_run = 0.f;   // l_run: this lane's share of the row's sum
 
             for (int t = x.t0; t < x.t1; ++t, ++it) {
@@ -350,11 +355,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                             if (!see) v[e] = -INFINITY;
                         }
                     }
+                    if (kScores && on) {
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2)
+                            *reinterpret_cast<float2*>(score_row + pos0 + 4 * e + 2 * tq) =
+                                make_float2(v[e], v[e + 1]);
+                    }
                     float mx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                     const float mn = fmaxf(m_run, mx), mf = finite_max(mn);
-                    const float corr = fast_exp2(m_run - mf), by = mf - (kFp8 ? kLift : 0.f);
+                    const float corr = fast_exp2(m_run - mf), by = mf - (kFp8 ? kFewLift : 0.f);
                     m_run = mn;
                     float pw[4], rs = 0.f;
 #pragma unroll
@@ -484,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     part.m[gr] = M;
                     part.l[gr] = den;
                 }
-                if (whole && p.lse && warp == 0 && tq == 0)
+                if (kScores && whole && warp == 0 && tq == 0)
                     *stat_at(p, x.b, node, head) = stat_of(p, M, den);
                 __nv_bfloat16* out =
                     p.O + (static_cast<int64_t>(x.s.first + node) * p.Hq + head) * D;
@@ -673,11 +684,11 @@ __global__ void __launch_bounds__(kMergeThreads)
     }
 }
 
-template <int D, bool kFp8>
+template <int D, bool kFp8, bool kScores>
 int launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int device,
            cudaStream_t st) {
     using C = Cfg<D, kFp8>;
-    auto kern = tree_attn_kernel<D, kFp8>;
+    auto kern = tree_attn_kernel<D, kFp8, kScores>;
     const size_t smem = 1024 + static_cast<size_t>(kStages) * C::STAGE + sizeof(Smem<D>);
     static PerDevice<bool> opted_in;
     if (!opted_in.get(device, [&] {
@@ -693,6 +704,16 @@ int launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     return cudaLaunchKernelEx(&cfg, kern, kmap, vmap, p);
+}
+
+template <bool kScores>
+int launch_few(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int D,
+               bool fp8, int device, cudaStream_t st) {
+    if (D == 128)
+        return fp8 ? launch<128, true, kScores>(kmap, vmap, p, device, st)
+                   : launch<128, false, kScores>(kmap, vmap, p, device, st);
+    return fp8 ? launch<64, true, kScores>(kmap, vmap, p, device, st)
+               : launch<64, false, kScores>(kmap, vmap, p, device, st);
 }
 
 int launch_merge(const TreeParams& p, int D, cudaStream_t st) {
@@ -732,7 +753,7 @@ struct Variant {
     int row_shift, tile_shift, ctas_per_sm, min_run, setup;
 };
 Variant variant(int rows, bool fp8) {
-    if (rows <= kRows) return {false, 3, 6, kCtasPerSm, 2, 1};
+    if (rows <= kRows) return {false, kFewRowShift, kFewTileShift, kCtasPerSm, kFewMinRun, kFewSetup};
     if (rows <= 128) return {true, 7, kTcTileShift, 2, 6, fp8 ? 8 : 4};
     return {true, 8, kTcTileShift, 1, 6, fp8 ? 8 : 4};
 }
@@ -807,6 +828,11 @@ int tree_setup(const qmm_kv_cache& c, const void* q, int64_t q_stride, void* O, 
     return cudaSuccess;
 }
 
+int launch_tree_scores(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int D,
+                       bool fp8, int device, cudaStream_t st) {
+    return launch_few<true>(kmap, vmap, p, D, fp8, device, st);
+}
+
 int launch_tree_attention(const qmm_kv_cache& c, const void* q, int64_t q_stride, void* O, int N,
                           int T, int Hq, const int* cu, const int* parents, float scale,
                           float* ws, int num_sms, void* stream, float* lse) {
@@ -821,17 +847,10 @@ int launch_tree_attention(const qmm_kv_cache& c, const void* q, int64_t q_stride
                                var.min_run, var.setup, &p, &kmap, &vmap);
     if (err != cudaSuccess) return err;
     p.lse = lse;
-    p.lift = fp8 ? (var.tc ? kTcLift : kLift) : 0.f;
+    p.lift = fp8 ? (var.tc ? kTcLift : kFewLift) : 0.f;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    int rc;
-    if (var.tc)
-        rc = launch_tree_tc(kmap, vmap, p, c.D, fp8, device, st);
-    else if (c.D == 128)
-        rc = fp8 ? launch<128, true>(kmap, vmap, p, device, st)
-                 : launch<128, false>(kmap, vmap, p, device, st);
-    else
-        rc = fp8 ? launch<64, true>(kmap, vmap, p, device, st)
-                 : launch<64, false>(kmap, vmap, p, device, st);
+    const int rc = var.tc ? launch_tree_tc(kmap, vmap, p, c.D, fp8, device, st)
+                          : launch_few<false>(kmap, vmap, p, c.D, fp8, device, st);
     return rc == cudaSuccess ? launch_merge(p, c.D, st) : rc;
 }
 
