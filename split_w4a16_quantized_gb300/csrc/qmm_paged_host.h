@@ -39,6 +39,10 @@ int launch_scored_attention(const qmm_kv_cache& c, const void* q, int64_t q_stri
                             int T, int Hq, const int* cu, float scale, float* mass,
                             int64_t mass_stride, float decay, float* ws, int num_sms,
                             void* stream);
+// The weights of more than 8 rows per KV head, once each row's lse is there (qmm_mass_tc.cu).
+int launch_mass_tc(const qmm_kv_cache& c, const void* q, int64_t q_stride, int N, int T, int Hq,
+                   const int* cu, float scale, const float* lse, float* mass, int64_t mass_stride,
+                   float decay, int num_sms, void* stream);
 // Tree attention with shared prefixes (qmm_prefix_attention.cu); rows: N * Hq.
 size_t prefix_attention_workspace(int D, int64_t rows, int num_sms);
 int launch_prefix_attention(const qmm_kv_cache& c, const qmm_prefix& pre, const void* q,
