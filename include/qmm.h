@@ -798,7 +798,7 @@ typedef struct {
  *     of at most T tokens, for all of them to see it;
  *   - the workspace is qmm_prefix_attention_workspace_bytes, which grows with N;
  *   - QMM_EINVAL also for a NULL prefix or array, G or max_pages below 1; QMM_ESHAPE for
- *     G above 65535, N Hq above 2^31 - 1, a prefix table of more than 2^31 - 65536 slots,
+ *     G above B, N Hq above 2^31 - 1, a prefix table of more than 2^31 - 65536 slots,
  *     or (s / 64 + 16) * (ceil(N Hq / (128 Hkv)) + G) * Hkv above 2^31 - 1, s being its
  *     slots; QMM_EALIGN for arrays that are not 4-byte aligned.
  * Two launches. */
@@ -807,8 +807,8 @@ int qmm_prefix_attention(const qmm_kv_cache *cache, const qmm_prefix *prefix, co
                          const int *parents, float scale, void *workspace, size_t ws_bytes,
                          void *stream);
 
-/* Workspace bytes of qmm_prefix_attention for this cache and N tokens, whatever the
- * lengths and prefixes.  num_sms <= 0 queries the device.  0 for invalid arguments.
+/* Workspace bytes of qmm_prefix_attention for this cache and N tokens, at most T a
+ * sequence, whatever the lengths and prefixes.  num_sms <= 0 queries the device.  0 for invalid arguments.
  * Host only. */
 size_t qmm_prefix_attention_workspace_bytes(const qmm_kv_cache *cache, int Hq, int N, int T,
                                             int num_sms);

@@ -1270,7 +1270,7 @@ int qmm_tree_attention(const qmm_kv_cache* cache, const void* q, int64_t q_strid
 static int check_prefix(const qmm_kv_cache* c, const qmm_prefix* pre, int Hq, int N) {
     if (pre->max_pages < 1 || pre->G < 1 || N < 1) return QMM_EINVAL;
     const int64_t cap = static_cast<int64_t>(pre->max_pages) * c->page_size;
-    if (pre->G > 65535 || cap > 0x7fff0000LL || static_cast<int64_t>(N) * Hq > INT_MAX)
+    if (pre->G > c->B || cap > 0x7fff0000LL || static_cast<int64_t>(N) * Hq > INT_MAX)
         return QMM_ESHAPE;
     // units of work in 32 bits, as in check_tree: row tiles of 128 rows, a last one of
     // each prefix in part
@@ -1284,7 +1284,7 @@ size_t qmm_prefix_attention_workspace_bytes(const qmm_kv_cache* cache, int Hq, i
         static_cast<int64_t>(N) * Hq > INT_MAX)
         return 0;
     if (num_sms <= 0 && device_sms(&num_sms) != QMM_OK) return 0;
-    return qmm::prefix_attention_workspace(cache->D, static_cast<int64_t>(N) * Hq, num_sms);
+    return qmm::prefix_attention_workspace(cache->D, static_cast<int64_t>(N) * Hq, cache->B, num_sms);
 }
 
 int qmm_prefix_attention(const qmm_kv_cache* cache, const qmm_prefix* prefix, const void* q,
@@ -1308,7 +1308,7 @@ int qmm_prefix_attention(const qmm_kv_cache* cache, const qmm_prefix* prefix, co
     rc = device_ready(&sms);
     if (rc != QMM_OK) return rc;
     if (!workspace || ws_bytes < qmm::prefix_attention_workspace(
-                                     cache->D, static_cast<int64_t>(N) * Hq, sms))
+                                     cache->D, static_cast<int64_t>(N) * Hq, cache->B, sms))
         return QMM_EWORKSPACE;
     if (!aligned(workspace, 16)) return QMM_EALIGN;
     const float sc = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(cache->D));

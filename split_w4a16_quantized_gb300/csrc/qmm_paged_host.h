@@ -44,7 +44,7 @@ int launch_mass_tc(const qmm_kv_cache& c, const void* q, int64_t q_stride, int N
                    const int* cu, float scale, const float* lse, float* mass, int64_t mass_stride,
                    float decay, int num_sms, void* stream);
 // Tree attention with shared prefixes (qmm_prefix_attention.cu); rows: N * Hq.
-size_t prefix_attention_workspace(int D, int64_t rows, int num_sms);
+size_t prefix_attention_workspace(int D, int64_t rows, int B, int num_sms);
 int launch_prefix_attention(const qmm_kv_cache& c, const qmm_prefix& pre, const void* q,
                             int64_t q_stride, void* O, int N, int T, int Hq, const int* cu,
                             const int* parents, float scale, float* ws, int num_sms,

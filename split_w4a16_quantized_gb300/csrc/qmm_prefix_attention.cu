@@ -23,78 +23,59 @@ namespace {
 
 constexpr int kRowShift = 7;
 constexpr int kCtasPerSm = 2;
-constexpr int kMergeThreads = 256;
-constexpr int kMergeRows = 16;
-
-// A block takes 16 query rows of a sequence's KV head, a thread a row and every 16th
-// (D = 128; 64: 8th) group of 4 columns.
-template <int D>
-__global__ void __launch_bounds__(kMergeThreads)
+// A block takes ROWS query rows of a sequence's KV head, a thread a row and every 16th
+// (D = 128; 64: each) group of 4 columns.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(16 * ROWS)
     prefix_merge_kernel(const __grid_constant__ TreeParams p, int chunks) {
-    __shared__ long long red[3][kMergeThreads / 32];
-    __shared__ int group_s;
-    __shared__ __align__(16) uint2 stage[kMergeRows][D / 4 + 2];   // BF16 rows, padded by 16 bytes
-    const int tid = threadIdx.x;
+    __shared__ __align__(16) uint2 stage[ROWS][D / 4 + 2];   // BF16 rows, padded by 16 bytes
+    const int tid = threadIdx.x, lane = tid & 31;
     const int chunk = blockIdx.x % chunks, g = blockIdx.x / chunks, b = blockIdx.y;
     pdl_trigger();
     pdl_wait();
     const Seq s = sequence<false, true>(p, p.pre.G + b);
-    const int rows = s.n * p.QG, row0 = chunk * kMergeRows;
+    const long long before_own = p.pre.plan[p.pre.G + b];
+    const long long len = run_length(p, p.pre.plan[p.pre.G + p.d.B]);
+    // the first prefix that holds the sequence
+    int group = -1;
+    for (int j0 = 0; group < 0 && j0 < p.pre.G; j0 += 32) {
+        int b0 = 0, b1 = 0;
+        if (j0 + lane < p.pre.G) group_range<false>(p, j0 + lane, &b0, &b1);
+        const uint32_t hit = __ballot_sync(0xffffffffu, b >= b0 && b < b1);
+        if (hit) group = j0 + __ffs(hit) - 1;
+    }
+    Seq shared = {};
+    long long before_pre = 0;
+    if (group >= 0) {
+        shared = sequence<false, true>(p, group);
+        before_pre = p.pre.plan[group];
+    }
+    const int rows = s.n * p.QG, row0 = chunk * ROWS;
     if (row0 >= rows) return;   // (the same for the whole block)
-    // the sequence's prefix: the first that holds it
-    if (tid == 0) group_s = p.pre.G;
-    __syncthreads();
-    for (int j = tid; j < p.pre.G; j += kMergeThreads) {
-        int b0, b1;
-        group_range<false>(p, j, &b0, &b1);
-        if (b >= b0 && b < b1) atomicMin(&group_s, j);
-    }
-    __syncthreads();
-    const int grp = group_s;
-    long long all = 0, before_own = 0, before_grp = 0;
-    {
-        long long a = 0, o = 0, q = 0;
-        for (int j = tid; j < p.pre.G + p.d.B; j += kMergeThreads) {
-            const long long u = units_of(p, sequence<false, true>(p, j));
-            a += u;
-            if (j < p.pre.G + b) o += u;
-            if (j < grp) q += u;
-        }
-        block_scan<kMergeThreads>(a, red[0], &all);
-        block_scan<kMergeThreads>(o, red[1], &before_own);
-        block_scan<kMergeThreads>(q, red[2], &before_grp);
-    }
-    const long long len = run_length(p, all);
-    Seq pre = {};
-    if (grp < p.pre.G) pre = sequence<false, true>(p, grp);
 
-    constexpr int GROUPS = D / 4;
-    constexpr int TURNS = GROUPS / (kMergeThreads / kMergeRows);   // column groups of a thread
-    constexpr int JUMP = kMergeThreads / kMergeRows;
-    const int i = tid % kMergeRows, r = row0 + i, j0 = tid / kMergeRows;
+    constexpr int JUMP = 16;               // threads of a row
+    constexpr int TURNS = D / 4 / JUMP;    // column groups of a thread
+    const int i = tid % ROWS, r = row0 + i, j0 = tid / ROWS;
     if (r < rows) {
         const int node = r / p.QG, head = g * p.QG + r - node * p.QG;
+        const int64_t row = static_cast<int64_t>(s.first + node) * p.Hq + head;
+        // the runs that hold the row's item of the sequence, and of its prefix
+        const Runs co = runs_of(p, s, before_own, g * s.row_tiles + (r >> p.row_shift), len);
+        const int at = (s.first - shared.first + node) * p.QG + r - node * p.QG;
+        Runs cp = {0, -1};
+        if (shared.row_tiles > 0 && at >= 0 && at < shared.n * p.QG)
+            cp = runs_of(p, shared, before_pre, g * shared.row_tiles + (at >> p.row_shift), len);
+        const int mine = co.c1 - co.c0 + 1, all = mine + cp.c1 - cp.c0 + 1;
         Acc<TURNS> acc;
-        // the states of one entry's item that holds the row (row `at` of the entry)
-        auto take = [&](const Seq& e, long long before, int at, int part) {
-            const int rt = at >> p.row_shift, in = at & ((1 << p.row_shift) - 1);
-            const Runs c = runs_of(p, e, before, g * e.row_tiles + rt, len);
-            if (c.c0 == c.c1) {
-                const DirectAt x =
-                    direct_at<D>(p, part, static_cast<int64_t>(s.first + node) * p.Hq + head);
-                float4 o[1][TURNS];
-#pragma unroll
-                for (int u = 0; u < TURNS; ++u)
-                    o[0][u] = *reinterpret_cast<const float4*>(x.o + 4 * (j0 + u * JUMP));
-                acc.template add<1>(x.m, x.l, o, 1);
-                return;
+        acc.add_all(all, j0, JUMP, [&](int k) -> StateAt {
+            const bool of_own = k < mine;
+            if (of_own ? co.c0 == co.c1 : cp.c0 == cp.c1) {
+                const DirectAt d = direct_at<D>(p, of_own ? 0 : 1, row);
+                return {d.m, d.l, d.o, 4};
             }
-            acc.template add_runs<D>(p, c, in, j0, JUMP);
-        };
-        take(s, before_own, r, 0);
-        const int64_t at = static_cast<int64_t>(s.first - pre.first + node) * p.QG + r - node * p.QG;
-        if (pre.row_tiles > 0 && at >= 0 && at < static_cast<int64_t>(pre.n) * p.QG)
-            take(pre, before_grp, static_cast<int>(at), 1);
+            return of_own ? run_state<D>(p, co.c0 + k, co.c0, r & ((1 << p.row_shift) - 1))
+                          : run_state<D>(p, cp.c0 + k - mine, cp.c0, at & ((1 << p.row_shift) - 1));
+        });
         const float inv = acc.inverse(p.vscale);
 #pragma unroll
         for (int u = 0; u < TURNS; ++u)
@@ -105,7 +86,7 @@ __global__ void __launch_bounds__(kMergeThreads)
     __syncthreads();
     constexpr int CH = D / 8;   // 16-byte chunks of a row
     const int ri = tid / CH, c = tid % CH, rr = row0 + ri;
-    if (ri < kMergeRows && rr < rows) {
+    if (ri < ROWS && rr < rows) {
         const int64_t to = static_cast<int64_t>(s.first + rr / p.QG) * p.Hq + g * p.QG + rr % p.QG;
         *reinterpret_cast<uint4*>(p.O + to * D + 8 * c) =
             *reinterpret_cast<const uint4*>(&stage[ri][2 * c]);
@@ -118,8 +99,13 @@ static size_t slot_floats(int D, int num_sms) {
     return (static_cast<size_t>(2 * kCtasPerSm * num_sms) << kRowShift) * (D + 2);
 }
 
-size_t prefix_attention_workspace(int D, int64_t rows, int num_sms) {
-    return (slot_floats(D, num_sms) + 2 * static_cast<size_t>(rows) * (D + 2)) * sizeof(float);
+// States by run, states by (token, head) of the sequences' own part and the prefixes', and
+// the units before each entry (no more prefixes than sequences).
+static size_t direct_floats(int D, int64_t rows) { return 2 * static_cast<size_t>(rows) * (D + 2); }
+
+size_t prefix_attention_workspace(int D, int64_t rows, int B, int num_sms) {
+    return (slot_floats(D, num_sms) + direct_floats(D, rows)) * sizeof(float) +
+           (2 * static_cast<size_t>(B) + 2) * sizeof(long long);
 }
 
 int launch_prefix_attention(const qmm_kv_cache& c, const qmm_prefix& pre, const void* q,
@@ -141,18 +127,25 @@ int launch_prefix_attention(const qmm_kv_cache& c, const qmm_prefix& pre, const 
     p.pre.max_pages = pre.max_pages;
     p.pre.cap = pre.max_pages * c.page_size;
     p.pre.direct = ws + slot_floats(c.D, num_sms);
+    p.pre.plan = reinterpret_cast<long long*>(
+        p.pre.direct + direct_floats(c.D, static_cast<int64_t>(N) * Hq));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     rc = launch_prefix_tc(kmap, vmap, p, c.D, fp8, device, st);
     if (rc != cudaSuccess) return rc;
-    const int chunks = (T * p.QG + kMergeRows - 1) / kMergeRows;
+    const int rows = T * p.QG, block_rows = rows <= 8 ? 8 : 16;
+    const int chunks = (rows + block_rows - 1) / block_rows;
     cudaLaunchConfig_t cfg = {};
     LaunchAttrs la;
     apply_pdl(cfg, la);
     cfg.gridDim = dim3(static_cast<unsigned>(chunks) * c.Hkv, c.B, 1);
-    cfg.blockDim = dim3(kMergeThreads, 1, 1);
+    cfg.blockDim = dim3(16 * block_rows, 1, 1);
     cfg.stream = st;
-    return c.D == 128 ? cudaLaunchKernelEx(&cfg, prefix_merge_kernel<128>, p, chunks)
-                      : cudaLaunchKernelEx(&cfg, prefix_merge_kernel<64>, p, chunks);
+    auto run = [&](auto kernel) {
+        return static_cast<int>(cudaLaunchKernelEx(&cfg, kernel, p, chunks));
+    };
+    if (c.D == 128)
+        return rows <= 8 ? run(prefix_merge_kernel<128, 8>) : run(prefix_merge_kernel<128, 16>);
+    return rows <= 8 ? run(prefix_merge_kernel<64, 8>) : run(prefix_merge_kernel<64, 16>);
 }
 
 }  // namespace qmm

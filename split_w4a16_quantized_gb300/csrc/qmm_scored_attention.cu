@@ -99,7 +99,8 @@ __global__ void __launch_bounds__(kFinishThreads)
         const int i = tid % ROWS, j0 = tid / ROWS;
         if (i < rows && j0 < D / 4) {
             Acc<TURNS> acc;
-            acc.template add_runs<D>(t, c, i, j0, JUMP);
+            acc.add_all(c.c1 - c.c0 + 1, j0, JUMP,
+                        [&](int k) { return run_state<D>(t, c.c0 + k, c.c0, i); });
             const float inv = acc.inverse(t.vscale);
 #pragma unroll
             for (int u = 0; u < TURNS; ++u)

@@ -29,6 +29,7 @@ struct SharedPrefixes {
     const int *table, *lens, *first;
     int G, max_pages, cap;
     float* direct;   // states of items that one run holds (DirectAt)
+    long long* plan; // units before each entry, and of all: for the merge
 };
 
 struct TreeParams {
@@ -220,6 +221,10 @@ __device__ __forceinline__ Run find_run(const TreeParams& p, RunShared& sh) {
         const int mine = lane < count ? units_of(p, s) : 0;
         long long all;
         const long long before = warp_scan(mine, &all);
+        if (kShared && blockIdx.x == 0 && threadIdx.x < 32) {
+            if (lane < count) p.pre.plan[lane] = before;
+            if (lane == 0) p.pre.plan[count] = all;
+        }
         const long long len = run_length(p, all), start = len * blockIdx.x;
         const uint32_t owner = __ballot_sync(0xffffffffu, start >= before && start < before + mine);
         r.b = owner ? __ffs(owner) - 1 : -1;
@@ -246,6 +251,15 @@ __device__ __forceinline__ Run find_run(const TreeParams& p, RunShared& sh) {
     const long long before = block_scan<kN>(mine, sh.red, &all);
     const long long len = run_length(p, all);
     const long long start = len * blockIdx.x;
+    if (kShared && blockIdx.x == 0) {
+        long long at = before;
+        for (int b = b0; b < b1; ++b) {
+            p.pre.plan[b] = at;
+            if (per > 1) s = sequence<false, kShared>(p, b);
+            at += units_of(p, s);
+        }
+        if (threadIdx.x == 0) p.pre.plan[count] = all;
+    }
     if (start >= before && start < before + mine) {
         // this thread's sequences hold the start
         long long at = start - before;

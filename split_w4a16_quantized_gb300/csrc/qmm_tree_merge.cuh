@@ -19,6 +19,18 @@ __device__ __forceinline__ Runs runs_of(const TreeParams& p, const Seq& s, long 
     return {static_cast<int>((start + p.setup) / len), static_cast<int>((start + units - 1) / len)};
 }
 
+// A row's state: its maximum, its sum, and columns 4 j .. 4 j + 3 at o + j step.
+struct StateAt {
+    const float *m, *l, *o;
+    int step;
+};
+// The one that run c left of row `in` of a cut item, c0 the item's first run.
+template <int D>
+__device__ __forceinline__ StateAt run_state(const TreeParams& p, int c, int c0, int in) {
+    const PartialAt x = partial_at<D>(p, 2 * c + (c == c0 ? 1 : 0));
+    return {x.m + in, x.l + in, x.at(in, 0), 4 << p.row_shift};
+}
+
 // A row's running state: the largest maximum so far, the sum and TURNS groups of 4
 // columns.
 template <int TURNS>
@@ -57,23 +69,23 @@ struct Acc {
             }
         }
     }
-    // The states of row `in` of a cut item, in run order; column groups j0, j0 + jump, ...
-    template <int D>
-    __device__ __forceinline__ void add_runs(const TreeParams& p, Runs c, int in, int j0, int jump) {
-        for (int k0 = c.c0; k0 <= c.c1; k0 += kMergeAhead) {
+    // n states, in order: at(k) says where state k lies; column groups j0, j0 + jump, ...
+    template <class F>
+    __device__ __forceinline__ void add_all(int n, int j0, int jump, F&& at) {
+        for (int k0 = 0; k0 < n; k0 += kMergeAhead) {
             float m[kMergeAhead], l[kMergeAhead];
             float4 o[kMergeAhead][TURNS];
 #pragma unroll
             for (int k = 0; k < kMergeAhead; ++k) {
-                if (k0 + k > c.c1) continue;
-                const PartialAt x = partial_at<D>(p, 2 * (k0 + k) + (k0 + k == c.c0 ? 1 : 0));
-                m[k] = x.m[in];
-                l[k] = x.l[in];
+                if (k0 + k >= n) continue;
+                const StateAt x = at(k0 + k);
+                m[k] = *x.m;
+                l[k] = *x.l;
 #pragma unroll
                 for (int u = 0; u < TURNS; ++u)
-                    o[k][u] = *reinterpret_cast<const float4*>(x.at(in, 4 * (j0 + u * jump)));
+                    o[k][u] = *reinterpret_cast<const float4*>(x.o + (j0 + u * jump) * x.step);
             }
-            add<kMergeAhead>(m, l, o, c.c1 - k0 + 1);
+            add<kMergeAhead>(m, l, o, n - k0);
         }
     }
     // 1 / the sum, with the scale of V: 0 for a row that sees nothing

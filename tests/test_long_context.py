@@ -82,8 +82,8 @@ ATTEND = [
 @pytest.mark.parametrize("kw,code", ATTEND + [
     (dict(null=True), Q.QMM_EINVAL), (dict(table=None), Q.QMM_EINVAL),
     (dict(lens=None), Q.QMM_EINVAL), (dict(first=None), Q.QMM_EINVAL), (dict(G=0), Q.QMM_EINVAL),
-    (dict(max_pages=0), Q.QMM_EINVAL), (dict(G=-1), Q.QMM_EINVAL), (dict(G=65536), Q.QMM_ESHAPE),
-    (dict(max_pages=1 << 27), Q.QMM_ESHAPE), (dict(max_pages=(1 << 27) - 4096, G=60), Q.QMM_ESHAPE),
+    (dict(max_pages=0), Q.QMM_EINVAL), (dict(G=-1), Q.QMM_EINVAL), (dict(G=5), Q.QMM_ESHAPE),
+    (dict(max_pages=1 << 27), Q.QMM_ESHAPE), (dict(max_pages=(1 << 27) - 4096, N=1 << 12, cu=PTR), Q.QMM_ESHAPE),
     (dict(N=1 << 27, cu=PTR), Q.QMM_ESHAPE), (dict(par=PTR + 2), Q.QMM_EALIGN),
     (dict(table=PTR + 2), Q.QMM_EALIGN), (dict(lens=PTR + 1), Q.QMM_EALIGN),
     (dict(first=PTR + 2), Q.QMM_EALIGN)])
@@ -170,7 +170,7 @@ def test_workspaces():
         return Q.qmm_scored_attention_workspace_bytes(_cache(**kw), Hq, T, 152)
     assert prefix(8) > 0 and prefix(8) % 16 == 0
     assert prefix(9) - prefix(8) == 2 * 32 * 130 * 4
-    assert prefix(8) == prefix(8, B=500, max_pages=9000)
+    assert prefix(8) == prefix(8, max_pages=9000) and prefix(8, B=500) - prefix(8) == 2 * 496 * 8
     assert prefix(0) == 0 and prefix(1 << 27) == 0
     assert scored() > 0 and scored() % 16 == 0
     assert scored(B=8) > scored() and scored(T=257) == 0 and scored(Hq=30) == 0
