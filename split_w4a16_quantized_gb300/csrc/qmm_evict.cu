@@ -13,15 +13,19 @@
 // the chosen ones between line and len - recent, instead of all rows behind the first
 // evicted slot.
 //
-// Two kernels.  evict_select: a block a column finds the threshold by its bits, 8 a
-// pass (a weight's bits, ordered as the weights are), then pairs evicted and chosen
-// slots from two queues filled in ascending order, and moves the weights.  evict_move:
-// blocks of (column, K or V, piece of the row's bytes) move the rows in ascending
-// order of their targets, a batch at a time: all of a batch is in registers before any
-// of it is stored.  A row moves to a lower slot, so a target is never the source of a
-// later batch, and the batches before have read theirs.
+// Two kernels.  evict_select, a block a column: the weights come to shared memory once;
+// the threshold is found by its bits, 8 a pass (a weight's bits, ordered as the weights
+// are); then every warp takes a stretch of the slots, and the ranks of evicted slots
+// below the line and of chosen ones behind it pair them.  Longer columns than shared
+// memory holds go through two queues filled in ascending order instead.
+// evict_move, a block a column of K or V (and, where columns are few, a piece of its
+// rows' bytes): moves the rows in ascending order of their targets, a batch at a time:
+// all of a batch is in registers before any of it is stored.  A row moves to a lower slot,
+// so a target is never the source of a later batch, and the batches before have read
+// theirs.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "qmm.h"
@@ -29,15 +33,16 @@
 #include "qmm_internal.h"
 #include "qmm_paged.cuh"
 #include "qmm_paged_host.h"
+#include "qmm_per_device.h"
 
 namespace qmm {
 namespace {
 
 constexpr int kSelectThreads = 512;
 constexpr int kMoveThreads = 256;
-constexpr int kMoveLanes = 4;  // lanes of a lane group: 64 bytes, a row's piece
-constexpr int kMoveRows = 8;   // rows a lane group has in flight
-constexpr int kBatch = kMoveThreads / kMoveLanes * kMoveRows;
+constexpr int kMoveRows = 8;      // rows a lane group has in flight
+// Slots of a column that shared memory holds: 5 bytes each, two blocks an SM.
+constexpr int kMostSlots = 16384;
 
 struct EvictParams {
     PagedDims d;
@@ -47,7 +52,8 @@ struct EvictParams {
     int *kept, *new_lens;
     int n, keep, sinks, recent;
     int first;                  // this launch's first layer
-    int elem, slices;           // bytes a value; pieces of a row
+    int elem, slices, lanes;    // bytes a value; pieces of a row, 16 * lanes bytes each
+    int held;                   // slots that the launch's shared memory holds
     uint8_t* pools[2 * kMaxEvictCaches];   // K and V of each layer
 };
 
@@ -80,16 +86,149 @@ __device__ __forceinline__ int scan_block(int v, int* red, int* total) {
     return before + x - v;
 }
 
+// The digit (of 256) that the `want`-th largest falls into, given that `above` are larger:
+// every warp reads the counts for itself.  *above and *count: larger ones, and those in
+// the digit.
+__device__ __forceinline__ int find_digit(const int* hist, int want, int* above, int* count) {
+    const int lane = threadIdx.x & 31;
+    // lane l: digits 255 - 8 l down to 248 - 8 l
+    const int4 lo = *reinterpret_cast<const int4*>(hist + 248 - 8 * lane);
+    const int4 hi = *reinterpret_cast<const int4*>(hist + 252 - 8 * lane);
+    const int c[8] = {hi.w, hi.z, hi.y, hi.x, lo.w, lo.z, lo.y, lo.x};
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += c[i];
+    int before = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += y;
+    }
+    before += *above - sum;   // larger than this lane's digits
+    int digit = -1, at = before, n = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (digit < 0 && at < want && at + c[i] >= want) digit = 255 - 8 * lane - i, n = c[i];
+        if (digit < 0) at += c[i];
+    }
+    const int from = __ffs(__ballot_sync(0xffffffffu, digit >= 0)) - 1;
+    *above = __shfl_sync(0xffffffffu, at, from);
+    *count = __shfl_sync(0xffffffffu, n, from);
+    return __shfl_sync(0xffffffffu, digit, from);
+}
+
+struct SelectShared {
+    alignas(16) int hist[4][256];
+    int red[2][kSelectThreads / 32];
+    int digit, above;
+    int queue[2][2 * kSelectThreads];   // evicted slots below the line, chosen ones behind
+};
+
+// A column of at most p.held slots: row, its weights; holes, room for the evicted slots
+// below the line (at most half of all); bits, one a slot.
+__device__ __forceinline__ void select_held(const EvictParams& p, SelectShared& sh, float* row,
+                                            uint16_t* holes, uint32_t* bits, int len,
+                                            const float* mass, float* mass_out, int* kept) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int keep = p.keep, m0 = p.sinks, m1 = len - p.recent, line = keep - p.recent;
+    const int want = line - m0;
+    for (int i = tid; i < 4 * 256; i += kSelectThreads) sh.hist[0][i] = 0;
+    // (rows are 16-byte aligned and a multiple of 4 slots long)
+#pragma unroll 4
+    for (int i = 4 * tid; i < len; i += 4 * kSelectThreads)
+        *reinterpret_cast<float4*>(row + i) = *reinterpret_cast<const float4*>(mass + i);
+    __syncthreads();
+    uint32_t top = 0;
+    int above = 0, ties = 0;
+    if (want > 0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int shift = 24 - 8 * k;
+            for (int i = m0 + tid; i < m1; i += kSelectThreads) {
+                const uint32_t r = rank_of(row[i]);
+                if (k == 0 || (r >> (shift + 8)) == (top >> (shift + 8)))
+                    atomicAdd(&sh.hist[k][(r >> shift) & 255u], 1);
+            }
+            __syncthreads();
+            top |= static_cast<uint32_t>(find_digit(sh.hist[k], want, &above, &ties)) << shift;
+        }
+    }
+    // of the slots equal to the threshold, the first `equal` stay
+    const int equal = want - above;
+    // a warp's stretch of the slots, 32 at a time
+    const int per = ((len + kSelectThreads - 1) / kSelectThreads) * 32;
+    const int s0 = warp * per, s1 = min(len, s0 + per);
+    // the warp's share of a count, and those of the warps before it
+    auto before_warp = [&](int mine, int* red) {
+        if (lane == 0) red[warp] = mine;
+        __syncthreads();
+        int n = lane < kSelectThreads / 32 && lane < warp ? red[lane] : 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+        return n;
+    };
+    int tie_at = 0;
+    if (want > 0 && equal < ties) {   // (the same for the whole block)
+        int mine = 0;
+        for (int i0 = s0; i0 < s1; i0 += 32) {
+            const int i = i0 + lane;
+            mine += __popc(__ballot_sync(0xffffffffu, i >= m0 && i < min(s1, m1) && rank_of(row[i]) == top));
+        }
+        tie_at = before_warp(mine, sh.red[0]);
+        __syncthreads();
+    }
+    int n_holes = 0, n_late = 0;
+    for (int i0 = s0; i0 < s1; i0 += 32) {
+        const int i = i0 + lane;
+        const bool in = want > 0 && i >= m0 && i < min(s1, m1);
+        const uint32_t r = in ? rank_of(row[i]) : 0u;
+        const bool tie = in && r == top;
+        const uint32_t same = __ballot_sync(0xffffffffu, tie);
+        const bool yes = in && (r > top || (tie && (equal >= ties || tie_at +
+                                            __popc(same & ((1u << lane) - 1u)) < equal)));
+        tie_at += __popc(same);
+        const uint32_t all = __ballot_sync(0xffffffffu, yes);
+        if (lane == 0) bits[i0 >> 5] = all;
+        n_holes += __popc(__ballot_sync(0xffffffffu, i >= m0 && i < min(s1, line) && !yes));
+        n_late += __popc(__ballot_sync(0xffffffffu, yes && i >= line));
+    }
+    int hole = before_warp(n_holes, sh.red[0]), late = before_warp(n_late, sh.red[1]);
+    for (int i0 = s0; i0 < s1 && i0 < line; i0 += 32) {
+        const int i = i0 + lane;
+        const bool evicted = i >= m0 && i < min(s1, line) && !((bits[i0 >> 5] >> lane) & 1u);
+        const uint32_t all = __ballot_sync(0xffffffffu, evicted);
+        if (evicted) {
+            holes[hole + __popc(all & ((1u << lane) - 1u))] = static_cast<uint16_t>(i);
+        } else if (i < min(s1, line)) {
+            kept[i] = i;
+            if (mass_out != mass) mass_out[i] = row[i];
+        }
+        hole += __popc(all);
+    }
+    __syncthreads();
+    for (int i0 = max(s0, line & ~31); i0 < s1; i0 += 32) {
+        const int i = i0 + lane;
+        const bool yes = i >= line && i < min(s1, m1) && ((bits[i0 >> 5] >> lane) & 1u);
+        const uint32_t all = __ballot_sync(0xffffffffu, yes);
+        int j = -1;
+        if (yes) j = holes[late + __popc(all & ((1u << lane) - 1u))];
+        if (i >= m1 && i < s1) j = i - (len - keep);
+        if (j >= 0) {
+            kept[j] = i;
+            mass_out[j] = row[i];
+        }
+        late += __popc(all);
+    }
+}
+
 __global__ void __launch_bounds__(kSelectThreads)
     evict_select_kernel(const __grid_constant__ EvictParams p) {
-    __shared__ int hist[256];
-    __shared__ int red[kSelectThreads / 32];
-    __shared__ int digit_s, above_s;
-    __shared__ int queue[2][2 * kSelectThreads];   // evicted slots below the line, chosen ones behind
+    extern __shared__ __align__(16) float select_row[];
+    __shared__ SelectShared sh;
     const int tid = threadIdx.x;
     const int h = blockIdx.x % p.d.Hkv, layer = p.first + blockIdx.x / p.d.Hkv, b = blockIdx.y;
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();
     const int len = cached_tokens(p.d, b), keep = p.keep;
     const int64_t col = static_cast<int64_t>(b) * p.d.Hkv + h;
     const float* mass = p.mass + layer * p.layer_stride + col * p.row_stride;
@@ -103,9 +242,18 @@ __global__ void __launch_bounds__(kSelectThreads)
         }
         return;
     }
+    if (len <= p.held) {
+        uint16_t* holes = reinterpret_cast<uint16_t*>(select_row + p.held);
+        select_held(p, sh, select_row, holes, reinterpret_cast<uint32_t*>(holes + p.held / 2), len,
+                    mass, mass_out, kept);
+        return;
+    }
     const int m0 = p.sinks, m1 = len - p.recent;        // the slots in question
     const int want = keep - p.sinks - p.recent;         // how many of them stay
     const int line = keep - p.recent;
+    int* const hist = sh.hist[0];
+    int* const red = sh.red[0];
+    int (*const queue)[2 * kSelectThreads] = sh.queue;
 
     // The want-th largest number: its digits from the top, 8 bits a pass.  `above`:
     // slots known to be larger.
@@ -126,12 +274,12 @@ __global__ void __launch_bounds__(kSelectThreads)
             int all;
             const int before = scan_block(mine, red, &all);
             if (tid < 256 && above + before < want && above + before + mine >= want) {
-                digit_s = 255 - tid;
-                above_s = above + before;
+                sh.digit = 255 - tid;
+                sh.above = above + before;
             }
             __syncthreads();
-            top |= static_cast<uint32_t>(digit_s) << shift;
-            above = above_s;
+            top |= static_cast<uint32_t>(sh.digit) << shift;
+            above = sh.above;
             __syncthreads();
         }
     }
@@ -213,64 +361,65 @@ __global__ void __launch_bounds__(kSelectThreads)
 
 __global__ void __launch_bounds__(kMoveThreads, 4)
     evict_move_kernel(const __grid_constant__ EvictParams p) {
-    __shared__ int64_t src[kBatch], dst[kBatch];   // bytes from the column's start
-    __shared__ int count_s;
-    const int tid = threadIdx.x, b = blockIdx.y;
+    __shared__ int64_t src[kMoveThreads], dst[kMoveThreads];   // bytes from the column's start
+    __shared__ int red[2][kMoveThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.y;
     int at = blockIdx.x;
     const int slice = at % p.slices;
     at /= p.slices;
     const int kv = at & 1;
     at >>= 1;
     const int h = at % p.d.Hkv, layer = at / p.d.Hkv;   // of this launch
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();
     const int len = cached_tokens(p.d, b), keep = p.keep;
     if (len <= keep) return;
     const int* kept = p.kept +
         ((static_cast<int64_t>(p.first + layer) * p.d.B + b) * p.d.Hkv + h) * keep;
     uint8_t* pool = p.pools[2 * layer + kv] + h * p.d.head_stride * p.elem +
-                    (slice * kMoveLanes + tid % kMoveLanes) * 16;
-    constexpr int kGroups = kMoveThreads / kMoveLanes;
-    const int group = tid / kMoveLanes;
-    if (tid == 0) count_s = 0;
-    __syncthreads();
-    for (int64_t j0 = p.sinks; j0 < keep;) {
-        // the next batch of rows that move
-        int count = 0;
-        while (j0 < keep && count + kMoveThreads <= kBatch) {
-            const int64_t j = j0 + tid;
-            int64_t from = -1, to = -1;
-            if (j < keep) {
-                const int k = kept[j];
-                if (k != j) {
-                    from = slot_offset(p.d, b, k);
-                    to = slot_offset(p.d, b, static_cast<int>(j));
-                }
-            }
-            if (from >= 0 && to >= 0) {   // (a missing page on either side: not moved)
-                const int i = atomicAdd(&count_s, 1);
-                src[i] = from * p.elem;
-                dst[i] = to * p.elem;
-            }
-            __syncthreads();
-            count = count_s;
-            __syncthreads();
-            j0 += kMoveThreads;
+                    (slice * p.lanes + tid % p.lanes) * 16;
+    const int groups = kMoveThreads / p.lanes, group = tid / p.lanes;
+    int odd = 0;
+    int64_t j = p.sinks + tid;
+    int from_slot = j < keep ? kept[j] : -1;
+    for (int64_t j0 = p.sinks; j0 < keep; j0 += kMoveThreads, j += kMoveThreads, odd ^= 1) {
+        // the rows that move, in order (a missing page on either side: not moved)
+        int64_t from = -1, to = -1;
+        if (j < keep && from_slot != j) {
+            from = slot_offset(p.d, b, from_slot);
+            to = slot_offset(p.d, b, static_cast<int>(j));
         }
-        if (tid == 0) count_s = 0;
-        uint4 x[kMoveRows];
+        from_slot = j + kMoveThreads < keep ? kept[j + kMoveThreads] : -1;
+        const bool moves = from >= 0 && to >= 0;
+        const uint32_t all = __ballot_sync(0xffffffffu, moves);
+        if (lane == 0) red[odd][warp] = __popc(all);
+        __syncthreads();   // (the batches before have been stored: src and dst are free)
+        int before = 0, count = 0;
 #pragma unroll
-        for (int u = 0; u < kMoveRows; ++u) {
-            const int r = group + u * kGroups;
-            if (r < count) x[u] = *reinterpret_cast<const uint4*>(pool + src[r]);
+        for (int w = 0; w < kMoveThreads / 32; ++w) {
+            if (w < warp) before += red[odd][w];
+            count += red[odd][w];
+        }
+        if (moves) {
+            const int i = before + __popc(all & ((1u << lane) - 1u));
+            src[i] = from * p.elem;
+            dst[i] = to * p.elem;
         }
         __syncthreads();
+        for (int r0 = group; r0 - group < count; r0 += kMoveRows * groups) {
+            uint4 x[kMoveRows];
 #pragma unroll
-        for (int u = 0; u < kMoveRows; ++u) {
-            const int r = group + u * kGroups;
-            if (r < count) *reinterpret_cast<uint4*>(pool + dst[r]) = x[u];
+            for (int u = 0; u < kMoveRows; ++u) {
+                const int r = r0 + u * groups;
+                if (r < count) x[u] = *reinterpret_cast<const uint4*>(pool + src[r]);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < kMoveRows; ++u) {
+                const int r = r0 + u * groups;
+                if (r < count) *reinterpret_cast<uint4*>(pool + dst[r]) = x[u];
+            }
         }
-        __syncthreads();
     }
 }
 
@@ -294,7 +443,23 @@ int launch_kv_evict(const qmm_kv_cache* caches, int n, int first, const float* m
     p.recent = recent;
     p.first = first;
     p.elem = c.dtype == QMM_CACHE_E4M3 ? 1 : 2;
-    p.slices = c.D * p.elem / (16 * kMoveLanes);
+    // whole rows, or pieces of at least 64 bytes where the columns would leave SMs idle
+    const int row_lanes = c.D * p.elem / 16;
+    const int64_t columns = static_cast<int64_t>(n) * c.Hkv * 2 * c.B;
+    p.slices = 1;
+    while (row_lanes / p.slices > 4 && columns * p.slices < 4 * 152) p.slices *= 2;
+    p.lanes = row_lanes / p.slices;
+    p.held = std::min((p.d.cap + 63) / 64 * 64, kMostSlots);
+    const size_t smem = static_cast<size_t>(p.held) * 5 + p.held / 8;
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) return cudaErrorInvalidDevice;
+    static PerDevice<bool> opted_in;
+    if (!opted_in.get(device, [&] {
+            return cudaFuncSetAttribute(evict_select_kernel,
+                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        kMostSlots * 5 + kMostSlots / 8) == cudaSuccess;
+        }))
+        return cudaErrorInvalidValue;
     for (int i = 0; i < n; ++i) {
         p.pools[2 * i] = static_cast<uint8_t*>(caches[i].K);
         p.pools[2 * i + 1] = static_cast<uint8_t*>(caches[i].V);
@@ -305,10 +470,12 @@ int launch_kv_evict(const qmm_kv_cache* caches, int n, int first, const float* m
     cfg.gridDim = dim3(static_cast<unsigned>(n * c.Hkv), c.B, 1);
     cfg.blockDim = dim3(kSelectThreads, 1, 1);
     cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.dynamicSmemBytes = smem;
     int rc = cudaLaunchKernelEx(&cfg, evict_select_kernel, p);
     if (rc != cudaSuccess) return rc;
     cfg.gridDim.x = static_cast<unsigned>(n * c.Hkv) * 2 * p.slices;
     cfg.blockDim = dim3(kMoveThreads, 1, 1);
+    cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, evict_move_kernel, p);
 }
 
