@@ -38,7 +38,7 @@
 namespace qmm {
 namespace {
 
-constexpr int kSelectThreads = 512;
+constexpr int kSelectThreads = 256;
 constexpr int kMoveThreads = 256;
 constexpr int kMoveRows = 8;      // rows a lane group has in flight
 // Slots of a column that shared memory holds: 5 bytes each, two blocks an SM.
@@ -144,13 +144,35 @@ __device__ __forceinline__ void select_held(const EvictParams& p, SelectShared& 
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int shift = 24 - 8 * k;
-            for (int i = m0 + tid; i < m1; i += kSelectThreads) {
-                const uint32_t r = rank_of(row[i]);
-                if (k == 0 || (r >> (shift + 8)) == (top >> (shift + 8)))
-                    atomicAdd(&sh.hist[k][(r >> shift) & 255u], 1);
+            int* const hist = sh.hist[k];
+            // Behind the first pass most slots are out of the running, and their bits as
+            // they are say so, where neither zeros nor NaN are near.
+            const uint32_t first = top >> 24;
+            if (k > 0 && first != 0 && first != 0x7f && first != 0x80 && first != 0xff) {
+                const uint32_t prefix = (top >> 31 ? top ^ 0x80000000u : ~top) >> ((shift + 8) & 31);
+                const uint32_t flip = top >> 31 ? 0u : 255u;
+                auto count = [&](float w) {
+                    const uint32_t u = __float_as_uint(w);
+                    if ((u >> ((shift + 8) & 31)) == prefix)
+                        atomicAdd(&hist[((u >> shift) & 255u) ^ flip], 1);
+                };
+                const int q0 = (m0 + 3) & ~3, q1 = m1 & ~3;   // whole quarters of 16 bytes
+                for (int i = q0 + 4 * tid; i < q1; i += 4 * kSelectThreads) {
+                    const float4 w = *reinterpret_cast<const float4*>(row + i);
+                    count(w.x), count(w.y), count(w.z), count(w.w);
+                }
+                // (and those that m0 and m1 cut)
+                const int i = tid < 4 ? m0 + tid : max(q0, q1) + tid - 4;
+                if (tid < 8 && i < m1 && (tid < 4 ? i < q0 : i >= q0)) count(row[i]);
+            } else {
+                for (int i = m0 + tid; i < m1; i += kSelectThreads) {
+                    const uint32_t r = rank_of(row[i]);
+                    if (k == 0 || (r >> ((shift + 8) & 31)) == (top >> ((shift + 8) & 31)))
+                        atomicAdd(&hist[(r >> shift) & 255u], 1);
+                }
             }
             __syncthreads();
-            top |= static_cast<uint32_t>(find_digit(sh.hist[k], want, &above, &ties)) << shift;
+            top |= static_cast<uint32_t>(find_digit(hist, want, &above, &ties)) << shift;
         }
     }
     // of the slots equal to the threshold, the first `equal` stay
@@ -167,61 +189,68 @@ __device__ __forceinline__ void select_held(const EvictParams& p, SelectShared& 
         for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
         return n;
     };
+    // a weight above the threshold, or equal to it (a threshold below everything: NaN)
+    const float least = __uint_as_float(top >> 31 ? top ^ 0x80000000u : ~top);
+    auto larger = [&](float w) { return top == 0 ? w == w : w > least; };
+    auto equals = [&](float w) { return top == 0 ? w != w : w == least; };
+    const bool all_ties = equal >= ties;
+    const uint32_t below = (1u << lane) - 1u;
+    const int e1 = min(s1, m1), l1 = min(s1, line);   // ends of the stretch's slots in question
     int tie_at = 0;
-    if (want > 0 && equal < ties) {   // (the same for the whole block)
+    if (want > 0 && !all_ties) {   // (the same for the whole block)
         int mine = 0;
-        for (int i0 = s0; i0 < s1; i0 += 32) {
-            const int i = i0 + lane;
-            mine += __popc(__ballot_sync(0xffffffffu, i >= m0 && i < min(s1, m1) && rank_of(row[i]) == top));
-        }
-        tie_at = before_warp(mine, sh.red[0]);
+        for (int i = s0 + lane; i < e1; i += 32) mine += i >= m0 && equals(row[i]);
+        tie_at = before_warp(__reduce_add_sync(0xffffffffu, mine), sh.red[0]);
         __syncthreads();
     }
-    int n_holes = 0, n_late = 0;
+    int n_holes = 0, n_late = 0;   // of this lane
     for (int i0 = s0; i0 < s1; i0 += 32) {
         const int i = i0 + lane;
-        const bool in = want > 0 && i >= m0 && i < min(s1, m1);
-        const uint32_t r = in ? rank_of(row[i]) : 0u;
-        const bool tie = in && r == top;
-        const uint32_t same = __ballot_sync(0xffffffffu, tie);
-        const bool yes = in && (r > top || (tie && (equal >= ties || tie_at +
-                                            __popc(same & ((1u << lane) - 1u)) < equal)));
-        tie_at += __popc(same);
+        const bool in = want > 0 && i >= m0 && i < e1;
+        const float w = in ? row[i] : 0.f;
+        bool yes = in && (larger(w) || (all_ties && equals(w)));
+        if (!all_ties) {
+            const bool tie = in && equals(w);
+            const uint32_t same = __ballot_sync(0xffffffffu, tie);
+            yes = yes || (tie && tie_at + __popc(same & below) < equal);
+            tie_at += __popc(same);
+        }
         const uint32_t all = __ballot_sync(0xffffffffu, yes);
         if (lane == 0) bits[i0 >> 5] = all;
-        n_holes += __popc(__ballot_sync(0xffffffffu, i >= m0 && i < min(s1, line) && !yes));
-        n_late += __popc(__ballot_sync(0xffffffffu, yes && i >= line));
+        n_holes += i >= m0 && i < l1 && !yes;
+        n_late += yes && i >= line;
     }
-    int hole = before_warp(n_holes, sh.red[0]), late = before_warp(n_late, sh.red[1]);
-    for (int i0 = s0; i0 < s1 && i0 < line; i0 += 32) {
+    int hole = before_warp(__reduce_add_sync(0xffffffffu, n_holes), sh.red[0]);
+    int late = before_warp(__reduce_add_sync(0xffffffffu, n_late), sh.red[1]);
+    for (int i0 = s0; i0 < l1; i0 += 32) {
         const int i = i0 + lane;
-        const bool evicted = i >= m0 && i < min(s1, line) && !((bits[i0 >> 5] >> lane) & 1u);
-        const uint32_t all = __ballot_sync(0xffffffffu, evicted);
+        const bool evicted = i >= m0 && i < l1 && !((bits[i0 >> 5] >> lane) & 1u);
+        const uint32_t out = __ballot_sync(0xffffffffu, evicted);
         if (evicted) {
-            holes[hole + __popc(all & ((1u << lane) - 1u))] = static_cast<uint16_t>(i);
-        } else if (i < min(s1, line)) {
+            holes[hole + __popc(out & below)] = static_cast<uint16_t>(i);
+        } else if (i < l1) {
             kept[i] = i;
             if (mass_out != mass) mass_out[i] = row[i];
         }
-        hole += __popc(all);
+        hole += __popc(out);
     }
     __syncthreads();
     for (int i0 = max(s0, line & ~31); i0 < s1; i0 += 32) {
         const int i = i0 + lane;
-        const bool yes = i >= line && i < min(s1, m1) && ((bits[i0 >> 5] >> lane) & 1u);
-        const uint32_t all = __ballot_sync(0xffffffffu, yes);
+        uint32_t in = bits[i0 >> 5];
+        if (i0 < line) in &= ~0u << (line - i0);   // (line - i0 < 32; the bits end at m1)
         int j = -1;
-        if (yes) j = holes[late + __popc(all & ((1u << lane) - 1u))];
+        if ((in >> lane) & 1u) j = holes[late + __popc(in & below)];
         if (i >= m1 && i < s1) j = i - (len - keep);
         if (j >= 0) {
             kept[j] = i;
             mass_out[j] = row[i];
         }
-        late += __popc(all);
+        late += __popc(in);
     }
 }
 
-__global__ void __launch_bounds__(kSelectThreads)
+__global__ void __launch_bounds__(kSelectThreads, 4)
     evict_select_kernel(const __grid_constant__ EvictParams p) {
     extern __shared__ __align__(16) float select_row[];
     __shared__ SelectShared sh;
