@@ -34,8 +34,8 @@ __global__ void __launch_bounds__(16 * ROWS)
     pdl_trigger();
     pdl_wait();
     const Seq s = sequence<false, true>(p, p.pre.G + b);
-    const long long before_own = p.pre.plan[p.pre.G + b];
-    const long long len = run_length(p, p.pre.plan[p.pre.G + p.d.B]);
+    const long long before_own = p.plan[p.pre.G + b];
+    const long long len = run_length(p, p.plan[p.pre.G + p.d.B]);
     // the first prefix that holds the sequence
     int group = -1;
     for (int j0 = 0; group < 0 && j0 < p.pre.G; j0 += 32) {
@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(16 * ROWS)
     long long before_pre = 0;
     if (group >= 0) {
         shared = sequence<false, true>(p, group);
-        before_pre = p.pre.plan[group];
+        before_pre = p.plan[group];
     }
     const int rows = s.n * p.QG, row0 = chunk * ROWS;
     if (row0 >= rows) return;   // (the same for the whole block)
@@ -127,7 +127,7 @@ int launch_prefix_attention(const qmm_kv_cache& c, const qmm_prefix& pre, const 
     p.pre.max_pages = pre.max_pages;
     p.pre.cap = pre.max_pages * c.page_size;
     p.pre.direct = ws + slot_floats(c.D, num_sms);
-    p.pre.plan = reinterpret_cast<long long*>(
+    p.plan = reinterpret_cast<long long*>(
         p.pre.direct + direct_floats(c.D, static_cast<int64_t>(N) * Hq));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     rc = launch_prefix_tc(kmap, vmap, p, c.D, fp8, device, st);

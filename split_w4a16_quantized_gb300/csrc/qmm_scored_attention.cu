@@ -18,125 +18,153 @@ namespace {
 
 // ---- up to 8 rows ----
 //
-// One launch behind the attention kernel.  Blocks of the first B Hkv finish an output
-// each: a thread a row and a few groups of 4 columns.  The others take equal runs of the
-// batch's chunks of positions: a warp a row for its lse, from the states or, where one
-// run held the item, from the attention kernel; then a thread 4 positions of a chunk.
+// One launch behind the attention kernel, whose first block wrote down what lies before
+// each sequence.  The first blocks take equal runs of the batch's chunks of positions: a
+// warp a row for its lse, from the states or, where one run held the item, from the
+// attention kernel; then a thread 4 positions of a chunk.  The others finish the outputs
+// of items that a run border cuts: a block an item or, where those are more, a border.
 constexpr int kFinishThreads = 256;
-constexpr int kChunk = 4 * kFinishThreads;
+static_assert(kChunk == 4 * kFinishThreads, "a thread takes 4 positions");
 
 struct FinishParams {
     TreeParams t;
     float* mass;
     int64_t mass_stride;
     float decay;
-    int outputs;   // blocks that finish an output
+    int adders;   // blocks that add up weights
+    int by_item;  // the others take an item each, or a border between runs
 };
 
-__device__ __forceinline__ int chunks_of(const Seq& s) {
-    return (s.total + kChunk - 1) / kChunk;
+// What lies before each sequence, of units of work and of chunks.  Up to 32 sequences:
+// every warp works it out for itself, a lane a sequence, ahead of the dependency wait and
+// so from L2 (one sequence of 1000: 9.7 us, as written down by the attention kernel 11.4);
+// more: as written down.
+struct Lists {
+    const TreeParams& t;
+    const bool few;
+    long long units = 0, chunks = 0, all_units = 0, all_chunks = 0;   // before this lane's
+    int my_units = 0;
+    long long my_chunks = 0;
+    __device__ __forceinline__ explicit Lists(const TreeParams& tp) : t(tp), few(tp.d.B <= 32) {
+        if (!few) return;
+        const int lane = threadIdx.x & 31;
+        if (lane < t.d.B) {
+            const Seq s = sequence<true>(t, lane);
+            my_units = units_of(t, s);
+            my_chunks = chunks_of(t, s);
+        }
+        units = warp_scan(my_units, &all_units);
+        chunks = warp_scan(my_chunks, &all_chunks);
+    }
+    // (behind the wait)
+    __device__ __forceinline__ void load() {
+        if (few) return;
+        all_units = t.plan[t.d.B];
+        all_chunks = t.chunks[t.d.B];
+    }
+    __device__ __forceinline__ long long units_before(int b) const {
+        return few ? __shfl_sync(0xffffffffu, units, b) : t.plan[b];
+    }
+    __device__ __forceinline__ long long chunks_before(int b) const {
+        return few ? __shfl_sync(0xffffffffu, chunks, b) : t.chunks[b];
+    }
+    // The sequence that holds unit (or chunk) `at`, -1 behind the last.  Whole block.
+    __device__ __forceinline__ int find(bool unit, long long at, int* found) const {
+        if (few) {
+            const long long from = unit ? units : chunks, n = unit ? my_units : my_chunks;
+            const uint32_t hit = __ballot_sync(0xffffffffu, at >= from && at < from + n);
+            return hit ? __ffs(hit) - 1 : -1;
+        }
+        const long long* before = unit ? t.plan : t.chunks;
+        if (threadIdx.x == 0) *found = -1;
+        __syncthreads();
+        for (int b = threadIdx.x; b < t.d.B; b += kFinishThreads)
+            if (at >= before[b] && at < before[b + 1]) *found = b;
+        __syncthreads();
+        return *found;
+    }
+};
+
+template <int D>
+__device__ __forceinline__ void finish_output(const FinishParams& p, const Lists& lists, int at) {
+    constexpr int ROWS = 1 << kFewRowShift;
+    __shared__ __align__(16) uint2 stage[ROWS][D / 4 + 2];
+    __shared__ int found;
+    const TreeParams& t = p.t;
+    const int tid = threadIdx.x;
+    const long long run = run_length(t, lists.all_units), unit = run * (at + 1);
+    const int b = p.by_item ? at / t.d.Hkv : lists.find(true, unit, &found);
+    if (b < 0) return;
+    const Seq s = sequence(t, b);
+    if (s.n == 0) return;
+    const long long before = lists.units_before(b);
+    const int g = p.by_item ? at % t.d.Hkv : static_cast<int>((unit - before) / item_units(t, s));
+    const Runs c = runs_of(t, s, before, g, run);
+    if (c.c0 == c.c1 || (!p.by_item && c.c0 != at)) return;   // whole, or of an earlier border
+    const int rows = s.n * t.QG;
+    constexpr int JUMP = kFinishThreads / ROWS;
+    constexpr int TURNS = D / 4 / JUMP > 0 ? D / 4 / JUMP : 1;
+    const int i = tid % ROWS, j0 = tid / ROWS;
+    if (i < rows && j0 < D / 4) {
+        Acc<TURNS> acc;
+        acc.add_all(c.c1 - c.c0 + 1, j0, JUMP,
+                    [&](int k) { return run_state<D>(t, c.c0 + k, c.c0, i); });
+        const float inv = acc.inverse(t.vscale);
+#pragma unroll
+        for (int u = 0; u < TURNS; ++u)
+            stage[i][j0 + u * JUMP] =
+                make_uint2(pack_bf16x2(acc.num[u].x * inv, acc.num[u].y * inv),
+                           pack_bf16x2(acc.num[u].z * inv, acc.num[u].w * inv));
+    }
+    __syncthreads();
+    constexpr int CH = D / 8;   // 16-byte chunks of a row
+    const int ri = tid / CH, ch = tid % CH;
+    if (ri < rows) {
+        const int node = ri / t.QG;
+        const int64_t to = static_cast<int64_t>(s.first + node) * t.Hq + g * t.QG + ri - node * t.QG;
+        *reinterpret_cast<uint4*>(t.O + to * D + 8 * ch) =
+            *reinterpret_cast<const uint4*>(&stage[ri][2 * ch]);
+    }
 }
 
 template <int D>
-__global__ void __launch_bounds__(kFinishThreads)
+__global__ void __launch_bounds__(kFinishThreads, 3)
     scored_finish_kernel(const __grid_constant__ FinishParams p) {
-    __shared__ long long red[3][kFinishThreads / 32];
-    __shared__ __align__(16) uint2 stage[1 << kFewRowShift][D / 4 + 2];
-    __shared__ float lse_s[1 << kFewRowShift];
-    __shared__ long long before_s, chunk_s;
-    __shared__ int b_s;
+    constexpr int ROWS = 1 << kFewRowShift;
+    __shared__ float lse_s[ROWS];
+    __shared__ int found;
     const TreeParams& t = p.t;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const bool adds = static_cast<int>(blockIdx.x) >= p.outputs;
-    // The batch's units of work and chunks.  Read from L2 ahead of the wait: the attention
-    // kernel's threads let this one start only behind their own wait for everything before.
-    const int per = (t.d.B + kFinishThreads - 1) / kFinishThreads;
-    const int b0 = min(t.d.B, tid * per), b1 = min(t.d.B, b0 + per);
-    long long units = 0, chunks = 0, all_units, all_chunks;
-    Seq s = {};
-    for (int b = b0; b < b1; ++b) {
-        s = sequence<true>(t, b);
-        units += units_of(t, s);
-        chunks += static_cast<long long>(chunks_of(s)) * t.d.Hkv;
-    }
-    if (tid == 0) b_s = -1;
-    const long long u0 = block_scan<kFinishThreads>(units, red[0], &all_units);
-    const long long c0 = block_scan<kFinishThreads>(chunks, red[1], &all_chunks);
-    const long long run = run_length(t, all_units);
-    const long long adders = gridDim.x - p.outputs;
-    const long long share = adders > 0 ? (all_chunks + adders - 1) / adders : 0;
-    const long long start = adds ? share * (blockIdx.x - p.outputs) : 0;
-    {   // the sequence that this block starts in, and the units before it
-        const int want = adds ? -1 : static_cast<int>(blockIdx.x) / t.d.Hkv;
-        long long u = u0, c = c0;
-        for (int b = b0; b < b1; ++b) {
-            if (per > 1) s = sequence<true>(t, b);
-            const long long mine = static_cast<long long>(chunks_of(s)) * t.d.Hkv;
-            if (adds ? start >= c && start < c + mine : b == want) {
-                b_s = b;
-                before_s = u;
-                chunk_s = start - c;
-            }
-            u += units_of(t, s);
-            c += mine;
-        }
-    }
-    __syncthreads();
-    int b = b_s;
-    long long before = before_s;
+    Lists lists(t);
     pdl_trigger();
     pdl_wait();
-    if (b < 0) return;
-    s = sequence<true>(t, b);
-    if (!adds) {
-        const int g = blockIdx.x % t.d.Hkv;
-        const int rows = s.n * t.QG;
-        if (rows == 0) return;
-        const Runs c = runs_of(t, s, before, g, run);
-        if (c.c0 == c.c1) return;   // written by the attention kernel
-        constexpr int ROWS = 1 << kFewRowShift, JUMP = kFinishThreads / ROWS;
-        constexpr int TURNS = D / 4 / JUMP > 0 ? D / 4 / JUMP : 1;
-        const int i = tid % ROWS, j0 = tid / ROWS;
-        if (i < rows && j0 < D / 4) {
-            Acc<TURNS> acc;
-            acc.add_all(c.c1 - c.c0 + 1, j0, JUMP,
-                        [&](int k) { return run_state<D>(t, c.c0 + k, c.c0, i); });
-            const float inv = acc.inverse(t.vscale);
-#pragma unroll
-            for (int u = 0; u < TURNS; ++u)
-                stage[i][j0 + u * JUMP] =
-                    make_uint2(pack_bf16x2(acc.num[u].x * inv, acc.num[u].y * inv),
-                               pack_bf16x2(acc.num[u].z * inv, acc.num[u].w * inv));
-        }
-        __syncthreads();
-        constexpr int CH = D / 8;   // 16-byte chunks of a row
-        const int ri = tid / CH, ch = tid % CH;
-        if (ri < rows) {
-            const int node = ri / t.QG;
-            const int64_t to = static_cast<int64_t>(s.first + node) * t.Hq + g * t.QG + ri - node * t.QG;
-            *reinterpret_cast<uint4*>(t.O + to * D + 8 * ch) =
-                *reinterpret_cast<const uint4*>(&stage[ri][2 * ch]);
-        }
+    lists.load();
+    if (static_cast<int>(blockIdx.x) >= p.adders) {
+        finish_output<D>(p, lists, static_cast<int>(blockIdx.x) - p.adders);
         return;
     }
-    // ---- weights ----
+    const long long all_chunks = lists.all_chunks, run = run_length(t, lists.all_units);
+    const long long share = (all_chunks + p.adders - 1) / p.adders, start = share * blockIdx.x;
+    int b = lists.find(false, start, &found);
+    if (b < 0) return;
+    Seq s = sequence(t, b);
+    long long before = lists.units_before(b), at = start - lists.chunks_before(b);
     long long left = all_chunks - start < share ? all_chunks - start : share;
-    long long at = chunk_s;
     const int all_rows = t.T * t.QG;
     while (left > 0) {
-        while (at >= static_cast<long long>(chunks_of(s)) * t.d.Hkv) {
-            at -= static_cast<long long>(chunks_of(s)) * t.d.Hkv;
-            before += units_of(t, s);
+        while (at >= chunks_of(t, s)) {
+            at -= chunks_of(t, s);
             if (++b >= t.d.B) return;   // (not reached: the run ends with the list)
-            s = sequence<true>(t, b);
+            s = sequence(t, b);
+            before = lists.units_before(b);
         }
-        const int per_head = chunks_of(s);
-        const int g = static_cast<int>(at / per_head), k0 = static_cast<int>(at - static_cast<long long>(g) * per_head);
+        const int per_head = (s.total + kChunk - 1) / kChunk;
+        const int g = static_cast<int>(at / per_head);
+        const int k0 = static_cast<int>(at - static_cast<long long>(g) * per_head);
         const int k1 = static_cast<int>(left < per_head - k0 ? k0 + left : per_head);
         at += k1 - k0;
         left -= k1 - k0;
-        const int rows = s.n * t.QG;
-        const int total = s.total;
+        const int rows = s.n * t.QG, total = s.total;
         // each row's lse
         __syncthreads();
         if (warp < rows) {
@@ -172,14 +200,22 @@ __global__ void __launch_bounds__(kFinishThreads)
             const int64_t pos = static_cast<int64_t>(k) * kChunk + 4 * tid;
             if (pos >= total) continue;
             float w[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int r = 0; r < rows; ++r) {
-                const float4 v = *reinterpret_cast<const float4*>(scores + r * t.score_stride + pos);
+            // (a multiple of 4 slots is the caller's: the slots and the strides are)
+            float4 old = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (p.decay != 0.f) old = *reinterpret_cast<const float4*>(mass + pos);
+            float4 v[ROWS];   // all in flight at once
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r)
+                if (r < rows)
+                    v[r] = *reinterpret_cast<const float4*>(scores + r * t.score_stride + pos);
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) {
+                if (r >= rows) break;
                 const float lse = lse_s[r];
-                w[0] += fast_exp2(v.x - lse), w[1] += fast_exp2(v.y - lse);
-                w[2] += fast_exp2(v.z - lse), w[3] += fast_exp2(v.w - lse);
+                w[0] += fast_exp2(v[r].x - lse), w[1] += fast_exp2(v[r].y - lse);
+                w[2] += fast_exp2(v[r].z - lse), w[3] += fast_exp2(v[r].w - lse);
             }
-            if (p.decay != 0.f) {   // (a multiple of 4 slots is the caller's: cap and strides are)
-                const float4 old = *reinterpret_cast<const float4*>(mass + pos);
+            if (p.decay != 0.f) {
                 if (pos < s.len) w[0] = fmaf(p.decay, old.x, w[0]);
                 if (pos + 1 < s.len) w[1] = fmaf(p.decay, old.y, w[1]);
                 if (pos + 2 < s.len) w[2] = fmaf(p.decay, old.z, w[2]);
@@ -206,10 +242,14 @@ static size_t lse_floats(const qmm_kv_cache& c, int T, int Hq) {
     return (static_cast<size_t>(c.B) * T * Hq + 3) / 4 * 4;
 }
 
+// One list of B + 1 values of 64 bits.
+static size_t plan_floats(int B) { return (2 * (static_cast<size_t>(B) + 1) + 3) / 4 * 4; }
+
 size_t scored_attention_workspace(const qmm_kv_cache& c, int T, int Hq, int num_sms) {
     const int rows = T * (Hq / c.Hkv);
     return tree_attention_workspace(c.D, rows, num_sms) +
-           (lse_floats(c, T, Hq) + (rows <= 1 << kFewRowShift ? scores_floats(c, rows) : 0)) *
+           (lse_floats(c, T, Hq) +
+            (rows <= 1 << kFewRowShift ? scores_floats(c, rows) + 2 * plan_floats(c.B) : 0)) *
                sizeof(float);
 }
 
@@ -228,7 +268,10 @@ static int launch_few_rows(const qmm_kv_cache& c, const void* q, int64_t q_strid
     if (rc != cudaSuccess) return rc;
     p.t.lse = lse;
     p.t.lift = fp8 ? kFewLift : 0.f;
-    p.t.scores = lse + lse_floats(c, T, Hq);
+    float* const plan = lse + lse_floats(c, T, Hq);
+    p.t.plan = reinterpret_cast<long long*>(plan);
+    p.t.chunks = reinterpret_cast<long long*>(plan + plan_floats(c.B));
+    p.t.scores = plan + 2 * plan_floats(c.B);
     p.t.score_stride = (static_cast<int64_t>(p.t.d.cap) + (1 << kFewTileShift) - 1) >>
                        kFewTileShift << kFewTileShift;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -237,13 +280,15 @@ static int launch_few_rows(const qmm_kv_cache& c, const void* q, int64_t q_strid
     p.mass = mass;
     p.mass_stride = mass_stride;
     p.decay = decay;
-    p.outputs = c.B * c.Hkv;
-    const int64_t chunks = (static_cast<int64_t>(p.t.d.cap) + kChunk - 1) / kChunk * p.outputs;
-    const int64_t adders = chunks < 4 * num_sms ? chunks : 4 * num_sms;
+    // equal runs for one wave of blocks, three an SM, beside those of the outputs
+    const int64_t chunks = (static_cast<int64_t>(p.t.d.cap) + kChunk - 1) / kChunk * c.B * c.Hkv;
+    p.adders = static_cast<int>(chunks < 3 * num_sms ? chunks : 3 * num_sms);
     cudaLaunchConfig_t cfg = {};
     LaunchAttrs la;
     apply_pdl(cfg, la);
-    cfg.gridDim = dim3(static_cast<unsigned>(p.outputs + adders), 1, 1);
+    const int64_t items = static_cast<int64_t>(c.B) * c.Hkv;
+    p.by_item = items < p.t.ctas;
+    cfg.gridDim = dim3(static_cast<unsigned>(p.adders + (p.by_item ? items : p.t.ctas - 1)), 1, 1);
     cfg.blockDim = dim3(kFinishThreads, 1, 1);
     cfg.stream = st;
     return c.D == 128 ? cudaLaunchKernelEx(&cfg, scored_finish_kernel<128>, p)

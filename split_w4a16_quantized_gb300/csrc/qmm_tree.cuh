@@ -29,7 +29,6 @@ struct SharedPrefixes {
     const int *table, *lens, *first;
     int G, max_pages, cap;
     float* direct;   // states of items that one run holds (DirectAt)
-    long long* plan; // units before each entry, and of all: for the merge
 };
 
 struct TreeParams {
@@ -53,6 +52,8 @@ struct TreeParams {
     float lift;      // log2 of the factor on the weights that the sums hold
     float* scores;   // [B][Hkv][T QG][score_stride]: each row's scores, for up to 8 rows
     int64_t score_stride;
+    long long* plan;     // units before each entry, and of all: for the merge
+    long long* chunks;   // the same of chunks of kChunk positions of a KV head
     SharedPrefixes pre;
 };
 
@@ -190,7 +191,15 @@ struct Run {
     int left;         // units of the run still to do
 };
 
-// The CTA's run: whole block of kN threads; sh: shared scratch.
+// Positions that the pass over the scores takes at a time, and a sequence's pieces of them.
+constexpr int kChunk = 1024;
+__device__ __forceinline__ long long chunks_of(const TreeParams& p, const Seq& s) {
+    return static_cast<long long>((s.total + kChunk - 1) / kChunk) * p.d.Hkv;
+}
+
+// The CTA's run: whole block of kN threads; sh: shared scratch.  kPlan: the first block
+// writes down what lies before each entry, for the launch that merges (p.plan and, where
+// it is not NULL, p.chunks).
 struct RunShared {   // (s and at hold nothing where b < 0)
     long long red[32];
     Seq s;
@@ -210,7 +219,7 @@ __device__ __forceinline__ long long warp_scan(long long v, long long* total) {
     return x - v;
 }
 
-template <int kN, bool kShared = false>
+template <int kN, bool kShared = false, bool kPlan = kShared>
 __device__ __forceinline__ Run find_run(const TreeParams& p, RunShared& sh) {
     Run r;
     const int count = entries<kShared>(p);
@@ -221,9 +230,15 @@ __device__ __forceinline__ Run find_run(const TreeParams& p, RunShared& sh) {
         const int mine = lane < count ? units_of(p, s) : 0;
         long long all;
         const long long before = warp_scan(mine, &all);
-        if (kShared && blockIdx.x == 0 && threadIdx.x < 32) {
-            if (lane < count) p.pre.plan[lane] = before;
-            if (lane == 0) p.pre.plan[count] = all;
+        if (kPlan && blockIdx.x == 0 && threadIdx.x < 32) {
+            if (lane < count) p.plan[lane] = before;
+            if (lane == 0) p.plan[count] = all;
+            if (p.chunks) {
+                long long total;
+                const long long c = warp_scan(lane < count ? chunks_of(p, s) : 0, &total);
+                if (lane < count) p.chunks[lane] = c;
+                if (lane == 0) p.chunks[count] = total;
+            }
         }
         const long long len = run_length(p, all), start = len * blockIdx.x;
         const uint32_t owner = __ballot_sync(0xffffffffu, start >= before && start < before + mine);
@@ -251,14 +266,25 @@ __device__ __forceinline__ Run find_run(const TreeParams& p, RunShared& sh) {
     const long long before = block_scan<kN>(mine, sh.red, &all);
     const long long len = run_length(p, all);
     const long long start = len * blockIdx.x;
-    if (kShared && blockIdx.x == 0) {
-        long long at = before;
+    if (kPlan && blockIdx.x == 0) {   // (the whole block)
+        long long at = before, chunks = 0, all_chunks;
         for (int b = b0; b < b1; ++b) {
-            p.pre.plan[b] = at;
+            p.plan[b] = at;
             if (per > 1) s = sequence<false, kShared>(p, b);
             at += units_of(p, s);
+            chunks += chunks_of(p, s);
         }
-        if (threadIdx.x == 0) p.pre.plan[count] = all;
+        if (threadIdx.x == 0) p.plan[count] = all;
+        if (p.chunks) {
+            __syncthreads();   // sh.red has been read
+            at = block_scan<kN>(chunks, sh.red, &all_chunks);
+            for (int b = b0; b < b1; ++b) {
+                p.chunks[b] = at;
+                if (per > 1) s = sequence<false, kShared>(p, b);
+                at += chunks_of(p, s);
+            }
+            if (threadIdx.x == 0) p.chunks[count] = all_chunks;
+        }
     }
     if (start >= before && start < before + mine) {
         // this thread's sequences hold the start
@@ -361,6 +387,19 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+// The same, whose lines are the first that L2 gives up.
+__device__ __forceinline__ void tma_load_4d_once(uint32_t dst, const CUtensorMap* map, uint64_t* bar,
+                                                 int c0, int c1, int c2, int c3) {
+    uint64_t policy;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;\n" : "=l"(policy));
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
+        "r"(smem_addr(bar)), "l"(policy)
+        : "memory");
+}
+
 // One lane of a converged warp, the same one every time.  The compiler knows
 // that a block under it has a single active thread, and feeds the copies' and
 // MMAs' uniform operands straight from registers; under `lane == 0` it goes
@@ -415,7 +454,8 @@ struct PageWalk {
 
 // The copies of one K or V tile, issued by one thread: page pieces by
 // column blocks of `kBox` bytes (kElems values), kTile rows of a block together.
-template <int kTile, int kBoxes, int kBox, int kElems>
+// kOnce: the tile is not read again.
+template <int kTile, int kBoxes, int kBox, int kElems, bool kOnce = false>
 __device__ __forceinline__ void copy_tile(const TreeParams& p, const CUtensorMap* map, uint64_t* bar,
                                           uint32_t dst, const int* pages, int t, int g) {
     const int pieces = kTile >> p.box_shift;
@@ -424,9 +464,12 @@ __device__ __forceinline__ void copy_tile(const TreeParams& p, const CUtensorMap
     for (int k = 0; k < pieces; ++k) {
         const int row = k << p.box_shift;
 #pragma unroll
-        for (int x = 0; x < kBoxes; ++x)
-            tma_load_4d(dst + x * (kTile * kBox) + row * kBox, map, bar, x * kElems,
-                        (t * kTile + row) & slot_mask, g, pages[k]);
+        for (int x = 0; x < kBoxes; ++x) {
+            const uint32_t to = dst + x * (kTile * kBox) + row * kBox;
+            const int slot = (t * kTile + row) & slot_mask;
+            if (kOnce) tma_load_4d_once(to, map, bar, x * kElems, slot, g, pages[k]);
+            else tma_load_4d(to, map, bar, x * kElems, slot, g, pages[k]);
+        }
     }
 }
 

@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // (after the wait: the merge kernel plans with lens and cu before its own)
     pdl_trigger();
     __syncthreads();
-    Run run = find_run<kThreads>(p, sm.run);
+    Run run = find_run<kThreads, false, kScores>(p, sm.run);
     const int pieces = kTile >> p.box_shift;     // copies of a tile, per column block and pool
     Stretch x;
 
@@ -185,9 +185,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     fence_proxy_async_smem();
                     mbar_arrive_expect_tx(&sm.full[st], C::STAGE);
                     constexpr int E = C::BOX / (kFp8 ? 1 : 2);
-                    copy_tile<kTile, C::BOXES, C::BOX, E>(p, &kmap, &sm.full[st], ring_a + st * C::STAGE,
+                    copy_tile<kTile, C::BOXES, C::BOX, E, kScores>(p, &kmap, &sm.full[st], ring_a + st * C::STAGE,
                                                    sm.pages, t, x.g);
-                    copy_tile<kTile, C::BOXES, C::BOX, E>(p, &vmap, &sm.full[st],
+                    copy_tile<kTile, C::BOXES, C::BOX, E, kScores>(p, &vmap, &sm.full[st],
                                                    ring_a + st * C::STAGE + C::TILE, sm.pages, t,
                                                    x.g);
                 }
