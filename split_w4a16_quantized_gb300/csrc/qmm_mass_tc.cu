@@ -14,7 +14,8 @@
 // than 256 rows are blocks of 256 that add to the same thread's slots one after the
 // other.  Roles:
 //   warp 0       copies K tiles into a ring
-//   warp 1       issues the MMAs, owns the tensor memory (two buffers of 256 columns)
+//   warp 1       issues the MMAs, owns the tensor memory: two buffers of 256 columns, or
+//                four of 128, so that products run ahead of the sums
 //   warps 2-3    bring a block's q (for an E4M3 cache as two E4M3 terms) and lse
 //   warps 4-11   two groups of 128 threads that take turns with the tiles
 #include <algorithm>
@@ -50,12 +51,14 @@ struct MassParams {
     float decay;
     int q_rows;    // rows of q kept: the call's largest block, a multiple of 32
     int slots;     // of the ring
+    int buffers;   // of scores
+    int q_buffers; // 1 or 2 blocks' q
 };
 
 struct MassSmem {
     uint64_t kfull[kMaxSlots], kempty[kMaxSlots];
-    uint64_t dfull[2], dfree[2];       // scores of a tile are there; have been read
-    uint64_t qready, qfree;            // a block's q and lse are there; its products are done
+    uint64_t dfull[4], dfree[4];       // scores of a tile are there; have been read
+    uint64_t qready[2], qfree[2];      // a block's q and lse are there; its products are done
     uint64_t lfree[2];                 // a block's lse has been read by all
     uint64_t drained;                  // abort: every MMA issued has ended
     uint32_t tmem;
@@ -87,13 +90,13 @@ __device__ __forceinline__ MassRun find_mass_run(const TreeParams& p, MassSmem& 
     const int b0 = min(p.d.B, tid * per), b1 = min(p.d.B, b0 + per);
     long long mine = 0, all;
     for (int b = b0; b < b1; ++b)
-        mine += static_cast<long long>(mass_item(sequence(p, b))) * p.d.Hkv;
+        mine += static_cast<long long>(mass_item(sequence<true>(p, b))) * p.d.Hkv;
     if (tid == 0) sm.b = -1;
     long long before = block_scan<kThreads>(mine, sm.red[0], &all);
     const long long len = (all + p.ctas - 1) / p.ctas, start = len * blockIdx.x;
     if (start >= before && start < before + mine)
         for (int b = b0; b < b1; ++b) {
-            const long long u = static_cast<long long>(mass_item(sequence(p, b))) * p.d.Hkv;
+            const long long u = static_cast<long long>(mass_item(sequence<true>(p, b))) * p.d.Hkv;
             if (start < before + u) {
                 sm.b = b;
                 sm.at = start - before;
@@ -106,7 +109,7 @@ __device__ __forceinline__ MassRun find_mass_run(const TreeParams& p, MassSmem& 
     r.b = sm.b;
     r.at = sm.at;
     r.left = r.b < 0 ? 0 : (all - start < len ? all - start : len);
-    if (r.b >= 0) r.s = sequence(p, r.b);
+    if (r.b >= 0) r.s = sequence<true>(p, r.b);
     return r;
 }
 // The next tiles of one item in the run: those whose first unit lies in it.
@@ -116,7 +119,7 @@ __device__ __forceinline__ bool next_tiles(const TreeParams& p, MassRun& r, Stre
         if (r.at >= static_cast<long long>(item) * p.d.Hkv) {
             r.at -= static_cast<long long>(item) * p.d.Hkv;
             if (++r.b >= p.d.B) return false;   // (not reached: the run ends with the list)
-            r.s = sequence(p, r.b);
+            r.s = sequence<true>(p, r.b);
             continue;
         }
         const int w = blocks_of(r.s);
@@ -145,7 +148,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const TreeParams& p = mp.t;
     uint8_t* q_s = base_s + kSmemHead;
     const int q_box = mp.q_rows * C::BOX;                 // (E4M3: the second term follows the first)
-    uint8_t* k_s = q_s + mp.q_rows * D * 2;
+    const int q_bytes = mp.q_rows * D * 2;
+    uint8_t* k_s = q_s + mp.q_buffers * q_bytes;
     volatile int* abort = &sm.abort;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -155,20 +159,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.kfull[i], 1);
             mbar_init(&sm.kempty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(&sm.dfull[i], 2);    // the commit, and the issuing thread
             mbar_init(&sm.dfree[i], 4);
-            mbar_init(&sm.lfree[i], 8);
         }
-        mbar_init(&sm.qready, 2);
-        mbar_init(&sm.qfree, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.lfree[i], 8);
+            mbar_init(&sm.qready[i], 2);
+            mbar_init(&sm.qfree[i], 1);
+        }
         mbar_init(&sm.drained, 1);
         mbar_fence_init();
         tma_prefetch_map(&kmap);
     }
-    // (tensor memory as in the attention kernel: taken behind the kernels before this
-    // one, and before the next may start)
-    pdl_wait();
+    // Everything but lse was final before the attention kernel let the merge start (its
+    // threads wait first, and only then let others start), so all of this kernel's work up to
+    // the scores may run beside the merge, from L2: only the warps that read lse and that
+    // touch the weights wait.  Tensor memory: the attention kernel's CTAs all have theirs by
+    // then, and the merge needs none.
     if (warp == 1) {
         tmem_alloc(&sm.tmem, 2 * kBlock);
         tmem_relinquish();
@@ -197,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         while (ok && next_tiles(p, run, &x)) {
             for (int rb = 0; ok && rb < blocks_of(x.s); ++rb) {
-                PageWalk<kTile> walk;
+                PageWalk<kTile, true> walk;
                 walk.start(p, x, lane);
                 for (int t = x.t0; ok && t < x.t1; ++t, ++it) {
                     const uint32_t have = walk.tile(p, t, lane, sm.pages[it & 1]);
@@ -225,40 +233,45 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t k_desc = sdesc_k_major<C::BOX>(smem_addr(k_s));
             Cursor kc;
             int nb = 0;            // blocks
-            int used[2] = {0, 0};  // times each buffer was written
+            uint32_t used = 0, phase = 0;   // of each buffer: written before; its next wait
             bool go = true;
             while (go && next_tiles(p, run, &x)) {
                 const int rows = x.s.n * p.QG;
                 for (int rb = 0; go && rb < blocks_of(x.s); ++rb, ++nb) {
                     const int n = max(16, (min(kBlock, rows - (rb << kBlockShift)) + 15) & ~15);
                     const uint32_t id = idesc(n, kFp8 ? 0u : 1u, false);
-                    if (!(go = wait_one(&sm.qready, nb & 1))) break;
+                    const int qb = nb & (mp.q_buffers - 1);
+                    if (!(go = wait_one(&sm.qready[qb], (nb >> (mp.q_buffers - 1)) & 1))) break;
+                    const uint64_t q0 = q_desc + static_cast<uint32_t>((qb * q_bytes) >> 4);
                     for (int t = x.t0; t < x.t1; ++t) {
-                        const int i = (t - x.t0) & 1;
-                        if (used[i] > 0 && !(go = wait_one(&sm.dfree[i], (used[i] - 1) & 1))) break;
+                        const int i = (t - x.t0) & (mp.buffers - 1);
+                        if ((used >> i) & 1u) {
+                            if (!(go = wait_one(&sm.dfree[i], (phase >> i) & 1u))) break;
+                            phase ^= 1u << i;
+                        }
                         if (!(go = wait_one(&sm.kfull[kc.slot], kc.phase))) break;
-                        ++used[i];
+                        used |= 1u << i;
                         tc_fence_after();
                         const uint64_t a = k_desc + static_cast<uint32_t>(kc.slot * C::SLOT >> 4);
-                        const uint32_t d = tmem + kBlock * i;
+                        const uint32_t d = tmem + (2 * kBlock / mp.buffers) * i;
                         if (kFp8) {
 #pragma unroll
                             for (int h = 0; h < 2; ++h)
 #pragma unroll
                                 for (int k = 0; k < D / 32; ++k)
                                     umma_ss<true>(d, a + ((k * 32) >> 4),
-                                                  q_desc + static_cast<uint32_t>((h * q_box + k * 32) >> 4),
+                                                  q0 + static_cast<uint32_t>((h * q_box + k * 32) >> 4),
                                                   id, h > 0 || k > 0);
                         } else {
 #pragma unroll
                             for (int k = 0; k < D / 16; ++k)
                                 umma_ss<false>(d, a + (((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4),
-                                               q_desc + static_cast<uint32_t>(((k >> 2) * q_box + (k & 3) * 32) >> 4),
+                                               q0 + static_cast<uint32_t>(((k >> 2) * q_box + (k & 3) * 32) >> 4),
                                                id, k > 0);
                         }
                         umma_commit(&sm.kempty[kc.slot]);
                         umma_commit(&sm.dfull[i]);
-                        if (t + 1 == x.t1) umma_commit(&sm.qfree);
+                        if (t + 1 == x.t1) umma_commit(&sm.qfree[qb]);
                         // this thread has seen the tile's copy complete, and with it the
                         // page bits, and the block's lse: hand that on
                         mbar_arrive(&sm.dfull[i]);
@@ -281,68 +294,78 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int all = x.s.n * p.QG;
             for (int rb = 0; go && rb < blocks_of(x.s); ++rb, ++nb) {
                 const int r0 = rb << kBlockShift, rows = min(kBlock, all - r0);
-                if (nb > 0 && !(go = waits(&sm.qfree, (nb - 1) & 1))) break;
+                const int qb = nb & (mp.q_buffers - 1), use = nb >> (mp.q_buffers - 1);
+                if (use > 0 && !(go = waits(&sm.qfree[qb], (use - 1) & 1))) break;
                 if (nb > 1 && !(go = waits(&sm.lfree[nb & 1], ((nb >> 1) - 1) & 1))) break;
                 fence_proxy_async_smem();
-                auto row_of = [&](int r) {   // row r of the block
-                    const int node = (r0 + r) / p.QG;
-                    return p.q + (x.s.first + node) * p.q_stride +
-                           static_cast<int64_t>(x.g * p.QG + r0 + r - node * p.QG) * D;
+                uint8_t* const q_at = q_s + qb * q_bytes;
+                // this thread's rows of the block, `step` apart, without a division each: a
+                // row further is D values on, a token further q_stride - QG D more
+                auto each_row = [&](int start, int step, int count, auto&& f) {
+                    int node = (r0 + start) / p.QG, head = r0 + start - node * p.QG;
+                    const __nv_bfloat16* src = p.q + (x.s.first + node) * p.q_stride +
+                                               static_cast<int64_t>(x.g * p.QG + head) * D;
+                    const int dn = step / p.QG, dh = step - dn * p.QG;
+                    const int64_t by = dn * p.q_stride + static_cast<int64_t>(dh) * D;
+                    const int64_t wrap = p.q_stride - static_cast<int64_t>(p.QG) * D;
+#pragma unroll 4
+                    for (int r = start; r < count; r += step) {
+                        f(r, src);
+                        src += by;
+                        head += dh;
+                        if (head >= p.QG) {
+                            head -= p.QG;
+                            src += wrap;
+                        }
+                    }
                 };
                 if (kFp8) {
                     // a group of lanes a row, 16 values a lane
-                    constexpr int LPR = D / 16, STEP = 64 / LPR, AHEAD = 4;
+                    constexpr int LPR = D / 16, STEP = 64 / LPR;
                     const int c = t64 % LPR;
-                    for (int rr = t64 / LPR; rr < ((rows + STEP - 1) / STEP) * STEP; rr += AHEAD * STEP) {
-                        uint4 v[AHEAD][2];
-#pragma unroll
-                        for (int u = 0; u < AHEAD; ++u) {
-                            const int r = rr + u * STEP;
-                            v[u][0] = v[u][1] = make_uint4(0, 0, 0, 0);
-                            if (r < rows) {
-                                const uint4* src = reinterpret_cast<const uint4*>(row_of(r)) + 2 * c;
-                                v[u][0] = src[0];
-                                v[u][1] = src[1];
-                            }
+                    // (whole passes: a row's lanes exchange its largest value)
+                    each_row(t64 / LPR, STEP, (rows + STEP - 1) / STEP * STEP,
+                             [&](int r, const __nv_bfloat16* src) {
+                        uint4 a = make_uint4(0, 0, 0, 0), b = a;
+                        if (r < rows) {
+                            a = __ldcg(reinterpret_cast<const uint4*>(src) + 2 * c);
+                            b = __ldcg(reinterpret_cast<const uint4*>(src) + 2 * c + 1);
                         }
+                        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                        uint32_t big = 0;
 #pragma unroll
-                        for (int u = 0; u < AHEAD; ++u) {
-                            const int r = rr + u * STEP;
-                            const uint32_t w[8] = {v[u][0].x, v[u][0].y, v[u][0].z, v[u][0].w,
-                                                   v[u][1].x, v[u][1].y, v[u][1].z, v[u][1].w};
-                            uint32_t big = 0;
+                        for (int i = 0; i < 8; ++i) big = bf16_magnitude(big, w[i]);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) big = bf16_magnitude(big, w[i]);
+                        for (int o = 1; o < LPR; o <<= 1)
+                            big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+                        float qs = p.qscale;
+                        const float up = e4m3_scaling(big, &qs);
+                        uint32_t t[2][4];
 #pragma unroll
-                            for (int o = 1; o < LPR; o <<= 1)
-                                big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
-                            float qs = p.qscale;
-                            const float up = e4m3_scaling(big, &qs);
-                            uint32_t t[2][4];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                uint32_t hi, lo;
-                                e4m3_terms(w[i], up, &hi, &lo);
-                                if (i % 2 == 0) t[0][i / 2] = hi, t[1][i / 2] = lo;
-                                else t[0][i / 2] |= hi << 16, t[1][i / 2] |= lo << 16;
-                            }
-                            if (r < rows) {
-                                uint8_t* at = q_s + tile_off<C::BOX, kBlock>(r, c);
-                                *reinterpret_cast<uint4*>(at) = make_uint4(t[0][0], t[0][1], t[0][2], t[0][3]);
-                                *reinterpret_cast<uint4*>(at + q_box) =
-                                    make_uint4(t[1][0], t[1][1], t[1][2], t[1][3]);
-                                if (c == 0) sm.qs[nb & 1][r] = qs;
-                            }
+                        for (int i = 0; i < 8; ++i) {
+                            uint32_t hi, lo;
+                            e4m3_terms(w[i], up, &hi, &lo);
+                            if (i % 2 == 0) t[0][i / 2] = hi, t[1][i / 2] = lo;
+                            else t[0][i / 2] |= hi << 16, t[1][i / 2] |= lo << 16;
                         }
-                    }
+                        if (r < rows) {
+                            uint8_t* at = q_at + tile_off<C::BOX, kBlock>(r, c);
+                            *reinterpret_cast<uint4*>(at) = make_uint4(t[0][0], t[0][1], t[0][2], t[0][3]);
+                            *reinterpret_cast<uint4*>(at + q_box) =
+                                make_uint4(t[1][0], t[1][1], t[1][2], t[1][3]);
+                            if (c == 0) sm.qs[nb & 1][r] = qs;
+                        }
+                    });
                 } else {
                     constexpr int CH = D / 8, STEP = 64 / CH;   // 16-byte chunks of a row; rows a pass
                     const int c = t64 % CH;
-                    const uint32_t dst = smem_addr(q_s) + (c >> 3) * q_box;
-                    for (int r = t64 / CH; r < rows; r += STEP)
-                        cp_async16(dst + tile_off<128, kBlock>(r, c & 7), row_of(r) + 8 * c, true);
+                    const uint32_t dst = smem_addr(q_at) + (c >> 3) * q_box;
+                    each_row(t64 / CH, STEP, rows, [&](int r, const __nv_bfloat16* src) {
+                        cp_async16(dst + tile_off<128, kBlock>(r, c & 7), src + 8 * c, true);
+                    });
                     cp_async_commit();
                 }
+                if (nb == 0) pdl_wait();
                 for (int r = t64; r < rows; r += 64) {
                     const int node = (r0 + r) / p.QG;
                     sm.nl[nb & 1][r] = -*stat_at(p, x.b, node, x.g * p.QG + r0 + r - node * p.QG);
@@ -350,16 +373,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!kFp8) cp_async_wait<0>();
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.qready);
+                if (lane == 0) mbar_arrive(&sm.qready[qb]);
             }
         }
     } else {
         // ---- sums: thread = position of a tile ----
         const int grp = (warp - 4) >> 2;
         const int gt = (warp & 3) * 32 + lane;
-        const uint32_t tS = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kBlock * grp;
-        int nb = 0, it0 = 0, used = 0;   // blocks; tiles before this block; times the buffer was read
+        const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        int nb = 0, it0 = 0;   // blocks; tiles before this block
+        uint32_t phase = 0;    // of each buffer's next wait
         bool go = true;
+        pdl_wait();
         while (go && next_tiles(p, run, &x)) {
             const int all = x.s.n * p.QG, nt = x.t1 - x.t0;
             float* mass = mp.mass + (static_cast<int64_t>(x.b) * p.d.Hkv + x.g) * mp.mass_stride;
@@ -373,8 +398,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float sum = 0.f;
                     if (pos < x.s.total && (rb > 0 || (pos < x.s.len && mp.decay != 0.f)))
                         sum = (rb > 0 ? 1.f : mp.decay) * mass[pos];
-                    if (!(go = waits(&sm.dfull[grp], used & 1))) break;
-                    ++used;
+                    const int buf = (t - x.t0) & (mp.buffers - 1);   // (as odd as the group)
+                    const uint32_t tS = lanes + (2 * kBlock / mp.buffers) * buf;
+                    if (!(go = waits(&sm.dfull[buf], (phase >> buf) & 1u))) break;
+                    phase ^= 1u << buf;
                     tc_fence_after();
                     const uint32_t have = static_cast<uint32_t>(sm.have[(it0 + t - x.t0) % kHave]);
                     const bool there = (have >> (gt >> p.box_shift)) & 1u;
@@ -405,16 +432,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                             acc[1] = add2(acc[1], f2(fast_exp2(y[1].x), fast_exp2(y[1].y)));
                         }
                     };
-                    for (int c0 = 0; c0 < rows; c0 += 32) {
-                        uint32_t v[32];
+                    for (int c0 = 0; c0 < rows; c0 += 64) {
+                        uint32_t v[64];
                         tmem_ld32(tS + c0, v);
+                        if (c0 + 32 < rows) tmem_ld32(tS + c0 + 32, v + 32);
                         tmem_ld_wait();
-                        if (cut || c0 + 32 > rows) chunk(v, c0, true);
+                        if (c0 + 64 >= rows) {   // all has been read
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&sm.dfree[buf]);
+                        }
+                        const bool check = cut || c0 + 64 > rows;
+                        if (check) chunk(v, c0, true);
                         else chunk(v, c0, false);
+                        if (c0 + 32 < rows) {
+                            if (check) chunk(v + 32, c0 + 32, true);
+                            else chunk(v + 32, c0 + 32, false);
+                        }
                     }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.dfree[grp]);
+                    if (rows <= 0 && lane == 0) mbar_arrive(&sm.dfree[buf]);
                     const float2 s2 = split(add2(acc[0], acc[1]));
                     if (pos < x.s.total) mass[pos] = there ? sum + (s2.x + s2.y) : sum;
                 }
@@ -437,8 +473,11 @@ int launch(const CUtensorMap& kmap, MassParams p, int device, cudaStream_t st) {
     const int limit =
         limits.get(device, [&] { return set_max_dynamic_smem(reinterpret_cast<const void*>(kern)); });
     p.q_rows = std::min(kBlock, (p.t.T * p.t.QG + 31) / 32 * 32);
-    const int fixed = 1024 + kSmemHead + p.q_rows * D * 2;
+    // two blocks' q where they are small: the next item's comes while this one's tiles run
+    p.q_buffers = p.q_rows <= kBlock / 2 ? 2 : 1;
+    const int fixed = 1024 + kSmemHead + p.q_buffers * p.q_rows * D * 2;
     p.slots = std::min((limit - fixed) / C::SLOT, kMaxSlots);
+    p.buffers = p.q_rows <= kBlock / 2 ? 4 : 2;
     if (limit < 0 || p.slots < 2) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     LaunchAttrs la;

@@ -414,12 +414,12 @@ __device__ __forceinline__ bool elect_one() {
 
 // The table entries of a stretch, looked up by a warp 32 pieces at a time and
 // one batch ahead.
-template <int kTile>
+template <int kTile, bool kFromL2 = false>
 struct PageWalk {
     const int* row;
     int c_end, c0, cur, nxt;
     __device__ __forceinline__ int entry(const TreeParams& p, int c) const {
-        return c < c_end ? row[(c << p.box_shift) >> p.d.page_shift] : -1;
+        return c < c_end ? plan_value<kFromL2>(row + ((c << p.box_shift) >> p.d.page_shift)) : -1;
     }
     template <bool kShared = false>
     __device__ __forceinline__ void start(const TreeParams& p, const Stretch& x, int lane) {
