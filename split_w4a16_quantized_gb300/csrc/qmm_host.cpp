@@ -1268,7 +1268,6 @@ int qmm_tree_attention(const qmm_kv_cache* cache, const void* q, int64_t q_strid
 
 // The sizes of a call with shared prefixes beside those of check_tree.
 static int check_prefix(const qmm_kv_cache* c, const qmm_prefix* pre, int Hq, int N) {
-    if (pre->max_pages < 1 || pre->G < 1 || N < 1) return QMM_EINVAL;
     const int64_t cap = static_cast<int64_t>(pre->max_pages) * c->page_size;
     if (pre->G > c->B || cap > 0x7fff0000LL || static_cast<int64_t>(N) * Hq > INT_MAX)
         return QMM_ESHAPE;

@@ -22,7 +22,9 @@ namespace qmm {
 namespace {
 
 constexpr int kRowShift = 7;
-constexpr int kCtasPerSm = 2;
+constexpr int kCtasPerSm = 2;   // of either kernel
+// Query rows per KV head of all tokens up to which the kernel for few rows is faster.
+constexpr int kFewRows = 16;
 // A block takes ROWS query rows of a sequence's KV head, a thread a row and every 16th
 // (D = 128; 64: each) group of 4 columns.
 template <int D, int ROWS>
@@ -117,8 +119,14 @@ int launch_prefix_attention(const qmm_kv_cache& c, const qmm_prefix& pre, const 
     const bool fp8 = c.dtype == QMM_CACHE_E4M3;
     TreeParams p;
     CUtensorMap kmap, vmap;
-    int rc = tree_setup(c, q, q_stride, O, N, T, Hq, cu, parents, scale, ws, kCtasPerSm * num_sms,
-                        kRowShift, kTcTileShift, 6, fp8 ? 8 : 4, &p, &kmap, &vmap);
+    const int QG = Hq / c.Hkv;
+    const bool few = T * QG <= 1 << kFewRowShift && static_cast<int64_t>(N) * QG <= kFewRows;
+    int rc = few ? tree_setup(c, q, q_stride, O, N, T, Hq, cu, parents, scale, ws,
+                              kFewCtasPerSm * num_sms, kFewRowShift, kFewTileShift, kFewMinRun,
+                              kFewSetup, &p, &kmap, &vmap)
+                 : tree_setup(c, q, q_stride, O, N, T, Hq, cu, parents, scale, ws,
+                              kCtasPerSm * num_sms, kRowShift, kTcTileShift, 6, fp8 ? 8 : 4, &p,
+                              &kmap, &vmap);
     if (rc != cudaSuccess) return rc;
     p.pre.table = pre.table;
     p.pre.lens = pre.lens;
@@ -130,7 +138,8 @@ int launch_prefix_attention(const qmm_kv_cache& c, const qmm_prefix& pre, const 
     p.plan = reinterpret_cast<long long*>(
         p.pre.direct + direct_floats(c.D, static_cast<int64_t>(N) * Hq));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    rc = launch_prefix_tc(kmap, vmap, p, c.D, fp8, device, st);
+    rc = few ? launch_tree_few_shared(kmap, vmap, p, c.D, fp8, device, st)
+             : launch_prefix_tc(kmap, vmap, p, c.D, fp8, device, st);
     if (rc != cudaSuccess) return rc;
     const int rows = T * p.QG, block_rows = rows <= 8 ? 8 : 16;
     const int chunks = (rows + block_rows - 1) / block_rows;

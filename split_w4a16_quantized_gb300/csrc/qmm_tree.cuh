@@ -527,10 +527,12 @@ constexpr int kTcTileShift = 6;
 constexpr float kTcLift = 7.f;   // log2 of its factor on F16 weights
 int launch_tree_tc(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int D,
                    bool fp8, int device, cudaStream_t st);
-// One launch of the kernel for up to 8 rows (qmm_tree_attention.cu) that also leaves
-// each row's scores in p.scores; the merge is the caller's.
+// One launch of the kernel for up to 8 rows (qmm_tree_attention.cu) with shared prefixes
+// (p.pre), or that also leaves each row's scores in p.scores; the merge is the caller's.
 constexpr int kFewRowShift = 3, kFewTileShift = 6, kFewCtasPerSm = 2, kFewMinRun = 2, kFewSetup = 1;
 constexpr float kFewLift = 15.f;   // log2 of its factor on F16 weights
+int launch_tree_few_shared(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p,
+                           int D, bool fp8, int device, cudaStream_t st);
 int launch_tree_scores(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int D,
                        bool fp8, int device, cudaStream_t st);
 // The tcgen05 kernel with shared prefixes (p.pre), items of up to 128 rows: every item leaves a

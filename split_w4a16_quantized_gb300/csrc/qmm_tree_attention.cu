@@ -131,7 +131,8 @@ __device__ __forceinline__ void mma16816(float d[4], const uint32_t a[4], uint32
 // the CTA winds down after its copies in flight have landed.
 // kScores: the scores go to p.scores, and the lse of an item's rows to p.lse, as well: one more store of 8 bytes for two of them
 // (32 rows of 1024 to 8192 positions: the kernel 84 us, without 78).
-template <int D, bool kFp8, bool kScores>
+// kShared: with shared prefixes in the list of work; every item leaves a state.
+template <int D, bool kFp8, bool kScores, bool kShared>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     tree_attn_kernel(const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap,
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // (after the wait: the merge kernel plans with lens and cu before its own)
     pdl_trigger();
     __syncthreads();
-    Run run = find_run<kThreads, false, kScores>(p, sm.run);
+    Run run = find_run<kThreads, kShared, kScores || kShared>(p, sm.run);
     const int pieces = kTile >> p.box_shift;     // copies of a tile, per column block and pool
     Stretch x;
 
@@ -169,9 +170,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         const uint32_t ring_a = smem_addr(ring);
         int it = 0;   // tiles copied so far
         bool ok = true;
-        while (ok && next_stretch(p, run, &x)) {
+        while (ok && next_stretch<kShared>(p, run, &x)) {
             PageWalk<kTile> walk;
-            walk.start(p, x, lane);
+            walk.template start<kShared>(p, x, lane);
             for (int t = x.t0; t < x.t1; ++t, ++it) {
                 const uint32_t have = walk.tile(p, t, lane, sm.pages);
                 const int st = it % kStages;
@@ -205,14 +206,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         const int mj = lane >> 3, mr = lane & 7;   // ldmatrix: matrix, row
         const int kb = warp * kKeys;               // the warp's first position in a tile
         int it = 0;
-        while (next_stretch(p, run, &x)) {
+        while (next_stretch<kShared>(p, run, &x)) {
             const int rows = min(kRows, x.s.n * p.QG - x.row0);
             // ---- ancestors of the rows' tokens, where the stretch reaches the
             // drafted slots; a chain needs none ----
             const bool on = gr < rows;
             const int row = x.row0 + min(gr, rows - 1);
-            const int node = row_node(p, row), head = x.g * p.QG + row - node * p.QG;
-            if (p.parents && x.t1 * kTile > x.s.len) {
+            const int node = row_node<kShared>(p, row), head = x.g * p.QG + row - node * p.QG;
+            if (p.parents && x.t1 * kTile > x.s.len && !(kShared && x.b < p.pre.G)) {
                 for (int i = tid; i < x.s.n; i += 32 * kWarps) {
                     const int v = p.parents[x.s.first + i];
                     sm.par[i] = static_cast<int16_t>(v >= 0 && v < i ? v : -1);
@@ -490,11 +491,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             const PartialAt part = partial_at<D>(p, 2 * blockIdx.x + (x.t0 == 0 ? 1 : 0));
             if (on) {
                 const float inv =
-                    whole ? (den > 0.f ? p.vscale / den : (den == 0.f ? 0.f : den)) : 1.f;
-                if (!whole && warp == 0 && tq == 0) {
-                    part.m[gr] = M;
-                    part.l[gr] = den;
+                    whole && !kShared ? (den > 0.f ? p.vscale / den : (den == 0.f ? 0.f : den)) : 1.f;
+                const bool output = whole && !kShared;   // else a state
+                DirectAt direct = {};
+                if (kShared)
+                    direct = direct_at<D>(p, x.b < p.pre.G,
+                                          static_cast<int64_t>(x.s.first + node) * p.Hq + head);
+                if (!output && warp == 0 && tq == 0) {
+                    *(kShared && whole ? direct.m : part.m + gr) = M;
+                    *(kShared && whole ? direct.l : part.l + gr) = den;
                 }
+                auto state_at = [&](int c) {
+                    return kShared && whole ? direct.o + c : part.at(gr, c);
+                };
                 if (kScores && whole && warp == 0 && tq == 0)
                     *stat_at(p, x.b, node, head) = stat_of(p, M, den);
                 __nv_bfloat16* out =
@@ -508,17 +517,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                         const int n1 = n + 1 < NQ ? n + 1 : n;
                         const float4 v = make_float4(acc[n][0] * inv, acc[n1][0] * inv,
                                                      acc[n][1] * inv, acc[n1][1] * inv);
-                        if (whole)
+                        if (output)
                             *reinterpret_cast<uint2*>(out + c) =
                                 make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
                         else
-                            *reinterpret_cast<float4*>(part.at(gr, c)) = v;
+                            *reinterpret_cast<float4*>(state_at(c)) = v;
                     } else {
                         const float2 v = make_float2(acc[n][0] * inv, acc[n][1] * inv);
-                        if (whole)
+                        if (output)
                             *reinterpret_cast<uint32_t*>(out + c) = pack_bf16x2(v.x, v.y);
                         else
-                            *reinterpret_cast<float2*>(part.at(gr, c)) = v;
+                            *reinterpret_cast<float2*>(state_at(c)) = v;
                     }
                 }
             }
@@ -684,11 +693,11 @@ __global__ void __launch_bounds__(kMergeThreads)
     }
 }
 
-template <int D, bool kFp8, bool kScores>
+template <int D, bool kFp8, bool kScores, bool kShared>
 int launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int device,
            cudaStream_t st) {
     using C = Cfg<D, kFp8>;
-    auto kern = tree_attn_kernel<D, kFp8, kScores>;
+    auto kern = tree_attn_kernel<D, kFp8, kScores, kShared>;
     const size_t smem = 1024 + static_cast<size_t>(kStages) * C::STAGE + sizeof(Smem<D>);
     static PerDevice<bool> opted_in;
     if (!opted_in.get(device, [&] {
@@ -706,14 +715,14 @@ int launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p
     return cudaLaunchKernelEx(&cfg, kern, kmap, vmap, p);
 }
 
-template <bool kScores>
+template <bool kScores, bool kShared>
 int launch_few(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int D,
                bool fp8, int device, cudaStream_t st) {
     if (D == 128)
-        return fp8 ? launch<128, true, kScores>(kmap, vmap, p, device, st)
-                   : launch<128, false, kScores>(kmap, vmap, p, device, st);
-    return fp8 ? launch<64, true, kScores>(kmap, vmap, p, device, st)
-               : launch<64, false, kScores>(kmap, vmap, p, device, st);
+        return fp8 ? launch<128, true, kScores, kShared>(kmap, vmap, p, device, st)
+                   : launch<128, false, kScores, kShared>(kmap, vmap, p, device, st);
+    return fp8 ? launch<64, true, kScores, kShared>(kmap, vmap, p, device, st)
+               : launch<64, false, kScores, kShared>(kmap, vmap, p, device, st);
 }
 
 int launch_merge(const TreeParams& p, int D, cudaStream_t st) {
@@ -828,9 +837,14 @@ int tree_setup(const qmm_kv_cache& c, const void* q, int64_t q_stride, void* O, 
     return cudaSuccess;
 }
 
+int launch_tree_few_shared(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p,
+                           int D, bool fp8, int device, cudaStream_t st) {
+    return launch_few<false, true>(kmap, vmap, p, D, fp8, device, st);
+}
+
 int launch_tree_scores(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int D,
                        bool fp8, int device, cudaStream_t st) {
-    return launch_few<true>(kmap, vmap, p, D, fp8, device, st);
+    return launch_few<true, false>(kmap, vmap, p, D, fp8, device, st);
 }
 
 int launch_tree_attention(const qmm_kv_cache& c, const void* q, int64_t q_stride, void* O, int N,
@@ -850,7 +864,7 @@ int launch_tree_attention(const qmm_kv_cache& c, const void* q, int64_t q_stride
     p.lift = fp8 ? (var.tc ? kTcLift : kFewLift) : 0.f;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int rc = var.tc ? launch_tree_tc(kmap, vmap, p, c.D, fp8, device, st)
-                          : launch_few<false>(kmap, vmap, p, c.D, fp8, device, st);
+                          : launch_few<false, false>(kmap, vmap, p, c.D, fp8, device, st);
     return rc == cudaSuccess ? launch_merge(p, c.D, st) : rc;
 }
 
