@@ -58,8 +58,9 @@ struct MassParams {
 struct MassSmem {
     uint64_t kfull[kMaxSlots], kempty[kMaxSlots];
     uint64_t dfull[4], dfree[4];       // scores of a tile are there; have been read
-    uint64_t qready[2], qfree[2];      // a block's q and lse are there; its products are done
-    uint64_t lfree[2];                 // a block's lse has been read by all
+    uint64_t qready[2];                // even and odd blocks' q and lse are there
+    uint64_t lfree[2];                 // have been read by all
+    uint64_t qfree[2];                 // by buffer of q: the block's products are done
     uint64_t drained;                  // abort: every MMA issued has ended
     uint32_t tmem;
     int abort;
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int n = max(16, (min(kBlock, rows - (rb << kBlockShift)) + 15) & ~15);
                     const uint32_t id = idesc(n, kFp8 ? 0u : 1u, false);
                     const int qb = nb & (mp.q_buffers - 1);
-                    if (!(go = wait_one(&sm.qready[qb], (nb >> (mp.q_buffers - 1)) & 1))) break;
+                    if (!(go = wait_one(&sm.qready[nb & 1], (nb >> 1) & 1))) break;
                     const uint64_t q0 = q_desc + static_cast<uint32_t>((qb * q_bytes) >> 4);
                     for (int t = x.t0; t < x.t1; ++t) {
                         const int i = (t - x.t0) & (mp.buffers - 1);
@@ -373,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!kFp8) cp_async_wait<0>();
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.qready[qb]);
+                if (lane == 0) mbar_arrive(&sm.qready[nb & 1]);
             }
         }
     } else {
@@ -390,6 +391,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             float* mass = mp.mass + (static_cast<int64_t>(x.b) * p.d.Hkv + x.g) * mp.mass_stride;
             for (int rb = 0; go && rb < blocks_of(x.s); ++rb, ++nb, it0 += nt) {
                 const int r0 = rb << kBlockShift, rows = min(kBlock, all - r0);
+                // A warp whose group has no tile in the block goes through it all the same, and
+                // no further ahead than this: block n + 2's q comes only once every warp is
+                // through block n, so none arrives twice for one phase of lfree.
+                if (!(go = waits(&sm.qready[nb & 1], (nb >> 1) & 1))) break;
                 const float* nl = sm.nl[nb & 1];
                 const float* qsr = sm.qs[nb & 1];
                 for (int t = x.t0 + grp; t < x.t1; t += 2) {
