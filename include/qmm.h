@@ -792,10 +792,9 @@ typedef struct {
  * those count the prefix too).  A prefix's keys and values are read once for 128 query
  * rows per KV head, not once for each of its sequences.
  * The arguments, checks and results are qmm_tree_attention's, but:
- *   - the weights are rounded once, to BF16 (F16 for an E4M3 cache), for any number of
- *     rows;
- *   - cu has to ascend without gaps within a prefix's sequences, and their ranges to be
- *     of at most T tokens, for all of them to see it;
+ *   - the weights are rounded as for more than 8 query rows per KV head, unless there are
+ *     at most 8 of a sequence (T Hq / Hkv) and 16 of all (N Hq / Hkv);
+ *   - cu has to ascend over a prefix's sequences for all of them to see it;
  *   - the workspace is qmm_prefix_attention_workspace_bytes, which grows with N;
  *   - QMM_EINVAL also for a NULL prefix or array, G or max_pages below 1; QMM_ESHAPE for
  *     G above B, N Hq above 2^31 - 1, a prefix table of more than 2^31 - 65536 slots,
@@ -853,8 +852,9 @@ int qmm_tree_accept(const qmm_kv_cache *caches, int n, const int *tokens, const 
  *          4 and at least max_pages * page_size.  Overlaps nothing else of the call
  *   decay  0 or more, finite; with 0 the old sums are not read
  * The other arguments, O and the errors are qmm_tree_attention's.  The workspace is
- * qmm_scored_attention_workspace_bytes, which grows with the table and the batch.  The
- * result does not depend on timing.  Three launches. */
+ * qmm_scored_attention_workspace_bytes; for up to 8 query rows per KV head (T Hq / Hkv) it
+ * holds the scores of every slot, 4 B Hq T max_pages page_size bytes and more.  The result
+ * does not depend on timing.  Two launches for up to 8 rows, else three. */
 int qmm_scored_attention(const qmm_kv_cache *cache, const void *q, int64_t q_stride, void *O,
                          int N, int T, int Hq, const int *cu, float scale, float *mass,
                          int64_t mass_stride, float decay, void *workspace, size_t ws_bytes,

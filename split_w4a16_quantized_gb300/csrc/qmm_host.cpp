@@ -1435,6 +1435,7 @@ int qmm_kv_evict(const qmm_kv_cache* caches, int n, const float* mass, float* ma
     if (n > 1 && (layer_stride % 4 || layer_stride < rows * mass_stride ||
                   layer_stride >= int64_t{1} << 48))
         return QMM_ESHAPE;
+    if (rows * keep > (int64_t{1} << 60) / n) return QMM_ESHAPE;   // (no memory holds kept)
     if (!aligned(mass_out, 16) || !aligned(kept, 4) || !aligned(new_lens, 4)) return QMM_EALIGN;
     // what one block writes another may yet read; a column's own weights are read first
     const int64_t cap = static_cast<int64_t>(c.max_pages) * c.page_size;

@@ -17,8 +17,8 @@
 // 3.1 us in a graph, latency.
 //
 // Positions of several axes (qmm_kv_append_axes): pair j turns by the position of
-// axis[j], so a lane's four pairs may take their cosines and sines from four rows of
-// the table.  A lane holds the position of one axis and the others ask it for theirs.
+// axis[j], so neighbouring pairs may take their cosines and sines from different rows of
+// the table.  A token's threads gather them once, a value each, and share them.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -106,11 +106,14 @@ __global__ void __launch_bounds__(kAppendThreads, 8) kv_append_kernel(const Appe
     const int group = threadIdx.x / L;
     const int step = p.per_token;                   // lane groups of a token
     const int sub = group & (step - 1);
-    const int tok = blockIdx.x * (kGroups / step) + group / step;
+    int tok = blockIdx.x * (kGroups / step) + group / step;
     pdl_wait();
     // A group's lanes leave together or not at all; the shuffles below name
-    // only the group's own lanes.
-    if (tok >= p.N) return;
+    // only the group's own lanes.  (kAxes: behind the barrier; until then a group
+    // without a token looks at the last one)
+    bool alive = tok < p.N;
+    if (!kAxes && !alive) return;
+    if (kAxes) tok = min(tok, p.N - 1);
     const uint32_t mask = ((1u << L) - 1u) << ((threadIdx.x & 31) / L * L);
 
     // where the lane's two pieces of four values start
@@ -148,10 +151,12 @@ __global__ void __launch_bounds__(kAppendThreads, 8) kv_append_kernel(const Appe
         for (int j = 1 + lane; j <= p.d.B; j += L) before += p.cu[j] <= tok;
 #pragma unroll
         for (int o = L / 2; o > 0; o >>= 1) before += __shfl_xor_sync(mask, before, o);
-        if (before >= p.d.B) return;
-        b = before;
+        if (!kAxes && before >= p.d.B) return;
+        alive = alive && before < p.d.B;
+        b = kAxes ? min(before, p.d.B - 1) : before;
         i = tok - max(p.cu[b], 0);   // clamped as token_range does
-        if (i < 0) return;
+        if (!kAxes && i < 0) return;
+        alive = alive && i >= 0;
     }
     int pos_given = 0;   // kAxes: of axis `lane`
     if (kAxes) {
@@ -162,7 +167,8 @@ __global__ void __launch_bounds__(kAppendThreads, 8) kv_append_kernel(const Appe
     const int len = cached_tokens(p.d, b);
     const int pos = kAxes || p.positions ? pos_given : len + i;
     const bool off_table = p.dim > 0 && (pos < 0 || pos >= p.rows);
-    if (kAxes ? __any_sync(mask, off_table) : off_table) return;
+    if (kAxes) alive = !__any_sync(mask, off_table) && alive;
+    else if (off_table) return;
     // (len <= cap < 2^31 - 65535 and i < N: the sum is tested before it is used)
     const int64_t slot = static_cast<int64_t>(len) + i;
     const int64_t at = slot < p.d.cap ? slot_offset(p.d, b, static_cast<int>(slot)) : -1;
@@ -170,18 +176,24 @@ __global__ void __launch_bounds__(kAppendThreads, 8) kv_append_kernel(const Appe
     // cosines and sines of the lane's four pairs
     F2 cs[2], sn[2], ns[2];
     if (kAxes) {
-        const uint32_t axis = p.axis4[lane];
-        float c[4], s[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int at_axis = __shfl_sync(mask, pos, (axis >> (8 * j)) & 0xffu, L);
-            const float* row = p.cos_sin + static_cast<int64_t>(at_axis) * p.dim + 4 * lane + j;
-            c[j] = turns ? row[0] : 0.f;
-            s[j] = turns ? row[p.dim / 2] : 0.f;
+        __shared__ __align__(16) float cs_s[kGroups][D];   // by token of the block
+        float* const mine = cs_s[group / step];
+        if (alive)
+            for (int v = sub * L + lane; v < p.dim; v += step * L) {
+                const int pair = v < p.dim / 2 ? v : v - p.dim / 2;
+                const int axis = (p.axis4[pair >> 2] >> (8 * (pair & 3))) & 0xffu;
+                const int at_axis = p.positions[static_cast<int64_t>(axis) * p.N + tok];
+                mine[v] = p.cos_sin[static_cast<int64_t>(at_axis) * p.dim + v];
+            }
+        __syncthreads();
+        if (!alive) return;
+        if (turns) {
+            const float4 c4 = *reinterpret_cast<const float4*>(mine + 4 * lane);
+            const float4 s4 = *reinterpret_cast<const float4*>(mine + p.dim / 2 + 4 * lane);
+            cs[0] = f2(c4.x, c4.y), cs[1] = f2(c4.z, c4.w);
+            sn[0] = f2(s4.x, s4.y), sn[1] = f2(s4.z, s4.w);
+            ns[0] = f2(-s4.x, -s4.y), ns[1] = f2(-s4.z, -s4.w);
         }
-        cs[0] = f2(c[0], c[1]), cs[1] = f2(c[2], c[3]);
-        sn[0] = f2(s[0], s[1]), sn[1] = f2(s[2], s[3]);
-        ns[0] = f2(-s[0], -s[1]), ns[1] = f2(-s[2], -s[3]);
     } else if (turns) {
         const float* row = p.cos_sin + static_cast<int64_t>(pos) * p.dim + 4 * lane;
         const float4 c4 = *reinterpret_cast<const float4*>(row);
