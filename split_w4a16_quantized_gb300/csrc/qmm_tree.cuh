@@ -179,7 +179,9 @@ __device__ __forceinline__ long long block_scan(long long v, long long* red, lon
 }
 
 __device__ __forceinline__ long long run_length(const TreeParams& p, long long all) {
-    const long long r = (all + p.ctas - 1) / p.ctas;
+    const long long sum = all + p.ctas - 1;
+    const long long r = (sum >> 32) == 0 ? static_cast<uint32_t>(sum) / static_cast<uint32_t>(p.ctas)
+                                         : sum / p.ctas;
     return r < p.min_run ? p.min_run : r;
 }
 

@@ -16,7 +16,12 @@ __device__ __forceinline__ Runs runs_of(const TreeParams& p, const Seq& s, long 
                                         int item, long long len) {
     const int units = item_units(p, s);
     const long long start = before + static_cast<long long>(item) * units;
-    return {static_cast<int>((start + p.setup) / len), static_cast<int>((start + units - 1) / len)};
+    const long long first = start + p.setup, last = start + units - 1;
+    // (a division of 64 bits takes ten times as long, and batches of that size are rare)
+    if (((last | len) >> 32) == 0)
+        return {static_cast<int>(static_cast<uint32_t>(first) / static_cast<uint32_t>(len)),
+                static_cast<int>(static_cast<uint32_t>(last) / static_cast<uint32_t>(len))};
+    return {static_cast<int>(first / len), static_cast<int>(last / len)};
 }
 
 // A row's state: its maximum, its sum, and columns 4 j .. 4 j + 3 at o + j step.
