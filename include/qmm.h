@@ -636,6 +636,11 @@ int qmm_decode_attention(const void *q, const void *K, const void *V, const int 
  * and, once per step for all layers,
  *   qmm_tree_accept     follow the target's choices down the tree and move the
  *                       accepted rows to the front of the drafted ones.
+ * For long contexts:
+ *   qmm_prefix_attention  attention of a batch whose sequences share long prefixes
+ *   qmm_scored_attention  attention of a chain that adds up the weight each slot receives
+ *   qmm_kv_evict          bring each sequence back to a budget of slots, by those weights
+ *   qmm_kv_append_axes    append with positions of several axes (images, video)
  *
  * The cache of one layer.  K and V are pools of pages of page_size slots,
  *   K, V   [num_pages, Hkv, page_size, D], dtype elements, the D values of a
@@ -893,7 +898,9 @@ size_t qmm_scored_attention_workspace_bytes(const qmm_kv_cache *cache, int Hq, i
  *   new_lens   device int32 [B]: min(lens[b], keep).  lens is not changed
  *   mass_out, kept and new_lens overlap neither one another nor what the call reads:
  *   QMM_EINVAL.
- * A row whose page is missing on either side is not moved.  Two launches per 64 caches.
+ * A row whose page is missing on either side is not moved.  Slots below keep may be
+ * written, so they belong to their sequence alone (a history that sequences share is read
+ * through qmm_prefix_attention, and stays).  Two launches per 64 caches.
  * Returns QMM_OK, QMM_EINVAL, QMM_ESHAPE, QMM_EALIGN, QMM_ENODEV or QMM_ECUDA. */
 int qmm_kv_evict(const qmm_kv_cache *caches, int n, const float *mass, float *mass_out,
                  int64_t layer_stride, int64_t mass_stride, int keep, int sinks, int recent,

@@ -23,6 +23,12 @@
 // all of a batch is in registers before any of it is stored.  A row moves to a lower slot,
 // so a target is never the source of a later batch, and the batches before have read
 // theirs.
+//
+// 16 sequences of 2500 to 7000 slots to 2048, 12 layers, D = 128, BF16: 381 us, floor 321:
+// the moves 326 us, 2.15 GB at 6.6 TB/s, in pieces of 64 bytes 400; the choice 55, bound
+// by its instructions (59 % of the issue slots), streamed from memory 113.  One sequence,
+// 1151 slots to 1024, 36 layers: 36 us, floor 16: 10 and 20 us, each a few trips to memory
+// in a row.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -472,7 +478,9 @@ int launch_kv_evict(const qmm_kv_cache* caches, int n, int first, const float* m
     p.recent = recent;
     p.first = first;
     p.elem = c.dtype == QMM_CACHE_E4M3 ? 1 : 2;
-    // whole rows, or pieces of at least 64 bytes where the columns would leave SMs idle
+    // whole rows, or pieces of at least 64 bytes where the columns would leave SMs idle (576
+    // columns of 256-byte rows, two pieces: 19.6 us, four 25.8; 3072: whole rows 326, four
+    // pieces 400)
     const int row_lanes = c.D * p.elem / 16;
     const int64_t columns = static_cast<int64_t>(n) * c.Hkv * 2 * c.B;
     p.slices = 1;

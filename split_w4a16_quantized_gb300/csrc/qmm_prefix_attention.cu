@@ -9,10 +9,25 @@
 // sequences, 128 to an item: its K and V are read once for 128 rows and not once for
 // each sequence.  Equal runs of the whole list keep the SMs busy whatever the lengths of
 // the prefixes and of what lies behind them: one launch of the tcgen05 kernel
-// (qmm_tree_attention_tc.cu), for few rows too, whose padding it hides behind the bytes
-// of their K and V.  Items that one run holds leave their state by (token, head), the
-// others by run as in tree attention, and the merge here adds a row's own states and its
-// prefix's, in that order and each in run order.
+// (qmm_tree_attention_tc.cu), for a sequence's few rows too, whose padding it hides behind
+// the bytes of their K and V.  Items that one run holds leave their state by (token, head),
+// the others by run as in tree attention; the merge adds a row's own states and its
+// prefix's, in that order and each in run order.  Which runs hold an item follows from the
+// units before its entry, which the attention launch's first block writes down: its CTAs
+// take all registers, so the merge could not work them out while that launch runs (64
+// sequences: 42 us, each merge block summing the list 46).
+//
+// What bounds it: the chain of a tile in a CTA.  64 sequences behind 8192 tokens: 42 us,
+// floor 20 (HBM); the CTAs end after 27 to 33 us, in tiles of 2000 clocks each of which
+// the softmax takes 1060 and waits 580 for scores, then 7 us of merge, a chain of four
+// trips to L2.  24 sequences of up to 8 tokens behind 16000, E4M3: 65 us, floor 13.5; a tile
+// takes 1950 clocks of a CTA, an SM's two CTAs 1000 (tensor pipe active 30 %).  48 of 4 tokens
+// behind five prefixes, D = 64: 88 us, floor 27; 1580 clocks, with the softmax at work for
+// 1030 of them.  Measured and slower: two groups of 128 rows and one CTA an SM (61, 64,
+// 115 us: items of few rows follow one another without overlap); the sequences' own part
+// and the prefixes as two launches side by side (64, 98, 136: two waves of CTAs, each with
+// its start and end); tiles that count by their rows (50, 80, 107: a few rows' tile
+// takes a CTA as long as a full one).
 #include <algorithm>
 
 #include "qmm.h"
@@ -23,7 +38,9 @@ namespace {
 
 constexpr int kRowShift = 7;
 constexpr int kCtasPerSm = 2;   // of either kernel
-// Query rows per KV head of all tokens up to which the kernel for few rows is faster.
+// Query rows per KV head of all tokens up to which the kernel for 8 rows takes the call.
+// Behind 500, 4000 and 20000 tokens: 16 rows 11.8, 16.1 and 40 us; 24 rows 12.2, 19.5 and
+// 47, the tcgen05 kernel, which reads a prefix once for all of them, 16.1, 19.9 and 32.
 constexpr int kFewRows = 16;
 // A block takes ROWS query rows of a sequence's KV head, a thread a row and every 16th
 // (D = 128; 64: each) group of 4 columns.

@@ -129,8 +129,9 @@ __device__ __forceinline__ void mma16816(float d[4], const uint32_t a[4], uint32
 //     of the columns from the other three.
 // Every wait is bounded (1 s): a wait that runs out sets the status word and
 // the CTA winds down after its copies in flight have landed.
-// kScores: the scores go to p.scores, and the lse of an item's rows to p.lse, as well: one more store of 8 bytes for two of them
-// (32 rows of 1024 to 8192 positions: the kernel 84 us, without 78).
+// kScores: the scores go to p.scores, and the lse of an item's rows to p.lse, as well, and K
+// and V leave L2 first, so that the scores stay for the launch that reads them (32 sequences
+// of 1024 to 8192: the kernel 78 us and that launch 9, without the hint 82 and 13).
 // kShared: with shared prefixes in the list of work; every item leaves a state.
 template <int D, bool kFp8, bool kScores, bool kShared>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
