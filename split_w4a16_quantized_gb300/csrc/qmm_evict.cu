@@ -13,22 +13,24 @@
 // the chosen ones between line and len - recent, instead of all rows behind the first
 // evicted slot.
 //
-// Two kernels.  evict_select, a block a column: the weights come to shared memory once;
-// the threshold is found by its bits, 8 a pass (a weight's bits, ordered as the weights
-// are); then every warp takes a stretch of the slots, and the ranks of evicted slots
-// below the line and of chosen ones behind it pair them.  Longer columns than shared
-// memory holds go through two queues filled in ascending order instead.
+// Two kernels.  evict_select, a block a column, or up to 8 in a cluster where a column is
+// long or columns are few: the weights come to shared memory once; the threshold is found
+// by its bits, 8 a pass (a weight's bits, ordered as the weights are); then every warp takes
+// a stretch of the slots, and the ranks of evicted slots below the line and of chosen ones
+// behind it pair them.  Columns that eight blocks do not hold go through two queues
+// filled in ascending order instead.
 // evict_move, a block a column of K or V (and, where columns are few, a piece of its
-// rows' bytes): moves the rows in ascending order of their targets, a batch at a time:
-// all of a batch is in registers before any of it is stored.  A row moves to a lower slot,
-// so a target is never the source of a later batch, and the batches before have read
-// theirs.
+// rows' bytes, and several blocks in a cluster): moves the rows in ascending order of their
+// targets, a batch at a time: all of a batch is in registers before any of it is stored.
+// A row moves to a lower slot, so a target is never the source of a later batch, and the
+// batches before have read theirs.
 //
-// 16 sequences of 2500 to 7000 slots to 2048, 12 layers, D = 128, BF16: 381 us, floor 321:
+// 16 sequences of 2500 to 7000 slots to 2048, 12 layers, D = 128, BF16: 372 us, floor 321:
 // the moves 326 us, 2.15 GB at 6.6 TB/s, in pieces of 64 bytes 400; the choice 55, bound
 // by its instructions (59 % of the issue slots), streamed from memory 113.  One sequence,
-// 1151 slots to 1024, 36 layers: 36 us, floor 16: 10 and 20 us, each a few trips to memory
-// in a row.
+// 1151 slots to 1024, 36 layers: 34 us, floor 16: 10 and 20 us, each a few trips to memory
+// in a row.  One of 100,000 to 16,384, one layer: 79 us; a block a column, through memory,
+// 484.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -40,15 +42,20 @@
 #include "qmm_paged.cuh"
 #include "qmm_paged_host.h"
 #include "qmm_per_device.h"
+#include "qmm_sm100.cuh"
 
 namespace qmm {
 namespace {
 
+// Neither kernel lets the next start early: blocks that wait take the room of those that
+// work (3072 columns, 377 us; the choice's blocks letting the moves start 457, 288: 34 and 38).
 constexpr int kSelectThreads = 256;
 constexpr int kMoveThreads = 256;
 constexpr int kMoveRows = 8;      // rows a lane group has in flight
-// Slots of a column that shared memory holds: 5 bytes each, two blocks an SM.
+// Slots of a column that a block's shared memory holds, 6 bytes each, two blocks an SM, and
+// most blocks of a column.
 constexpr int kMostSlots = 16384;
+constexpr int kMostBlocks = 8;
 
 struct EvictParams {
     PagedDims d;
@@ -59,7 +66,9 @@ struct EvictParams {
     int n, keep, sinks, recent;
     int first;                  // this launch's first layer
     int elem, slices, lanes;    // bytes a value; pieces of a row, 16 * lanes bytes each
-    int held;                   // slots that the launch's shared memory holds
+    int held;                   // slots that a block's shared memory holds
+    int cluster, spread;        // blocks of a column; whether it takes them all
+    int movers;                 // blocks of a column's piece
     uint8_t* pools[2 * kMaxEvictCaches];   // K and V of each layer
 };
 
@@ -125,23 +134,49 @@ __device__ __forceinline__ int find_digit(const int* hist, int want, int* above,
 
 struct SelectShared {
     alignas(16) int hist[4][256];
+    alignas(16) int total[256];         // of a cluster's blocks
     int red[2][kSelectThreads / 32];
+    int count[3];                       // of this block: ties, evicted below the line, chosen behind
     int digit, above;
     int queue[2][2 * kSelectThreads];   // evicted slots below the line, chosen ones behind
 };
 
-// A column of at most p.held slots: row, its weights; holes, room for the evicted slots
-// below the line (at most half of all); bits, one a slot.
+__device__ __forceinline__ uint32_t cluster_ld32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];\n" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t cluster_ld16(uint32_t addr) {
+    uint16_t v;
+    asm volatile("ld.shared::cluster.u16 %0, [%1];\n" : "=h"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// A column in the shared memory of C blocks of a cluster, `seg` slots each (a multiple of
+// 32, at most p.held; one block: all of them).  row: this block's weights; holes: room for
+// its evicted slots below the line, from its first slot on; bits: one a slot.
+// kMany: C may be over 1.
+template <bool kMany>
 __device__ __forceinline__ void select_held(const EvictParams& p, SelectShared& sh, float* row,
-                                            uint16_t* holes, uint32_t* bits, int len,
-                                            const float* mass, float* mass_out, int* kept) {
+                                            uint16_t* holes, uint32_t* bits, int len, int blocks,
+                                            int me, int seg, const float* mass, float* mass_out,
+                                            int* kept) {
+    const int C = kMany ? blocks : 1;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int keep = p.keep, m0 = p.sinks, m1 = len - p.recent, line = keep - p.recent;
-    const int want = line - m0;
+    const int keep = p.keep, line = keep - p.recent, want = line - p.sinks;
+    const int a0 = min(len, me * seg), a1 = min(len, a0 + seg);   // this block's slots
+    const int m0 = max(p.sinks, a0), m1 = min(len - p.recent, a1);   // of them, those in question
+    row -= a0;   // (by slot)
+    bits -= a0 >> 5;
+    // every block of the column; the order of what they wrote to shared memory
+    auto meet = [&] {
+        if (C > 1) cluster_barrier();
+        else __syncthreads();
+    };
     for (int i = tid; i < 4 * 256; i += kSelectThreads) sh.hist[0][i] = 0;
     // (rows are 16-byte aligned and a multiple of 4 slots long)
 #pragma unroll 4
-    for (int i = 4 * tid; i < len; i += 4 * kSelectThreads)
+    for (int i = a0 + 4 * tid; i < a1; i += 4 * kSelectThreads)
         *reinterpret_cast<float4*>(row + i) = *reinterpret_cast<const float4*>(mass + i);
     __syncthreads();
     uint32_t top = 0;
@@ -177,23 +212,37 @@ __device__ __forceinline__ void select_held(const EvictParams& p, SelectShared& 
                         atomicAdd(&hist[(r >> shift) & 255u], 1);
                 }
             }
-            __syncthreads();
-            top |= static_cast<uint32_t>(find_digit(hist, want, &above, &ties)) << shift;
+            meet();
+            if (C > 1) {
+                int sum = 0;
+                for (int r = 0; r < C; ++r) sum += cluster_ld32(cluster_map(smem_addr(&hist[tid]), r));
+                sh.total[tid] = sum;   // (the blocks met since it was last read)
+                __syncthreads();
+            }
+            top |= static_cast<uint32_t>(find_digit(C > 1 ? sh.total : hist, want, &above, &ties)) << shift;
         }
     }
     // of the slots equal to the threshold, the first `equal` stay
     const int equal = want - above;
-    // a warp's stretch of the slots, 32 at a time
-    const int per = ((len + kSelectThreads - 1) / kSelectThreads) * 32;
-    const int s0 = warp * per, s1 = min(len, s0 + per);
-    // the warp's share of a count, and those of the warps before it
-    auto before_warp = [&](int mine, int* red) {
+    // a warp's stretch of the block's slots, 32 at a time
+    const int per = ((a1 - a0 + kSelectThreads - 1) / kSelectThreads) * 32;
+    const int s0 = a0 + warp * per, s1 = min(a1, s0 + per);
+    // of a count by lanes: those of the warps before this one; the block's to sh.count[at]
+    auto before_warp = [&](int mine, int* red, int at) {
+        mine = __reduce_add_sync(0xffffffffu, mine);
         if (lane == 0) red[warp] = mine;
         __syncthreads();
-        int n = lane < kSelectThreads / 32 && lane < warp ? red[lane] : 0;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-        return n;
+        const int n = lane < kSelectThreads / 32 ? red[lane] : 0;
+        if (warp == 0) {
+            const int all = __reduce_add_sync(0xffffffffu, n);
+            if (lane == 0) sh.count[at] = all;
+        }
+        return __reduce_add_sync(0xffffffffu, lane < warp ? n : 0);
+    };
+    // the same of the blocks before block r
+    auto before_block = [&](int at, int r) {
+        const int n = lane < r ? static_cast<int>(cluster_ld32(cluster_map(smem_addr(&sh.count[at]), lane))) : 0;
+        return __reduce_add_sync(0xffffffffu, n);
     };
     // a weight above the threshold, or equal to it (a threshold below everything: NaN)
     const float least = __uint_as_float(top >> 31 ? top ^ 0x80000000u : ~top);
@@ -203,11 +252,12 @@ __device__ __forceinline__ void select_held(const EvictParams& p, SelectShared& 
     const uint32_t below = (1u << lane) - 1u;
     const int e1 = min(s1, m1), l1 = min(s1, line);   // ends of the stretch's slots in question
     int tie_at = 0;
-    if (want > 0 && !all_ties) {   // (the same for the whole block)
+    if (want > 0 && !all_ties) {   // (the same for all blocks)
         int mine = 0;
         for (int i = s0 + lane; i < e1; i += 32) mine += i >= m0 && equals(row[i]);
-        tie_at = before_warp(__reduce_add_sync(0xffffffffu, mine), sh.red[0]);
-        __syncthreads();
+        tie_at = before_warp(mine, sh.red[0], 0);
+        meet();
+        if (C > 1) tie_at += before_block(0, me);
     }
     int n_holes = 0, n_late = 0;   // of this lane
     for (int i0 = s0; i0 < s1; i0 += 32) {
@@ -226,50 +276,81 @@ __device__ __forceinline__ void select_held(const EvictParams& p, SelectShared& 
         n_holes += i >= m0 && i < l1 && !yes;
         n_late += yes && i >= line;
     }
-    int hole = before_warp(__reduce_add_sync(0xffffffffu, n_holes), sh.red[0]);
-    int late = before_warp(__reduce_add_sync(0xffffffffu, n_late), sh.red[1]);
+    int hole = before_warp(n_holes, sh.red[0], 1), late = before_warp(n_late, sh.red[1], 2);
     for (int i0 = s0; i0 < l1; i0 += 32) {
         const int i = i0 + lane;
         const bool evicted = i >= m0 && i < l1 && !((bits[i0 >> 5] >> lane) & 1u);
         const uint32_t out = __ballot_sync(0xffffffffu, evicted);
         if (evicted) {
-            holes[hole + __popc(out & below)] = static_cast<uint16_t>(i);
+            holes[hole + __popc(out & below)] = static_cast<uint16_t>(i - a0);
         } else if (i < l1) {
             kept[i] = i;
             if (mass_out != mass) mass_out[i] = row[i];
         }
         hole += __popc(out);
     }
-    __syncthreads();
+    meet();
+    int first_hole = 0;   // lane r: of the column's, block r's first
+    if (C > 1) {
+        late += before_block(2, me);
+        int n = lane < C ? static_cast<int>(cluster_ld32(cluster_map(smem_addr(&sh.count[1]), lane))) : 0;
+        int x = n;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        first_hole = x - n;
+    }
     for (int i0 = max(s0, line & ~31); i0 < s1; i0 += 32) {
         const int i = i0 + lane;
         uint32_t in = bits[i0 >> 5];
         if (i0 < line) in &= ~0u << (line - i0);   // (line - i0 < 32; the bits end at m1)
+        const bool yes = (in >> lane) & 1u;
+        const int at = late + __popc(in & below);
         int j = -1;
-        if ((in >> lane) & 1u) j = holes[late + __popc(in & below)];
-        if (i >= m1 && i < s1) j = i - (len - keep);
+        if (C > 1) {
+            int r = 0, from = 0;   // the block that holds evicted slot `at`
+            for (int k = 1; k < C; ++k) {
+                const int f = __shfl_sync(0xffffffffu, first_hole, k);
+                if (f <= at) r = k, from = f;
+            }
+            if (yes) j = r * seg + cluster_ld16(cluster_map(smem_addr(holes + (at - from)), r));
+        } else if (yes) {
+            j = holes[at];
+        }
+        if (i >= len - p.recent && i < s1) j = i - (len - keep);
         if (j >= 0) {
             kept[j] = i;
             mass_out[j] = row[i];
         }
         late += __popc(in);
     }
+    if (C > 1) cluster_barrier();   // nobody reads this block's shared memory any more
 }
 
+template <bool kMany>
 __global__ void __launch_bounds__(kSelectThreads, 4)
     evict_select_kernel(const __grid_constant__ EvictParams p) {
     extern __shared__ __align__(16) float select_row[];
     __shared__ SelectShared sh;
     const int tid = threadIdx.x;
-    const int h = blockIdx.x % p.d.Hkv, layer = p.first + blockIdx.x / p.d.Hkv, b = blockIdx.y;
+    const int cluster = kMany ? p.cluster : 1;
+    const int me = blockIdx.x % cluster, column = blockIdx.x / cluster;
+    const int h = column % p.d.Hkv, layer = p.first + column / p.d.Hkv, b = blockIdx.y;
     pdl_wait();
-    pdl_trigger();
     const int len = cached_tokens(p.d, b), keep = p.keep;
     const int64_t col = static_cast<int64_t>(b) * p.d.Hkv + h;
     const float* mass = p.mass + layer * p.layer_stride + col * p.row_stride;
     float* mass_out = p.mass_out + layer * p.layer_stride + col * p.row_stride;
     int* kept = p.kept + (static_cast<int64_t>(layer) * p.d.B * p.d.Hkv + col) * keep;
-    if (layer == 0 && h == 0 && tid == 0) p.new_lens[b] = min(len, keep);
+    if (layer == 0 && h == 0 && me == 0 && tid == 0) p.new_lens[b] = min(len, keep);
+    // Blocks of the cluster that the column takes (the others leave): all where columns are
+    // few, else as many as hold it.
+    const int C = p.spread ? cluster : min(cluster, (len - 1) / p.held + 1);
+    const int seg = ((len + C - 1) / C + 31) & ~31;
+    const bool fits = len > keep && seg <= p.held;
+    if (me >= (fits ? C : 1)) return;
     if (len <= keep) {
         for (int64_t j = tid; j < keep; j += kSelectThreads) {
             kept[j] = j < len ? static_cast<int>(j) : -1;
@@ -277,10 +358,10 @@ __global__ void __launch_bounds__(kSelectThreads, 4)
         }
         return;
     }
-    if (len <= p.held) {
+    if (fits) {
         uint16_t* holes = reinterpret_cast<uint16_t*>(select_row + p.held);
-        select_held(p, sh, select_row, holes, reinterpret_cast<uint32_t*>(holes + p.held / 2), len,
-                    mass, mass_out, kept);
+        select_held<kMany>(p, sh, select_row, holes, reinterpret_cast<uint32_t*>(holes + (kMany ? p.held : p.held / 2)), len, C,
+                    me, seg, mass, mass_out, kept);
         return;
     }
     const int m0 = p.sinks, m1 = len - p.recent;        // the slots in question
@@ -394,37 +475,43 @@ __global__ void __launch_bounds__(kSelectThreads, 4)
     }
 }
 
+// kMany: the p.movers blocks of a cluster take the parts of a batch in turn (each part in
+// registers at once: pieces of 64 bytes).
+template <bool kMany>
 __global__ void __launch_bounds__(kMoveThreads, 4)
     evict_move_kernel(const __grid_constant__ EvictParams p) {
     __shared__ int64_t src[kMoveThreads], dst[kMoveThreads];   // bytes from the column's start
     __shared__ int red[2][kMoveThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.y;
+    const int movers = kMany ? p.movers : 1;
     int at = blockIdx.x;
+    const int me = at % movers;
+    at /= movers;
     const int slice = at % p.slices;
     at /= p.slices;
     const int kv = at & 1;
     at >>= 1;
     const int h = at % p.d.Hkv, layer = at / p.d.Hkv;   // of this launch
     pdl_wait();
-    pdl_trigger();
     const int len = cached_tokens(p.d, b), keep = p.keep;
-    if (len <= keep) return;
+    if (len <= keep) return;   // (the same for the whole cluster)
     const int* kept = p.kept +
         ((static_cast<int64_t>(p.first + layer) * p.d.B + b) * p.d.Hkv + h) * keep;
     uint8_t* pool = p.pools[2 * layer + kv] + h * p.d.head_stride * p.elem +
                     (slice * p.lanes + tid % p.lanes) * 16;
     const int groups = kMoveThreads / p.lanes, group = tid / p.lanes;
     int odd = 0;
-    int64_t j = p.sinks + tid;
+    const int step = movers * kMoveThreads;
+    int64_t j = p.sinks + static_cast<int64_t>(me) * kMoveThreads + tid;
     int from_slot = j < keep ? kept[j] : -1;
-    for (int64_t j0 = p.sinks; j0 < keep; j0 += kMoveThreads, j += kMoveThreads, odd ^= 1) {
+    for (int64_t j0 = p.sinks; j0 < keep; j0 += step, j += step, odd ^= 1) {
         // the rows that move, in order (a missing page on either side: not moved)
         int64_t from = -1, to = -1;
         if (j < keep && from_slot != j) {
             from = slot_offset(p.d, b, from_slot);
             to = slot_offset(p.d, b, static_cast<int>(j));
         }
-        from_slot = j + kMoveThreads < keep ? kept[j + kMoveThreads] : -1;
+        from_slot = j + step < keep ? kept[j + step] : -1;
         const bool moves = from >= 0 && to >= 0;
         const uint32_t all = __ballot_sync(0xffffffffu, moves);
         if (lane == 0) red[odd][warp] = __popc(all);
@@ -441,14 +528,15 @@ __global__ void __launch_bounds__(kMoveThreads, 4)
             dst[i] = to * p.elem;
         }
         __syncthreads();
-        for (int r0 = group; r0 - group < count; r0 += kMoveRows * groups) {
+        for (int r0 = group; kMany ? r0 == group : r0 - group < count; r0 += kMoveRows * groups) {
             uint4 x[kMoveRows];
 #pragma unroll
             for (int u = 0; u < kMoveRows; ++u) {
                 const int r = r0 + u * groups;
                 if (r < count) x[u] = *reinterpret_cast<const uint4*>(pool + src[r]);
             }
-            __syncthreads();
+            if (kMany) cluster_barrier();
+            else __syncthreads();
 #pragma unroll
             for (int u = 0; u < kMoveRows; ++u) {
                 const int r = r0 + u * groups;
@@ -480,40 +568,71 @@ int launch_kv_evict(const qmm_kv_cache* caches, int n, int first, const float* m
     p.elem = c.dtype == QMM_CACHE_E4M3 ? 1 : 2;
     // whole rows, or pieces of at least 64 bytes where the columns would leave SMs idle (576
     // columns of 256-byte rows, two pieces: 19.6 us, four 25.8; 3072: whole rows 326, four
-    // pieces 400)
+    // pieces 400), and several blocks a piece where that is not enough
     const int row_lanes = c.D * p.elem / 16;
     const int64_t columns = static_cast<int64_t>(n) * c.Hkv * 2 * c.B;
     p.slices = 1;
     while (row_lanes / p.slices > 4 && columns * p.slices < 4 * 152) p.slices *= 2;
     p.lanes = row_lanes / p.slices;
-    p.held = std::min((p.d.cap + 63) / 64 * 64, kMostSlots);
-    const size_t smem = static_cast<size_t>(p.held) * 5 + p.held / 8;
+    p.movers = 1;
+    while (p.lanes == 4 && p.movers < kMostBlocks && columns * p.slices * p.movers < 2 * 152 &&
+           keep / p.movers > kMoveThreads)
+        p.movers *= 2;
+    // Blocks of a column: as many as its slots need, or more where the columns alone would
+    // leave SMs idle.
+    const int64_t all = static_cast<int64_t>(n) * c.Hkv * c.B;
+    const int cap = p.d.cap;
+    p.cluster = 1;
+    while (p.cluster < kMostBlocks && (cap - 1) / p.cluster + 1 > kMostSlots) p.cluster *= 2;
+    while (p.cluster < kMostBlocks && all * p.cluster < 152 && cap / p.cluster > 2048) {
+        p.cluster *= 2;
+        p.spread = 1;
+    }
+    p.held = std::min(((cap - 1) / p.cluster + 64) / 64 * 64, kMostSlots);
+    const size_t smem = static_cast<size_t>(p.held) * (p.cluster > 1 ? 6 : 5) + p.held / 8;
     int device = 0;
     if (cudaGetDevice(&device) != cudaSuccess) return cudaErrorInvalidDevice;
     static PerDevice<bool> opted_in;
     if (!opted_in.get(device, [&] {
-            return cudaFuncSetAttribute(evict_select_kernel,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        kMostSlots * 5 + kMostSlots / 8) == cudaSuccess;
+            auto opt_in = [](auto kernel) {
+                return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            kMostSlots * 6 + kMostSlots / 8) == cudaSuccess;
+            };
+            return opt_in(evict_select_kernel<false>) && opt_in(evict_select_kernel<true>);
         }))
         return cudaErrorInvalidValue;
     for (int i = 0; i < n; ++i) {
         p.pools[2 * i] = static_cast<uint8_t*>(caches[i].K);
         p.pools[2 * i + 1] = static_cast<uint8_t*>(caches[i].V);
     }
-    cudaLaunchConfig_t cfg = {};
-    LaunchAttrs la;
-    apply_pdl(cfg, la);
-    cfg.gridDim = dim3(static_cast<unsigned>(n * c.Hkv), c.B, 1);
-    cfg.blockDim = dim3(kSelectThreads, 1, 1);
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cfg.dynamicSmemBytes = smem;
-    int rc = cudaLaunchKernelEx(&cfg, evict_select_kernel, p);
+    // a launch in clusters of `blocks`
+    auto run = [&](auto kernel, int64_t grid, int threads, size_t dynamic, int blocks) {
+        cudaLaunchConfig_t cfg = {};
+        LaunchAttrs la;
+        apply_pdl(cfg, la);
+        cudaLaunchAttribute attrs[2];
+        if (blocks > 1) {
+            attrs[0].id = cudaLaunchAttributeClusterDimension;
+            attrs[0].val.clusterDim.x = static_cast<unsigned>(blocks);
+            attrs[0].val.clusterDim.y = attrs[0].val.clusterDim.z = 1;
+            if (cfg.numAttrs > 0) attrs[1] = la.attr[0];
+            ++cfg.numAttrs;
+            cfg.attrs = attrs;
+        }
+        cfg.gridDim = dim3(static_cast<unsigned>(grid * blocks), c.B, 1);
+        cfg.blockDim = dim3(threads, 1, 1);
+        cfg.dynamicSmemBytes = dynamic;
+        cfg.stream = static_cast<cudaStream_t>(stream);
+        return static_cast<int>(cudaLaunchKernelEx(&cfg, kernel, p));
+    };
+    const int64_t heads = static_cast<int64_t>(n) * c.Hkv;
+    const int rc = p.cluster > 1
+                       ? run(evict_select_kernel<true>, heads, kSelectThreads, smem, p.cluster)
+                       : run(evict_select_kernel<false>, heads, kSelectThreads, smem, 1);
     if (rc != cudaSuccess) return rc;
-    cfg.gridDim.x = static_cast<unsigned>(n * c.Hkv) * 2 * p.slices;
-    cfg.blockDim = dim3(kMoveThreads, 1, 1);
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, evict_move_kernel, p);
+    return p.movers > 1
+               ? run(evict_move_kernel<true>, heads * 2 * p.slices, kMoveThreads, 0, p.movers)
+               : run(evict_move_kernel<false>, heads * 2 * p.slices, kMoveThreads, 0, 1);
 }
 
 }  // namespace qmm

@@ -582,9 +582,32 @@ def test_evict_missing_pages():
     _check_evict([300, 200], 100, 3, 30, missing=[(0, 1), (0, 4), (0, 9), (0, 18), (1, 3), (1, 12)])
 
 
-def test_evict_long_rows():
-    """Rows that no block's shared memory holds."""
-    _check_evict([100000, 70001, 64000], 40000, 4, 9000, 1, 64, 64, "e4m3", kind="near",
+@pytest.mark.parametrize("lens,keep,sinks,recent,Hkv,kind,in_place", [
+    ([140000, 70001, 131073], 40000, 4, 9000, 1, "near", True),   # beyond eight blocks' memory
+    ([131072, 131071, 100000], 70000, 0, 1, 1, "ties", False),
+    ([16384], 5000, 3, 100, 2, "ties", True), ([16385], 16000, 0, 0, 2, "odd", False),
+    ([40000, 33000, 16000, 300], 8000, 4, 500, 1, "equal", True),
+    ([40000, 33000, 16000, 300], 20000, 4, 0, 1, "odd", True),
+    ([9000], 33, 1, 32, 1, "spread", False), ([9000], 8999, 0, 8999, 1, "spread", True),
+    ([9000], 8990, 17, 70, 3, "rising", True), ([9000], 4500, 17, 70, 3, "falling", False),
+    ([4097], 64, 0, 0, 1, "near", True), ([30000], 10, 0, 10, 1, "ties", False),
+])
+def test_evict_long_rows(lens, keep, sinks, recent, Hkv, kind, in_place):
+    """Columns that several blocks share, and longer ones that go through memory."""
+    _check_evict(lens, keep, sinks, recent, Hkv, 64, 64, "e4m3", kind=kind, in_place=in_place)
+
+
+@pytest.mark.parametrize("dtype,D,layout", [("bf16", 128, "nhd"), ("bf16", 64, "hnd"), ("e4m3", 128, "hnd")])
+def test_evict_rows_in_pieces_by_several_blocks(dtype, D, layout):
+    """Few columns: a row's pieces and the parts of a batch go to different blocks, and rows
+    that move by less than a batch."""
+    _check_evict([9000], 8990, 17, 70, 2, D, 16, dtype, layout, kind="spread", in_place=True)
+    _check_evict([5000, 4000], 3900, 0, 3000, 1, D, 32, dtype, layout, kind="ties")
+
+
+def test_evict_long_tables_of_many_columns():
+    """Tables far longer than what stands in them: a block a column, the others leave."""
+    _check_evict([600, 20000, 33, 16385] * 5, 500, 4, 60, 8, 64, 64, "e4m3", kind="ties",
                  in_place=True)
 
 
