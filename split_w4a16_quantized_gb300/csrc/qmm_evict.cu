@@ -48,7 +48,8 @@ namespace qmm {
 namespace {
 
 // Neither kernel lets the next start early: blocks that wait take the room of those that
-// work (3072 columns, 377 us; the choice's blocks letting the moves start 457, 288: 34 and 38).
+// work (16 sequences of 12 layers 377 us, the choice's blocks letting the moves start 457;
+// one of 36 layers 34 and 38).
 constexpr int kSelectThreads = 256;
 constexpr int kMoveThreads = 256;
 constexpr int kMoveRows = 8;      // rows a lane group has in flight
@@ -567,8 +568,8 @@ int launch_kv_evict(const qmm_kv_cache* caches, int n, int first, const float* m
     p.first = first;
     p.elem = c.dtype == QMM_CACHE_E4M3 ? 1 : 2;
     // whole rows, or pieces of at least 64 bytes where the columns would leave SMs idle (576
-    // columns of 256-byte rows, two pieces: 19.6 us, four 25.8; 3072: whole rows 326, four
-    // pieces 400), and several blocks a piece where that is not enough
+    // columns of 256-byte rows, two pieces: 19.6 us, four 25.8; 16 sequences of 12
+    // layers: whole rows 326, four pieces 400), and several blocks a piece where that is not enough
     const int row_lanes = c.D * p.elem / 16;
     const int64_t columns = static_cast<int64_t>(n) * c.Hkv * 2 * c.B;
     p.slices = 1;

@@ -233,6 +233,69 @@ def test_evict_budgets_beyond_the_table_and_many_sequences():
             assert torch.equal(K.view(torch.int16)[at[0]], old[at[1]])
 
 
+@pytest.mark.parametrize("lens,keep,again,Hkv", [
+    ([40000, 20001], 9000, 3000, 1),     # a column shared by blocks, and its moves
+    ([150000], 20000, 700, 1),           # more than the blocks of a column hold
+    ([5000, 1, 3300], 2500, 600, 2),
+])
+def test_evictions_in_a_row_captured_and_replayed(lens, keep, again, Hkv):
+    """Two evictions, the second of what the first left, in place and in one graph, replayed
+    on a stream of its own with other weights and lengths: what single calls leave."""
+    B, page, D = len(lens), 64, 64
+    width = -(-max(lens) // page)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    K0, V0 = (torch.randint(-2 ** 15, 2 ** 15, (B * width, Hkv, page, D), generator=g, device="cuda",
+                            dtype=torch.int16) for _ in "kv")
+    table = torch.randperm(B * width, generator=g, device="cuda").int().view(B, width)
+
+    def state():
+        K, V = K0.clone(), V0.clone()
+        d_lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+        mid, new = torch.zeros_like(d_lens), torch.zeros_like(d_lens)
+        mass = torch.zeros((B, Hkv, width * page), device="cuda")
+        kept = [torch.zeros((1, B, Hkv, k), dtype=torch.int32, device="cuda") for k in (keep, again)]
+        caches = [Q.kv_caches([Q.kv_cache(K.view(torch.bfloat16), V.view(torch.bfloat16), table, x)])
+                  for x in (d_lens, mid)]
+        return dict(K=K, V=V, lens=d_lens, mid=mid, new=new, mass=mass, kept=kept, caches=caches)
+
+    def load(st, ln, seed):
+        w = torch.Generator(device="cuda").manual_seed(seed)
+        st["lens"].copy_(torch.tensor(ln, dtype=torch.int32))
+        st["mass"].copy_(torch.rand(st["mass"].shape, generator=w, device="cuda"))
+        st["K"].copy_(K0), st["V"].copy_(V0)
+
+    def call(st, i):
+        Q.qmm_kv_evict(st["caches"][i], st["mass"], (keep, again)[i], st["kept"][i],
+                       st[("mid", "new")[i]], sinks=4, recent=200)
+
+    graphed, single = state(), state()
+    load(graphed, lens, 1)
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        call(graphed, 0), call(graphed, 1)
+    for seed, ln in ((2, lens), (3, [x // 2 for x in lens]), (4, [min(x, keep) for x in lens])):
+        load(graphed, ln, seed), load(single, ln, seed)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            graph.replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            call(single, i)
+            torch.cuda.synchronize()
+        for name in ("K", "V", "mid", "new"):
+            assert torch.equal(graphed[name], single[name])
+        assert _same(graphed["mass"], single["mass"])
+        assert all(torch.equal(x, y) for x, y in zip(graphed["kept"], single["kept"]))
+        w = torch.rand(graphed["mass"].shape, generator=torch.Generator(device="cuda").manual_seed(seed),
+                       device="cuda").cpu().numpy()
+        for b, x in enumerate(ln):   # and the first of the two is the formula's
+            for h in range(Hkv):
+                k = _kept(w[b, h], x, keep, 4, 200)
+                assert graphed["kept"][0][0, b, h, :len(k)].tolist() == k.tolist()
+
+
 def test_attention_is_the_same_behind_an_eviction():
     """The order of the kept slots changes nothing but the order of sums: attention over the
     evicted cache is attention over the kept rows."""
