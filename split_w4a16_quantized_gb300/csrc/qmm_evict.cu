@@ -27,7 +27,7 @@
 //
 // 16 sequences of 2500 to 7000 slots to 2048, 12 layers, D = 128, BF16: 372 us, floor 321:
 // the moves 326 us, 2.15 GB at 6.6 TB/s, in pieces of 64 bytes 400; the choice 55, bound
-// by its instructions (59 % of the issue slots), streamed from memory 113.  One sequence,
+// by its instructions (53 % of the issue slots), streamed from memory 113.  One sequence,
 // 1151 slots to 1024, 36 layers: 34 us, floor 16: 10 and 20 us, each a few trips to memory
 // in a row.  One of 100,000 to 16,384, one layer: 79 us; a block a column, through memory,
 // 484.
