@@ -885,7 +885,8 @@ size_t qmm_scored_attention_workspace_bytes(const qmm_kv_cache *cache, int Hq, i
  * Keys keep the rotation that they were stored with: later tokens are appended with
  * positions of their own (qmm_kv_append's default, the cached length, no longer is the
  * token's position).
- *   caches     host, n of them, as in qmm_tree_accept; n may be 1 .. 1024
+ *   caches     host, n of them, as in qmm_tree_accept; n may be 1 .. 1024.  A pool that
+ *              stands twice (or as K and V): QMM_EINVAL
  *   mass       device FP32 [n, B, Hkv, mass_stride], mass_stride at least max_pages *
  *              page_size: the weight of each slot (qmm_scored_attention).  Layers are
  *              layer_stride values apart (at least B * Hkv * mass_stride; not looked at

@@ -7,6 +7,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <functional>
 #include <mutex>
 #include <queue>
 #include <vector>
@@ -1327,8 +1328,9 @@ static bool overlap(const Words& a, const Words& b) {
 }
 
 // check_cache for the n caches of one call, which differ in their pools alone.
+constexpr int kMaxCaches = 1024;
 static int check_caches(const qmm_kv_cache* caches, int n) {
-    if (!caches || n < 1 || n > 1024) return QMM_EINVAL;
+    if (!caches || n < 1 || n > kMaxCaches) return QMM_EINVAL;
     int rc = QMM_OK;
     for (int i = 0; i < n; ++i) {
         const int r = check_cache(&caches[i]);
@@ -1381,7 +1383,8 @@ int qmm_tree_accept(const qmm_kv_cache* caches, int n, const int* tokens, const 
 static int check_mass(const qmm_kv_cache& c, const float* mass, int64_t mass_stride) {
     if (!mass) return QMM_EINVAL;
     if (mass_stride < static_cast<int64_t>(c.max_pages) * c.page_size || mass_stride % 4 ||
-        mass_stride >= int64_t{1} << 38)
+        mass_stride >= int64_t{1} << 38 ||
+        mass_stride > (int64_t{1} << 56) / (static_cast<int64_t>(c.B) * c.Hkv))   // (no memory)
         return QMM_ESHAPE;
     return aligned(mass, 16) ? QMM_OK : QMM_EALIGN;
 }
@@ -1449,6 +1452,11 @@ int qmm_kv_evict(const qmm_kv_cache* caches, int n, const float* mass, float* ma
         for (const Words* other = out; other != &o; ++other)
             if (overlap(o, *other)) return QMM_EINVAL;
     }
+    // each pool once: two blocks would move its rows at the same time
+    const void* pools[2 * kMaxCaches];
+    for (int i = 0; i < n; ++i) pools[2 * i] = caches[i].K, pools[2 * i + 1] = caches[i].V;
+    std::sort(pools, pools + 2 * n, std::less<const void*>());
+    if (std::adjacent_find(pools, pools + 2 * n) != pools + 2 * n) return QMM_EINVAL;
     rc = device_ready(nullptr);
     for (int i = 0; i < n && rc == QMM_OK; i += qmm::kMaxEvictCaches)
         rc = launched(qmm::launch_kv_evict(caches + i, std::min(n - i, qmm::kMaxEvictCaches), i,

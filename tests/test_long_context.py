@@ -114,6 +114,28 @@ def test_evict_refusals(kw, code):
     assert _evict([_cache(lens=5 << 20, table=6 << 20)] * 2, **kw) == code
 
 
+@pytest.mark.parametrize("pools", [
+    ((1, 2), (1, 2)), ((1, 2), (1, 3)), ((1, 2), (3, 2)), ((1, 2), (3, 1)), ((1, 1),),
+    ((1, 2), (3, 4), (5, 5)), ((1, 2), (3, 4), (5, 6), (7, 8), (6, 9))])
+def test_evict_refuses_a_pool_that_stands_twice(pools):
+    """Two blocks would move its rows at once."""
+    c = [_cache(lens=5 << 20, table=6 << 20, K=k << 34, V=v << 34) for k, v in pools]
+    kw = dict(mass=1 << 40, out=1 << 40, ls=4 * 8 * 320)
+    assert _evict(c, **kw) == Q.QMM_EINVAL
+    for i, x in enumerate(c):
+        x.K, x.V = (2 * i + 1) << 34, (2 * i + 2) << 34
+    if not torch.cuda.is_available():   # (made-up pointers: never with a device to launch on)
+        assert _evict(c, **kw) == Q.QMM_ENODEV
+
+
+def test_weights_beyond_any_memory_are_refused():
+    """B Hkv mass_stride of 2^66 values: no 64-bit sum of them is formed."""
+    c = _cache(B=32768, Hkv=32768, lens=5 << 20, table=6 << 20, head_stride=16 * 128,
+               page_stride=32768 * 16 * 128, K=1 << 34, V=2 << 34)
+    assert _evict([c], mass=1 << 40, out=1 << 40, ls=0, ms=1 << 36) == Q.QMM_ESHAPE
+    assert _scored(c, Hq=32768, qs=32768 * 128, N=32768, T=1, ms=1 << 36) == Q.QMM_ESHAPE
+
+
 # what the call of two layers reads and writes, in 32-bit values
 READ = dict(mass=(1 << 28, 2 * 4 * 8 * 320), lens=(2 << 28, 4), table=(3 << 28, 4 * 20))
 WRITTEN = dict(out=(4 << 28, 2 * 4 * 8 * 320), kept=(5 << 28, 2 * 4 * 8 * 16), new=(6 << 28, 4))
@@ -133,8 +155,9 @@ def test_evict_refuses_outputs_over_what_it_reads(out, other):
         if p["out"] == p["mass"]:
             continue
         assert place < at + 4 * n and at < place + 4 * WRITTEN[out][1]
-        c = _cache(lens=p["lens"], table=p["table"], K=1 << 34, V=2 << 34)
-        assert _evict([c, c], mass=p["mass"], out=p["out"], kept=p["kept"],
+        c = [_cache(lens=p["lens"], table=p["table"], K=(1 + 2 * i) << 34, V=(2 + 2 * i) << 34)
+             for i in range(2)]
+        assert _evict(c, mass=p["mass"], out=p["out"], kept=p["kept"],
                       new=p["new"]) == Q.QMM_EINVAL
 
 
