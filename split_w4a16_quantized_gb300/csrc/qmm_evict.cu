@@ -346,8 +346,8 @@ __global__ void __launch_bounds__(kSelectThreads, 4)
     float* mass_out = p.mass_out + layer * p.layer_stride + col * p.row_stride;
     int* kept = p.kept + (static_cast<int64_t>(layer) * p.d.B * p.d.Hkv + col) * keep;
     if (layer == 0 && h == 0 && me == 0 && tid == 0) p.new_lens[b] = min(len, keep);
-    // Blocks of the cluster that the column takes (the others leave): all where columns are
-    // few, else as many as hold it.
+    // Blocks of the cluster that the column takes (the others leave): all where they run at
+    // once, else as many as hold it.
     const int C = p.spread ? cluster : min(cluster, (len - 1) / p.held + 1);
     const int seg = ((len + C - 1) / C + 31) & ~31;
     const bool fits = len > keep && seg <= p.held;
@@ -589,6 +589,10 @@ int launch_kv_evict(const qmm_kv_cache* caches, int n, int first, const float* m
         p.cluster *= 2;
         p.spread = 1;
     }
+    // A long table's columns take their whole cluster, however short, where all blocks run at
+    // once (two an SM; 8 columns of 14000 slots in a table of 131,072: 20 us, as many blocks as
+    // hold them 32; 32 columns 45 and 63; 2000 slots 15.1 and 14.0).
+    if (p.cluster > 1 && all * p.cluster <= 2 * 152) p.spread = 1;
     p.held = std::min(((cap - 1) / p.cluster + 64) / 64 * 64, kMostSlots);
     const size_t smem = static_cast<size_t>(p.held) * (p.cluster > 1 ? 6 : 5) + p.held / 8;
     int device = 0;

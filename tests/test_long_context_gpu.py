@@ -605,6 +605,14 @@ def test_evict_rows_in_pieces_by_several_blocks(dtype, D, layout):
     _check_evict([5000, 4000], 3900, 0, 3000, 1, D, 32, dtype, layout, kind="ties")
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_short_columns_of_a_long_table(in_place):
+    """Columns in fewer slots than their cluster has blocks, beside one that needs them all."""
+    _check_evict([40000, 3, 0, 33, 1100], 30, 2, 11, 1, kind="ties", in_place=in_place)
+    _check_evict([1, 65, 140000, 31, 32], 31, 31, 0, 1, page=64, in_place=in_place)
+    _check_evict([32, 64, 20000, 96], 1, 0, 0, 2, page=32, kind="odd", in_place=in_place)
+
+
 def test_evict_long_tables_of_many_columns():
     """Tables far longer than what stands in them: a block a column, the others leave."""
     _check_evict([600, 20000, 33, 16385] * 5, 500, 4, 60, 8, 64, 64, "e4m3", kind="ties",
