@@ -797,8 +797,7 @@ typedef struct {
  * those count the prefix too).  A prefix's keys and values are read once for 128 query
  * rows per KV head, not once for each of its sequences.
  * The arguments, checks and results are qmm_tree_attention's, but:
- *   - the weights are rounded as for more than 8 query rows per KV head, unless there are
- *     at most 8 of a sequence (T Hq / Hkv) and 16 of all (N Hq / Hkv);
+ *   - a BF16 cache's weights are rounded to two BF16 terms, whatever the number of rows;
  *   - cu has to ascend over a prefix's sequences for all of them to see it;
  *   - the workspace is qmm_prefix_attention_workspace_bytes, which grows with N;
  *   - QMM_EINVAL also for a NULL prefix or array, G or max_pages below 1; QMM_ESHAPE for

@@ -40,6 +40,14 @@
 // RMS, with the second term 0.0017), and the second term would double the P V
 // products: 16 sequences of 64 tokens 166 us instead of 128, 64 ragged ones of up to
 // 5 tokens, D = 64, 142 instead of 118, 8 of 8 tokens 25.5 instead of 24.1.
+// With shared prefixes (kShared) a BF16 cache's P keeps both terms: most of those calls
+// are decode, a sequence's few rows are here for its neighbours' sake alone, and the
+// tensor cores have room (64 sequences behind 8192 tokens: 46 us, with one term 42; 48 of
+// 4 tokens behind five prefixes, D = 64: 105 and 88; error against 64 bits 0.00165 and
+// 0.00226 of the outputs' RMS).  The second term takes the half of S that the first
+// leaves.  An E4M3 cache's P is one F16 term there too: a second would take 73 us instead
+// of 65 (24 sequences of up to 8 tokens behind 16000) for an error of 0.001665 instead of
+// 0.001676, both of them the rounding of the output.
 //
 // What bounds it (152 SMs; a tile is 64 positions, D = 128; clocks a tile are those
 // that 8000 more positions add to a history of 4000, 19 sequences of 8 KV heads).
@@ -141,6 +149,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
+// What a pair of weights leaves of its first BF16 terms (`w`), as a pair of second ones.
+__device__ __forceinline__ uint32_t rest_of(float a, float b, uint32_t w) {
+    return pack_bf16x2(a - __uint_as_float(w << 16), b - __uint_as_float(w & 0xffff0000u));
+}
+
 __device__ __forceinline__ uint64_t low_bits(int n) {
     return n <= 0 ? 0ull : (n >= 64 ? ~0ull : (1ull << n) - 1ull);
 }
@@ -168,13 +181,15 @@ struct Layout {
     int q_rows, conv_slots, k_slots, v_slots;
 };
 
-// kShared: with shared prefixes in the list of work; every item leaves a state.
+// kShared: with shared prefixes in the list of work; every item leaves a state, and a BF16
+// cache's P is two terms.
 template <int D, bool kFp8, int kGroups, bool kShared>
 __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGroups>::CTAS_PER_SM)
     tree_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap, const __grid_constant__ TreeParams p,
                    const Layout lay) {
     using C = Tc<D, kFp8, kGroups>;
+    constexpr bool kTwo = kShared && !kFp8;   // P as two terms
     extern __shared__ uint8_t tree_tc_smem_raw[];
     uint8_t* base_s = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(tree_tc_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -342,14 +357,15 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                 // copy warp's page bits: hand that on
                 mbar_arrive(&sm.sfull[s]);
             };
-            // O of group g (+)= P of its buffer times the V tile at vc
+            // O of group g (+)= P of its buffer times the V tile at vc (kTwo: the first
+            // terms' columns, then the second ones')
             auto pv = [&](int odd, int g, bool first) {
                 const int s = 2 * g + odd;
                 const uint64_t b = v_desc + static_cast<uint32_t>(vc.slot * VSLOT >> 4);
 #pragma unroll
-                for (int k = 0; k < kTile / 16; ++k)
+                for (int k = 0; k < (kTwo ? 2 : 1) * kTile / 16; ++k)
                     umma_bf16_tmem_a(tmem + C::COL_O + D * g, tmem + kTile * s + 8 * k,
-                                     b + ((k * 2048) >> 4), ipv, !first || k > 0);
+                                     b + ((k % (kTile / 16) * 2048) >> 4), ipv, !first || k > 0);
             };
             // Two groups: one thread waits and issues, because a vote or an issuing
             // block of its own after each wait costs 200 clocks, in which the tensor
@@ -672,18 +688,25 @@ __global__ void __launch_bounds__(Tc<D, kFp8, kGroups>::THREADS, Tc<D, kFp8, kGr
                 const float sub = finite_max(ref) - (kFp8 ? kTcLift : 0.f);
                 const F2 q2 = f2(qs, qs), s2 = f2(-sub, -sub);
                 F2 part[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+                constexpr int kPart = kTwo ? 16 : 32;   // (with two terms 32 spill)
 #pragma unroll
-                for (int h = 0; h < kTile; h += 32) {
-                    uint32_t pw[16];
+                for (int h = 0; h < kTile; h += kPart) {
+                    uint32_t pw[kPart / 2], pl[kPart / 2];
 #pragma unroll
-                    for (int c = 0; c < 32; c += 2) {
+                    for (int c = 0; c < kPart; c += 2) {
                         const float2 y = split(fma2(
                             f2(__uint_as_float(v[h + c]), __uint_as_float(v[h + c + 1])), q2, s2));
                         const float a = fast_exp2(y.x), b = fast_exp2(y.y);
                         part[c / 2 & 1] = add2(part[c / 2 & 1], f2(a, b));
                         pw[c / 2] = kFp8 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
+                        if (kTwo) pl[c / 2] = rest_of(a, b, pw[c / 2]);
                     }
-                    tmem_st16(tS + h / 2, pw);
+                    if constexpr (kTwo) {
+                        tmem_st8(tS + h / 2, pw);
+                        tmem_st8(tS + kTile / 2 + h / 2, pl);
+                    } else {
+                        tmem_st16(tS + h / 2, pw);
+                    }
                 }
                 const float2 more = split(add2(part[0], part[1]));
                 sum += more.x + more.y;

@@ -1,0 +1,46 @@
+"""The paged cache's long-context calls on a GB300: what their interface promises of bits,
+of slots out of sight and of device data out of range."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from test_long_context_gpu import Shared, _prefix64, _run_prefix, _same, _within
+from test_paged_gpu import BF16_HALF, F32_HALF, _tree
+from split_w4a16_quantized_gb300 import qmm as Q
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _status():
+    yield
+    torch.cuda.synchronize()
+    assert Q.qmm_kernel_status(clear=True) == 0
+
+
+# ---- shared prefixes -----------------------------------------------------------------
+
+@pytest.mark.parametrize("plens,first,lens,n,Hq,Hkv,D,page,layout,kind", [
+    ([40], [0, 3], [5, 9, 0], [1] * 3, 8, 2, 128, 16, "hnd", "chain"),           # 12 rows
+    ([40], [0, 12], list(range(12)), [1] * 12, 8, 2, 128, 16, "hnd", "chain"),   # 48
+    ([50], [0, 40], [i % 9 for i in range(40)], [1] * 40, 16, 4, 64, 16, "nhd", "chain"),
+    ([30, 61], [0, 5, 9], [5, 7, 0, 6, 3, 3, 4, 9, 1], [8] * 9, 16, 4, 128, 16, "nhd", "tree"),
+    ([64], [1, 3], [5, 3, 0], [7, 9, 5], 8, 2, 64, 32, "hnd", "tree"),
+], ids=["12", "48", "160", "groups", "ragged"])
+def test_prefix_bf16_weights_have_two_terms(plens, first, lens, n, Hq, Hkv, D, page, layout, kind):
+    """A BF16 cache's weights are two BF16 terms for any number of rows: the first is off by
+    at most 2^-8 of the weight, the second by 2^-8 of that.  Beside it, as wholes of 2^-23
+    (the tensor cores may cut where a sum would be rounded): scores of D products, in the
+    weight and in their sum; sums over the positions; exp2 (2 ulp) and the divisions."""
+    sh = Shared(plens, first, lens, n, Hkv, D, page, "bf16", layout)
+    rng = np.random.default_rng(7)
+    q = torch.from_numpy(0.1 * rng.standard_normal((sh.N, Hq, D))).bfloat16()
+    parents = np.concatenate([_tree(rng, m, kind) for m in n]).astype(np.int32)
+    got = _run_prefix(sh, q.cuda(), None if kind == "chain" else parents)
+    O, A, S = _prefix64(sh, q, parents, 1 / math.sqrt(D))
+    positions = max(plens) + max(lens) + max(n)
+    lim = BF16_HALF * O.abs() + A * (BF16_HALF ** 2 + 2 * F32_HALF * (
+        2 * (D + 2) * S[..., None] + positions + 8)) + 1e-30
+    _within(got.cpu(), O, lim)
