@@ -216,8 +216,13 @@ __global__ void __launch_bounds__(kFinishThreads, 3)
             for (int r = 0; r < ROWS; ++r) {
                 if (r >= rows) break;
                 const float lse = lse_s[r];
-                w[0] += fast_exp2(v[r].x - lse), w[1] += fast_exp2(v[r].y - lse);
-                w[2] += fast_exp2(v[r].z - lse), w[3] += fast_exp2(v[r].w - lse);
+                if (lse == lse) {
+                    w[0] += fast_exp2(v[r].x - lse), w[1] += fast_exp2(v[r].y - lse);
+                    w[2] += fast_exp2(v[r].z - lse), w[3] += fast_exp2(v[r].w - lse);
+                } else {   // NaN for what the row sees (out of its sight: -inf)
+                    w[0] += v[r].x == -INFINITY ? 0.f : lse, w[1] += v[r].y == -INFINITY ? 0.f : lse;
+                    w[2] += v[r].z == -INFINITY ? 0.f : lse, w[3] += v[r].w == -INFINITY ? 0.f : lse;
+                }
             }
             if (p.decay != 0.f) {
                 if (pos < s.len) w[0] = fmaf(p.decay, old.x, w[0]);

@@ -102,6 +102,13 @@ __device__ __forceinline__ void mma16816(float d[4], const uint32_t a[4], uint32
         mma_bf16_16816(d, a, b0, b1);
 }
 
+// -infinity as the lowest finite number, everything else (NaN too) as it is.
+__device__ __forceinline__ float above_minus_infinity(float x) {
+    float y;
+    asm("max.NaN.f32 %0, %1, 0fFF7FFFFF;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // ---- the kernel -------------------------------------------------------------
 //
 // Up to 8 query rows per KV head (plain decode): half of an m16n8k16 fragment.
@@ -129,7 +136,8 @@ __device__ __forceinline__ void mma16816(float d[4], const uint32_t a[4], uint32
 //     of the columns from the other three.
 // Every wait is bounded (1 s): a wait that runs out sets the status word and
 // the CTA winds down after its copies in flight have landed.
-// kScores: the scores go to p.scores, and the lse of an item's rows to p.lse, as well, and K
+// kScores: the scores go to p.scores (-inf where the row does not see the slot, and nowhere
+// else), and the lse of an item's rows to p.lse, as well, and K
 // and V leave L2 first, so that the scores stay for the launch that reads them (32 sequences
 // of 1024 to 8192: the kernel 78 us and that launch 9, without the hint 82 and 13).
 // kShared: with shared prefixes in the list of work; every item leaves a state.
@@ -345,6 +353,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     float v[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v[e] = sc[e >> 1][e & 1] * qs;
+                    float held[4];   // kScores: what the row sees, -inf out of its sight alone
+                    if (kScores)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) held[e] = above_minus_infinity(v[e]);
                     if (!plain) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -354,14 +366,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                             if (see && j >= 0)
                                 see = p.parents ? (sm.anc[min(gr, rows - 1)][j >> 5] >> (j & 31)) & 1u
                                                 : j <= node;
-                            if (!see) v[e] = -INFINITY;
+                            if (!see) {
+                                v[e] = -INFINITY;
+                                if (kScores) held[e] = -INFINITY;
+                            }
                         }
                     }
                     if (kScores && on) {
 #pragma unroll
                         for (int e = 0; e < 4; e += 2)
                             *reinterpret_cast<float2*>(score_row + pos0 + 4 * e + 2 * tq) =
-                                make_float2(v[e], v[e + 1]);
+                                make_float2(held[e], held[e + 1]);
                     }
                     float mx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));

@@ -6,8 +6,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_long_context_gpu import Shared, _prefix64, _run_prefix, _same, _within
-from test_paged_gpu import BF16_HALF, F32_HALF, _tree
+from test_long_context_gpu import Shared, _prefix64, _run_prefix, _run_scored, _same, _within
+from test_paged_gpu import BF16_HALF, F32_HALF, Problem, _tree
 from split_w4a16_quantized_gb300 import qmm as Q
 
 pytestmark = pytest.mark.gpu
@@ -44,3 +44,38 @@ def test_prefix_bf16_weights_have_two_terms(plens, first, lens, n, Hq, Hkv, D, p
     lim = BF16_HALF * O.abs() + A * (BF16_HALF ** 2 + 2 * F32_HALF * (
         2 * (D + 2) * S[..., None] + positions + 8)) + 1e-30
     _within(got.cpu(), O, lim)
+
+
+# ---- weights by slot -----------------------------------------------------------------
+
+@pytest.mark.parametrize("what", ["nan in q", "inf in q", "nan in k"])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 2, 24])
+def test_scored_not_numbers_stay_in_sight(n, dtype, what):
+    """A row that is not a number leaves none in slots out of its sight, those of later
+    tokens and those without a page, and all others of its sequence's head are; with few
+    rows and with many."""
+    pb = Problem([130, 5], [n, n], 2, 128, 16, dtype)
+    pb.table[0, 2] = -1
+    pb.bind()
+    q = torch.randn((pb.N, 8, 128), device="cuda").bfloat16()
+    old = torch.rand((2, 2, pb.width * 16), device="cuda")
+    clean, mass = old.clone(), old.clone()
+    _run_scored(pb, q, clean, 0.5)
+    sees = torch.ones(130 + n, dtype=torch.bool)          # of slots, by the rows in question
+    if what == "nan in k":
+        # of the last token, which alone sees its own slot
+        page, at = int(pb.table[0, (129 + n) // 16]), (129 + n) % 16
+        pb.K.view(torch.uint8 if dtype == "e4m3" else torch.int16)[page, 0, at, 7] = \
+            0x7f if dtype == "e4m3" else 0x7fc0
+    else:
+        q[0, 1, 5] = float(what[:3])
+        sees[131:] = False
+    _run_scored(pb, q, mass, 0.5)
+    sees[32:48] = False
+    assert _same(mass[1], clean[1]) and _same(mass[0, 1], clean[0, 1])
+    got, want = mass[0, 0].cpu(), clean[0, 0].cpu()
+    assert torch.isnan(got[:130 + n][sees]).all()
+    assert _same(got[:130 + n][~sees], want[:130 + n][~sees])
+    assert _same(got[130 + n:], want[130 + n:])
+    assert _same(want[32:48], 0.5 * old[0, 0, 32:48].cpu())
