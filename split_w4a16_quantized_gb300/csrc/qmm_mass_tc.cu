@@ -184,7 +184,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // threads wait first, and only then let others start), so all of this kernel's work up to
     // the scores may run beside the merge, from L2: only the warps that read lse and that
     // touch the weights wait.  Tensor memory: the attention kernel's CTAs all have theirs by
-    // then, and the merge needs none.
+    // then, and the merge needs none.  The dependency wait has no limit, and no wait that has one
+    // starts ahead of it where it needs what comes behind: the limit times this launch alone.
     if (warp == 1) {
         tmem_alloc(&sm.tmem, 2 * kBlock);
         tmem_relinquish();
@@ -216,6 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 PageWalk<kTile, true> walk;
                 walk.start(p, x, lane);
                 for (int t = x.t0; ok && t < x.t1; ++t, ++it) {
+                    if (it == mp.slots) pdl_wait();   // (the first slot to wait for)
                     const uint32_t have = walk.tile(p, t, lane, sm.pages[it & 1]);
                     if (elect_one() && wait_one(&sm.kempty[kc.slot], kc.phase ^ 1)) {
                         sm.have[it % kHave] = static_cast<int>(have);
@@ -243,6 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int nb = 0;            // blocks
             uint32_t used = 0, phase = 0;   // of each buffer: written before; its next wait
             bool go = true;
+            pdl_wait();
             while (go && next_tiles(p, run, &x)) {
                 const int rows = x.s.n * p.QG;
                 for (int rb = 0; go && rb < blocks_of(x.s); ++rb, ++nb) {
