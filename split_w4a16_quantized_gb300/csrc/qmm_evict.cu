@@ -38,6 +38,7 @@
 
 #include "qmm.h"
 #include "qmm_device.cuh"
+#include "qmm_evict_split.h"
 #include "qmm_internal.h"
 #include "qmm_paged.cuh"
 #include "qmm_paged_host.h"
@@ -51,12 +52,8 @@ namespace {
 // work (16 sequences of 12 layers 377 us, the choice's blocks letting the moves start 457;
 // one of 36 layers 34 and 38).
 constexpr int kSelectThreads = 256;
-constexpr int kMoveThreads = 256;
+constexpr int kMoveThreads = kEvictMoveThreads;
 constexpr int kMoveRows = 8;      // rows a lane group has in flight
-// Slots of a column that a block's shared memory holds, 6 bytes each, two blocks an SM, and
-// most blocks of a column.
-constexpr int kMostSlots = 16384;
-constexpr int kMostBlocks = 8;
 
 struct EvictParams {
     PagedDims d;
@@ -551,7 +548,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4)
 
 int launch_kv_evict(const qmm_kv_cache* caches, int n, int first, const float* mass,
                     float* mass_out, int64_t layer_stride, int64_t row_stride, int keep, int sinks,
-                    int recent, int* kept, int* new_lens, void* stream) {
+                    int recent, int* kept, int* new_lens, int num_sms, void* stream) {
     const qmm_kv_cache& c = caches[0];
     EvictParams p = {};
     p.d = paged_dims(c);
@@ -567,33 +564,14 @@ int launch_kv_evict(const qmm_kv_cache* caches, int n, int first, const float* m
     p.recent = recent;
     p.first = first;
     p.elem = c.dtype == QMM_CACHE_E4M3 ? 1 : 2;
-    // whole rows, or pieces of at least 64 bytes where the columns would leave SMs idle (576
-    // columns of 256-byte rows, two pieces: 19.6 us, four 25.8; 16 sequences of 12
-    // layers: whole rows 326, four pieces 400), and several blocks a piece where that is not enough
-    const int row_lanes = c.D * p.elem / 16;
-    const int64_t columns = static_cast<int64_t>(n) * c.Hkv * 2 * c.B;
-    p.slices = 1;
-    while (row_lanes / p.slices > 4 && columns * p.slices < 4 * 152) p.slices *= 2;
-    p.lanes = row_lanes / p.slices;
-    p.movers = 1;
-    while (p.lanes == 4 && p.movers < kMostBlocks && columns * p.slices * p.movers < 2 * 152 &&
-           keep / p.movers > kMoveThreads)
-        p.movers *= 2;
-    // Blocks of a column: as many as its slots need, or more where the columns alone would
-    // leave SMs idle.
-    const int64_t all = static_cast<int64_t>(n) * c.Hkv * c.B;
-    const int cap = p.d.cap;
-    p.cluster = 1;
-    while (p.cluster < kMostBlocks && (cap - 1) / p.cluster + 1 > kMostSlots) p.cluster *= 2;
-    while (p.cluster < kMostBlocks && all * p.cluster < 152 && cap / p.cluster > 2048) {
-        p.cluster *= 2;
-        p.spread = 1;
-    }
-    // A long table's columns take their whole cluster, however short, where all blocks run at
-    // once (two an SM; 8 columns of 14000 slots in a table of 131,072: 20 us, as many blocks as
-    // hold them 32; 32 columns 45 and 63; 2000 slots 15.1 and 14.0).
-    if (p.cluster > 1 && all * p.cluster <= 2 * 152) p.spread = 1;
-    p.held = std::min(((cap - 1) / p.cluster + 64) / 64 * 64, kMostSlots);
+    const EvictSplit split =
+        evict_split(static_cast<int64_t>(n) * c.Hkv * c.B, p.d.cap, keep, c.D * p.elem / 16, num_sms);
+    p.slices = split.slices;
+    p.lanes = split.lanes;
+    p.movers = split.movers;
+    p.cluster = split.cluster;
+    p.spread = split.spread;
+    p.held = split.held;
     const size_t smem = static_cast<size_t>(p.held) * (p.cluster > 1 ? 6 : 5) + p.held / 8;
     int device = 0;
     if (cudaGetDevice(&device) != cudaSuccess) return cudaErrorInvalidDevice;
@@ -601,7 +579,7 @@ int launch_kv_evict(const qmm_kv_cache* caches, int n, int first, const float* m
     if (!opted_in.get(device, [&] {
             auto opt_in = [](auto kernel) {
                 return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                            kMostSlots * 6 + kMostSlots / 8) == cudaSuccess;
+                                            kEvictSlots * 6 + kEvictSlots / 8) == cudaSuccess;
             };
             return opt_in(evict_select_kernel<false>) && opt_in(evict_select_kernel<true>);
         }))

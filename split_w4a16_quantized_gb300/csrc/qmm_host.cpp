@@ -1457,11 +1457,12 @@ int qmm_kv_evict(const qmm_kv_cache* caches, int n, const float* mass, float* ma
     for (int i = 0; i < n; ++i) pools[2 * i] = caches[i].K, pools[2 * i + 1] = caches[i].V;
     std::sort(pools, pools + 2 * n, std::less<const void*>());
     if (std::adjacent_find(pools, pools + 2 * n) != pools + 2 * n) return QMM_EINVAL;
-    rc = device_ready(nullptr);
+    int sms = 0;
+    rc = device_ready(&sms);
     for (int i = 0; i < n && rc == QMM_OK; i += qmm::kMaxEvictCaches)
         rc = launched(qmm::launch_kv_evict(caches + i, std::min(n - i, qmm::kMaxEvictCaches), i,
                                            mass, mass_out, layer_stride, mass_stride, keep, sinks,
-                                           recent, kept, new_lens, stream));
+                                           recent, kept, new_lens, sms, stream));
     return rc;
 }
 

@@ -26,7 +26,7 @@ int launch_tree_accept(const qmm_kv_cache* caches, int n, const int* tokens, con
 constexpr int kMaxEvictCaches = 64;
 int launch_kv_evict(const qmm_kv_cache* caches, int n, int first, const float* mass,
                     float* mass_out, int64_t layer_stride, int64_t row_stride, int keep, int sinks,
-                    int recent, int* kept, int* new_lens, void* stream);
+                    int recent, int* kept, int* new_lens, int num_sms, void* stream);
 // Tree attention (qmm_tree_attention.cu).  lse: nullable, [B][T][Hq], log2 of each row's
 // sum of 2^(score log2(e)).
 size_t tree_attention_workspace(int D, int rows, int num_sms);
