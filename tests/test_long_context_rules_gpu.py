@@ -6,8 +6,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_long_context_gpu import Shared, _prefix64, _run_prefix, _run_scored, _same, _within
-from test_paged_gpu import BF16_HALF, F32_HALF, Problem, _tree
+from test_long_context_gpu import Shared, _o_limit, _prefix64, _run_prefix, _run_scored, _same, _within
+from test_paged_gpu import BF16_HALF, F32_HALF, Problem, _dev, _tree
 from split_w4a16_quantized_gb300 import qmm as Q
 
 pytestmark = pytest.mark.gpu
@@ -79,3 +79,66 @@ def test_scored_not_numbers_stay_in_sight(n, dtype, what):
     assert _same(got[:130 + n][~sees], want[:130 + n][~sees])
     assert _same(got[130 + n:], want[130 + n:])
     assert _same(want[32:48], 0.5 * old[0, 0, 32:48].cpu())
+
+
+def _seen(pools, table, slots, page):
+    """K and V of a table's first slots in 64 bits, and which of them have pages."""
+    pages = pools[0].shape[0]
+    ids = torch.tensor([int(table[s // page]) for s in range(slots)], dtype=torch.int64)
+    there = (ids >= 0) & (ids < pages)
+    at = torch.arange(slots) % page
+    return [p[ids.clamp(0, pages - 1), :, at].double() for p in pools], there
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("Hq", [2, 8])      # 12 and 48 rows per KV head
+@pytest.mark.parametrize("cu", [None, [0, 99, 3, 12, 12], [-5, 4, 8, 2 ** 31 - 1, 0],
+                                [12, 8, 4, 0, 0], [0, 2, 5, 9, 2 ** 31 - 1]])
+def test_prefix_of_clamped_device_values(cu, Hq, dtype):
+    """first, lens and cu out of range count as clamped, for a sequence's rows and for those
+    that see its prefix; rows of no sequence stay as they are."""
+    N, T, B, D, page = 12, 3, 4, 64, 16
+    sh = Shared([100, 50], [0, 2, 4], [30, 7, 3, 0], [T] * B, 2, D, page, dtype)
+    pb, pools = sh.pb, []
+    for pool, scale in zip((pb.K, pb.V), pb.scales):    # (slots that hold nothing: zeros)
+        bits = pool.view(torch.uint8 if dtype == "e4m3" else torch.int16)
+        bits[torch.isnan(pool.float())] = 0
+        pools.append(pool.float().cpu() * scale)
+    q = torch.randn((N, Hq, D)).bfloat16()
+    ws = torch.empty(Q.qmm_prefix_attention_workspace_bytes(sh.cache, Hq, N, T), dtype=torch.uint8,
+                     device="cuda")
+    cap = pb.table.shape[1] * page
+    tokens = np.arange(0, N + 1, T) if cu is None else np.clip(cu, 0, N)
+    for first in ([-5, 2, 99], [4, 2, 0], [2 ** 31 - 1, -2 ** 31, 3], [1, 1, 1], [1, 3, 3]):
+        for plens in ([100, 50], [-3, 2 ** 31 - 1], [0, 1]):
+            sh.d_first.copy_(_dev(np.asarray(first, np.int32)))
+            sh.d_plens.copy_(_dev(np.asarray(plens, np.int32)))
+            O = torch.full((N, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+            Q.qmm_prefix_attention(sh.cache, sh.prefix, q.cuda(), O, T, workspace=ws,
+                                   cu=None if cu is None else _dev(np.asarray(cu, np.int32)))
+            want, A, S = (torch.zeros(s, dtype=torch.float64) for s in (O.shape, O.shape, O.shape[:2]))
+            inside = torch.zeros(N, dtype=torch.bool)
+            for b in range(B):
+                start, end = int(tokens[b]), int(max(tokens[b], tokens[b + 1]))
+                groups = [(min(max(first[g], 0), B), min(first[g + 1], B)) for g in range(2)]
+                g = next((i for i, (lo, hi) in enumerate(groups) if lo <= b < hi), None)
+                for i in range(min(end - start, T)):
+                    r = start + i
+                    inside[r] = True
+                    parts = [(pb.table[b], sh.lens[b] + i + 1)]
+                    if g is not None and tokens[groups[g][0]] <= r < tokens[groups[g][1]]:
+                        parts.append((pb.table[B + g], min(max(plens[g], 0), cap)))
+                    K, V, there = [], [], []
+                    for table, slots in parts:
+                        (k, v), t = _seen(pools, table, slots, page)
+                        K.append(k), V.append(v), there.append(t)
+                    there = torch.cat(there)
+                    K, V = torch.cat(K)[there], torch.cat(V)[there]
+                    x = q[r].double().view(2, -1, D)
+                    p = (torch.einsum("hgd,lhd->hgl", x, K) / 8).softmax(-1)
+                    want[r] = torch.einsum("hgl,lhd->hgd", p, V).reshape(Hq, D)
+                    A[r] = torch.einsum("hgl,lhd->hgd", p, V.abs()).reshape(Hq, D)
+                    S[r] = torch.einsum("hgd,lhd->hgl", x.abs(), K.abs()).amax(-1).reshape(Hq) / 8
+            got = O.cpu()
+            assert (got[~inside] == 7.0).all(), "a row of no sequence was written"
+            _within(got[inside], want[inside], _o_limit(dtype == "e4m3", want, A, S, D)[inside])
