@@ -38,10 +38,16 @@ namespace {
 
 constexpr int kRowShift = 7;
 constexpr int kCtasPerSm = 2;   // of either kernel
-// Query rows per KV head of all tokens up to which the kernel for 8 rows takes the call.
-// Behind 500, 4000 and 20000 tokens: 16 rows 11.8, 16.1 and 40 us; 24 rows 12.2, 19.5 and
-// 47, the tcgen05 kernel, which reads a prefix once for all of them, 16.1, 19.9 and 32.
-constexpr int kFewRows = 16;
+// The kernel for 8 rows takes calls of up to 8 query rows per KV head in all, and more where
+// the prefixes' tables are so short that reading them once for 8 rows costs less than the
+// tcgen05 kernel's longer start: slots of a table, and slots of all KV heads times the 8 rows'
+// pieces.  One prefix, BF16, the kernel for 8 rows and the tcgen05 kernel, us (measured for 2, 8
+// and 32 KV heads, 8 to 128 rows, 250 to 8000 slots; the rule's choice at most 6 % behind):
+//   8 KV heads, 16 rows   500 slots 10.1 15.7   4000 15.7 18.7   8000 21.5 20.5
+//               64 rows   500 slots 12.8 16.1   1000 16.4 17.0   2000 19.7 17.3
+//   32 KV heads, 16 rows  500 slots 12.7 16.6   1000 16.3 17.4   2000 19.5 18.8
+//   2 KV heads, 16 rows   500 slots  8.9 14.9   4000 15.7 16.6   8000 21.9 18.8
+constexpr int64_t kFewSlots = 4096, kFewReads = 80 * 1024;
 // A block takes ROWS query rows of a sequence's KV head, a thread a row and every 16th
 // (D = 128; 64: each) group of 4 columns.
 template <int D, int ROWS>
@@ -137,7 +143,10 @@ int launch_prefix_attention(const qmm_kv_cache& c, const qmm_prefix& pre, const 
     TreeParams p;
     CUtensorMap kmap, vmap;
     const int QG = Hq / c.Hkv;
-    const bool few = T * QG <= 1 << kFewRowShift && static_cast<int64_t>(N) * QG <= kFewRows;
+    const int64_t pieces = (static_cast<int64_t>(N) * QG + (1 << kFewRowShift) - 1) >> kFewRowShift;
+    const int64_t slots = static_cast<int64_t>(pre.max_pages) * c.page_size;
+    const bool few = T * QG <= 1 << kFewRowShift &&
+                     (pieces == 1 || (slots <= kFewSlots && pieces * slots * c.Hkv <= kFewReads));
     int rc = few ? tree_setup(c, q, q_stride, O, N, T, Hq, cu, parents, scale, ws,
                               kFewCtasPerSm * num_sms, kFewRowShift, kFewTileShift, kFewMinRun,
                               kFewSetup, &p, &kmap, &vmap)

@@ -6,7 +6,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_long_context_gpu import Shared, _o_limit, _prefix64, _run_prefix, _run_scored, _same, _within
+from test_long_context_gpu import PREFIX, Shared, _check_prefix, _o_limit, _prefix64, _run_prefix, \
+    _run_scored, _same, _within
 from test_paged_gpu import BF16_HALF, F32_HALF, Problem, _dev, _tree
 from split_w4a16_quantized_gb300 import qmm as Q
 
@@ -22,6 +23,30 @@ def _status():
 
 # ---- shared prefixes -----------------------------------------------------------------
 
+def _width(page, long):
+    """Pages of a table: as many as are needed, or so many that a call of more than 8 rows
+    takes the tcgen05 kernel."""
+    return 8192 // page if long else None
+
+
+@pytest.mark.parametrize("plens,first,lens,n,Hq,Hkv,D,page,dtype,layout,kind", PREFIX,
+                         ids=["%d" % i for i in range(len(PREFIX))])
+def test_prefix_of_long_tables(plens, first, lens, n, Hq, Hkv, D, page, dtype, layout, kind):
+    _check_prefix(Shared(plens, first, lens, n, Hkv, D, page, dtype, layout, width=_width(page, True)),
+                  Hq, kind)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 5])
+def test_prefix_of_long_tables_many_sequences_and_groups(n, dtype):
+    rng = np.random.default_rng(5)
+    lens = [int(v) for v in rng.integers(0, 90, 300)]
+    first = [0] + sorted(int(v) for v in rng.integers(0, 300, 39)) + [300]
+    plens = [int(v) for v in rng.integers(0, 400, 40)]
+    _check_prefix(Shared(plens, first, lens, [n] * 300, 1, 64, 16, dtype, seed=3, width=_width(16, True)), 4)
+
+
+@pytest.mark.parametrize("long", [False, True])
 @pytest.mark.parametrize("plens,first,lens,n,Hq,Hkv,D,page,layout,kind", [
     ([40], [0, 3], [5, 9, 0], [1] * 3, 8, 2, 128, 16, "hnd", "chain"),           # 12 rows
     ([40], [0, 12], list(range(12)), [1] * 12, 8, 2, 128, 16, "hnd", "chain"),   # 48
@@ -29,12 +54,13 @@ def _status():
     ([30, 61], [0, 5, 9], [5, 7, 0, 6, 3, 3, 4, 9, 1], [8] * 9, 16, 4, 128, 16, "nhd", "tree"),
     ([64], [1, 3], [5, 3, 0], [7, 9, 5], 8, 2, 64, 32, "hnd", "tree"),
 ], ids=["12", "48", "160", "groups", "ragged"])
-def test_prefix_bf16_weights_have_two_terms(plens, first, lens, n, Hq, Hkv, D, page, layout, kind):
+def test_prefix_bf16_weights_have_two_terms(plens, first, lens, n, Hq, Hkv, D, page, layout, kind,
+                                             long):
     """A BF16 cache's weights are two BF16 terms for any number of rows: the first is off by
     at most 2^-8 of the weight, the second by 2^-8 of that.  Beside it, as wholes of 2^-23
     (the tensor cores may cut where a sum would be rounded): scores of D products, in the
     weight and in their sum; sums over the positions; exp2 (2 ulp) and the divisions."""
-    sh = Shared(plens, first, lens, n, Hkv, D, page, "bf16", layout)
+    sh = Shared(plens, first, lens, n, Hkv, D, page, "bf16", layout, width=_width(page, long))
     rng = np.random.default_rng(7)
     q = torch.from_numpy(0.1 * rng.standard_normal((sh.N, Hq, D))).bfloat16()
     parents = np.concatenate([_tree(rng, m, kind) for m in n]).astype(np.int32)
