@@ -61,7 +61,7 @@ struct EvictParams {
     float* mass_out;
     int64_t layer_stride, row_stride;   // of the weights
     int *kept, *new_lens;
-    int n, keep, sinks, recent;
+    int keep, sinks, recent;
     int first;                  // this launch's first layer
     int elem, slices, lanes;    // bytes a value; pieces of a row, 16 * lanes bytes each
     int held;                   // slots that a block's shared memory holds
@@ -139,12 +139,12 @@ struct SelectShared {
     int queue[2][2 * kSelectThreads];   // evicted slots below the line, chosen ones behind
 };
 
-__device__ __forceinline__ uint32_t cluster_ld32(uint32_t addr) {
+__device__ __forceinline__ uint32_t cluster_ld_u32(uint32_t addr) {
     uint32_t v;
     asm volatile("ld.shared::cluster.u32 %0, [%1];\n" : "=r"(v) : "r"(addr) : "memory");
     return v;
 }
-__device__ __forceinline__ uint32_t cluster_ld16(uint32_t addr) {
+__device__ __forceinline__ uint32_t cluster_ld_u16(uint32_t addr) {
     uint16_t v;
     asm volatile("ld.shared::cluster.u16 %0, [%1];\n" : "=h"(v) : "r"(addr) : "memory");
     return v;
@@ -213,7 +213,7 @@ __device__ __forceinline__ void select_held(const EvictParams& p, SelectShared& 
             meet();
             if (C > 1) {
                 int sum = 0;
-                for (int r = 0; r < C; ++r) sum += cluster_ld32(cluster_map(smem_addr(&hist[tid]), r));
+                for (int r = 0; r < C; ++r) sum += cluster_ld_u32(cluster_map(smem_addr(&hist[tid]), r));
                 sh.total[tid] = sum;   // (the blocks met since it was last read)
                 __syncthreads();
             }
@@ -239,7 +239,7 @@ __device__ __forceinline__ void select_held(const EvictParams& p, SelectShared& 
     };
     // the same of the blocks before block r
     auto before_block = [&](int at, int r) {
-        const int n = lane < r ? static_cast<int>(cluster_ld32(cluster_map(smem_addr(&sh.count[at]), lane))) : 0;
+        const int n = lane < r ? static_cast<int>(cluster_ld_u32(cluster_map(smem_addr(&sh.count[at]), lane))) : 0;
         return __reduce_add_sync(0xffffffffu, n);
     };
     // a weight above the threshold, or equal to it (a threshold below everything: NaN)
@@ -291,7 +291,7 @@ __device__ __forceinline__ void select_held(const EvictParams& p, SelectShared& 
     int first_hole = 0;   // lane r: of the column's, block r's first
     if (C > 1) {
         late += before_block(2, me);
-        int n = lane < C ? static_cast<int>(cluster_ld32(cluster_map(smem_addr(&sh.count[1]), lane))) : 0;
+        int n = lane < C ? static_cast<int>(cluster_ld_u32(cluster_map(smem_addr(&sh.count[1]), lane))) : 0;
         int x = n;
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) {
@@ -313,7 +313,7 @@ __device__ __forceinline__ void select_held(const EvictParams& p, SelectShared& 
                 const int f = __shfl_sync(0xffffffffu, first_hole, k);
                 if (f <= at) r = k, from = f;
             }
-            if (yes) j = r * seg + cluster_ld16(cluster_map(smem_addr(holes + (at - from)), r));
+            if (yes) j = r * seg + cluster_ld_u16(cluster_map(smem_addr(holes + (at - from)), r));
         } else if (yes) {
             j = holes[at];
         }
@@ -558,7 +558,6 @@ int launch_kv_evict(const qmm_kv_cache* caches, int n, int first, const float* m
     p.row_stride = row_stride;
     p.kept = kept;
     p.new_lens = new_lens;
-    p.n = n;
     p.keep = keep;
     p.sinks = sinks;
     p.recent = recent;

@@ -75,7 +75,7 @@ struct MassSmem {
     int pages[2][16];                  // of the tiles being copied
     alignas(16) float nl[2][kBlock];   // -lse of a block's rows
     alignas(16) float qs[2][kBlock];   // E4M3: factor on their scores
-    long long red[2][kThreads / 32];
+    long long red[kThreads / 32];
     long long at;
     int b;
 };
@@ -100,7 +100,7 @@ __device__ __forceinline__ MassRun find_mass_run(const TreeParams& p, MassSmem& 
     for (int b = b0; b < b1; ++b)
         mine += static_cast<long long>(mass_item(sequence<true>(p, b))) * p.d.Hkv;
     if (tid == 0) sm.b = -1;
-    long long before = block_scan<kThreads>(mine, sm.red[0], &all);
+    long long before = block_scan<kThreads>(mine, sm.red, &all);
     const long long len = (all + p.ctas - 1) / p.ctas, start = len * blockIdx.x;
     if (start >= before && start < before + mine)
         for (int b = b0; b < b1; ++b) {
