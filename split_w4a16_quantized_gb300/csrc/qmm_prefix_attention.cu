@@ -15,19 +15,19 @@
 // prefix's, in that order and each in run order.  Which runs hold an item follows from the
 // units before its entry, which the attention launch's first block writes down: its CTAs
 // take all registers, so the merge could not work them out while that launch runs (64
-// sequences: 42 us, each merge block summing the list 46).
+// sequences, one BF16 term of a weight: 42 us, each merge block summing the list 46).
 //
-// What bounds it: the chain of a tile in a CTA.  64 sequences behind 8192 tokens: 42 us,
-// floor 20 (HBM); the CTAs end after 27 to 33 us, in tiles of 2000 clocks each of which
-// the softmax takes 1060 and waits 580 for scores, then 7 us of merge, a chain of four
-// trips to L2.  24 sequences of up to 8 tokens behind 16000, E4M3: 65 us, floor 13.5; a tile
-// takes 1950 clocks of a CTA, an SM's two CTAs 1000 (tensor pipe active 30 %).  48 of 4 tokens
-// behind five prefixes, D = 64: 88 us, floor 27; 1580 clocks, with the softmax at work for
-// 1030 of them.  Measured and slower: two groups of 128 rows and one CTA an SM (61, 64,
-// 115 us: items of few rows follow one another without overlap); the sequences' own part
-// and the prefixes as two launches side by side (64, 98, 136: two waves of CTAs, each with
-// its start and end); tiles that count by their rows (50, 80, 107: a few rows' tile
-// takes a CTA as long as a full one).
+// What bounds it: the chain of a tile in a CTA.  64 sequences behind 8192 tokens: 46 us,
+// floor 20 (HBM), in tiles of 2690 clocks each of which the softmax takes 1850 with both
+// terms of its weights and waits 570 for scores (tensor pipe active 44 %), then 7 us of merge,
+// a chain of four trips to L2.  24 sequences of up to 8 tokens behind 16000, E4M3: 65 us, floor
+// 13.5; a tile takes 1940 clocks of a CTA, 1020 of them softmax, an SM's two CTAs 1000 (tensor
+// pipe active 35 %).  48 of 4 tokens behind five prefixes, D = 64: 105 us, floor 27; 1940 clocks,
+// with the softmax at work for 1290 of them.  Measured and slower, with one BF16 term of a weight
+// (42, 65 and 88 us): two groups of 128 rows and one CTA an SM (61, 64, 115 us: items of few rows
+// follow one another without overlap); the sequences' own part and the prefixes as two launches
+// side by side (64, 98, 136: two waves of CTAs, each with its start and end); tiles that count by
+// their rows (50, 80, 107: a few rows' tile takes a CTA as long as a full one).
 #include <algorithm>
 
 #include "qmm.h"
@@ -42,12 +42,13 @@ constexpr int kCtasPerSm = 2;   // of either kernel
 // the prefixes' tables are so short that reading them once for 8 rows costs less than the
 // tcgen05 kernel's longer start: slots of a table, and slots of all KV heads times the 8 rows'
 // pieces.  One prefix, BF16, the kernel for 8 rows and the tcgen05 kernel, us (measured for 2, 8
-// and 32 KV heads, 8 to 128 rows, 250 to 8000 slots; the rule's choice at most 6 % behind):
+// and 32 KV heads, 12 to 128 rows, 250 to 8000 slots; the rule's choice at most 7 % behind):
 //   8 KV heads, 16 rows   500 slots 10.1 15.7   4000 15.7 18.7   8000 21.5 20.5
 //               64 rows   500 slots 12.8 16.1   1000 16.4 17.0   2000 19.7 17.3
 //   32 KV heads, 16 rows  500 slots 12.7 16.6   1000 16.3 17.4   2000 19.5 18.8
 //   2 KV heads, 16 rows   500 slots  8.9 14.9   4000 15.7 16.6   8000 21.9 18.8
-constexpr int64_t kFewSlots = 4096, kFewReads = 80 * 1024;
+// (8 rows: 8 KV heads 8000 slots 18.4 20.2, 20000 28.7 28.8; 2 KV heads 8000 21.3 18.5.)
+constexpr int64_t kFewSlots = 4096, kFewReads = 96 * 1024;
 // A block takes ROWS query rows of a sequence's KV head, a thread a row and every 16th
 // (D = 128; 64: each) group of 4 columns.
 template <int D, int ROWS>
