@@ -19,7 +19,7 @@
 // Positions of several axes (qmm_kv_append_axes): pair j turns by the position of
 // axis[j], so neighbouring pairs may take their cosines and sines from different rows of
 // the table.  A token's threads gather them once, a value each, and share them (9001 tokens
-// of 40 heads into an E4M3 cache: 48.7 us, each lane its own 49.4; floor 30.5.  Bound by
+// of 40 heads into an E4M3 cache: 49.0 us, each lane its own 50.4, timed in turn; floor 30.5.  Bound by
 // instructions, 70 % of the issue slots: norm, rotation and the division by the scale).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>

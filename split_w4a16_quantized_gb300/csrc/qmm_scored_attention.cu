@@ -9,7 +9,7 @@
 //     4 bytes a row and position beside the 4 D of K and V, and the merge kernel's other
 //     blocks add the weights up;
 //     (32 sequences of 1024 to 8192: 89 us, floor 68, tree attention alone 78; scores formed
-//     again from K 223.  64 of 300 to 12000, E4M3, D = 64, 8 rows: 87 us, floor 33: 70 the
+//     again from K 223.  64 of 300 to 12000, E4M3, D = 64, 8 rows: 88 us, floor 33: 70 the
 //     attention kernel, bound as for tree attention by a tile's chain of conversions,
 //     products and exp2; the scores are as many bytes as a quarter of K and V.)
 //   more rows: the scores are formed again from K (qmm_mass_tc.cu), behind attention and
