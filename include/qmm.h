@@ -851,8 +851,9 @@ int qmm_tree_accept(const qmm_kv_cache *caches, int n, const int *tokens, const 
  * Slots of the call's own tokens start at 0, whatever stood there, and those behind them
  * are left alone.  The weights are the softmax's own, not as rounded for the product
  * with V.  A slot without a page, and every slot of a sequence without tokens, keeps
- * decay times its sum.  A row that is not a number (of q, or of a key that it sees) makes
- * NaN of the slots that it sees alone.
+ * decay times its sum.  A row that is not a number, because of q or of a key that it sees,
+ * makes NaN of the slots that it sees and of no others.  There is no form with shared prefixes
+ * (qmm_prefix) or with trees.
  *   mass   device FP32 [B, Hkv, mass_stride], 16-byte aligned, mass_stride a multiple of
  *          4 and at least max_pages * page_size.  Overlaps nothing else of the call
  *   decay  0 or more, finite; with 0 the old sums are not read
